@@ -58,8 +58,9 @@ DEFAULT_WORKLOAD = "mlp_moe_large"
 METRIC = "Muon NS step matrices/s + TFLOP/s and % bf16 MFMA peak, 1\u00d7MI355X"
 ADAMW_METRIC = "adamw route elements/s (owner 1-D parameters), 1\u00d7MI355X"
 ADAMW_DEFAULT_WORKLOAD = "adamw_stream"
-# sources that decide what a launch does: the kernels and the planner (grouping, tiling)
-KERNELS_SRC = [os.path.join(ROOT, "matrix_optimizer_muon_amd", "csrc", f) for f in ("kernels.hip", "abi.cpp")]
+# sources that decide what a launch of the step does: the contraction core, the kernels and
+# the planner (grouping, tiling)
+KERNELS_SRC = [os.path.join(ROOT, "matrix_optimizer_muon_amd", "csrc", f) for f in ("core.hpp", "kernels.hip", "abi.cpp")]
 PROFILES = os.path.join(ROOT, "profiles")
 
 
