@@ -15,7 +15,9 @@
  *     W ← (1 − lr·wd)·W − lr·O;  optionally P = bf16(W) (the published copy)
  *
  *   and, for the owner's small and 1-D parameters (the "adamw" route), one
- *   AdamW step per element (dmuon_adamw_step).
+ *   AdamW step per element (dmuon_adamw_step); and the training operators that
+ *   produce gradients in the layout the steps read (dmuon_linear_ce,
+ *   dmuon_embedding, dmuon_ckpt8_*).
  *
  *   DMuon "架构设计" (Architecture design) page, §1 (the Newton–Schulz
  *   equation with coefficients α, β, γ = a, b, c) and §2 (the owner alone runs
@@ -47,8 +49,9 @@
  * - DMUON_TEST_FAIL_AT (environment, for failure-handling tests) makes a valid
  *   call return DMUON_E_HIP at a named point as a failed HIP call would:
  *   "plan" (before anything is enqueued), "table" (the table copy) or a phase
- *   name ("ingest", "norm", "gram", "square", "apply", "update", "adamw": that
- *   phase's first launch, the earlier launches being enqueued).
+ *   name ("ingest", "norm", "gram", "square", "apply", "update", "adamw", or one of
+ *   the training gradients' phases 8 to 15 below: that phase's first launch, the
+ *   earlier launches being enqueued).
  * - DMUON_DEBUG_SYNC (environment, for debugging; set and not "0") waits for
  *   each launch to finish before the next is enqueued, so a call returns only
  *   when its work is done, and returns DMUON_E_HIP naming the launch ("table"
@@ -58,7 +61,8 @@
  *   then gives a message (thread-local, valid until the next call on the thread).
  * - After DMUON_E_HIP (a HIP launch/copy failed after validation) the contents
  *   of the momentum, master and output buffers are unspecified.
- * - Non-finite inputs are not checked; they propagate.
+ * - Non-finite inputs are not checked; they propagate.  Device data (ids, targets,
+ *   offsets) is not checked either; the training operators define every value.
  * - Results are deterministic: identical inputs give bit-identical outputs
  *   (fixed-order reductions, no floating-point atomics).
  */
@@ -301,6 +305,131 @@ int dmuon_adamw_step_workspace_size(const dmuon_adamw_tensor* tensors, int32_t n
 int dmuon_adamw_step(const dmuon_adamw_tensor* tensors, int32_t n_tensors, const dmuon_adamw_cfg* cfg,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- training gradients -------------------------------------------------
+ * The operators that produce the gradients the two routes step: the loss at the
+ * head, the embedding table, and the weight gradient of a linear layer whose
+ * input was kept in 8 bits.  The architecture page §2 and the routing page's route
+ * table take these gradients as given (embeddings and lm_head on an AdamW route);
+ * the operators are this library's own.  Types: bf16 or fp32; bf16 products run on
+ * the bf16 matrix cores with fp32 accumulation; fp32 operands enter them as three
+ * bf16 terms whose sum is the fp32 value, so fp32 products keep fp32 accuracy.
+ * Matrices are row-major with the last dim contiguous; a row stride (ld*, in
+ * elements) may exceed the row.  Outputs are dense.  Every sum has a fixed order.
+ * Alignment never matters for correctness: 16-byte aligned rows are read in place
+ * or with 16-byte accesses, other rows are copied or read element by element.
+ * Data on the device is not validated on the host; what an id, target or offset
+ * out of range does is stated at each entry point. */
+
+typedef enum { DMUON_I32 = 0, DMUON_I64 = 1 } dmuon_index_dtype;
+
+/* Softmax cross entropy of `tokens` hidden states against a vocabulary:
+ *   z(t, v) = Σ_d h(t, d)·w(v, d)
+ *   lse(t) = log Σ_v exp z(t, v),   loss(t) = lse(t) − z(t, target(t))
+ * The logits are computed in pieces of the vocabulary and never kept.
+ *   dtype        dmuon_dtype of h and w (and of grad_h, grad_w)
+ *   index_dtype  dmuon_index_dtype of targets
+ *   h            device [tokens, width], row stride ldh
+ *   w            device [vocab, width], row stride ldw
+ *   targets      device [tokens]; a token whose target equals ignore_index has
+ *                loss 0, lse 0 and no part in any gradient, whatever its hidden
+ *                state holds; any other target outside [0, vocab) gives a loss of
+ *                NaN and no gradient
+ * 0 ≤ tokens ≤ 2^24, 1 ≤ width ≤ 65536, 1 ≤ vocab ≤ 2^30. */
+typedef struct {
+  int64_t tokens, width, vocab;
+  int32_t dtype;
+  int32_t index_dtype;
+  const void* h;
+  int64_t ldh;
+  const void* w;
+  int64_t ldw;
+  const void* targets;
+  int64_t ignore_index;
+} dmuon_ce_problem;
+
+/* Bytes of workspace of dmuon_linear_ce (backward = 0) or dmuon_linear_ce_backward
+ * (backward = 1) on this problem (host only, no HIP call; the pointers count: their
+ * alignment decides whether w is copied). */
+int dmuon_linear_ce_workspace_size(const dmuon_ce_problem* problem, int32_t backward, size_t* bytes);
+
+/* losses, lse: device fp32 [tokens]. */
+int dmuon_linear_ce(const dmuon_ce_problem* problem, float* losses, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* With dz(t, v) = grad_losses(t)·(exp(z(t, v) − lse(t)) − [v = target(t)]):
+ *   grad_h = dz·w  [tokens, width],   grad_w = dzᵀ·h  [vocab, width]
+ * lse: as dmuon_linear_ce returned it (or the joined value of a sharded
+ * vocabulary).  grad_losses: device fp32 [tokens], for a mean 1/n at every token;
+ * a token whose value is 0 is treated as ignored.  grad_h, grad_w: device, dense,
+ * of the problem's dtype, fully written; NULL where not wanted.  For bf16, dz is
+ * rounded to bf16 once (relative to the largest |grad_losses|). */
+int dmuon_linear_ce_backward(const dmuon_ce_problem* problem, const float* lse, const float* grad_losses,
+                             void* grad_h, void* grad_w, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* out(t) = scale·table(ids(t)), rounded once; zeros for an id outside [0, rows)
+ * (so a shard of a table can be looked up with shifted ids).  table: device
+ * [rows, width], row stride ldt, dtype; out: device [tokens, width], same dtype.
+ * tokens, rows ≤ 2^30, 1 ≤ width ≤ 65536, scale finite. */
+int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const void* table, int64_t ldt,
+                    int64_t rows, int64_t width, int32_t dtype, float scale, void* out, void* stream);
+
+/* The gradient of the lookup: grad_table(v) = scale·Σ over the tokens with id v of
+ * grad_out(t), the tokens in rising order in fixed groups (they are sorted by id),
+ * fp32 sums, rounded once to out_dtype.  Ids outside [0, rows) and equal to
+ * padding_id (−1: none) contribute nothing.  grad_out: device [tokens, width], row
+ * stride ldg, grad_dtype.  grad_table: device [rows, width], out_dtype, fully
+ * written; with accumulate = 1 the sum is added to what it holds (for a table tied
+ * to the head) and rows without tokens are left as they are. */
+int dmuon_embedding_backward_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t* bytes);
+int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t tokens, const void* grad_out,
+                             int64_t ldg, int32_t grad_dtype, int64_t rows, int64_t width, float scale,
+                             int64_t padding_id, void* grad_table, int32_t out_dtype, int32_t accumulate,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Activation checkpoints in 8 bits.  The 32 columns 32j … 32j + 31 of a row (fewer
+ * at its end) share the byte exps(row, j) = b and hold q·2^(b − 133), q a signed
+ * byte: b is the biased fp32 exponent of their largest magnitude, or one more where
+ * that would round to 128 (not past 254, where q saturates at ±127), and
+ * q = rint(x·2^(133 − b)), half to even.  So every value is kept to within half a
+ * step 2^(b − 134), at most 2^−7 of the block's largest.  Blocks below 2^−126 become
+ * zeros (b = 0); a block with an infinity or NaN reads back as NaN throughout
+ * (b = 255).  Every value is exact in bf16.
+ * x: device [rows, cols], row stride ldx; q: device int8 [rows, cols]; exps: device
+ * uint8 [rows, ceil(cols/32)]; out: device [rows, cols].  rows ≤ 2^30, cols ≤ 65536. */
+int dmuon_ckpt8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* q,
+                         uint8_t* exps, void* stream);
+int dmuon_ckpt8_dequantize(const int8_t* q, const uint8_t* exps, int64_t rows, int64_t cols, void* out,
+                           int32_t dtype, void* stream);
+
+/* The weight gradient of y = x·Wᵀ from the kept x (W is n×k):
+ *   out(n, k) = Σ_t grad_out(t, n)·x(t, k),   x(t, k) = q(t, k)·2^(b(t, k/32) − 133)
+ * grad_out: device [tokens, n], row stride ldg, grad_dtype; q, exps: as written by
+ * dmuon_ckpt8_quantize for [tokens, k]; out: device [n, k], out_dtype, fully
+ * written, the layout dmuon_tensor reads a gradient in.
+ * With offsets (device int32 [groups + 1], NULL for one product over all tokens),
+ * out is [groups, n, k] and group g sums the rows offsets(g) … offsets(g + 1) − 1
+ * (the tokens of one expert; an empty group gives zeros); rows outside every group
+ * are not used.  Offsets are clamped to [0, tokens], a falling one makes an empty
+ * group.  groups ≤ 2^20 (ignored without offsets). */
+typedef struct {
+  int64_t tokens, n, k;
+  int32_t grad_dtype;
+  int32_t out_dtype;
+  const void* grad_out;
+  int64_t ldg;
+  const int8_t* q;
+  const uint8_t* exps;
+  const int32_t* offsets;
+  int32_t groups;
+  int32_t reserved;         /* must be 0 */
+  void* out;
+} dmuon_ckpt8_wgrad_problem;
+
+int dmuon_ckpt8_wgrad_workspace_size(const dmuon_ckpt8_wgrad_problem* problem, size_t* bytes);
+int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* problem, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* Plain NT product C = A·Bᵀ on the matrix-core kernel the step uses (a test hook
  * for the contraction core).  A: M×K (lda elements per row), B: N×K (ldb), both
  * dtype (bf16 or fp32), device; C: M×N fp32 (ldc), device.  lda and ldb must be
@@ -351,7 +480,9 @@ int dmuon_debug_slice_buffers(const dmuon_tensor* tensors, int32_t n_tensors, co
  * each phase p < n the summed milliseconds ms[p] and the launch count count[p],
  * then clears the record.  Phases: 0 ingest (momentum, partial norms, operand
  * copies), 1 norm finalize, 2 Gram, 3 square+poly, 4 apply, 5 update (k = 0
- * only), 6 gemm_nt, 7 adamw. */
+ * only), 6 gemm_nt, 7 adamw, and of the training gradients 8 ce_pack (list of
+ * tokens, operand copies), 9 ce_logits, 10 ce_rows (losses), 11 ce_grads (the two
+ * products), 12 embed, 13 embed_grad (sort and sums), 14 ckpt_codec, 15 ckpt_wgrad. */
 int dmuon_phase_timing(int32_t enable);
 int dmuon_phase_timing_read(double* ms, int64_t* count, int32_t n);
 

@@ -9,16 +9,23 @@ unless a ``stream`` is given.
     adamw_step(params, grads, exp_avgs, exp_avg_sqs, step=1, ...)  # the "adamw" route
     ns_batched(x, coeffs=(3.4445, -4.775, 2.0315), steps=5, ...)
     lpt_assign(rows, cols, batch, layer_id, n_slots, ...)   # host only
+
+and, from ``training``, the operators that produce gradients the steps read:
+cross entropy over a large vocabulary, embedding, 8-bit activation checkpoints.
 """
 from __future__ import annotations
 
 import ctypes
 
 from . import _binding as _b
+from .training import (checkpoint_dequantize, checkpoint_quantize, checkpoint_wgrad, embedding,  # noqa: F401
+                       embedding_backward, linear_cross_entropy, linear_cross_entropy_backward)
 from .workloads import HYPER  # noqa: F401
 
 __all__ = ["muon_step", "muon_step_workspace_size", "adamw_step", "MuonStep", "AdamwStep",
            "ns_batched", "lpt_assign", "gemm_nt",
+           "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
+           "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize", "checkpoint_wgrad",
            "phase_timing", "phase_timing_read", "abi_version", "load_library", "HYPER"]
 
 QUINTIC = (HYPER["a"], HYPER["b"], HYPER["c"])

@@ -29,13 +29,20 @@ ERRORS = {
 }
 F32, BF16 = 0, 1
 PREC = {"bf16": 0, "f32": 1}
-PHASES = ["ingest", "norm", "gram", "square", "apply", "update", "gemm_nt", "adamw"]
+I32, I64 = 0, 1
+PHASES = ["ingest", "norm", "gram", "square", "apply", "update", "gemm_nt", "adamw",
+          "ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec",
+          "ckpt_wgrad"]
 EXPORTED = ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_muon_step",
             "dmuon_muon_step_prepare", "dmuon_muon_step_run", "dmuon_muon_step_noalloc",
             "dmuon_ns_batched_workspace_size",
             "dmuon_ns_batched", "dmuon_lpt_assign", "dmuon_adamw_step_workspace_size",
             "dmuon_adamw_step", "dmuon_gemm_nt", "dmuon_phase_timing", "dmuon_phase_timing_read",
-            "dmuon_debug_slice_buffers", "dmuon_last_error", "dmuon_abi_version"]
+            "dmuon_debug_slice_buffers", "dmuon_last_error", "dmuon_abi_version",
+            "dmuon_linear_ce_workspace_size", "dmuon_linear_ce", "dmuon_linear_ce_backward",
+            "dmuon_embedding", "dmuon_embedding_backward_workspace_size",
+            "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
+            "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad"]
 ABI_VERSION = 5
 
 
@@ -79,6 +86,22 @@ class AdamwCfg(ctypes.Structure):
                 ("grad_scale", ctypes.c_float), ("step", ctypes.c_int32)]
 
 
+class CeProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("index_dtype", ctypes.c_int32),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("targets", ctypes.c_void_p),
+                ("ignore_index", ctypes.c_int64)]
+
+
+class Ckpt8WgradProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("grad_out", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("exps", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("groups", ctypes.c_int32), ("reserved", ctypes.c_int32), ("out", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -109,6 +132,17 @@ def lib():
     L.dmuon_debug_slice_buffers.argtypes = [P(Tensor), i32, P(StepCfg), vp, sz, i32, i64, P(DebugSlice)]
     L.dmuon_phase_timing.argtypes = [i32]
     L.dmuon_phase_timing_read.argtypes = [vp, vp, i32]
+    L.dmuon_linear_ce_workspace_size.argtypes = [P(CeProblem), i32, P(sz)]
+    L.dmuon_linear_ce.argtypes = [P(CeProblem), vp, vp, vp, sz, vp]
+    L.dmuon_linear_ce_backward.argtypes = [P(CeProblem), vp, vp, vp, vp, vp, sz, vp]
+    L.dmuon_embedding.argtypes = [vp, i32, i64, vp, i64, i64, i64, i32, f32, vp, vp]
+    L.dmuon_embedding_backward_workspace_size.argtypes = [i64, i64, i64, P(sz)]
+    L.dmuon_embedding_backward.argtypes = [vp, i32, i64, vp, i64, i32, i64, i64, f32, i64, vp, i32, i32,
+                                           vp, sz, vp]
+    L.dmuon_ckpt8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.dmuon_ckpt8_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, vp]
+    L.dmuon_ckpt8_wgrad_workspace_size.argtypes = [P(Ckpt8WgradProblem), P(sz)]
+    L.dmuon_ckpt8_wgrad.argtypes = [P(Ckpt8WgradProblem), vp, sz, vp]
     L.dmuon_last_error.restype = ctypes.c_char_p
     L.dmuon_last_error.argtypes = []
     L.dmuon_abi_version.restype = i32
@@ -116,7 +150,11 @@ def lib():
                  "dmuon_muon_step_prepare", "dmuon_muon_step_run", "dmuon_muon_step_noalloc",
                  "dmuon_ns_batched_workspace_size", "dmuon_ns_batched", "dmuon_lpt_assign",
                  "dmuon_adamw_step_workspace_size", "dmuon_adamw_step",
-                 "dmuon_gemm_nt", "dmuon_phase_timing", "dmuon_phase_timing_read"]:
+                 "dmuon_gemm_nt", "dmuon_phase_timing", "dmuon_phase_timing_read",
+                 "dmuon_linear_ce_workspace_size", "dmuon_linear_ce", "dmuon_linear_ce_backward",
+                 "dmuon_embedding", "dmuon_embedding_backward_workspace_size",
+                 "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
+                 "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad"]:
         getattr(L, name).restype = ctypes.c_int
     if L.dmuon_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH} has ABI {L.dmuon_abi_version()}, expected {ABI_VERSION}: rebuild it")

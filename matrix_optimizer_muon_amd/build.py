@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdmuon_ns.so")
 PROBE_LIB = os.path.join(HERE, "libdmuon_probe.so")
 OBJ = os.path.join(HERE, "_build")
-SOURCES = ["kernels.hip", "abi.cpp", "lpt.cpp"]
+SOURCES = ["kernels.hip", "grads.hip", "abi.cpp", "grads.cpp", "lpt.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 ARCH = os.environ.get("DMUON_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

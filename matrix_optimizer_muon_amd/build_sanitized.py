@@ -4,7 +4,7 @@
 
 The host sources (argument validation, planning, table building, LPT) are
 compiled by g++ with AddressSanitizer and UndefinedBehaviorSanitizer; the HIP
-kernels are linked from the regular build's object unchanged (no GPU code is
+kernels are linked from the regular build's objects unchanged (no GPU code is
 instrumented).  A Python process loads the result with the ASan runtime
 preloaded (``LD_PRELOAD``) and ``DMUON_LIBRARY`` pointing at it.
 """
@@ -16,7 +16,8 @@ import sys
 
 from . import build as _build
 
-HOST_SOURCES = ["abi.cpp", "lpt.cpp"]
+HOST_SOURCES = ["abi.cpp", "grads.cpp", "lpt.cpp"]
+KERNEL_SOURCES = ["kernels.hip", "grads.hip"]
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer"]
 
 
@@ -27,8 +28,8 @@ def asan_runtime() -> str:
 
 def build(out_dir: str) -> str:
     os.makedirs(out_dir, exist_ok=True)
-    kobj = os.path.join(_build.OBJ, "kernels.hip.o")
-    if not os.path.exists(kobj):
+    kobjs = [os.path.join(_build.OBJ, src + ".o") for src in KERNEL_SOURCES]
+    if not all(os.path.exists(o) for o in kobjs):
         _build.build()
     objs = []
     for src in HOST_SOURCES:
@@ -41,7 +42,7 @@ def build(out_dir: str) -> str:
             raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}{r.stderr}")
         objs.append(obj)
     lib = os.path.join(out_dir, "libdmuon_ns_san.so")
-    cmd = ["g++", "-shared", *SAN, *objs, kobj, "-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib",
+    cmd = ["g++", "-shared", *SAN, *objs, *kobjs, "-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib",
            "-lamdhip64", "-o", lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

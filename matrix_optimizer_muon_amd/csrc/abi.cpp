@@ -18,13 +18,14 @@
 #include <vector>
 
 #include "../../include/dmuon_ns.h"
+#include "host.hpp"
 #include "internal.hpp"
 
 namespace dmuon {
 
 static thread_local std::string g_err;
 
-static int fail(int code, const std::string& msg) {
+int fail(int code, const std::string& msg) {
   g_err = msg;
   return code;
 }
@@ -107,13 +108,11 @@ static uint32_t fnv1a(const char* p, size_t n) {
 // the next is enqueued and returns DMUON_E_HIP naming the launch whose wait
 // reported an error, so an asynchronous fault is tied to its phase.  The wait
 // is skipped on a stream under graph capture, where it is not allowed.
-static const char* const kPhaseNames[PH_COUNT] = {"ingest", "norm",   "gram",    "square",
-                                                  "apply",  "update", "gemm_nt", "adamw"};
-struct CallEnv {
-  int where = -3;     // -3 none, -2 plan, -1 table, else a phase id
-  bool sync = false;  // DMUON_DEBUG_SYNC
-};
-static CallEnv call_env() {
+static const char* const kPhaseNames[PH_TOTAL] = {
+    "ingest",  "norm",      "gram",    "square",   "apply", "update",     "gemm_nt",    "adamw",
+    "ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec", "ckpt_wgrad"};
+const char* phase_name(int phase) { return kPhaseNames[phase]; }
+CallEnv call_env() {
   CallEnv f;
   const char* d = std::getenv("DMUON_DEBUG_SYNC");
   f.sync = d && *d && std::strcmp(d, "0") != 0;
@@ -121,15 +120,15 @@ static CallEnv call_env() {
   if (!v) return f;
   if (std::strcmp(v, "plan") == 0) f.where = -2;
   else if (std::strcmp(v, "table") == 0) f.where = -1;
-  for (int i = 0; i < PH_COUNT; ++i)
+  for (int i = 0; i < PH_TOTAL; ++i)
     if (std::strcmp(v, kPhaseNames[i]) == 0) f.where = i;
   return f;
 }
-static int forced(const CallEnv& f, int where) {
+int forced(const CallEnv& f, int where) {
   if (f.where != where) return DMUON_OK;
   return fail(DMUON_E_HIP, std::string("forced failure (DMUON_TEST_FAIL_AT=") + std::getenv("DMUON_TEST_FAIL_AT") + ")");
 }
-static int settle(const CallEnv& f, void* stream, const char* what) {
+int settle(const CallEnv& f, void* stream, const char* what) {
   if (!f.sync) return DMUON_OK;
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   int r = (int)hipStreamIsCapturing((hipStream_t)stream, &cs);
@@ -183,8 +182,6 @@ static std::vector<char> seal(Plan& pl) {
   fill();
   return host;
 }
-
-static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Lay out the workspace for the items; with base == nullptr only sizes are computed.
 static int build_plan(const std::vector<Item>& items, int prec_f32, Plan& pl, char* base) {
@@ -449,12 +446,7 @@ static int launch_groups(GroupPlan& gp, char* ws, int prec_f32, const LaunchScal
 // ---------------------------------------------------------------------------
 // validation helpers
 // ---------------------------------------------------------------------------
-struct Range {
-  uintptr_t lo, hi;
-  bool ro;
-};
-
-static int check_alias(std::vector<Range>& rs) {
+int check_alias(std::vector<Range>& rs) {
   std::sort(rs.begin(), rs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
   // sweep: any writable range must not intersect any other range
   uintptr_t max_hi_any = 0, max_hi_w = 0;
@@ -520,7 +512,7 @@ static int collect_items(const dmuon_tensor* t, int32_t n, std::vector<Item>& it
   return DMUON_OK;
 }
 
-static int check_workspace(void* ws, size_t have, size_t need) {
+int check_workspace(void* ws, size_t have, size_t need) {
   if (need == 0) return DMUON_OK;
   if (!ws) return fail(DMUON_E_WORKSPACE, "workspace is NULL");
   if ((uintptr_t)ws & 255) return fail(DMUON_E_WORKSPACE, "workspace must be 256-byte aligned");

@@ -1,0 +1,797 @@
+// C entry points of the training gradients: cross entropy over a large
+// vocabulary, embedding lookup and gradient, 8-bit activation checkpoints and the
+// weight gradient computed from them.  Validation and planning on the host, then
+// launches on the caller's stream; every buffer is the caller's.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <string>
+#include <vector>
+
+#include "../../include/dmuon_ns.h"
+#include "grads.hpp"
+#include "host.hpp"
+
+namespace dmuon {
+namespace {
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 24;    // rows of one cross-entropy or wgrad call
+constexpr int64_t kMaxIds = (int64_t)1 << 30;       // ids of one embedding call
+constexpr int64_t kMaxWidth = 65536;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;      // vocabulary, table rows
+constexpr int64_t kMaxLd = (int64_t)1 << 20;        // row strides the kernels take in place
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+// C entry bodies: nothing thrown on the host (an allocation that fails) leaves them
+template <typename F>
+int guarded(F&& f) {
+  clear_error();
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(DMUON_E_HIP, std::string("host error: ") + e.what());
+  }
+}
+
+int hip_fail(int e) { return fail(DMUON_E_HIP, std::string("launch failed: ") + hip_error_string(e)); }
+
+// one launch under the debugging switches
+template <typename F>
+int go(const CallEnv& env, int phase, void* stream, F&& launch) {
+  int e = forced(env, phase);
+  if (e) return e;
+  const int r = launch();
+  if (r) return hip_fail(r);
+  return settle(env, stream, phase_name(phase));
+}
+
+bool float_type(int32_t t) { return t == DMUON_F32 || t == DMUON_BF16; }
+int64_t type_bytes(int32_t t) { return t == DMUON_F32 ? 4 : 2; }
+bool index_type(int32_t t) { return t == DMUON_I32 || t == DMUON_I64; }
+
+void add_range(std::vector<Range>& rs, const void* p, int64_t bytes, bool ro) {
+  if (p && bytes > 0) rs.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, ro});
+}
+int64_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  return rows > 0 ? ((rows - 1) * ld + cols) * es : 0;
+}
+
+// the workspace's size, and that it meets none of the call's buffers
+int check_ws(void* ws, size_t have, size_t need, const std::vector<Range>& rs) {
+  int e = check_workspace(ws, have, need);
+  if (e) return e;
+  const uintptr_t lo = (uintptr_t)ws, hi = lo + need;
+  for (const Range& r : rs)
+    if (r.lo < hi && lo < r.hi) return fail(DMUON_E_ALIAS, "workspace overlaps a buffer of the call");
+  return DMUON_OK;
+}
+
+struct Carver {
+  char* base;
+  size_t off = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = base ? (T*)(base + off) : nullptr;
+    off = align256(off + (size_t)std::max<int64_t>(n, 1) * sizeof(T));
+    return p;
+  }
+};
+
+// K splits of a product with few tiles, so that all 256 CUs have work: whole
+// stages of 32, at least 8 of them per workgroup
+int pick_splits(int64_t tiles, int64_t k) {
+  const int64_t stages = cdiv(k, 32);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), stages / 8));
+}
+
+// May the core read this bf16 matrix K-major in place?  16-byte rows, and no tile
+// column may reach past the last row's end: the rows touch, or whole tiles.
+bool kmajor_in_place(const void* p, int64_t ld, int64_t cols) {
+  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && ld <= kMaxLd && (ld == cols || cols % kTile == 0);
+}
+
+// ---- cross entropy ------------------------------------------------------------
+// Bytes of gradient logits (and operand copies of W) that one piece of the
+// vocabulary may take.
+constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+
+struct CePlan {
+  bool f32, direct_w;
+  int planes;
+  int64_t T, D, V, ldd, piece, ldz;
+  int tiles_t, tiles_v, splits_h, splits_w;
+  // workspace
+  int32_t *rows, *pos, *tgt, *count;
+  float *clse, *cg, *gmax, *zt, *part_h, *part_w;
+  uint16_t *h, *w, *dz;
+  CeStat* stats;
+  size_t bytes;
+};
+
+CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
+  CePlan pl{};
+  pl.f32 = p.dtype == DMUON_F32;
+  pl.planes = pl.f32 ? kPlanes : 1;
+  pl.T = p.tokens;
+  pl.D = p.width;
+  pl.V = p.vocab;
+  pl.ldd = round_up(pl.D, kLdAlign);
+  pl.direct_w = !pl.f32 && pl.D % kLdAlign == 0 && kmajor_in_place(p.w, p.ldw, pl.D);
+  // the piece: gradient logits of every token (backward) and the copy of W's rows
+  const int64_t per_row = (backward ? pl.T * 2 * pl.planes : 0) + (pl.direct_w ? 0 : pl.ldd * 2 * pl.planes);
+  int64_t piece = per_row ? std::max<int64_t>(kPieceBytes / per_row, 8 * kTile) : pl.V;
+  const int64_t n = cdiv(pl.V, std::min(piece, pl.V));
+  pl.piece = std::min(round_up(cdiv(pl.V, n), kTile), round_up(pl.V, kTile));
+  pl.ldz = round_up(std::min(pl.piece, pl.V), kLdAlign);
+  pl.tiles_t = (int)cdiv(pl.T, kTile);
+  pl.tiles_v = (int)cdiv(pl.V, kTile);
+  const int64_t td = cdiv(pl.D, kTile), piece_rows = std::min(pl.piece, pl.V);
+  pl.splits_h = pick_splits(pl.tiles_t * td, piece_rows);
+  pl.splits_w = pick_splits(cdiv(piece_rows, kTile) * td, pl.T);
+  Carver c{base};
+  pl.rows = c.take<int32_t>(pl.T);
+  pl.tgt = c.take<int32_t>(pl.T);
+  pl.count = c.take<int32_t>(1);
+  pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
+  if (!pl.direct_w) pl.w = c.take<uint16_t>(pl.planes * piece_rows * pl.ldd);
+  if (backward) {
+    pl.pos = c.take<int32_t>(pl.T);
+    pl.clse = c.take<float>(pl.T);
+    pl.cg = c.take<float>(pl.T);
+    pl.gmax = c.take<float>(1);
+    pl.dz = c.take<uint16_t>(pl.planes * pl.T * pl.ldz);
+    pl.part_h = c.take<float>(pl.splits_h * pl.T * pl.ldd);
+    if (pl.splits_w > 1) pl.part_w = c.take<float>(pl.splits_w * piece_rows * pl.ldd);
+  } else {
+    pl.zt = c.take<float>(pl.T);
+    pl.stats = c.take<CeStat>((int64_t)pl.tiles_v * pl.T);
+  }
+  pl.bytes = c.off;
+  return pl;
+}
+
+int check_ce(const dmuon_ce_problem* p, std::vector<Range>* rs) {
+  if (!p) return fail(DMUON_E_NULL, "problem is NULL");
+  if (!float_type(p->dtype)) return fail(DMUON_E_DTYPE, "dtype must be DMUON_F32 or DMUON_BF16");
+  if (!index_type(p->index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
+  if (p->tokens < 0 || p->tokens > kMaxTokens) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^24]");
+  if (p->width < 1 || p->width > kMaxWidth) return fail(DMUON_E_SHAPE, "width must be in [1, 65536]");
+  if (p->vocab < 1 || p->vocab > kMaxRows) return fail(DMUON_E_SHAPE, "vocab must be in [1, 2^30]");
+  if (p->ldh < p->width || p->ldw < p->width || p->ldh > kMaxStride || p->ldw > kMaxStride)
+    return fail(DMUON_E_SHAPE, "ldh and ldw must be at least width");
+  if (cdiv(p->tokens, kTile) * cdiv(p->vocab, kTile) > INT32_MAX) return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
+  if (p->tokens > 0 && (!p->h || !p->targets)) return fail(DMUON_E_NULL, "h and targets must be set");
+  if (!p->w) return fail(DMUON_E_NULL, "w must be set");
+  if (rs) {
+    const int64_t es = type_bytes(p->dtype);
+    add_range(*rs, p->h, strided_bytes(p->tokens, p->width, p->ldh, es), true);
+    add_range(*rs, p->w, strided_bytes(p->vocab, p->width, p->ldw, es), true);
+    add_range(*rs, p->targets, p->tokens * (p->index_dtype == DMUON_I64 ? 8 : 4), true);
+  }
+  return DMUON_OK;
+}
+
+// the compact list of tokens and the operand copy of their hidden states
+int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const float* lse_in, const float* grad_losses,
+             float* losses, float* lse, const CallEnv& env, void* stream) {
+  CeScanArgs s{};
+  s.targets = p.targets;
+  s.idx64 = p.index_dtype == DMUON_I64;
+  s.backward = backward;
+  s.ignore = p.ignore_index;
+  s.tokens = (int32_t)pl.T;
+  s.vocab = (int32_t)pl.V;
+  s.grad_losses = grad_losses;
+  s.lse_in = lse_in;
+  s.losses = losses;
+  s.lse = lse;
+  s.rows = pl.rows;
+  s.pos = pl.pos;
+  s.tgt = pl.tgt;
+  s.clse = pl.clse;
+  s.cg = pl.cg;
+  s.count = pl.count;
+  s.gmax = pl.gmax;
+  int e = go(env, PH_CE_PACK, stream, [&] { return launch_ce_scan(s, stream); });
+  if (e) return e;
+  PackArgs a{};
+  a.src = p.h;
+  a.ld = p.ldh;
+  a.f32 = pl.f32;
+  a.cols = (int32_t)pl.D;
+  a.rows = pl.T;
+  a.gather = pl.rows;
+  a.count = pl.count;
+  a.dst = pl.h;
+  a.plane = pl.T * pl.ldd;
+  a.ldd = (int32_t)pl.ldd;
+  return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
+}
+
+// one piece of W as the core reads it
+int ce_piece(const dmuon_ce_problem& p, const CePlan& pl, int64_t v0, int64_t rows, const uint16_t** w, int64_t* ldw,
+             int64_t* plane, const CallEnv& env, void* stream) {
+  if (pl.direct_w) {
+    *w = (const uint16_t*)p.w + v0 * p.ldw;
+    *ldw = p.ldw;
+    *plane = 0;
+    return DMUON_OK;
+  }
+  PackArgs a{};
+  a.src = (const char*)p.w + v0 * p.ldw * type_bytes(p.dtype);
+  a.ld = p.ldw;
+  a.f32 = pl.f32;
+  a.cols = (int32_t)pl.D;
+  a.rows = rows;
+  a.dst = pl.w;
+  a.plane = rows * pl.ldd;
+  a.ldd = (int32_t)pl.ldd;
+  *w = pl.w;
+  *ldw = pl.ldd;
+  *plane = a.plane;
+  return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
+}
+
+CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64_t w_plane, int64_t v0, int64_t rows) {
+  CeLogitsArgs g{};
+  g.w = w;
+  g.w_plane = w_plane;
+  g.ldw = ldw;
+  g.h = pl.h;
+  g.h_plane = pl.T * pl.ldd;
+  g.ldh = pl.ldd;
+  g.pairs = plane_pairs(pl.planes, pl.planes);
+  g.kt = (int32_t)(pl.ldd / 32);
+  g.v0 = (int32_t)v0;
+  g.vrows = (int32_t)rows;
+  g.tokens = (int32_t)pl.T;
+  g.tiles_v = (int32_t)cdiv(rows, kTile);
+  g.tiles_t = pl.tiles_t;
+  g.count = pl.count;
+  g.tgt = pl.tgt;
+  return g;
+}
+
+// zeros, as the join of no partial sums
+int fill_zero(void* out, int32_t dtype, int64_t rows, int64_t cols, int phase, const CallEnv& env, void* stream) {
+  if (rows * cols == 0) return DMUON_OK;
+  JoinArgs j{};
+  j.rows = rows;
+  j.cols = (int32_t)cols;
+  j.out = out;
+  j.out_f32 = dtype == DMUON_F32;
+  return go(env, phase, stream, [&] { return launch_join(j, phase, stream); });
+}
+
+// ---- weight gradient from a checkpoint ------------------------------------------
+struct WgradPlan {
+  bool direct_g;
+  int planes, splits;
+  int64_t ldn, ldk, tiles_r, tiles_c;
+  uint16_t *x, *g;
+  float* part;
+  size_t bytes;
+};
+
+WgradPlan wgrad_plan(const dmuon_ckpt8_wgrad_problem& p, char* base) {
+  WgradPlan pl{};
+  pl.planes = p.grad_dtype == DMUON_F32 ? kPlanes : 1;
+  pl.direct_g = p.grad_dtype == DMUON_BF16 && kmajor_in_place(p.grad_out, p.ldg, p.n);
+  pl.ldn = round_up(p.n, kLdAlign);
+  pl.ldk = round_up(p.k, kLdAlign);
+  pl.tiles_r = cdiv(p.n, kTile);
+  pl.tiles_c = cdiv(p.k, kTile);
+  const int64_t groups = p.offsets ? p.groups : 1;
+  pl.splits = pick_splits(pl.tiles_r * pl.tiles_c * groups, p.tokens / std::max<int64_t>(groups, 1));
+  Carver c{base};
+  pl.x = c.take<uint16_t>(p.tokens * pl.ldk);
+  if (!pl.direct_g) pl.g = c.take<uint16_t>(pl.planes * p.tokens * pl.ldn);
+  if (pl.splits > 1) pl.part = c.take<float>(pl.splits * groups * p.n * pl.ldk);
+  pl.bytes = c.off;
+  return pl;
+}
+
+int check_wgrad(const dmuon_ckpt8_wgrad_problem* p, std::vector<Range>* rs) {
+  if (!p) return fail(DMUON_E_NULL, "problem is NULL");
+  if (!float_type(p->grad_dtype) || !float_type(p->out_dtype))
+    return fail(DMUON_E_DTYPE, "grad_dtype and out_dtype must be DMUON_F32 or DMUON_BF16");
+  if (p->tokens < 0 || p->tokens > kMaxTokens) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^24]");
+  if (p->n < 1 || p->n > kMaxWidth || p->k < 1 || p->k > kMaxWidth) return fail(DMUON_E_SHAPE, "n and k must be in [1, 65536]");
+  if (p->ldg < p->n || p->ldg > kMaxStride) return fail(DMUON_E_SHAPE, "ldg must be at least n");
+  if (p->groups < 0 || p->groups > (1 << 20)) return fail(DMUON_E_SHAPE, "groups must be in [0, 2^20]");
+  if (p->reserved != 0) return fail(DMUON_E_SHAPE, "reserved must be 0");
+  if (!p->offsets && p->groups > 1) return fail(DMUON_E_NULL, "offsets must be set for more than one group");
+  const int64_t groups = p->offsets ? p->groups : 1;
+  if (cdiv(p->n, kTile) * cdiv(p->k, kTile) * std::max<int64_t>(groups, 1) > INT32_MAX / 256)
+    return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
+  if (p->tokens > 0 && (!p->grad_out || !p->q || !p->exps)) return fail(DMUON_E_NULL, "grad_out, q and exps must be set");
+  if (groups > 0 && !p->out) return fail(DMUON_E_NULL, "out must be set");
+  if (rs) {
+    add_range(*rs, p->grad_out, strided_bytes(p->tokens, p->n, p->ldg, type_bytes(p->grad_dtype)), true);
+    add_range(*rs, p->q, p->tokens * p->k, true);
+    add_range(*rs, p->exps, p->tokens * cdiv(p->k, 32), true);
+    add_range(*rs, p->offsets, (groups + 1) * 4, true);
+    add_range(*rs, p->out, groups * p->n * p->k * type_bytes(p->out_dtype), false);
+  }
+  return DMUON_OK;
+}
+
+// ---- embedding ------------------------------------------------------------------
+struct EmbedPlan {
+  uint32_t *keys[2], *idx[2], *hist;
+  float* part[3];
+  int blocks, passes;
+  size_t bytes;
+};
+
+EmbedPlan embed_plan(int64_t tokens, int64_t rows, int64_t width, char* base) {
+  EmbedPlan pl{};
+  pl.blocks = (int)cdiv(tokens, kSortItems);
+  int bits = 0;
+  while (rows >> bits) ++bits;           // keys are 0 … rows
+  pl.passes = (int)cdiv(bits, 8);
+  Carver c{base};
+  for (int i = 0; i < 2; ++i) {
+    pl.keys[i] = c.take<uint32_t>(tokens);
+    pl.idx[i] = c.take<uint32_t>(tokens);
+  }
+  pl.hist = c.take<uint32_t>((int64_t)256 * pl.blocks);
+  const int64_t ld = round_up(width, 8);
+  int64_t span = kRun;
+  for (int l = 0; l < 3; ++l, span *= kRun) pl.part[l] = c.take<float>(tokens / span * ld);
+  pl.bytes = c.off;
+  return pl;
+}
+
+int check_embed_sizes(int64_t tokens, int64_t rows, int64_t width) {
+  if (tokens < 0 || tokens > kMaxIds) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^30]");
+  if (rows < 0 || rows > kMaxRows) return fail(DMUON_E_SHAPE, "rows must be in [0, 2^30]");
+  if (width < 1 || width > kMaxWidth) return fail(DMUON_E_SHAPE, "width must be in [1, 65536]");
+  return DMUON_OK;
+}
+
+int check_codec(int64_t rows, int64_t cols, int32_t dtype) {
+  if (!float_type(dtype)) return fail(DMUON_E_DTYPE, "dtype must be DMUON_F32 or DMUON_BF16");
+  if (rows < 0 || rows > kMaxIds) return fail(DMUON_E_SHAPE, "rows must be in [0, 2^30]");
+  if (cols < 0 || cols > kMaxWidth) return fail(DMUON_E_SHAPE, "cols must be in [0, 65536]");
+  return DMUON_OK;
+}
+
+bool rows16(const void* p, int64_t ld, int64_t cols, int64_t es) {
+  return ((uintptr_t)p & 15) == 0 && ld * es % 16 == 0 && cols % 8 == 0;
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" {
+
+int dmuon_linear_ce_workspace_size(const dmuon_ce_problem* p, int32_t backward, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
+    if (backward != 0 && backward != 1) return fail(DMUON_E_CFG, "backward must be 0 or 1");
+    int e = check_ce(p, nullptr);
+    if (e) return e;
+    *bytes = p->tokens ? ce_plan(*p, backward != 0, nullptr).bytes : 0;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_linear_ce(const dmuon_ce_problem* p, float* losses, float* lse, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  return guarded([&]() -> int {
+    std::vector<Range> rs;
+    int e = check_ce(p, &rs);
+    if (e) return e;
+    if (p->tokens == 0) return DMUON_OK;
+    if (!losses || !lse) return fail(DMUON_E_NULL, "losses and lse must be set");
+    add_range(rs, losses, p->tokens * 4, false);
+    add_range(rs, lse, p->tokens * 4, false);
+    if ((e = check_alias(rs))) return e;
+    if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, false, nullptr).bytes, rs))) return e;
+    const CePlan pl = ce_plan(*p, false, (char*)workspace);
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    if ((e = ce_start(*p, pl, false, nullptr, nullptr, losses, lse, env, stream))) return e;
+    for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
+      const int64_t rows = std::min(pl.piece, pl.V - v0);
+      const uint16_t* w;
+      int64_t ldw, plane;
+      if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
+      CeLogitsArgs g = logits_args(pl, w, ldw, plane, v0, rows);
+      g.stats = pl.stats;
+      g.zt = pl.zt;
+      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 0, pl.f32, stream); }))) return e;
+    }
+    CeRowsArgs r{};
+    r.stats = pl.stats;
+    r.zt = pl.zt;
+    r.tgt = pl.tgt;
+    r.rows = pl.rows;
+    r.count = pl.count;
+    r.tokens = (int32_t)pl.T;
+    r.tiles_v = pl.tiles_v;
+    r.losses = losses;
+    r.lse = lse;
+    return go(env, PH_CE_ROWS, stream, [&] { return launch_ce_rows(r, stream); });
+  });
+}
+
+int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const float* grad_losses, void* grad_h,
+                             void* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    std::vector<Range> rs;
+    int e = check_ce(p, &rs);
+    if (e) return e;
+    if (!grad_h && !grad_w) return DMUON_OK;
+    if (p->tokens > 0 && (!lse || !grad_losses)) return fail(DMUON_E_NULL, "lse and grad_losses must be set");
+    const int64_t es = type_bytes(p->dtype);
+    add_range(rs, lse, p->tokens * 4, true);
+    add_range(rs, grad_losses, p->tokens * 4, true);
+    add_range(rs, grad_h, p->tokens * p->width * es, false);
+    add_range(rs, grad_w, p->vocab * p->width * es, false);
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if (p->tokens == 0) {
+      if ((e = forced(env, -2))) return e;
+      return grad_w ? fill_zero(grad_w, p->dtype, p->vocab, p->width, PH_CE_GRADS, env, stream) : DMUON_OK;
+    }
+    if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, true, nullptr).bytes, rs))) return e;
+    const CePlan pl = ce_plan(*p, true, (char*)workspace);
+    if ((e = forced(env, -2))) return e;
+    if ((e = ce_start(*p, pl, true, lse, grad_losses, nullptr, nullptr, env, stream))) return e;
+    const int64_t td = cdiv(pl.D, kTile);
+    for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
+      const int64_t rows = std::min(pl.piece, pl.V - v0);
+      const uint16_t* w;
+      int64_t ldw, plane;
+      if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
+      CeLogitsArgs g = logits_args(pl, w, ldw, plane, v0, rows);
+      g.clse = pl.clse;
+      g.cg = pl.cg;
+      g.dz = pl.dz;
+      g.dz_plane = pl.T * pl.ldz;
+      g.ldz = (int32_t)pl.ldz;
+      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 1, pl.f32, stream); }))) return e;
+      if (grad_w) {
+        ProductArgs q{};
+        q.a = pl.h;
+        q.a_plane = pl.T * pl.ldd;
+        q.lda = pl.ldd;
+        q.b = pl.dz;
+        q.b_plane = g.dz_plane;
+        q.ldb = pl.ldz;
+        q.pairs = plane_pairs(pl.planes, pl.planes);
+        q.rows = (int32_t)rows;
+        q.cols = (int32_t)pl.D;
+        q.k = pl.T;
+        q.count = pl.count;
+        q.groups = 1;
+        q.tiles_r = (int32_t)cdiv(rows, kTile);
+        q.tiles_c = (int32_t)td;
+        q.splits = pl.splits_w;
+        q.scale = pl.gmax;
+        q.out = (char*)grad_w + v0 * pl.D * es;
+        q.out_f32 = pl.f32;
+        if (q.splits > 1) {
+          q.part = pl.part_w;
+          q.ldp = (int32_t)pl.ldd;
+          q.part_split = rows * pl.ldd;
+        }
+        if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
+        if (q.splits > 1) {
+          JoinArgs j{};
+          j.part = q.part;
+          j.part_split = q.part_split;
+          j.splits = q.splits;
+          j.ldp = q.ldp;
+          j.scale = pl.gmax;
+          j.rows = rows;
+          j.cols = (int32_t)pl.D;
+          j.out = q.out;
+          j.out_f32 = pl.f32;
+          if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); }))) return e;
+        }
+      }
+      if (grad_h) {
+        ProductArgs q{};
+        q.a = w;
+        q.a_plane = plane;
+        q.lda = ldw;
+        q.b = pl.dz;
+        q.b_plane = g.dz_plane;
+        q.ldb = pl.ldz;
+        q.pairs = plane_pairs(pl.planes, pl.planes);
+        q.b_rows = 1;
+        q.rows = (int32_t)pl.T;
+        q.cols = (int32_t)pl.D;
+        q.k = rows;
+        q.count = pl.count;
+        q.groups = 1;
+        q.tiles_r = pl.tiles_t;
+        q.tiles_c = (int32_t)td;
+        q.splits = pl.splits_h;
+        q.part = pl.part_h;
+        q.ldp = (int32_t)pl.ldd;
+        q.part_split = pl.T * pl.ldd;
+        q.add = v0 > 0;
+        if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
+      }
+    }
+    if (!grad_h) return DMUON_OK;
+    JoinArgs j{};
+    j.part = pl.part_h;
+    j.part_split = pl.T * pl.ldd;
+    j.splits = pl.splits_h;
+    j.ldp = (int32_t)pl.ldd;
+    j.pos = pl.pos;
+    j.scale = pl.gmax;
+    j.rows = pl.T;
+    j.cols = (int32_t)pl.D;
+    j.out = grad_h;
+    j.out_f32 = pl.f32;
+    return go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); });
+  });
+}
+
+int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const void* table, int64_t ldt, int64_t rows,
+                    int64_t width, int32_t dtype, float scale, void* out, void* stream) {
+  return guarded([&]() -> int {
+    if (!index_type(index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
+    if (!float_type(dtype)) return fail(DMUON_E_DTYPE, "dtype must be DMUON_F32 or DMUON_BF16");
+    int e = check_embed_sizes(tokens, rows, width);
+    if (e) return e;
+    if (ldt < width || ldt > kMaxStride) return fail(DMUON_E_SHAPE, "ldt must be at least width");
+    if (!std::isfinite(scale)) return fail(DMUON_E_CFG, "scale must be finite");
+    if (tokens == 0) return DMUON_OK;
+    if (!ids || !out || (rows > 0 && !table)) return fail(DMUON_E_NULL, "ids, table and out must be set");
+    const int64_t es = type_bytes(dtype);
+    std::vector<Range> rs;
+    add_range(rs, ids, tokens * (index_dtype == DMUON_I64 ? 8 : 4), true);
+    add_range(rs, table, strided_bytes(rows, width, ldt, es), true);
+    add_range(rs, out, tokens * width * es, false);
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    EmbedArgs a{};
+    a.ids = ids;
+    a.idx64 = index_dtype == DMUON_I64;
+    a.f32 = dtype == DMUON_F32;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.width = (int32_t)width;
+    a.vec = rows16(table, ldt, width, es) && rows16(out, width, width, es);
+    a.table = table;
+    a.ldt = ldt;
+    a.out = out;
+    a.scale = scale;
+    return go(env, PH_EMBED, stream, [&] { return launch_embed(a, stream); });
+  });
+}
+
+int dmuon_embedding_backward_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
+    int e = check_embed_sizes(tokens, rows, width);
+    if (e) return e;
+    *bytes = tokens && rows ? embed_plan(tokens, rows, width, nullptr).bytes : 0;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t tokens, const void* grad_out, int64_t ldg,
+                             int32_t grad_dtype, int64_t rows, int64_t width, float scale, int64_t padding_id,
+                             void* grad_table, int32_t out_dtype, int32_t accumulate, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    if (!index_type(index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
+    if (!float_type(grad_dtype) || !float_type(out_dtype))
+      return fail(DMUON_E_DTYPE, "grad_dtype and out_dtype must be DMUON_F32 or DMUON_BF16");
+    int e = check_embed_sizes(tokens, rows, width);
+    if (e) return e;
+    if (ldg < width || ldg > kMaxStride) return fail(DMUON_E_SHAPE, "ldg must be at least width");
+    if (!std::isfinite(scale)) return fail(DMUON_E_CFG, "scale must be finite");
+    if (accumulate != 0 && accumulate != 1) return fail(DMUON_E_CFG, "accumulate must be 0 or 1");
+    if (rows == 0) return DMUON_OK;
+    if (!grad_table || (tokens > 0 && (!ids || !grad_out))) return fail(DMUON_E_NULL, "ids, grad_out and grad_table must be set");
+    const CallEnv env = call_env();
+    if (tokens == 0) {
+      if ((e = forced(env, -2))) return e;
+      return accumulate ? DMUON_OK : fill_zero(grad_table, out_dtype, rows, width, PH_EMBED_GRAD, env, stream);
+    }
+    std::vector<Range> rs;
+    add_range(rs, ids, tokens * (index_dtype == DMUON_I64 ? 8 : 4), true);
+    add_range(rs, grad_out, strided_bytes(tokens, width, ldg, type_bytes(grad_dtype)), true);
+    add_range(rs, grad_table, rows * width * type_bytes(out_dtype), false);
+    if ((e = check_alias(rs))) return e;
+    if ((e = check_ws(workspace, workspace_bytes, embed_plan(tokens, rows, width, nullptr).bytes, rs))) return e;
+    const EmbedPlan pl = embed_plan(tokens, rows, width, (char*)workspace);
+    if ((e = forced(env, -2))) return e;
+    SortArgs s{};
+    s.ids = ids;
+    s.idx64 = index_dtype == DMUON_I64;
+    s.tokens = (int32_t)tokens;
+    s.rows = (int32_t)rows;
+    s.hist = pl.hist;
+    s.blocks = pl.blocks;
+    for (int k = 0; k < pl.passes; ++k) {
+      s.keys_in = k ? pl.keys[(k + 1) & 1] : nullptr;
+      s.idx_in = k ? pl.idx[(k + 1) & 1] : nullptr;
+      s.keys_out = pl.keys[k & 1];
+      s.idx_out = pl.idx[k & 1];
+      s.shift = 8 * k;
+      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_pass(s, stream); }))) return e;
+    }
+    EmbedGradArgs a{};
+    a.keys = pl.keys[(pl.passes - 1) & 1];
+    a.idx = pl.idx[(pl.passes - 1) & 1];
+    a.tokens = (int32_t)tokens;
+    a.rows = (int32_t)rows;
+    a.width = (int32_t)width;
+    a.padding = padding_id >= 0 && padding_id < rows ? (int32_t)padding_id : -1;
+    a.grad = grad_out;
+    a.ldg = ldg;
+    a.grad_f32 = grad_dtype == DMUON_F32;
+    a.out_f32 = out_dtype == DMUON_F32;
+    a.accumulate = accumulate;
+    a.vec_in = rows16(grad_out, ldg, width, type_bytes(grad_dtype));
+    a.vec_out = rows16(grad_table, width, width, type_bytes(out_dtype));
+    a.scale = scale;
+    a.out = grad_table;
+    for (int l = 0; l < 3; ++l) a.part[l] = pl.part[l];
+    int64_t span = kRun;
+    for (int l = 0; l < 3 && span <= tokens; ++l, span *= kRun)
+      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_embed_run(a, l, stream); }))) return e;
+    return go(env, PH_EMBED_GRAD, stream, [&] { return launch_embed_grad(a, stream); });
+  });
+}
+
+int dmuon_ckpt8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* q, uint8_t* exps,
+                         void* stream) {
+  return guarded([&]() -> int {
+    int e = check_codec(rows, cols, dtype);
+    if (e) return e;
+    if (ldx < cols || ldx > kMaxStride) return fail(DMUON_E_SHAPE, "ldx must be at least cols");
+    if (rows * cols == 0) return DMUON_OK;
+    if (!x || !q || !exps) return fail(DMUON_E_NULL, "x, q and exps must be set");
+    const int64_t es = type_bytes(dtype), blocks = cdiv(cols, 32);
+    std::vector<Range> rs;
+    add_range(rs, x, strided_bytes(rows, cols, ldx, es), true);
+    add_range(rs, q, rows * cols, false);
+    add_range(rs, exps, rows * blocks, false);
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    CodecArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.f32 = dtype == DMUON_F32;
+    a.cols = (int32_t)cols;
+    a.blocks = (int32_t)blocks;
+    a.rows = rows;
+    a.vec = ((uintptr_t)x & 15) == 0 && ldx * es % 16 == 0;
+    a.q = q;
+    a.exps = exps;
+    return go(env, PH_CKPT_CODEC, stream, [&] { return launch_ckpt_quantize(a, stream); });
+  });
+}
+
+int dmuon_ckpt8_dequantize(const int8_t* q, const uint8_t* exps, int64_t rows, int64_t cols, void* out, int32_t dtype,
+                           void* stream) {
+  return guarded([&]() -> int {
+    int e = check_codec(rows, cols, dtype);
+    if (e) return e;
+    if (rows * cols == 0) return DMUON_OK;
+    if (!q || !exps || !out) return fail(DMUON_E_NULL, "q, exps and out must be set");
+    const int64_t es = type_bytes(dtype), blocks = cdiv(cols, 32);
+    std::vector<Range> rs;
+    add_range(rs, q, rows * cols, true);
+    add_range(rs, exps, rows * blocks, true);
+    add_range(rs, out, rows * cols * es, false);
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    CodecArgs a{};
+    a.f32 = dtype == DMUON_F32;
+    a.cols = (int32_t)cols;
+    a.blocks = (int32_t)blocks;
+    a.rows = rows;
+    a.vec = ((uintptr_t)out & 15) == 0 && cols * es % 16 == 0;
+    a.q = (int8_t*)q;
+    a.exps = (uint8_t*)exps;
+    a.out = out;
+    a.ldo = cols;
+    return go(env, PH_CKPT_CODEC, stream, [&] { return launch_ckpt_read(a, PH_CKPT_CODEC, stream); });
+  });
+}
+
+int dmuon_ckpt8_wgrad_workspace_size(const dmuon_ckpt8_wgrad_problem* p, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
+    int e = check_wgrad(p, nullptr);
+    if (e) return e;
+    *bytes = p->tokens && !(p->offsets && p->groups == 0) ? wgrad_plan(*p, nullptr).bytes : 0;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* p, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    std::vector<Range> rs;
+    int e = check_wgrad(p, &rs);
+    if (e) return e;
+    const int64_t groups = p->offsets ? p->groups : 1;
+    if (groups == 0) return DMUON_OK;
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if (p->tokens == 0) {
+      if ((e = forced(env, -2))) return e;
+      return fill_zero(p->out, p->out_dtype, groups * p->n, p->k, PH_CKPT_WGRAD, env, stream);
+    }
+    if ((e = check_ws(workspace, workspace_bytes, wgrad_plan(*p, nullptr).bytes, rs))) return e;
+    const WgradPlan pl = wgrad_plan(*p, (char*)workspace);
+    if ((e = forced(env, -2))) return e;
+    CodecArgs r{};
+    r.cols = (int32_t)p->k;
+    r.blocks = (int32_t)cdiv(p->k, 32);
+    r.rows = p->tokens;
+    r.vec = 1;
+    r.q = (int8_t*)p->q;
+    r.exps = (uint8_t*)p->exps;
+    r.out = pl.x;
+    r.ldo = pl.ldk;
+    if ((e = go(env, PH_CKPT_WGRAD, stream, [&] { return launch_ckpt_read(r, PH_CKPT_WGRAD, stream); }))) return e;
+    if (!pl.direct_g) {
+      PackArgs a{};
+      a.src = p->grad_out;
+      a.ld = p->ldg;
+      a.f32 = p->grad_dtype == DMUON_F32;
+      a.cols = (int32_t)p->n;
+      a.rows = p->tokens;
+      a.dst = pl.g;
+      a.plane = p->tokens * pl.ldn;
+      a.ldd = (int32_t)pl.ldn;
+      if ((e = go(env, PH_CKPT_WGRAD, stream, [&] { return launch_pack(a, PH_CKPT_WGRAD, stream); }))) return e;
+    }
+    ProductArgs q{};
+    q.a = pl.x;
+    q.lda = pl.ldk;
+    q.b = pl.direct_g ? (const uint16_t*)p->grad_out : pl.g;
+    q.ldb = pl.direct_g ? p->ldg : pl.ldn;
+    q.b_plane = p->tokens * pl.ldn;
+    q.pairs = plane_pairs(1, pl.planes);
+    q.rows = (int32_t)p->n;
+    q.cols = (int32_t)p->k;
+    q.k = p->tokens;
+    q.offsets = p->offsets;
+    q.groups = (int32_t)groups;
+    q.tiles_r = (int32_t)pl.tiles_r;
+    q.tiles_c = (int32_t)pl.tiles_c;
+    q.splits = pl.splits;
+    q.out = p->out;
+    q.out_f32 = p->out_dtype == DMUON_F32;
+    if (q.splits > 1) {
+      q.part = pl.part;
+      q.ldp = (int32_t)pl.ldk;
+      q.part_split = groups * p->n * pl.ldk;
+    }
+    if ((e = go(env, PH_CKPT_WGRAD, stream, [&] { return launch_product(q, PH_CKPT_WGRAD, stream); }))) return e;
+    if (q.splits == 1) return DMUON_OK;
+    JoinArgs j{};
+    j.part = q.part;
+    j.part_split = q.part_split;
+    j.splits = q.splits;
+    j.ldp = q.ldp;
+    j.rows = groups * p->n;
+    j.cols = (int32_t)p->k;
+    j.out = p->out;
+    j.out_f32 = q.out_f32;
+    return go(env, PH_CKPT_WGRAD, stream, [&] { return launch_join(j, PH_CKPT_WGRAD, stream); });
+  });
+}
+
+}  // extern "C"

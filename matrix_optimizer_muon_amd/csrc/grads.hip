@@ -1,0 +1,1057 @@
+// HIP kernels of the training gradients for gfx950 (MI355X): softmax cross entropy
+// over a large vocabulary, embedding lookup and its gradient, activation
+// checkpoints in 8 bits and the weight gradient computed from them.
+//
+// Every matrix product runs on the step's bf16 contraction core (core.hpp).  fp32
+// operands enter it as three bf16 planes whose sum is the fp32 value.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <mutex>
+
+#include "core.hpp"
+#include "grads.hpp"
+
+namespace dmuon {
+
+// ---------------------------------------------------------------------------
+// small helpers
+// ---------------------------------------------------------------------------
+// 8 consecutive elements as fp32: 16-byte loads where `vec`, else element by
+// element with zeros from column `left` on
+__device__ __forceinline__ void unpack8(const u32x4_t& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(gptr<const uint16_t> p, bool vec, int left, float (&v)[8]) {
+  if (vec) {
+    const u32x4_t u = *(gptr<const u32x4_t>)p;
+    unpack8(u, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? bf16_to_f32(p[e]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(gptr<const float> p, bool vec, int left, float (&v)[8]) {
+  if (vec) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t a = ((gptr<const f32x4_t>)p)[h];
+      v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.f;
+  }
+}
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+  return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+__device__ __forceinline__ void store8(gptr<uint16_t> p, bool vec, int left, const float (&v)[8]) {
+  if (vec) {
+    *(gptr<u32x4_t>)p = pack8(v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) p[e] = f32_to_bf16(v[e]);
+  }
+}
+__device__ __forceinline__ void store8(gptr<float> p, bool vec, int left, const float (&v)[8]) {
+  if (vec) {
+    ((gptr<f32x4_t>)p)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+    ((gptr<f32x4_t>)p)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) p[e] = v[e];
+  }
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t i) {
+  return idx64 ? glob((const int64_t*)p)[i] : (int64_t)glob((const int32_t*)p)[i];
+}
+
+// x = hi + mid + lo, each a bf16 value: hi is x rounded to bf16 (cut off where
+// rounding would overflow), mid the rest rounded, lo the rest of that: 24 bits.
+// An infinity or NaN sits in hi alone.
+__device__ __forceinline__ void split3(float x, float (&p)[3]) {
+  const bool special = (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+  float hi = bf16_to_f32(f32_to_bf16(x));
+  if ((__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u && !special) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  const float r = x - hi;
+  const float mid = bf16_to_f32(f32_to_bf16(r));
+  p[0] = hi;
+  p[1] = special ? 0.f : mid;
+  p[2] = special ? 0.f : bf16_to_f32(f32_to_bf16(r - mid));
+}
+
+// ---------------------------------------------------------------------------
+// operand copies: rows of a matrix (gathered by an index list or in order) as
+// zero-padded bf16 planes.  Bound by HBM: read once, written once.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
+  const int64_t rows = a.count ? (int64_t)*a.count : a.rows;
+  const int per = a.ldd >> 3;                       // 8-element pieces per row
+  const int64_t n = rows * per;
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  const bool vec = (a.ld & 7) == 0 && ((uintptr_t)a.src & 15) == 0;
+  for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < n; id += step) {
+    const int64_t r = id / per;
+    const int c = (int)(id - r * per) * 8;
+    const int64_t sr = a.gather ? (int64_t)a.gather[r] : r;
+    const int left = a.cols - c;
+    gptr<uint16_t> d = glob(a.dst) + r * a.ldd + c;
+    float v[8];
+    if (a.f32) {
+      load8(glob((const float*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
+      float p[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float s[3];
+        split3(v[e], s);
+        p[0][e] = s[0]; p[1][e] = s[1]; p[2][e] = s[2];
+      }
+#pragma unroll
+      for (int q = 0; q < kPlanes; ++q) *(gptr<u32x4_t>)(d + q * a.plane) = pack8(p[q]);
+    } else {
+      load8(glob((const uint16_t*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
+      *(gptr<u32x4_t>)d = pack8(v);                 // bf16 → fp32 → bf16 is exact
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// cross entropy: the compact list of tokens that take part.  One workgroup; every
+// thread owns a contiguous range of tokens, so the list keeps their order.
+// Forward: tokens whose target is not ignore_index (the others get loss and lse
+// 0).  Backward: those whose target also lies in the vocabulary and whose weight
+// is not zero; weights are stored divided by the largest magnitude, which the
+// products' epilogues multiply back, so that dZ is rounded to bf16 relative to
+// (p − δ) alone (a uniform weight leaves p − δ unscaled) and tiny weights do not
+// underflow.
+// ---------------------------------------------------------------------------
+constexpr int kScanThreads = 1024;
+__global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
+  __shared__ int wave_sum[kScanThreads / 64];
+  __shared__ float wave_max[kScanThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int chunk = (a.tokens + kScanThreads - 1) / kScanThreads;
+  const int64_t t0 = (int64_t)tid * chunk;
+  const int64_t t1 = t0 + chunk < a.tokens ? t0 + chunk : a.tokens;
+  auto takes_part = [&](int64_t t, int64_t y) {
+    if (y == a.ignore) return false;
+    return !a.backward || (y >= 0 && y < a.vocab && !(a.grad_losses[t] == 0.f));
+  };
+  int n = 0;
+  float gm = 0.f;
+  for (int64_t t = t0; t < t1; ++t)
+    if (takes_part(t, load_index(a.targets, a.idx64, t))) {
+      ++n;
+      if (a.backward) gm = fmaxf(gm, fabsf(a.grad_losses[t]));
+    }
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += up;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor(gm, o, 64));
+  if (lane == 63) wave_sum[wave] = incl;
+  if (lane == 0) wave_max[wave] = gm;
+  __syncthreads();
+  int base = 0, total = 0;
+  gm = 0.f;
+  for (int w = 0; w < kScanThreads / 64; ++w) {
+    if (w < wave) base += wave_sum[w];
+    total += wave_sum[w];
+    gm = fmaxf(gm, wave_max[w]);
+  }
+  if (tid == 0) {
+    *a.count = total;
+    if (a.backward) *a.gmax = gm;
+  }
+  int i = base + incl - n;
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t y = load_index(a.targets, a.idx64, t);
+    const bool in = takes_part(t, y);
+    if (a.backward) a.pos[t] = in ? i : -1;
+    if (in) {
+      a.rows[i] = (int32_t)t;
+      a.tgt[i] = y >= 0 && y < a.vocab ? (int32_t)y : -1;
+      if (a.backward) {
+        a.clse[i] = a.lse_in[t];
+        a.cg[i] = a.grad_losses[t] / gm;
+      }
+      ++i;
+    } else if (!a.backward) {
+      a.losses[t] = 0.f;
+      a.lse[t] = 0.f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products on the core
+// ---------------------------------------------------------------------------
+// acc = Σ over the plane pairs of op, whose a and b point at plane 0
+template <bool TA, bool TB>
+__device__ __forceinline__ void gemm_planes(const Operands& op, int64_t a_plane, int64_t b_plane, const PlanePairs& pp,
+                                            char* smem, f32x16_t (&acc)[4][2]) {
+  if (pp.n == 1) {
+    gemm_mainloop<uint16_t, TA, TB>(op, smem, acc);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+#pragma unroll 1
+  for (int p = 0; p < pp.n; ++p) {
+    Operands o = op;
+    o.a += (int64_t)((pp.a >> (4 * p)) & 15) * a_plane * 2;
+    o.b += (int64_t)((pp.b >> (4 * p)) & 15) * b_plane * 2;
+    gemm_mainloop<uint16_t, TA, TB, 0, 1>(o, smem, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) quarters_to_32x32(acc[i][j]);
+}
+
+// A tile whose lanes hold output rows (acc_col) and whose registers hold
+// consecutive output columns (acc_row + e) goes out through LDS as whole rows of
+// 16-byte pieces.  f(i, j, r) is the value of register r of block (i, j).
+// Rows ≥ rows and columns ≥ cols are dropped; `vec` says that whole pieces may be
+// stored as such.
+template <typename F>
+__device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+  // 512-byte rows; 16-byte pieces XOR-swizzled by the row, so that the 32 rows one
+  // 8-byte write instruction touches fall in all banks
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int rq = 0; rq < 4; ++rq) {
+        const int row = wc * 64 + j * 32 + r32;
+        const int piece = wr * 16 + i * 4 + rq;
+        const uint2 v = make_uint2(pack_bf16x2(f(i, j, 4 * rq), f(i, j, 4 * rq + 1)),
+                                   pack_bf16x2(f(i, j, 4 * rq + 2), f(i, j, 4 * rq + 3)));
+        *(uint2*)(smem + row * 512 + ((piece ^ (row & 31)) << 4) + h * 8) = v;
+      }
+  __syncthreads();
+#pragma unroll 4
+  for (int q = 0; q < 16; ++q) {
+    const int id = tid + kGemmThreads * q;
+    const int row = id >> 5, piece = id & 31;
+    const u32x4_t v = *(const u32x4_t*)(smem + row * 512 + ((piece ^ (row & 31)) << 4));
+    const int left = cols - piece * 8;
+    if (row >= rows || left <= 0) continue;
+    gptr<uint16_t> d = glob(out) + (int64_t)row * ld + piece * 8;
+    if (vec && left >= 8) {
+      *(gptr<u32x4_t>)d = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+  __syncthreads();
+}
+// fp32: 1 KiB rows, 128 of them at a time
+template <typename F>
+__device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+#pragma unroll 1
+  for (int hf = 0; hf < 2; ++hf) {
+    if ((wc >> 1) == hf) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int rq = 0; rq < 4; ++rq) {
+            const int row = (wc & 1) * 64 + j * 32 + r32;
+            const int piece = wr * 32 + i * 8 + rq * 2 + h;
+            *(float4*)(smem + row * 1024 + ((piece ^ (row & 31)) << 4)) =
+                make_float4(f(i, j, 4 * rq), f(i, j, 4 * rq + 1), f(i, j, 4 * rq + 2), f(i, j, 4 * rq + 3));
+          }
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int q = 0; q < 16; ++q) {
+      const int id = tid + kGemmThreads * q;
+      const int lr = id >> 6, piece = id & 63, row = hf * 128 + lr;
+      const f32x4_t v = *(const f32x4_t*)(smem + lr * 1024 + ((piece ^ (lr & 31)) << 4));
+      const int left = cols - piece * 4;
+      if (row >= rows || left <= 0) continue;
+      gptr<float> d = glob(out) + (int64_t)row * ld + piece * 4;
+      if (vec && left >= 4) {
+        *(gptr<f32x4_t>)d = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) d[e] = v[e];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// logits tiles, 256 vocabulary rows × 256 tokens: z(v, t) = Σ_d W(v, d)·H(t, d).
+// W is the core's A operand, so a lane's registers hold vocabulary entries of one
+// token: the softmax statistics of a tile are register reductions, one exchange
+// between the two lane halves and one between the two wave groups, through LDS.
+// The logits themselves are never stored.
+//   forward:  per tile and token the largest logit and Σ exp(z − largest), and the
+//             target's logit;
+//   backward: dZ(t, v) = g_t·(exp(z − lse_t) − [v = target]), rounded to bf16 (one
+//             rounding; the matrix cores take bf16; fp32 operands: three planes).
+// ---------------------------------------------------------------------------
+template <bool BACKWARD, bool F32>
+__global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
+  extern __shared__ __align__(16) char smem[];
+  int tt, tv;
+  band_tile(xcd_logical_block<64>(), g.tiles_t, g.tiles_v, tt, tv);
+  const int count = *g.count;
+  const int row0 = tv * kTile, col0 = tt * kTile;   // vocabulary (in the piece), tokens
+  if (col0 >= count) return;
+  Operands op;
+  op.a = (const char*)(g.w + (int64_t)row0 * g.ldw);
+  op.b = (const char*)(g.h + (int64_t)col0 * g.ldh);
+  op.lda_b = (int)(g.ldw * 2);
+  op.ldb_b = (int)(g.ldh * 2);
+  op.rows_a = g.vrows - row0;
+  op.rows_b = count - col0;
+  op.cola_b = op.colb_b = 0;
+  op.ktiles = g.kt;
+  f32x16_t acc[4][2];
+  gemm_planes<false, false>(op, g.w_plane, g.h_plane, g.pairs, smem, acc);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+  const int vleft = g.vrows - row0 - wr * 128 - h * 4;       // valid while register row < vleft
+  const bool ragged = g.vrows - row0 < kTile;
+  // register row of the target of column j's token, or −1
+  int want[2];
+  float L[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+  int tok[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    tok[j] = col0 + wc * 64 + j * 32 + r32;
+    want[j] = -1;
+    if (tok[j] < count) {
+      const int y = g.tgt[tok[j]] - g.v0 - row0;
+      if (y >= 0 && y < kTile && g.tgt[tok[j]] >= 0 && (y >> 7) == wr && ((y >> 2) & 1) == h) want[j] = (y & 127) - 4 * h;
+      if constexpr (BACKWARD) {
+        L[j] = g.clse[tok[j]];
+        w[j] = g.cg[tok[j]];
+      }
+    }
+  }
+  auto reg_row = [](int i, int r) { return i * 32 + (r >> 2) * 8 + (r & 3); };
+
+  if constexpr (!BACKWARD) {
+    CeStat* st = (CeStat*)smem;                              // [wave group][256]
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float m = -INFINITY, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if (ragged && reg_row(i, r) >= vleft) acc[i][j][r] = -INFINITY;
+          m = fmaxf(m, acc[i][j][r]);
+          if (reg_row(i, r) == want[j]) z = acc[i][j][r];
+        }
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      const float m0 = m == -INFINITY ? 0.f : m;             // then s is 0, or NaN if a logit is
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s += __expf(acc[i][j][r] - m0);
+      s += __shfl_xor(s, 32, 64);
+      if (h == 0) st[wr * kTile + wc * 64 + j * 32 + r32] = CeStat{m, s};
+      if (want[j] >= 0) g.zt[tok[j]] = z;
+    }
+    __syncthreads();
+    if (tid < kTile && col0 + tid < count) {
+      const CeStat a = st[tid], b = st[kTile + tid];
+      const float m = fmaxf(a.m, b.m);
+      const float sa = a.m == -INFINITY ? a.s : a.s * __expf(a.m - m);
+      const float sb = b.m == -INFINITY ? b.s : b.s * __expf(b.m - m);
+      g.stats[(int64_t)(g.v0 / kTile + tv) * g.tokens + col0 + tid] = CeStat{m, sa + sb};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float p = __expf(acc[i][j][r] - L[j]);
+          if (reg_row(i, r) == want[j]) p -= 1.f;
+          p *= w[j];
+          acc[i][j][r] = ragged && reg_row(i, r) >= vleft ? 0.f : p;
+        }
+    uint16_t* out = g.dz + (int64_t)col0 * g.ldz + row0;
+    const int rows = count - col0, cols = g.ldz - row0;
+    if constexpr (F32) {
+      // three planes: each stores what bf16 holds of the rest (exact differences)
+#pragma unroll 1
+      for (int q = 0; q < kPlanes; ++q) {
+        store_tile(out + q * g.dz_plane, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] -= bf16_to_f32(f32_to_bf16(acc[i][j][r]));
+      }
+    } else {
+      store_tile(out, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the tiles' statistics of each token joined: lse = M + log Σ s·exp(m − M),
+// loss = lse − z_target (NaN for a target outside the vocabulary).  16 tokens per
+// workgroup, 16 threads per token.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
+  __shared__ CeStat part[16][17];
+  const int count = *a.count;
+  const int i0 = blockIdx.x * 16;
+  if (i0 >= count) return;
+  const int ti = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int i = i0 + ti;
+  float M = -INFINITY, S = 0.f;
+  if (i < count) {
+    for (int v = k; v < a.tiles_v; v += 64) {
+      CeStat x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        x[u] = v + 16 * u < a.tiles_v ? a.stats[(int64_t)(v + 16 * u) * a.tokens + i] : CeStat{-INFINITY, 0.f};
+      const float m = fmaxf(fmaxf(fmaxf(x[0].m, x[1].m), fmaxf(x[2].m, x[3].m)), M);
+      float s = M == -INFINITY ? S : S * __expf(M - m);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        s += x[u].m == -INFINITY ? x[u].s : x[u].s * __expf(x[u].m - m);    // a NaN in s stays
+      M = m;
+      S = s;
+    }
+  }
+  part[k][ti] = CeStat{M, S};
+  __syncthreads();
+  if (threadIdx.x < 16 && i < count) {
+    float m = -INFINITY;
+    for (int q = 0; q < 16; ++q) m = fmaxf(m, part[q][ti].m);
+    float s = 0.f;
+    for (int q = 0; q < 16; ++q) s += part[q][ti].m == -INFINITY ? part[q][ti].s : part[q][ti].s * __expf(part[q][ti].m - m);
+    const float lse = m + logf(s);
+    const int t = a.rows[i];
+    a.lse[t] = lse;
+    a.losses[t] = a.tgt[i] >= 0 ? lse - a.zt[i] : __uint_as_float(0x7fc00000u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradient products: C[row][col] = Σ_k B(k, row)·A(k, col), A K-major, B K-major
+// (weight gradients: k = tokens) or row-major (hidden-state gradient: k =
+// vocabulary).  The lanes hold rows and the registers consecutive columns.  The K
+// range may be split over `splits` workgroups per tile, which then leave fp32
+// partial sums for k_join; the hidden-state gradient adds up its vocabulary
+// pieces that way too.
+// ---------------------------------------------------------------------------
+template <bool TB>
+__global__ __launch_bounds__(kGemmThreads) void k_product(ProductArgs g) {
+  extern __shared__ __align__(16) char smem[];
+  int u = xcd_logical_block<64>();
+  const int tiles = g.tiles_r * g.tiles_c;
+  const int split = u / (tiles * g.groups);
+  u -= split * tiles * g.groups;
+  const int group = u / tiles;
+  u -= group * tiles;
+  int tr, tc;
+  if (g.tiles_c <= g.tiles_r) band_tile(u, g.tiles_c, g.tiles_r, tc, tr);
+  else band_tile(u, g.tiles_r, g.tiles_c, tr, tc);
+  const int row0 = tr * kTile, col0 = tc * kTile;
+  int rows = g.rows;
+  int64_t k0 = 0, k1 = g.k;
+  if (g.count) {
+    const int n = *g.count;
+    if (TB) k1 = n < k1 ? n : k1;
+    else rows = n < rows ? n : rows;
+  }
+  if (g.offsets) {                       // clamped, so that no offset leaves the operands
+    const int64_t a = g.offsets[group], b = g.offsets[group + 1];
+    k0 = a < 0 ? 0 : (a < g.k ? a : g.k);
+    k1 = b < k0 ? k0 : (b < g.k ? b : g.k);
+  }
+  if (row0 >= rows) return;
+  if (g.splits > 1) {                    // whole stages per split
+    const int64_t st = (k1 - k0 + 31) / 32, per = (st + g.splits - 1) / g.splits;
+    const int64_t lo = k0 + per * split * 32, hi = lo + per * 32;
+    k1 = hi < k1 ? hi : k1;
+    k0 = lo < k1 ? lo : k1;
+  }
+  Operands op;
+  op.a = (const char*)(g.a + k0 * g.lda);
+  op.lda_b = (int)(g.lda * 2);
+  op.rows_a = (int)(k1 - k0);
+  op.cola_b = col0 * 2;
+  op.ldb_b = (int)(g.ldb * 2);
+  if (TB) {
+    op.b = (const char*)(g.b + k0 * g.ldb);
+    op.rows_b = (int)(k1 - k0);
+    op.colb_b = row0 * 2;
+  } else {
+    op.b = (const char*)(g.b + (int64_t)row0 * g.ldb + k0);
+    op.rows_b = rows - row0;
+    op.colb_b = 0;
+  }
+  op.ktiles = (int)((k1 - k0 + 31) / 32);
+  f32x16_t acc[4][2];
+  gemm_planes<true, TB>(op, g.a_plane, g.b_plane, g.pairs, smem, acc);
+
+  if (g.part) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+    gptr<float> part = glob(g.part) + split * g.part_split + (int64_t)group * g.rows * g.ldp;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = row0 + wc * 64 + j * 32 + r32;
+      if (row >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int rq = 0; rq < 4; ++rq) {
+          const int col = col0 + wr * 128 + i * 32 + rq * 8 + h * 4;
+          if (col >= g.ldp) continue;
+          gptr<f32x4_t> p = (gptr<f32x4_t>)(part + (int64_t)row * g.ldp + col);
+          f32x4_t v = {acc[i][j][4 * rq], acc[i][j][4 * rq + 1], acc[i][j][4 * rq + 2], acc[i][j][4 * rq + 3]};
+          if (g.add) {
+            const f32x4_t o = *p;
+            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+          }
+          *p = v;
+        }
+    }
+    return;
+  }
+  const float s = g.scale ? *g.scale : 1.f;
+  const int64_t at = ((int64_t)group * g.rows + row0) * g.cols + col0;
+  const int rl = rows - row0, cl = g.cols - col0;
+  if (g.out_f32)
+    store_tile((float*)g.out + at, g.cols, rl, cl, (g.cols & 3) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
+               [&](int i, int j, int r) { return acc[i][j][r] * s; });
+  else
+    store_tile((uint16_t*)g.out + at, g.cols, rl, cl, (g.cols & 7) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
+               [&](int i, int j, int r) { return acc[i][j][r] * s; });
+}
+
+// partial sums joined in a fixed order, scaled and rounded to the output's type
+__global__ __launch_bounds__(kThreads) void k_join(JoinArgs a) {
+  const int per = (a.cols + 7) >> 3;
+  const int64_t n = a.rows * per, step = (int64_t)gridDim.x * kThreads;
+  const float s = a.scale ? *a.scale : 1.f;
+  const bool vec = (a.cols & 7) == 0 && ((uintptr_t)a.out & 15) == 0;
+  for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < n; id += step) {
+    const int64_t t = id / per;
+    const int c = (int)(id - t * per) * 8;
+    const int left = a.cols - c;
+    const int64_t r = a.pos ? (int64_t)a.pos[t] : t;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r >= 0) {
+      for (int q = 0; q < a.splits; ++q) {
+        float x[8];
+        load8(glob((const float*)a.part) + q * a.part_split + r * a.ldp + c, true, 8, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= s;
+    }
+    if (a.out_f32) store8(glob((float*)a.out) + t * a.cols + c, vec, left, v);
+    else store8(glob((uint16_t*)a.out) + t * a.cols + c, vec, left, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// embedding lookup: out[t] = scale·table[id_t], zeros for an id outside the table.
+// One piece of 8 elements per thread and step, a wave covers whole cache lines.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a) {
+  const int per = (a.width + 7) >> 3;
+  const int64_t n = a.tokens * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < n; q += step) {
+    const int64_t t = q / per;
+    const int c = (int)(q - t * per) * 8;
+    const int left = a.width - c;
+    const int64_t id = load_index(a.ids, a.idx64, t);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (id >= 0 && id < a.rows) {
+      load8(glob((const T*)a.table) + id * a.ldt + c, a.vec, left, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+    }
+    store8(glob((T*)a.out) + t * a.width + c, a.vec, left, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// stable radix sort of (id, token) pairs, 8 bits of the id per pass: digit counts
+// per workgroup, one scan over [digit][workgroup], stable placement.  Inside a
+// workgroup each wave owns a contiguous quarter and places 64 pairs at a time by
+// the rank among equal digits (ballots), so equal ids keep the order of their
+// tokens whatever the timing.
+// ---------------------------------------------------------------------------
+constexpr int kSortWaves = kThreads / 64;
+constexpr int kSortRounds = kSortItems / kThreads;
+
+__device__ __forceinline__ void sort_pair(const SortArgs& a, int64_t i, uint32_t& key, uint32_t& idx) {
+  if (a.keys_in) {
+    key = a.keys_in[i];
+    idx = a.idx_in[i];
+  } else {
+    const int64_t id = load_index(a.ids, a.idx64, i);
+    key = id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
+    idx = (uint32_t)i;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_sort_count(SortArgs a) {
+  __shared__ uint32_t cnt[256];
+  cnt[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kSortItems;
+#pragma unroll 4
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = base + r * kThreads + threadIdx.x;
+    if (i < a.tokens) {
+      uint32_t key, idx;
+      sort_pair(a, i, key, idx);
+      atomicAdd(&cnt[(key >> a.shift) & 255], 1u);
+    }
+  }
+  __syncthreads();
+  a.hist[threadIdx.x * a.blocks + blockIdx.x] = cnt[threadIdx.x];
+}
+
+// exclusive scan of hist[256·blocks] in place, one workgroup
+__global__ __launch_bounds__(kScanThreads) void k_sort_scan(SortArgs a) {
+  __shared__ uint32_t wave_sum[kScanThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = 256 * a.blocks, chunk = (n + kScanThreads - 1) / kScanThreads;
+  const int i0 = tid * chunk, i1 = i0 + chunk < n ? i0 + chunk : n;
+  uint32_t s = 0;
+  for (int i = i0; i < i1; ++i) s += a.hist[i];
+  uint32_t incl = s;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 63) wave_sum[wave] = incl;
+  __syncthreads();
+  uint32_t at = incl - s;
+  for (int w = 0; w < wave; ++w) at += wave_sum[w];
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t x = a.hist[i];
+    a.hist[i] = at;
+    at += x;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_sort_place(SortArgs a) {
+  __shared__ uint32_t at[kSortWaves][256];           // next slot of each wave and digit
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) at[w][tid] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kSortItems + wave * (kSortItems / kSortWaves);
+  uint32_t key[kSortRounds], idx[kSortRounds];
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = base + r * 64 + lane;
+    key[r] = idx[r] = 0;
+    if (i < a.tokens) {
+      sort_pair(a, i, key[r], idx[r]);
+      atomicAdd(&at[wave][(key[r] >> a.shift) & 255], 1u);
+    }
+  }
+  __syncthreads();
+  uint32_t first = a.hist[tid * a.blocks + blockIdx.x];
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    const uint32_t c = at[w][tid];
+    at[w][tid] = first;
+    first += c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = base + r * 64 + lane;
+    const bool on = i < a.tokens;
+    const uint32_t d = (key[r] >> a.shift) & 255;
+    uint64_t same = __ballot(on);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t m = __ballot((d >> b) & 1);
+      same &= (d >> b) & 1 ? m : ~m;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    uint32_t slot = 0;
+    if (on) slot = at[wave][d];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before the leaders add
+    __builtin_amdgcn_wave_barrier();
+    if (on && rank == 0) at[wave][d] = slot + (uint32_t)__popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (on) {
+      a.keys_out[slot + rank] = key[r];
+      a.idx_out[slot + rank] = idx[r];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the table's gradient from the sorted tokens.
+// A row's gradient is the sum over a contiguous range of sorted tokens.  Ranges
+// are cut at fixed multiples of 32, 1024 and 32768: a whole aligned run of equal
+// ids is summed once by k_embed_run (level 0 from the tokens, levels 1 and 2 from
+// 32 sums of the level below), and k_embed_grad adds at most 62 tokens and 62 sums
+// per level to a row, so a frequent token is spread over many workgroups and the
+// order of every sum is fixed.
+// ---------------------------------------------------------------------------
+template <typename G>
+__device__ __forceinline__ void add_tokens(const EmbedGradArgs& a, int s, int e, int c, float (&v)[8]) {
+  const int left = a.width - c;
+  int i = s;
+  for (; i + 4 <= e; i += 4) {
+    float x[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load8(glob((const G*)a.grad) + (int64_t)a.idx[i + u] * a.ldg + c, a.vec_in, left, x[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += x[u][k];
+  }
+  for (; i < e; ++i) {
+    float x[8];
+    load8(glob((const G*)a.grad) + (int64_t)a.idx[i] * a.ldg + c, a.vec_in, left, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += x[k];
+  }
+}
+__device__ __forceinline__ void add_sums(const float* part, int ld, int s, int e, int c, float (&v)[8]) {
+#pragma unroll 4
+  for (int i = s; i < e; ++i) {
+    float x[8];
+    load8(glob(part) + (int64_t)i * ld + c, true, 8, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += x[k];
+  }
+}
+
+template <typename G, int LEVEL>
+__global__ __launch_bounds__(kThreads) void k_embed_run(EmbedGradArgs a) {
+  constexpr int span = LEVEL == 0 ? kRun : (LEVEL == 1 ? kRun * kRun : kRun * kRun * kRun);
+  const int64_t s = (int64_t)blockIdx.x * span;
+  if (s + span > a.tokens) return;
+  const uint32_t key = a.keys[s];
+  if (key != a.keys[s + span - 1] || key >= (uint32_t)a.rows || (int64_t)key == (int64_t)a.padding) return;
+  const int ld = (a.width + 7) & ~7;
+  for (int c = threadIdx.x * 8; c < ld; c += kThreads * 8) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if constexpr (LEVEL == 0) add_tokens<G>(a, (int)s, (int)s + kRun, c, v);
+    else add_sums(a.part[LEVEL - 1], ld, blockIdx.x * kRun, blockIdx.x * kRun + kRun, c, v);
+    store8(glob(a.part[LEVEL]) + (int64_t)blockIdx.x * ld + c, true, 8, v);
+  }
+}
+
+// [s, e) of sorted positions added to v: whole aligned runs through their sums
+template <typename G>
+__device__ __forceinline__ void add_range(const EmbedGradArgs& a, int s, int e, int c, float (&v)[8]) {
+  const int ld = (a.width + 7) & ~7;
+  const int s0 = (s + kRun - 1) / kRun, e0 = e / kRun;          // whole first-level runs [s0, e0)
+  if (s0 >= e0) {
+    add_tokens<G>(a, s, e, c, v);
+    return;
+  }
+  add_tokens<G>(a, s, s0 * kRun, c, v);
+  const int s1 = (s0 + kRun - 1) / kRun, e1 = e0 / kRun;
+  if (s1 >= e1) {
+    add_sums(a.part[0], ld, s0, e0, c, v);
+  } else {
+    add_sums(a.part[0], ld, s0, s1 * kRun, c, v);
+    const int s2 = (s1 + kRun - 1) / kRun, e2 = e1 / kRun;
+    if (s2 >= e2) {
+      add_sums(a.part[1], ld, s1, e1, c, v);
+    } else {
+      add_sums(a.part[1], ld, s1, s2 * kRun, c, v);
+      add_sums(a.part[2], ld, s2, e2, c, v);
+      add_sums(a.part[1], ld, e2 * kRun, e1, c, v);
+    }
+    add_sums(a.part[0], ld, e1 * kRun, e0, c, v);
+  }
+  add_tokens<G>(a, e0 * kRun, e, c, v);
+}
+
+constexpr int kEmbedRows = 32;           // table rows per workgroup
+template <typename G, typename O>
+__global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
+  __shared__ int start[kEmbedRows + 1];
+  const int64_t v0 = (int64_t)blockIdx.x * kEmbedRows;
+  if (threadIdx.x <= kEmbedRows) {       // first sorted position with an id ≥ v0 + thread
+    const int64_t want = v0 + threadIdx.x;
+    int lo = 0, hi = a.tokens;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)a.keys[mid] < want) lo = mid + 1; else hi = mid;
+    }
+    start[threadIdx.x] = lo;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int r = wave; r < kEmbedRows; r += kThreads / 64) {
+    const int64_t v = v0 + r;
+    if (v >= a.rows) return;
+    const int s = start[r], e = v == a.padding ? s : start[r + 1];
+    if (s == e && a.accumulate) continue;
+    gptr<O> out = glob((O*)a.out) + v * a.width;
+    for (int c = lane * 8; c < a.width; c += 512) {
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (s != e) {
+        add_range<G>(a, s, e, c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= a.scale;
+        if (a.accumulate) {
+          float o[8];
+          load8((gptr<const O>)out + c, a.vec_out, a.width - c, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] += o[k];
+        }
+      }
+      store8(out + c, a.vec_out, a.width - c, x);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit checkpoints.  32 columns of a row share the exponent byte b, q is a signed
+// byte and the value q·2^(b − 133).  b is the biased fp32 exponent of the block's
+// largest magnitude (one more where that would round to 128, unless b = 254, where
+// q saturates at 127), so that q = rint(x·2^(133 − b)) has |q| ≤ 127 and every
+// value is kept to within 2^(b − 134), half a step.  A block whose largest
+// magnitude is below 2^−126 becomes zeros (b = 0); a block that holds an infinity
+// or NaN reads back as NaN (b = 255).  q·2^(b − 133) is exact in bf16.
+// Four threads share a block, 8 columns each.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_ckpt_quantize(CodecArgs a) {
+  const int64_t n = a.rows * a.blocks * 4, step = (int64_t)gridDim.x * kThreads;
+  const bool vec_q = (a.cols & 7) == 0 && ((uintptr_t)a.q & 7) == 0;
+  // whole waves step together: the exchanges below are among four neighbours
+  for (int64_t id0 = (int64_t)blockIdx.x * kThreads; id0 < n; id0 += step) {
+    const int64_t id = id0 + threadIdx.x;
+    const bool on = id < n;
+    const int64_t blk = id >> 2;
+    const int64_t r = on ? blk / a.blocks : 0;
+    const int b = (int)(blk - r * a.blocks);
+    const int c = b * 32 + (int)(id & 3) * 8;
+    const int left = a.cols - c;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (on && left > 0) load8(glob((const T*)a.x) + r * a.ldx + c, a.vec && left >= 8, left, v);
+    uint32_t m = 0;                                            // largest magnitude's bits (NaN above inf)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
+      m = u > m ? u : m;
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint32_t u = (uint32_t)__shfl_xor((int)m, o, 64);
+      m = u > m ? u : m;
+    }
+    int eb = (int)(m >> 23);                                   // 0: zeros, 255: not finite
+    if (eb > 0 && eb < 254 && (m & 0x7fffffu) >= 0x7f0000u) ++eb;   // 127.5/64 = 1.9921875 and up
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float q = eb > 0 && eb < 255 ? rintf(__builtin_amdgcn_ldexpf(v[e], 133 - eb)) : 0.f;
+      q = fminf(fmaxf(q, -127.f), 127.f);
+      w[e >> 2] |= ((uint32_t)(int)q & 255u) << (8 * (e & 3));
+    }
+    if (!on) continue;
+    gptr<int8_t> d = glob(a.q) + r * a.cols + c;
+    if (vec_q && left >= 8) {
+      typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+      *(gptr<u32x2>)d = u32x2{w[0], w[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) d[e] = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
+    }
+    if ((id & 3) == 0) glob(a.exps)[blk] = (uint8_t)eb;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_ckpt_read(CodecArgs a) {
+  const int per = (a.cols + 7) >> 3;
+  const int64_t n = a.rows * per, step = (int64_t)gridDim.x * kThreads;
+  const bool vec_q = (a.cols & 7) == 0 && ((uintptr_t)a.q & 7) == 0;
+  for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < n; id += step) {
+    const int64_t r = id / per;
+    const int c = (int)(id - r * per) * 8;
+    const int left = a.cols - c;
+    const int eb = glob((const uint8_t*)a.exps)[r * a.blocks + (c >> 5)];
+    gptr<const int8_t> q = glob((const int8_t*)a.q) + r * a.cols + c;
+    uint32_t w[2] = {0u, 0u};
+    if (vec_q) {
+      typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 u = *(gptr<const u32x2>)q;
+      w[0] = u.x;
+      w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) w[e >> 2] |= ((uint32_t)q[e] & 255u) << (8 * (e & 3));
+    }
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = __builtin_amdgcn_ldexpf((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), eb - 133);
+      v[e] = eb == 255 ? __uint_as_float(0x7fc00000u) : x;
+    }
+    store8(glob((T*)a.out) + r * a.ldo + c, a.vec && left >= 8, left, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+// Workgroups of a grid-stride kernel: enough to fill 256 CUs several times over
+static unsigned stride_grid(int64_t items) {
+  const int64_t wg = cdiv(items, kThreads);
+  return (unsigned)(wg < 1 ? 1 : (wg < 16384 ? wg : 16384));
+}
+
+// Dynamic LDS limit of the contraction kernels, raised once per device (first
+// calls may come from several threads).
+static int ensure_lds() {
+  static std::atomic<uint64_t> ready{0};
+  static std::mutex mu;
+  int dev = 0;
+  int e = (int)hipGetDevice(&dev);
+  if (e) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+  if (bit && (ready.load(std::memory_order_acquire) & bit)) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (bit && (ready.load(std::memory_order_relaxed) & bit)) return 0;
+  const void* ks[] = {(const void*)k_ce_logits<false, false>, (const void*)k_ce_logits<true, false>,
+                      (const void*)k_ce_logits<true, true>, (const void*)k_product<false>, (const void*)k_product<true>};
+  for (const void* k : ks)
+    if ((e = (int)hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kGemmLds))) return e;
+  if (bit) ready.fetch_or(bit, std::memory_order_release);
+  return 0;
+}
+
+#define DMUON_LAUNCH(phase, stream, kernel, grid, block, lds, args)                            \
+  do {                                                                                         \
+    timing_before(phase, stream);                                                              \
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, (hipStream_t)(stream), args);     \
+    const int err_ = (int)hipGetLastError();                                                   \
+    timing_after(phase, stream);                                                               \
+    return err_;                                                                               \
+  } while (0)
+
+int launch_pack(const PackArgs& a, int phase, void* stream) {
+  DMUON_LAUNCH(phase, stream, k_pack, stride_grid(a.rows * (a.ldd / 8)), kThreads, 0, a);
+}
+int launch_ce_scan(const CeScanArgs& a, void* stream) {
+  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan, 1, kScanThreads, 0, a);
+}
+int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream) {
+  const int e = ensure_lds();
+  if (e) return e;
+  const unsigned grid = (unsigned)(a.tiles_t * a.tiles_v);
+  if (!backward) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<false, false>), grid, kGemmThreads, kGemmLds, a);
+  if (f32) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<true, true>), grid, kGemmThreads, kGemmLds, a);
+  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<true, false>), grid, kGemmThreads, kGemmLds, a);
+}
+int launch_ce_rows(const CeRowsArgs& a, void* stream) {
+  DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
+}
+int launch_product(const ProductArgs& a, int phase, void* stream) {
+  const int e = ensure_lds();
+  if (e) return e;
+  const unsigned grid = (unsigned)(a.tiles_r * a.tiles_c * a.groups * a.splits);
+  if (a.b_rows) DMUON_LAUNCH(phase, stream, k_product<false>, grid, kGemmThreads, kGemmLds, a);
+  DMUON_LAUNCH(phase, stream, k_product<true>, grid, kGemmThreads, kGemmLds, a);
+}
+int launch_join(const JoinArgs& a, int phase, void* stream) {
+  DMUON_LAUNCH(phase, stream, k_join, stride_grid(a.rows * cdiv(a.cols, 8)), kThreads, 0, a);
+}
+int launch_embed(const EmbedArgs& a, void* stream) {
+  const unsigned grid = stride_grid(a.tokens * cdiv(a.width, 8));
+  if (a.f32) DMUON_LAUNCH(PH_EMBED, stream, k_embed<float>, grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_EMBED, stream, k_embed<uint16_t>, grid, kThreads, 0, a);
+}
+int launch_sort_pass(const SortArgs& a, void* stream) {
+  timing_before(PH_EMBED_GRAD, stream);
+  hipLaunchKernelGGL(k_sort_count, dim3(a.blocks), dim3(kThreads), 0, (hipStream_t)stream, a);
+  hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(kScanThreads), 0, (hipStream_t)stream, a);
+  hipLaunchKernelGGL(k_sort_place, dim3(a.blocks), dim3(kThreads), 0, (hipStream_t)stream, a);
+  const int e = (int)hipGetLastError();
+  timing_after(PH_EMBED_GRAD, stream);
+  return e;
+}
+int launch_embed_run(const EmbedGradArgs& a, int level, void* stream) {
+  const int span = level == 0 ? kRun : (level == 1 ? kRun * kRun : kRun * kRun * kRun);
+  const unsigned grid = (unsigned)(a.tokens / span);
+  if (level == 0) {
+    if (a.grad_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 0>), grid, kThreads, 0, a);
+    DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<uint16_t, 0>), grid, kThreads, 0, a);
+  }
+  if (level == 1) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 1>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 2>), grid, kThreads, 0, a);
+}
+int launch_embed_grad(const EmbedGradArgs& a, void* stream) {
+  const unsigned grid = (unsigned)cdiv(a.rows, kEmbedRows);
+  if (a.grad_f32) {
+    if (a.out_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, float>), grid, kThreads, 0, a);
+    DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, uint16_t>), grid, kThreads, 0, a);
+  }
+  if (a.out_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<uint16_t, float>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<uint16_t, uint16_t>), grid, kThreads, 0, a);
+}
+int launch_ckpt_quantize(const CodecArgs& a, void* stream) {
+  const unsigned grid = stride_grid(a.rows * a.blocks * 4);
+  if (a.f32) DMUON_LAUNCH(PH_CKPT_CODEC, stream, k_ckpt_quantize<float>, grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_CKPT_CODEC, stream, k_ckpt_quantize<uint16_t>, grid, kThreads, 0, a);
+}
+int launch_ckpt_read(const CodecArgs& a, int phase, void* stream) {
+  const unsigned grid = stride_grid(a.rows * cdiv(a.cols, 8));
+  if (a.f32) DMUON_LAUNCH(phase, stream, k_ckpt_read<float>, grid, kThreads, 0, a);
+  DMUON_LAUNCH(phase, stream, k_ckpt_read<uint16_t>, grid, kThreads, 0, a);
+}
+
+}  // namespace dmuon

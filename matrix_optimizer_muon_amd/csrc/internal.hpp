@@ -27,7 +27,16 @@ enum Phase : int {
   PH_UPDATE = 5,     // W ← (1 − lr wd) W − lr X0 (only when k = 0)
   PH_GEMM = 6,       // test hook: plain NT product
   PH_ADAMW = 7,      // the adamw route (its own launch table)
-  PH_COUNT = 8
+  PH_COUNT = 8,      // phases of the step's launch tables
+  PH_CE_PACK = 8,    // cross entropy: compact rows, operand copies
+  PH_CE_LOGITS = 9,  // logits tiles: softmax statistics, or their gradient
+  PH_CE_ROWS = 10,   // statistics joined: losses, log-sum-exp
+  PH_CE_GRADS = 11,  // gradient products
+  PH_EMBED = 12,     // embedding lookup
+  PH_EMBED_GRAD = 13,  // token sort and the table's gradient
+  PH_CKPT_CODEC = 14,  // 8-bit activation checkpoints: store, read back
+  PH_CKPT_WGRAD = 15,  // weight gradient from a checkpoint
+  PH_TOTAL = 16
 };
 
 // One tensor (2-D = batch 1, or 3-D batch of slices) as the kernels see it.
