@@ -321,26 +321,28 @@ int check_wgrad(const dmuon_ckpt8_wgrad_problem* p, std::vector<Range>* rs) {
 // ---- embedding ------------------------------------------------------------------
 struct EmbedPlan {
   uint32_t *keys[2], *idx[2], *hist;
-  float* part[3];
-  int blocks, passes;
+  float* part[2];
+  int blocks, passes, key_bits, index_bits;
+  bool one;                              // the one-workgroup sort
   size_t bytes;
 };
 
 EmbedPlan embed_plan(int64_t tokens, int64_t rows, int64_t width, char* base) {
   EmbedPlan pl{};
   pl.blocks = (int)cdiv(tokens, kSortItems);
-  int bits = 0;
-  while (rows >> bits) ++bits;           // keys are 0 … rows
-  pl.passes = (int)cdiv(bits, 8);
+  while (rows >> pl.key_bits) ++pl.key_bits;           // keys are 0 … rows
+  while ((tokens - 1) >> pl.index_bits) ++pl.index_bits;
+  pl.one = tokens <= kSortBlockMax && pl.key_bits + pl.index_bits <= 32;
+  pl.passes = (int)cdiv(pl.key_bits, 8);
   Carver c{base};
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (pl.one ? 1 : 2); ++i) {
     pl.keys[i] = c.take<uint32_t>(tokens);
     pl.idx[i] = c.take<uint32_t>(tokens);
   }
-  pl.hist = c.take<uint32_t>((int64_t)256 * pl.blocks);
+  if (!pl.one) pl.hist = c.take<uint32_t>((int64_t)256 * pl.blocks);
   const int64_t ld = round_up(width, 8);
   int64_t span = kRun;
-  for (int l = 0; l < 3; ++l, span *= kRun) pl.part[l] = c.take<float>(tokens / span * ld);
+  for (int l = 0; l < 2; ++l, span *= kRun) pl.part[l] = c.take<float>(tokens / span * ld);
   pl.bytes = c.off;
   return pl;
 }
@@ -453,6 +455,7 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
       CeLogitsArgs g = logits_args(pl, w, ldw, plane, v0, rows);
       g.clse = pl.clse;
       g.cg = pl.cg;
+      g.gmax = pl.gmax;
       g.dz = pl.dz;
       g.dz_plane = pl.T * pl.ldz;
       g.ldz = (int32_t)pl.ldz;
@@ -618,17 +621,23 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     s.rows = (int32_t)rows;
     s.hist = pl.hist;
     s.blocks = pl.blocks;
-    for (int k = 0; k < pl.passes; ++k) {
-      s.keys_in = k ? pl.keys[(k + 1) & 1] : nullptr;
-      s.idx_in = k ? pl.idx[(k + 1) & 1] : nullptr;
-      s.keys_out = pl.keys[k & 1];
-      s.idx_out = pl.idx[k & 1];
-      s.shift = 8 * k;
-      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_pass(s, stream); }))) return e;
-    }
     EmbedGradArgs a{};
-    a.keys = pl.keys[(pl.passes - 1) & 1];
-    a.idx = pl.idx[(pl.passes - 1) & 1];
+    if (pl.one) {
+      s.key_bits = pl.key_bits;
+      s.index_bits = pl.index_bits;
+      a.keys = s.keys_out = pl.keys[0];
+      a.idx = s.idx_out = pl.idx[0];
+      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_block(s, stream); }))) return e;
+    } else {
+      for (int k = 0; k < pl.passes; ++k) {
+        s.keys_in = k ? pl.keys[(k + 1) & 1] : nullptr;
+        s.idx_in = k ? pl.idx[(k + 1) & 1] : nullptr;
+        a.keys = s.keys_out = pl.keys[k & 1];
+        a.idx = s.idx_out = pl.idx[k & 1];
+        s.shift = 8 * k;
+        if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_pass(s, stream); }))) return e;
+      }
+    }
     a.tokens = (int32_t)tokens;
     a.rows = (int32_t)rows;
     a.width = (int32_t)width;
@@ -642,9 +651,11 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     a.vec_out = rows16(grad_table, width, width, type_bytes(out_dtype));
     a.scale = scale;
     a.out = grad_table;
-    for (int l = 0; l < 3; ++l) a.part[l] = pl.part[l];
+    a.tpr = 1;
+    while (a.tpr < kThreads && a.tpr * 8 < width) a.tpr *= 2;
+    for (int l = 0; l < 2; ++l) a.part[l] = pl.part[l];
     int64_t span = kRun;
-    for (int l = 0; l < 3 && span <= tokens; ++l, span *= kRun)
+    for (int l = 0; l < 2 && span <= tokens; ++l, span *= kRun)
       if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_embed_run(a, l, stream); }))) return e;
     return go(env, PH_EMBED_GRAD, stream, [&] { return launch_embed_grad(a, stream); });
   });

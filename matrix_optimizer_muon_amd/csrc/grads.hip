@@ -126,73 +126,95 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// cross entropy: the compact list of tokens that take part.  One workgroup; every
-// thread owns a contiguous range of tokens, so the list keeps their order.
+// cross entropy: the compact list of tokens that take part, in order.  One
+// workgroup walks the tokens 8192 at a time, the loads of a step issued together:
+// places come from ballots and one scan over (row of 1024 tokens, wave).
 // Forward: tokens whose target is not ignore_index (the others get loss and lse
 // 0).  Backward: those whose target also lies in the vocabulary and whose weight
-// is not zero; weights are stored divided by the largest magnitude, which the
-// products' epilogues multiply back, so that dZ is rounded to bf16 relative to
-// (p − δ) alone (a uniform weight leaves p − δ unscaled) and tiny weights do not
-// underflow.
+// is not zero.  The largest |weight| goes out too: dZ uses weights relative to it
+// and the products' epilogues multiply it back, so that a uniform weight leaves
+// p − δ unscaled when it is rounded to bf16 and tiny weights do not underflow.
+// Latency bound: 4 µs for 8192 tokens (a walk over one range per thread: 39).
 // ---------------------------------------------------------------------------
 constexpr int kScanThreads = 1024;
+constexpr int kScanRows = 8;
 __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
-  __shared__ int wave_sum[kScanThreads / 64];
-  __shared__ float wave_max[kScanThreads / 64];
+  constexpr int waves = kScanThreads / 64, parts = kScanRows * waves;      // 128 partial counts
+  __shared__ int place[parts];
+  __shared__ int total;
+  __shared__ float wave_max[waves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int chunk = (a.tokens + kScanThreads - 1) / kScanThreads;
-  const int64_t t0 = (int64_t)tid * chunk;
-  const int64_t t1 = t0 + chunk < a.tokens ? t0 + chunk : a.tokens;
-  auto takes_part = [&](int64_t t, int64_t y) {
-    if (y == a.ignore) return false;
-    return !a.backward || (y >= 0 && y < a.vocab && !(a.grad_losses[t] == 0.f));
-  };
-  int n = 0;
   float gm = 0.f;
-  for (int64_t t = t0; t < t1; ++t)
-    if (takes_part(t, load_index(a.targets, a.idx64, t))) {
-      ++n;
-      if (a.backward) gm = fmaxf(gm, fabsf(a.grad_losses[t]));
-    }
-  int incl = n;
+  int base = 0;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kScanRows * kScanThreads) {
+    int64_t y[kScanRows];
+    float g[kScanRows], l[kScanRows];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += up;
+    for (int k = 0; k < kScanRows; ++k) {
+      const int64_t t = t0 + k * kScanThreads + tid;
+      y[k] = a.ignore;
+      g[k] = l[k] = 0.f;
+      if (t < a.tokens) {
+        y[k] = load_index(a.targets, a.idx64, t);
+        if (a.backward) {
+          g[k] = a.grad_losses[t];
+          l[k] = a.lse_in[t];
+        }
+      }
+    }
+    uint64_t in[kScanRows];
+#pragma unroll
+    for (int k = 0; k < kScanRows; ++k) {
+      const bool part = y[k] != a.ignore && (!a.backward || (y[k] >= 0 && y[k] < a.vocab && !(g[k] == 0.f)));
+      in[k] = __ballot(part);
+      if (part) gm = fmaxf(gm, fabsf(g[k]));
+      if (lane == 0) place[k * waves + wave] = __popcll(in[k]);
+    }
+    __syncthreads();
+    if (wave == 0) {                        // exclusive scan of the 128 counts, two per lane
+      const int c0 = place[2 * lane], c1 = place[2 * lane + 1];
+      int incl = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += up;
+      }
+      place[2 * lane] = base + incl - c0 - c1;
+      place[2 * lane + 1] = base + incl - c1;
+      if (lane == 63) total = base + incl;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kScanRows; ++k) {
+      const int64_t t = t0 + k * kScanThreads + tid;
+      if (t >= a.tokens) continue;
+      const bool part = (in[k] >> lane) & 1;
+      const int i = place[k * waves + wave] + __popcll(in[k] & ((1ull << lane) - 1));
+      if (a.backward) a.pos[t] = part ? i : -1;
+      if (part) {
+        a.rows[i] = (int32_t)t;
+        a.tgt[i] = y[k] >= 0 && y[k] < a.vocab ? (int32_t)y[k] : -1;
+        if (a.backward) {
+          a.clse[i] = l[k];
+          a.cg[i] = g[k];
+        }
+      } else if (!a.backward) {
+        a.losses[t] = 0.f;
+        a.lse[t] = 0.f;
+      }
+    }
+    base = total;
+    __syncthreads();
   }
+  if (tid == 0) *a.count = base;
+  if (!a.backward) return;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor(gm, o, 64));
-  if (lane == 63) wave_sum[wave] = incl;
   if (lane == 0) wave_max[wave] = gm;
   __syncthreads();
-  int base = 0, total = 0;
-  gm = 0.f;
-  for (int w = 0; w < kScanThreads / 64; ++w) {
-    if (w < wave) base += wave_sum[w];
-    total += wave_sum[w];
-    gm = fmaxf(gm, wave_max[w]);
-  }
   if (tid == 0) {
-    *a.count = total;
-    if (a.backward) *a.gmax = gm;
-  }
-  int i = base + incl - n;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t y = load_index(a.targets, a.idx64, t);
-    const bool in = takes_part(t, y);
-    if (a.backward) a.pos[t] = in ? i : -1;
-    if (in) {
-      a.rows[i] = (int32_t)t;
-      a.tgt[i] = y >= 0 && y < a.vocab ? (int32_t)y : -1;
-      if (a.backward) {
-        a.clse[i] = a.lse_in[t];
-        a.cg[i] = a.grad_losses[t] / gm;
-      }
-      ++i;
-    } else if (!a.backward) {
-      a.losses[t] = 0.f;
-      a.lse[t] = 0.f;
-    }
+    for (int w = 1; w < waves; ++w) gm = fmaxf(gm, wave_max[w]);
+    *a.gmax = gm;
   }
 }
 
@@ -358,7 +380,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
       if (y >= 0 && y < kTile && g.tgt[tok[j]] >= 0 && (y >> 7) == wr && ((y >> 2) & 1) == h) want[j] = (y & 127) - 4 * h;
       if constexpr (BACKWARD) {
         L[j] = g.clse[tok[j]];
-        w[j] = g.cg[tok[j]];
+        w[j] = g.cg[tok[j]] / *g.gmax;
       }
     }
   }
@@ -616,15 +638,114 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// stable radix sort of (id, token) pairs, 8 bits of the id per pass: digit counts
-// per workgroup, one scan over [digit][workgroup], stable placement.  Inside a
-// workgroup each wave owns a contiguous quarter and places 64 pairs at a time by
-// the rank among equal digits (ballots), so equal ids keep the order of their
-// tokens whatever the timing.
+// stable radix sort of (id, token) pairs, 8 bits of the id per pass.  Ids outside
+// the table get the key `rows` and sort last.
+//
+// Up to 32768 tokens whose id and index fit 32 bits together are sorted by one
+// workgroup in one launch (k_sort_block): the words stay in registers, a pass
+// ranks 64 of them at a time among equal digits by ballots, exchanges them through
+// LDS and reads them back.  Every wave owns a contiguous part, so equal ids keep
+// the order of their tokens whatever the timing.  Measured with the gradient of
+// 8192 tokens (2 passes): one launch instead of six.
 // ---------------------------------------------------------------------------
 constexpr int kSortWaves = kThreads / 64;
 constexpr int kSortRounds = kSortItems / kThreads;
+constexpr int kBlockWaves = kScanThreads / 64;
 
+// Lanes whose digit equals this lane's, among those `on`; ballots over `bits` bits
+__device__ __forceinline__ uint64_t match_digit(uint32_t d, int bits, uint64_t on) {
+  uint64_t same = on;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t m = __ballot((d >> b) & 1);
+    same &= (d >> b) & 1 ? m : ~m;
+  }
+  return same;
+}
+// LDS reads and writes of one wave stay in order, and are not moved across this
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int ITEMS>
+__global__ __launch_bounds__(kScanThreads) void k_sort_block(SortArgs a) {
+  extern __shared__ __align__(16) uint32_t words[];        // kScanThreads·ITEMS
+  __shared__ uint32_t cnt[kBlockWaves][256];
+  __shared__ uint32_t wave_sum[kBlockWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int first = wave * 64 * ITEMS + lane;              // item r of this lane: first + 64 r
+  uint32_t w[ITEMS];
+  uint32_t at[ITEMS];
+#pragma unroll
+  for (int r = 0; r < ITEMS; ++r) {
+    const int i = first + 64 * r;
+    w[r] = 0xffffffffu;                                    // past the end: last, and stays last
+    if (i < a.tokens) {
+      const int64_t id = load_index(a.ids, a.idx64, i);
+      const uint32_t key = id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
+      w[r] = (key << a.index_bits) | (uint32_t)i;
+    }
+  }
+  for (int shift = 0; shift < a.key_bits; shift += 8) {
+    const int bits = a.key_bits - shift < 8 ? a.key_bits - shift : 8;
+    const uint32_t mask = (1u << bits) - 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cnt[wave][lane + 64 * k] = 0;
+    wave_order();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      const uint32_t d = (w[r] >> (a.index_bits + shift)) & mask;
+      const uint64_t same = match_digit(d, bits, ~0ull);
+      const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
+      const uint32_t before = cnt[wave][d];
+      at[r] = before + rank;
+      wave_order();                                        // every lane has read before the first of each digit adds
+      if (rank == 0) cnt[wave][d] = before + (uint32_t)__popcll(same);
+      wave_order();
+    }
+    __syncthreads();
+    // exclusive scan over (digit, wave): thread t holds waves 4(t & 3) … + 3 of digit t >> 2
+    const int d0 = tid >> 2, v0 = 4 * (tid & 3);
+    uint32_t c[4], s = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c[k] = cnt[v0 + k][d0];
+      s += c[k];
+    }
+    uint32_t incl = s;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t up = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    uint32_t base = incl - s;
+    for (int v = 0; v < wave; ++v) base += wave_sum[v];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      cnt[v0 + k][d0] = base;
+      base += c[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) words[cnt[wave][(w[r] >> (a.index_bits + shift)) & mask] + at[r]] = w[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) w[r] = words[first + 64 * r];
+  }
+#pragma unroll
+  for (int r = 0; r < ITEMS; ++r) {
+    const int i = first + 64 * r;
+    if (i < a.tokens) {
+      a.keys_out[i] = w[r] >> a.index_bits;
+      a.idx_out[i] = w[r] & ((1u << a.index_bits) - 1);
+    }
+  }
+}
+
+// The same for any number of tokens: per pass the digit counts of every workgroup,
+// one scan over [digit][workgroup], and the stable placement.
 __device__ __forceinline__ void sort_pair(const SortArgs& a, int64_t i, uint32_t& key, uint32_t& idx) {
   if (a.keys_in) {
     key = a.keys_in[i];
@@ -651,12 +772,12 @@ __global__ __launch_bounds__(kThreads) void k_sort_count(SortArgs a) {
     }
   }
   __syncthreads();
-  a.hist[threadIdx.x * a.blocks + blockIdx.x] = cnt[threadIdx.x];
+  a.hist[(int64_t)threadIdx.x * a.blocks + blockIdx.x] = cnt[threadIdx.x];
 }
 
 // exclusive scan of hist[256·blocks] in place, one workgroup
 __global__ __launch_bounds__(kScanThreads) void k_sort_scan(SortArgs a) {
-  __shared__ uint32_t wave_sum[kScanThreads / 64];
+  __shared__ uint32_t wave_sum[kBlockWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = 256 * a.blocks, chunk = (n + kScanThreads - 1) / kScanThreads;
   const int i0 = tid * chunk, i1 = i0 + chunk < n ? i0 + chunk : n;
@@ -697,7 +818,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(SortArgs a) {
     }
   }
   __syncthreads();
-  uint32_t first = a.hist[tid * a.blocks + blockIdx.x];
+  uint32_t first = a.hist[(int64_t)tid * a.blocks + blockIdx.x];
 #pragma unroll
   for (int w = 0; w < kSortWaves; ++w) {
     const uint32_t c = at[w][tid];
@@ -710,20 +831,13 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(SortArgs a) {
     const int64_t i = base + r * 64 + lane;
     const bool on = i < a.tokens;
     const uint32_t d = (key[r] >> a.shift) & 255;
-    uint64_t same = __ballot(on);
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const uint64_t m = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? m : ~m;
-    }
+    const uint64_t same = match_digit(d, 8, __ballot(on));
     const int rank = __popcll(same & ((1ull << lane) - 1));
     uint32_t slot = 0;
     if (on) slot = at[wave][d];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before the leaders add
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
     if (on && rank == 0) at[wave][d] = slot + (uint32_t)__popcll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
     if (on) {
       a.keys_out[slot + rank] = key[r];
       a.idx_out[slot + rank] = idx[r];
@@ -734,55 +848,101 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(SortArgs a) {
 // ---------------------------------------------------------------------------
 // the table's gradient from the sorted tokens.
 // A row's gradient is the sum over a contiguous range of sorted tokens.  Ranges
-// are cut at fixed multiples of 32, 1024 and 32768: a whole aligned run of equal
-// ids is summed once by k_embed_run (level 0 from the tokens, levels 1 and 2 from
-// 32 sums of the level below), and k_embed_grad adds at most 62 tokens and 62 sums
-// per level to a row, so a frequent token is spread over many workgroups and the
-// order of every sum is fixed.
+// are cut at fixed multiples of 32 and 1024: a whole aligned run of equal ids is
+// summed once by k_embed_run (level 0 from the tokens, level 1 from 32 sums of
+// level 0), and k_embed_grad adds at most 62 tokens and 62 first-level sums to a
+// row besides its second-level ones, so a frequent token is spread over many
+// workgroups and the order of every sum is fixed.
 // ---------------------------------------------------------------------------
+template <typename G> struct Raw8;                   // 8 elements as loaded
+template <> struct Raw8<uint16_t> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = *(gptr<const u32x4_t>)p; }
+  __device__ __forceinline__ void add(float (&v)[8]) const {
+    float x[8];
+    unpack8(u, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += x[k];
+  }
+};
+template <> struct Raw8<float> {
+  f32x4_t u[2];
+  __device__ __forceinline__ void load(gptr<const float> p) {
+    u[0] = ((gptr<const f32x4_t>)p)[0];
+    u[1] = ((gptr<const f32x4_t>)p)[1];
+  }
+  __device__ __forceinline__ void add(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] += u[0][k];
+      v[4 + k] += u[1][k];
+    }
+  }
+};
+
+// v += Σ of rows s … e − 1 (of row(i)), in order, 8 loads in flight
+template <typename G, typename R>
+__device__ __forceinline__ void add_rows(int s, int e, bool vec, int left, float (&v)[8], R row) {
+  constexpr int kAhead = 8;
+  int i = s;
+  if (vec) {
+    for (; i + kAhead <= e; i += kAhead) {
+      Raw8<G> x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u].load(row(i + u));
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u].add(v);
+    }
+#pragma unroll 1
+    for (; i < e; ++i) {
+      Raw8<G> x;
+      x.load(row(i));
+      x.add(v);
+    }
+  } else {
+#pragma unroll 1
+    for (; i < e; ++i) {
+      float x[8];
+      load8(row(i), false, left, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += x[k];
+    }
+  }
+}
 template <typename G>
 __device__ __forceinline__ void add_tokens(const EmbedGradArgs& a, int s, int e, int c, float (&v)[8]) {
-  const int left = a.width - c;
-  int i = s;
-  for (; i + 4 <= e; i += 4) {
-    float x[4][8];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) load8(glob((const G*)a.grad) + (int64_t)a.idx[i + u] * a.ldg + c, a.vec_in, left, x[u]);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += x[u][k];
-  }
-  for (; i < e; ++i) {
-    float x[8];
-    load8(glob((const G*)a.grad) + (int64_t)a.idx[i] * a.ldg + c, a.vec_in, left, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += x[k];
-  }
+  add_rows<G>(s, e, a.vec_in, a.width - c, v, [&](int i) { return glob((const G*)a.grad) + (int64_t)a.idx[i] * a.ldg + c; });
 }
 __device__ __forceinline__ void add_sums(const float* part, int ld, int s, int e, int c, float (&v)[8]) {
-#pragma unroll 4
-  for (int i = s; i < e; ++i) {
-    float x[8];
-    load8(glob(part) + (int64_t)i * ld + c, true, 8, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += x[k];
-  }
+  add_rows<float>(s, e, true, 8, v, [&](int i) { return glob(part) + (int64_t)i * ld + c; });
 }
 
+// One whole run of equal ids per workgroup and 512 columns; each wave sums a
+// quarter of it, the quarters are added in order.
 template <typename G, int LEVEL>
 __global__ __launch_bounds__(kThreads) void k_embed_run(EmbedGradArgs a) {
-  constexpr int span = LEVEL == 0 ? kRun : (LEVEL == 1 ? kRun * kRun : kRun * kRun * kRun);
+  constexpr int span = LEVEL == 0 ? kRun : kRun * kRun;
+  __shared__ float sum[kThreads / 64][512];
   const int64_t s = (int64_t)blockIdx.x * span;
   if (s + span > a.tokens) return;
   const uint32_t key = a.keys[s];
   if (key != a.keys[s + span - 1] || key >= (uint32_t)a.rows || (int64_t)key == (int64_t)a.padding) return;
   const int ld = (a.width + 7) & ~7;
-  for (int c = threadIdx.x * 8; c < ld; c += kThreads * 8) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if constexpr (LEVEL == 0) add_tokens<G>(a, (int)s, (int)s + kRun, c, v);
-    else add_sums(a.part[LEVEL - 1], ld, blockIdx.x * kRun, blockIdx.x * kRun + kRun, c, v);
-    store8(glob(a.part[LEVEL]) + (int64_t)blockIdx.x * ld + c, true, 8, v);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.y * 512 + lane * 8;
+  constexpr int quarter = kRun / (kThreads / 64);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < ld) {
+    const int i = (LEVEL == 0 ? (int)s : (int)blockIdx.x * kRun) + wave * quarter;
+    if constexpr (LEVEL == 0) add_tokens<G>(a, i, i + quarter, c, v);
+    else add_sums(a.part[0], ld, i, i + quarter, c, v);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[wave][lane * 8 + k] = v[k];
+  __syncthreads();
+  for (int k = threadIdx.x; k < 512; k += kThreads) {
+    const int col = blockIdx.y * 512 + k;
+    if (col < ld) glob(a.part[LEVEL])[(int64_t)blockIdx.x * ld + col] = (sum[0][k] + sum[1][k]) + (sum[2][k] + sum[3][k]);
   }
 }
 
@@ -801,27 +961,46 @@ __device__ __forceinline__ void add_range(const EmbedGradArgs& a, int s, int e, 
     add_sums(a.part[0], ld, s0, e0, c, v);
   } else {
     add_sums(a.part[0], ld, s0, s1 * kRun, c, v);
-    const int s2 = (s1 + kRun - 1) / kRun, e2 = e1 / kRun;
-    if (s2 >= e2) {
-      add_sums(a.part[1], ld, s1, e1, c, v);
-    } else {
-      add_sums(a.part[1], ld, s1, s2 * kRun, c, v);
-      add_sums(a.part[2], ld, s2, e2, c, v);
-      add_sums(a.part[1], ld, e2 * kRun, e1, c, v);
-    }
+    add_sums(a.part[1], ld, s1, e1, c, v);
     add_sums(a.part[0], ld, e1 * kRun, e0, c, v);
   }
   add_tokens<G>(a, e0 * kRun, e, c, v);
 }
 
-constexpr int kEmbedRows = 32;           // table rows per workgroup
+// first sorted position with an id ≥ want, by one wave: 64 probes per step
+__device__ __forceinline__ int wave_lower_bound(const uint32_t* keys, int n, int64_t want) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = n;                                // the answer is in [lo, hi]
+  while (hi - lo > 0) {
+    const int step = (hi - lo + 63) / 64;
+    const int at = lo + lane * step;                 // probe: keys[at] < want?
+    const bool below = at < hi && (int64_t)keys[at] < want;
+    const int k = __popcll(__ballot(below));         // the probes below come first
+    if (k == 0) return lo;
+    const int nlo = lo + (k - 1) * step + 1;
+    const int nhi = k < 64 ? (lo + k * step < hi ? lo + k * step : hi) : hi;
+    lo = nlo;
+    hi = nhi;
+  }
+  return lo;
+}
+
+// 32 table rows per workgroup; `tpr` threads share a row, 8 columns each, so that
+// a row with many tokens has the whole workgroup (or a wide row's wave) at it.
+constexpr int kEmbedRows = 32;
 template <typename G, typename O>
 __global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
   __shared__ int start[kEmbedRows + 1];
   const int64_t v0 = (int64_t)blockIdx.x * kEmbedRows;
-  if (threadIdx.x <= kEmbedRows) {       // first sorted position with an id ≥ v0 + thread
+  const int wave = threadIdx.x >> 6;
+  if (wave < 2) {
+    const int at = wave_lower_bound(a.keys, a.tokens, wave ? v0 + kEmbedRows : v0);
+    if ((threadIdx.x & 63) == 0) start[wave ? kEmbedRows : 0] = at;
+  }
+  __syncthreads();
+  if (threadIdx.x > 0 && threadIdx.x < kEmbedRows) {
     const int64_t want = v0 + threadIdx.x;
-    int lo = 0, hi = a.tokens;
+    int lo = start[0], hi = start[kEmbedRows];
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if ((int64_t)a.keys[mid] < want) lo = mid + 1; else hi = mid;
@@ -829,14 +1008,14 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
     start[threadIdx.x] = lo;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int r = wave; r < kEmbedRows; r += kThreads / 64) {
+  const int per = kThreads / a.tpr;                  // rows at a time
+  for (int r = threadIdx.x / a.tpr; r < kEmbedRows; r += per) {
     const int64_t v = v0 + r;
     if (v >= a.rows) return;
     const int s = start[r], e = v == a.padding ? s : start[r + 1];
     if (s == e && a.accumulate) continue;
     gptr<O> out = glob((O*)a.out) + v * a.width;
-    for (int c = lane * 8; c < a.width; c += 512) {
+    for (int c = (threadIdx.x & (a.tpr - 1)) * 8; c < a.width; c += a.tpr * 8) {
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (s != e) {
         add_range<G>(a, s, e, c, x);
@@ -954,10 +1133,9 @@ static unsigned stride_grid(int64_t items) {
   return (unsigned)(wg < 1 ? 1 : (wg < 16384 ? wg : 16384));
 }
 
-// Dynamic LDS limit of the contraction kernels, raised once per device (first
-// calls may come from several threads).
-static int ensure_lds() {
-  static std::atomic<uint64_t> ready{0};
+// Dynamic LDS limit of a kernel, raised once per device (first calls may come from
+// several threads); `ready` holds one bit per device.
+static int raise_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
   static std::mutex mu;
   int dev = 0;
   int e = (int)hipGetDevice(&dev);
@@ -965,13 +1143,9 @@ static int ensure_lds() {
   const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
   if (bit && (ready.load(std::memory_order_acquire) & bit)) return 0;
   std::lock_guard<std::mutex> lk(mu);
-  if (bit && (ready.load(std::memory_order_relaxed) & bit)) return 0;
-  const void* ks[] = {(const void*)k_ce_logits<false, false>, (const void*)k_ce_logits<true, false>,
-                      (const void*)k_ce_logits<true, true>, (const void*)k_product<false>, (const void*)k_product<true>};
-  for (const void* k : ks)
-    if ((e = (int)hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kGemmLds))) return e;
-  if (bit) ready.fetch_or(bit, std::memory_order_release);
-  return 0;
+  e = (int)hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == 0 && bit) ready.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 #define DMUON_LAUNCH(phase, stream, kernel, grid, block, lds, args)                            \
@@ -990,7 +1164,11 @@ int launch_ce_scan(const CeScanArgs& a, void* stream) {
   DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan, 1, kScanThreads, 0, a);
 }
 int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream) {
-  const int e = ensure_lds();
+  static std::atomic<uint64_t> ready[3];
+  const int v = backward ? (f32 ? 2 : 1) : 0;
+  const void* const kernels[3] = {(const void*)k_ce_logits<false, false>, (const void*)k_ce_logits<true, false>,
+                                  (const void*)k_ce_logits<true, true>};
+  const int e = raise_lds(kernels[v], kGemmLds, ready[v]);
   if (e) return e;
   const unsigned grid = (unsigned)(a.tiles_t * a.tiles_v);
   if (!backward) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<false, false>), grid, kGemmThreads, kGemmLds, a);
@@ -1001,7 +1179,9 @@ int launch_ce_rows(const CeRowsArgs& a, void* stream) {
   DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
 }
 int launch_product(const ProductArgs& a, int phase, void* stream) {
-  const int e = ensure_lds();
+  static std::atomic<uint64_t> ready[2];
+  const void* const kernels[2] = {(const void*)k_product<true>, (const void*)k_product<false>};
+  const int e = raise_lds(kernels[a.b_rows ? 1 : 0], kGemmLds, ready[a.b_rows ? 1 : 0]);
   if (e) return e;
   const unsigned grid = (unsigned)(a.tiles_r * a.tiles_c * a.groups * a.splits);
   if (a.b_rows) DMUON_LAUNCH(phase, stream, k_product<false>, grid, kGemmThreads, kGemmLds, a);
@@ -1015,6 +1195,21 @@ int launch_embed(const EmbedArgs& a, void* stream) {
   if (a.f32) DMUON_LAUNCH(PH_EMBED, stream, k_embed<float>, grid, kThreads, 0, a);
   DMUON_LAUNCH(PH_EMBED, stream, k_embed<uint16_t>, grid, kThreads, 0, a);
 }
+template <int ITEMS>
+static int sort_block(const SortArgs& a, void* stream) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr int lds = kScanThreads * ITEMS * 4;
+  int e = 0;
+  if (lds > 64 * 1024 && (e = raise_lds((const void*)k_sort_block<ITEMS>, lds, ready))) return e;
+  DMUON_LAUNCH(PH_EMBED_GRAD, stream, k_sort_block<ITEMS>, 1, kScanThreads, lds, a);
+}
+int launch_sort_block(const SortArgs& a, void* stream) {
+  if (a.tokens <= kScanThreads) return sort_block<1>(a, stream);
+  if (a.tokens <= 4 * kScanThreads) return sort_block<4>(a, stream);
+  if (a.tokens <= 8 * kScanThreads) return sort_block<8>(a, stream);
+  if (a.tokens <= 16 * kScanThreads) return sort_block<16>(a, stream);
+  return sort_block<32>(a, stream);
+}
 int launch_sort_pass(const SortArgs& a, void* stream) {
   timing_before(PH_EMBED_GRAD, stream);
   hipLaunchKernelGGL(k_sort_count, dim3(a.blocks), dim3(kThreads), 0, (hipStream_t)stream, a);
@@ -1025,14 +1220,10 @@ int launch_sort_pass(const SortArgs& a, void* stream) {
   return e;
 }
 int launch_embed_run(const EmbedGradArgs& a, int level, void* stream) {
-  const int span = level == 0 ? kRun : (level == 1 ? kRun * kRun : kRun * kRun * kRun);
-  const unsigned grid = (unsigned)(a.tokens / span);
-  if (level == 0) {
-    if (a.grad_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 0>), grid, kThreads, 0, a);
-    DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<uint16_t, 0>), grid, kThreads, 0, a);
-  }
+  const dim3 grid((unsigned)(a.tokens / (level == 0 ? kRun : kRun * kRun)), (unsigned)cdiv(a.width, 512));
   if (level == 1) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 1>), grid, kThreads, 0, a);
-  DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 2>), grid, kThreads, 0, a);
+  if (a.grad_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<float, 0>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<uint16_t, 0>), grid, kThreads, 0, a);
 }
 int launch_embed_grad(const EmbedGradArgs& a, void* stream) {
   const unsigned grid = (unsigned)cdiv(a.rows, kEmbedRows);

@@ -56,7 +56,7 @@ struct CeScanArgs {
   int32_t* pos;                // compact row of token t, or −1
   int32_t* tgt;                // target of compact row i (−1: outside the vocabulary)
   float* clse;                 // backward: lse of compact row i
-  float* cg;                   // backward: gradient weight of compact row i ÷ gmax
+  float* cg;                   // backward: gradient weight of compact row i
   int32_t* count;              // number of compact rows
   float* gmax;                 // backward: largest |weight|
 };
@@ -83,6 +83,7 @@ struct CeLogitsArgs {
   // backward
   const float* clse;
   const float* cg;
+  const float* gmax;
   uint16_t* dz;                // [plane][tokens][ldz]
   int64_t dz_plane;
   int32_t ldz;
@@ -160,6 +161,7 @@ struct SortArgs {
   uint32_t* idx_out;
   uint32_t* hist;              // [256][blocks]
   int32_t blocks, shift;
+  int32_t key_bits, index_bits;  // one-workgroup sort: bits of a key and of a token index
 };
 
 struct EmbedGradArgs {
@@ -173,7 +175,8 @@ struct EmbedGradArgs {
   int32_t vec_in, vec_out;
   float scale;
   void* out;
-  float* part[3];              // sums of whole aligned runs of 32, 1024, 32768 equal keys
+  int32_t tpr;                 // threads per row (a power of two)
+  float* part[2];              // sums of whole aligned runs of 32 and 1024 equal keys
 };
 
 // ---- 8-bit checkpoints -----------------------------------------------------------
@@ -191,7 +194,8 @@ struct CodecArgs {
 };
 
 constexpr int kSortItems = 4096;         // per workgroup of a sort pass
-constexpr int kRun = 32;                 // sorted tokens per first-level sum
+constexpr int kRun = 32;                 // sorted tokens per first-level sum, and those per second-level one
+constexpr int kSortBlockMax = 32768;     // tokens of the one-workgroup sort
 
 int launch_pack(const PackArgs& a, int phase, void* stream);
 int launch_ce_scan(const CeScanArgs& a, void* stream);
@@ -200,6 +204,7 @@ int launch_ce_rows(const CeRowsArgs& a, void* stream);
 int launch_product(const ProductArgs& a, int phase, void* stream);
 int launch_join(const JoinArgs& a, int phase, void* stream);
 int launch_embed(const EmbedArgs& a, void* stream);
+int launch_sort_block(const SortArgs& a, void* stream);
 int launch_sort_pass(const SortArgs& a, void* stream);
 int launch_embed_run(const EmbedGradArgs& a, int level, void* stream);
 int launch_embed_grad(const EmbedGradArgs& a, void* stream);

@@ -14,7 +14,6 @@ graph: a caller wires them into its backward pass.  Gradients come in the layout
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -80,31 +79,68 @@ def _dense(t, what, dtype=None, shape=None):
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
-    """The stream a call runs on, current inside (so that what is allocated there
-    belongs to it).  The tensors must lie on its device; those the caller used on
-    another stream are recorded, so that their blocks outlive the queued work."""
-    import torch
-    st = _b.resolve_stream(stream)
-    for t in tensors:
-        if t is not None and t.device != st.device:
-            raise ValueError(f"a tensor is on {t.device}, the stream on {st.device}")
-    if st != torch.cuda.current_stream(st.device):
+class _Here:
+    """The current stream of the current device (``stream`` None)."""
+
+    def __init__(self, index):
+        import torch
+        self.handle = ctypes.c_void_p(torch.cuda.current_stream(index).cuda_stream)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+    def workspace(self, ws, need, device):
+        import torch
+        if ws is None:
+            return torch.empty(need or 1, dtype=torch.uint8, device=device)
+        _check_workspace(ws, device)
+        _b.keep_until_done(ws, [torch.cuda.current_stream(device)])
+        return ws
+
+
+class _On(_Here):
+    """Another stream, current inside, so that what is allocated there belongs to
+    it.  Tensors that were used on the caller's stream are recorded to it: their
+    blocks outlive the queued work."""
+
+    def __init__(self, st, tensors):
+        import torch
+        self.st = st
+        self.handle = ctypes.c_void_p(st.cuda_stream)
         for t in tensors:
             _b.keep_until_done(t, [st])
-    with torch.cuda.stream(st):
-        yield st
+        self.scope = torch.cuda.stream(st)
+
+    def __enter__(self):
+        self.scope.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self.scope.__exit__(*exc)
+
+    def workspace(self, ws, need, device):
+        ws = super().workspace(ws, need, device)
+        _b.keep_until_done(ws, [self.st])
+        return ws
 
 
-def _workspace(workspace, need, st):
-    if workspace is None:
-        return _b.alloc_workspace(need, st.device, st)
-    _b._check_dev(workspace, "workspace")
-    if workspace.device != st.device:
-        raise ValueError(f"workspace is on {workspace.device}, the stream on {st.device}")
-    _b.keep_until_done(workspace, [st])
-    return workspace
+def _check_workspace(ws, device):
+    _b._check_dev(ws, "workspace")
+    if ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, the call on {device}")
+
+
+def _on(stream, *tensors):
+    """The scope a call allocates and enqueues in; its tensors must lie on the stream's device."""
+    import torch
+    index = torch.cuda.current_device() if stream is None else stream.device.index
+    for t in tensors:
+        if t is not None and t.device.index != index:
+            raise ValueError(f"a tensor is on {t.device}, the stream on cuda:{index}")
+    return _Here(index) if stream is None else _On(stream, tensors)
 
 
 def _ws_args(ws):
@@ -126,10 +162,10 @@ def _ce_problem(h, w, targets, ignore_index):
                         h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), int(ignore_index))
 
 
-def _ce_workspace(prob, backward, workspace, st):
+def _ce_workspace(prob, backward, workspace, on, device):
     need = ctypes.c_size_t(0)
     _b.check(_b.lib().dmuon_linear_ce_workspace_size(ctypes.byref(prob), backward, ctypes.byref(need)))
-    return _workspace(workspace, need.value, st)
+    return on.workspace(workspace, need.value, device)
 
 
 def linear_cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, stream=None):
@@ -144,12 +180,12 @@ def linear_cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, st
     """
     import torch
     prob = _ce_problem(h, w, targets, ignore_index)
-    with _on(stream, h, w, targets) as st:
+    with _on(stream, h, w, targets) as on:
         losses = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
         lse = torch.empty_like(losses)
-        ws = _ce_workspace(prob, 0, workspace, st)
+        ws = _ce_workspace(prob, 0, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_ce(ctypes.byref(prob), _ptr(losses), _ptr(lse), *_ws_args(ws),
-                                          ctypes.c_void_p(st.cuda_stream)))
+                                          on.handle))
     return losses, lse
 
 
@@ -173,14 +209,14 @@ def linear_cross_entropy_backward(h, w, targets, lse, grad_losses, *, ignore_ind
             raise ValueError(f"{what} is given but not needed")
         if t is not None:
             _dense(t, what, like.dtype, like.shape)
-    with _on(stream, h, w, targets, lse, grad_losses, grad_h, grad_w) as st:
+    with _on(stream, h, w, targets, lse, grad_losses, grad_h, grad_w) as on:
         if need_h and grad_h is None:
             grad_h = torch.empty(h.shape, dtype=h.dtype, device=h.device)
         if need_w and grad_w is None:
             grad_w = torch.empty(w.shape, dtype=w.dtype, device=w.device)
-        ws = _ce_workspace(prob, 1, workspace, st)
+        ws = _ce_workspace(prob, 1, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_ce_backward(ctypes.byref(prob), _ptr(lse), _ptr(grad_losses), _ptr(grad_h),
-                                                   _ptr(grad_w), *_ws_args(ws), ctypes.c_void_p(st.cuda_stream)))
+                                                   _ptr(grad_w), *_ws_args(ws), on.handle))
     return grad_h, grad_w
 
 
@@ -197,11 +233,11 @@ def embedding(ids, table, *, scale=1.0, out=None, stream=None):
     code, icode = _float_code(table.dtype, "table"), _index_code(ids, "ids")
     if out is not None:
         _dense(out, "out", table.dtype, (*ids.shape, width))
-    with _on(stream, ids, table, out) as st:
+    with _on(stream, ids, table, out) as on:
         if out is None:
             out = torch.empty((*ids.shape, width), dtype=table.dtype, device=table.device)
         _b.check(_b.lib().dmuon_embedding(_ptr(ids), icode, ids.numel(), _ptr(table), ldt, rows, width, code,
-                                          float(scale), _ptr(out), ctypes.c_void_p(st.cuda_stream)))
+                                          float(scale), _ptr(out), on.handle))
     return out
 
 
@@ -237,14 +273,14 @@ def embedding_backward(ids, grad_out, rows, *, scale=1.0, padding_id=None, out_d
     ocode = _float_code(out_dtype, "out_dtype")
     need = ctypes.c_size_t(0)
     _b.check(_b.lib().dmuon_embedding_backward_workspace_size(tokens, rows, width, ctypes.byref(need)))
-    with _on(stream, ids, grad_out, out) as st:
+    with _on(stream, ids, grad_out, out) as on:
         if out is None:
             out = torch.empty((rows, width), dtype=out_dtype, device=grad_out.device)
-        ws = _workspace(workspace, need.value, st)
+        ws = on.workspace(workspace, need.value, grad_out.device)
         _b.check(_b.lib().dmuon_embedding_backward(
             _ptr(ids), icode, tokens, _ptr(grad_out), ldg, gcode, rows, width, float(scale),
             -1 if padding_id is None else int(padding_id), _ptr(out), ocode, 1 if accumulate else 0, *_ws_args(ws),
-            ctypes.c_void_p(st.cuda_stream)))
+            on.handle))
     return out
 
 
@@ -264,12 +300,12 @@ def checkpoint_quantize(x, *, out=None, stream=None):
         q, exps = out
         _dense(q, "q", torch.int8, x.shape)
         _dense(exps, "exps", torch.uint8, eshape)
-    with _on(stream, x, *(out or ())) as st:
+    with _on(stream, x, *(out or ())) as on:
         if out is None:
             q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
             exps = torch.empty(eshape, dtype=torch.uint8, device=x.device)
         _b.check(_b.lib().dmuon_ckpt8_quantize(_ptr(x), code, rows, cols, ldx, _ptr(q), _ptr(exps),
-                                               ctypes.c_void_p(st.cuda_stream)))
+                                               on.handle))
     return q, exps
 
 
@@ -290,11 +326,11 @@ def checkpoint_dequantize(q, exps, *, dtype=None, out=None, stream=None):
         dtype = out.dtype
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _float_code(dtype, "dtype")
-    with _on(stream, q, exps, out) as st:
+    with _on(stream, q, exps, out) as on:
         if out is None:
             out = torch.empty(q.shape, dtype=dtype, device=q.device)
         _b.check(_b.lib().dmuon_ckpt8_dequantize(_ptr(q), _ptr(exps), math.prod(q.shape[:-1]), q.shape[-1], _ptr(out),
-                                                 code, ctypes.c_void_p(st.cuda_stream)))
+                                                 code, on.handle))
     return out
 
 
@@ -327,7 +363,7 @@ def checkpoint_wgrad(grad_out, q, exps, *, offsets=None, out_dtype=None, out=Non
         out_dtype = out.dtype
     out_dtype = grad_out.dtype if out_dtype is None else out_dtype
     ocode = _float_code(out_dtype, "out_dtype")
-    with _on(stream, grad_out, q, exps, offsets, out) as st:
+    with _on(stream, grad_out, q, exps, offsets, out) as on:
         if out is None:
             out = torch.empty(shape, dtype=out_dtype, device=q.device)
         prob = _b.Ckpt8WgradProblem(tokens, n, k, gcode, ocode, grad_out.data_ptr(), ldg, q.data_ptr(),
@@ -335,6 +371,6 @@ def checkpoint_wgrad(grad_out, q, exps, *, offsets=None, out_dtype=None, out=Non
                                     out.data_ptr())
         need = ctypes.c_size_t(0)
         _b.check(_b.lib().dmuon_ckpt8_wgrad_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
-        ws = _workspace(workspace, need.value, st)
-        _b.check(_b.lib().dmuon_ckpt8_wgrad(ctypes.byref(prob), *_ws_args(ws), ctypes.c_void_p(st.cuda_stream)))
+        ws = on.workspace(workspace, need.value, q.device)
+        _b.check(_b.lib().dmuon_ckpt8_wgrad(ctypes.byref(prob), *_ws_args(ws), on.handle))
     return out
