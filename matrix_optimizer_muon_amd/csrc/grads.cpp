@@ -320,10 +320,10 @@ int check_wgrad(const dmuon_ckpt8_wgrad_problem* p, std::vector<Range>* rs) {
 
 // ---- embedding ------------------------------------------------------------------
 struct EmbedPlan {
-  uint32_t *keys[2], *idx[2], *hist;
+  uint32_t *keys[2], *idx[2], *hist, *words;
   float* part[2];
-  int blocks, passes, key_bits, index_bits;
-  bool one;                              // the one-workgroup sort
+  int blocks, passes, key_bits;
+  bool runs;                             // the sort by runs
   size_t bytes;
 };
 
@@ -331,15 +331,15 @@ EmbedPlan embed_plan(int64_t tokens, int64_t rows, int64_t width, char* base) {
   EmbedPlan pl{};
   pl.blocks = (int)cdiv(tokens, kSortItems);
   while (rows >> pl.key_bits) ++pl.key_bits;           // keys are 0 … rows
-  while ((tokens - 1) >> pl.index_bits) ++pl.index_bits;
-  pl.one = tokens <= kSortBlockMax && pl.key_bits + pl.index_bits <= 32;
+  pl.runs = tokens <= kSortRunsMax && rows + 1 < (int64_t)1 << (32 - kSortRunBits);   // id + 1 fits beside an index
   pl.passes = (int)cdiv(pl.key_bits, 8);
   Carver c{base};
-  for (int i = 0; i < (pl.one ? 1 : 2); ++i) {
+  for (int i = 0; i < (pl.runs ? 1 : 2); ++i) {
     pl.keys[i] = c.take<uint32_t>(tokens);
     pl.idx[i] = c.take<uint32_t>(tokens);
   }
-  if (!pl.one) pl.hist = c.take<uint32_t>((int64_t)256 * pl.blocks);
+  if (!pl.runs) pl.hist = c.take<uint32_t>((int64_t)256 * pl.blocks);
+  else if (tokens > kSortRun) pl.words = c.take<uint32_t>(tokens);
   const int64_t ld = round_up(width, 8);
   int64_t span = kRun;
   for (int l = 0; l < 2; ++l, span *= kRun) pl.part[l] = c.take<float>(tokens / span * ld);
@@ -351,6 +351,8 @@ int check_embed_sizes(int64_t tokens, int64_t rows, int64_t width) {
   if (tokens < 0 || tokens > kMaxIds) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^30]");
   if (rows < 0 || rows > kMaxRows) return fail(DMUON_E_SHAPE, "rows must be in [0, 2^30]");
   if (width < 1 || width > kMaxWidth) return fail(DMUON_E_SHAPE, "width must be in [1, 65536]");
+  if (cdiv(tokens, kEmbedHeads * (kThreads / 64)) * cdiv(width, 512) + cdiv(rows, kEmbedRows) > INT32_MAX)
+    return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
   return DMUON_OK;
 }
 
@@ -622,12 +624,12 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     s.hist = pl.hist;
     s.blocks = pl.blocks;
     EmbedGradArgs a{};
-    if (pl.one) {
+    if (pl.runs) {
       s.key_bits = pl.key_bits;
-      s.index_bits = pl.index_bits;
+      s.words = pl.words;
       a.keys = s.keys_out = pl.keys[0];
       a.idx = s.idx_out = pl.idx[0];
-      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_block(s, stream); }))) return e;
+      if ((e = go(env, PH_EMBED_GRAD, stream, [&] { return launch_sort_runs(s, stream); }))) return e;
     } else {
       for (int k = 0; k < pl.passes; ++k) {
         s.keys_in = k ? pl.keys[(k + 1) & 1] : nullptr;
@@ -651,8 +653,8 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     a.vec_out = rows16(grad_table, width, width, type_bytes(out_dtype));
     a.scale = scale;
     a.out = grad_table;
-    a.tpr = 1;
-    while (a.tpr < kThreads && a.tpr * 8 < width) a.tpr *= 2;
+    a.slabs = (int32_t)cdiv(width, 512);
+    a.seg_wg = cdiv(tokens, kEmbedHeads * (kThreads / 64)) * a.slabs;
     for (int l = 0; l < 2; ++l) a.part[l] = pl.part[l];
     int64_t span = kRun;
     for (int l = 0; l < 2 && span <= tokens; ++l, span *= kRun)

@@ -72,8 +72,12 @@ __device__ __forceinline__ void store8(gptr<float> p, bool vec, int left, const 
   }
 }
 
+// An int32 or int64 index, as its dwords and without a branch, so that several
+// loads of a thread are in flight together.
 __device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t i) {
-  return idx64 ? glob((const int64_t*)p)[i] : (int64_t)glob((const int32_t*)p)[i];
+  const gptr<const int32_t> q = glob((const int32_t*)p) + (i << idx64);
+  const int32_t lo = q[0], hi = q[idx64];
+  return (int64_t)(((uint64_t)(uint32_t)(idx64 ? hi : lo >> 31) << 32) | (uint32_t)lo);
 }
 
 // x = hi + mid + lo, each a bf16 value: hi is x rounded to bf16 (cut off where
@@ -152,15 +156,14 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
 #pragma unroll
     for (int k = 0; k < kScanRows; ++k) {
       const int64_t t = t0 + k * kScanThreads + tid;
-      y[k] = a.ignore;
+      const int64_t u = t < a.tokens ? t : a.tokens - 1;
+      y[k] = load_index(a.targets, a.idx64, u);
       g[k] = l[k] = 0.f;
-      if (t < a.tokens) {
-        y[k] = load_index(a.targets, a.idx64, t);
-        if (a.backward) {
-          g[k] = a.grad_losses[t];
-          l[k] = a.lse_in[t];
-        }
+      if (a.backward) {
+        g[k] = glob(a.grad_losses)[u];
+        l[k] = glob(a.lse_in)[u];
       }
+      if (t >= a.tokens) y[k] = a.ignore;
     }
     uint64_t in[kScanRows];
 #pragma unroll
@@ -641,50 +644,56 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a) {
 // stable radix sort of (id, token) pairs, 8 bits of the id per pass.  Ids outside
 // the table get the key `rows` and sort last.
 //
-// Up to 32768 tokens whose id and index fit 32 bits together are sorted by one
-// workgroup in one launch (k_sort_block): the words stay in registers, a pass
-// ranks 64 of them at a time among equal digits by ballots, exchanges them through
-// LDS and reads them back.  Every wave owns a contiguous part, so equal ids keep
-// the order of their tokens whatever the timing.  Measured with the gradient of
-// 8192 tokens (2 passes): one launch instead of six.
+// Up to 65536 tokens (and ids below 2^19) take two launches: k_sort_block sorts runs
+// of 8192 tokens, one workgroup each, and k_sort_merge places every pair by its rank
+// in the other runs (one launch when one run is all).  In a run the words (id, index
+// in the run) stay in registers; a pass ranks 64 of them at a time among equal
+// digits by ballots, exchanges them through LDS and reads them back.  Every wave owns
+// a contiguous part, so equal ids keep the order of their tokens whatever the timing.
+// More tokens take three launches per pass.  Measured: 8192 tokens 14 µs (six
+// launches of the general path: 40 and their gaps).
 // ---------------------------------------------------------------------------
 constexpr int kSortWaves = kThreads / 64;
 constexpr int kSortRounds = kSortItems / kThreads;
 constexpr int kBlockWaves = kScanThreads / 64;
 
-// Lanes whose digit equals this lane's, among those `on`; ballots over `bits` bits
-__device__ __forceinline__ uint64_t match_digit(uint32_t d, int bits, uint64_t on) {
-  uint64_t same = on;
-  for (int b = 0; b < bits; ++b) {
+// Lanes whose 8-bit digit equals this lane's, among those `on`.  Per bit: the lanes
+// that have it (a ballot), complemented where this lane has not.
+__device__ __forceinline__ uint64_t match_digit(uint32_t d, uint64_t on) {
+  uint32_t lo = (uint32_t)on, hi = (uint32_t)(on >> 32);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
     const uint64_t m = __ballot((d >> b) & 1);
-    same &= (d >> b) & 1 ? m : ~m;
+    const uint32_t mine = (uint32_t)((int32_t)(d << (31 - b)) >> 31);     // all ones where this lane has the bit
+    lo &= ~((uint32_t)m ^ mine);
+    hi &= ~((uint32_t)(m >> 32) ^ mine);
   }
-  return same;
+  return ((uint64_t)hi << 32) | lo;
 }
 // LDS reads and writes of one wave stay in order, and are not moved across this
 __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_sched_barrier(0);     // nor is the ballots' arithmetic, which would hold registers for every round
 }
 
 template <int ITEMS>
 __global__ __launch_bounds__(kScanThreads) void k_sort_block(SortArgs a) {
-  extern __shared__ __align__(16) uint32_t words[];        // kScanThreads·ITEMS
+  __shared__ uint32_t words[kScanThreads * ITEMS];
   __shared__ uint32_t cnt[kBlockWaves][256];
   __shared__ uint32_t wave_sum[kBlockWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int first = wave * 64 * ITEMS + lane;              // item r of this lane: first + 64 r
+  const int64_t run0 = (int64_t)blockIdx.x * kSortRun;
+  const int n = (int)(a.tokens - run0 < kSortRun ? a.tokens - run0 : kSortRun);
   uint32_t w[ITEMS];
-  uint32_t at[ITEMS];
+  uint32_t at[ITEMS];                                      // rank in the wave's part
 #pragma unroll
   for (int r = 0; r < ITEMS; ++r) {
     const int i = first + 64 * r;
-    w[r] = 0xffffffffu;                                    // past the end: last, and stays last
-    if (i < a.tokens) {
-      const int64_t id = load_index(a.ids, a.idx64, i);
-      const uint32_t key = id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
-      w[r] = (key << a.index_bits) | (uint32_t)i;
-    }
+    const int64_t id = load_index(a.ids, a.idx64, run0 + (i < n ? i : n - 1));
+    const uint32_t key = id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
+    w[r] = i < n ? (key << kSortRunBits) | (uint32_t)i : 0xffffffffu;     // past the end: last, and stays last
   }
   for (int shift = 0; shift < a.key_bits; shift += 8) {
     const int bits = a.key_bits - shift < 8 ? a.key_bits - shift : 8;
@@ -694,8 +703,8 @@ __global__ __launch_bounds__(kScanThreads) void k_sort_block(SortArgs a) {
     wave_order();
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r) {
-      const uint32_t d = (w[r] >> (a.index_bits + shift)) & mask;
-      const uint64_t same = match_digit(d, bits, ~0ull);
+      const uint32_t d = (w[r] >> (kSortRunBits + shift)) & mask;
+      const uint64_t same = match_digit(d, ~0ull);
       const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
       const uint32_t before = cnt[wave][d];
       at[r] = before + rank;
@@ -729,19 +738,58 @@ __global__ __launch_bounds__(kScanThreads) void k_sort_block(SortArgs a) {
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < ITEMS; ++r) words[cnt[wave][(w[r] >> (a.index_bits + shift)) & mask] + at[r]] = w[r];
+    for (int r = 0; r < ITEMS; ++r) words[cnt[wave][(w[r] >> (kSortRunBits + shift)) & mask] + at[r]] = w[r];
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r) w[r] = words[first + 64 * r];
   }
+  const bool all = a.tokens <= kSortRun;                   // the run is everything: write pairs, else words
 #pragma unroll
   for (int r = 0; r < ITEMS; ++r) {
     const int i = first + 64 * r;
-    if (i < a.tokens) {
-      a.keys_out[i] = w[r] >> a.index_bits;
-      a.idx_out[i] = w[r] & ((1u << a.index_bits) - 1);
+    if (i >= n) continue;
+    if (all) {
+      a.keys_out[i] = w[r] >> kSortRunBits;
+      a.idx_out[i] = w[r] & (kSortRun - 1);
+    } else {
+      a.words[run0 + i] = w[r];
     }
   }
+}
+
+// Rank of every word among all runs: its place in its own, plus the words of the
+// earlier runs with an id not above its own and of the later ones with an id below
+// it.  The searches of a thread advance together, one probe of every run per step.
+__global__ __launch_bounds__(kThreads) void k_sort_merge(SortArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= a.tokens) return;
+  const int run = (int)(i / kSortRun), runs = (a.tokens + kSortRun - 1) / kSortRun;
+  const uint32_t w = a.words[i], key = w >> kSortRunBits;
+  constexpr int kMaxRuns = kSortRunsMax / kSortRun;
+  int lo[kMaxRuns], hi[kMaxRuns];
+#pragma unroll
+  for (int q = 0; q < kMaxRuns; ++q) {
+    lo[q] = 0;
+    hi[q] = 0;
+    if (q < runs && q != run) hi[q] = a.tokens - q * kSortRun < kSortRun ? a.tokens - q * kSortRun : kSortRun;
+  }
+  // first word of run q at or above `bound`: the id itself, or the next one for an
+  // earlier run (the planner keeps rows + 1 below 2^19, so the bound fits)
+  for (int step = 0; step <= kSortRunBits; ++step) {
+#pragma unroll
+    for (int q = 0; q < kMaxRuns; ++q) {
+      if (lo[q] >= hi[q]) continue;
+      const int mid = (lo[q] + hi[q]) >> 1;
+      const uint32_t bound = (key + (q < run ? 1u : 0u)) << kSortRunBits;
+      if (glob(a.words)[(int64_t)q * kSortRun + mid] < bound) lo[q] = mid + 1;
+      else hi[q] = mid;
+    }
+  }
+  int at = (int)(i - (int64_t)run * kSortRun);
+#pragma unroll
+  for (int q = 0; q < kMaxRuns; ++q) at += lo[q];
+  a.keys_out[at] = key;
+  a.idx_out[at] = (uint32_t)(run * kSortRun) + (w & (kSortRun - 1));
 }
 
 // The same for any number of tokens: per pass the digit counts of every workgroup,
@@ -831,7 +879,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(SortArgs a) {
     const int64_t i = base + r * 64 + lane;
     const bool on = i < a.tokens;
     const uint32_t d = (key[r] >> a.shift) & 255;
-    const uint64_t same = match_digit(d, 8, __ballot(on));
+    const uint64_t same = match_digit(d, __ballot(on));
     const int rank = __popcll(same & ((1ull << lane) - 1));
     uint32_t slot = 0;
     if (on) slot = at[wave][d];
@@ -884,24 +932,19 @@ template <> struct Raw8<float> {
 template <typename G, typename R>
 __device__ __forceinline__ void add_rows(int s, int e, bool vec, int left, float (&v)[8], R row) {
   constexpr int kAhead = 8;
-  int i = s;
   if (vec) {
-    for (; i + kAhead <= e; i += kAhead) {
+    for (int i = s; i < e; i += kAhead) {
       Raw8<G> x[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) x[u].load(row(i + u));
+      for (int u = 0; u < kAhead; ++u)
+        if (i + u < e) x[u].load(row(i + u));
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) x[u].add(v);
-    }
-#pragma unroll 1
-    for (; i < e; ++i) {
-      Raw8<G> x;
-      x.load(row(i));
-      x.add(v);
+      for (int u = 0; u < kAhead; ++u)
+        if (i + u < e) x[u].add(v);
     }
   } else {
 #pragma unroll 1
-    for (; i < e; ++i) {
+    for (int i = s; i < e; ++i) {
       float x[8];
       load8(row(i), false, left, x);
 #pragma unroll
@@ -985,52 +1028,144 @@ __device__ __forceinline__ int wave_lower_bound(const uint32_t* keys, int n, int
   return lo;
 }
 
-// 32 table rows per workgroup; `tpr` threads share a row, 8 columns each, so that
-// a row with many tokens has the whole workgroup (or a wide row's wave) at it.
-constexpr int kEmbedRows = 32;
+// One launch, two kinds of workgroups, interleaved so that both run all the time
+// (the sums wait on latency, the zeros on bandwidth):
+//   sums:  one wave per 8 sorted positions and 512 columns.  It owns the ranges that
+//          begin there: the rows of their tokens among the 8 are loaded at once, added
+//          in order, and a range that ends is written (or added) to its row.  A range
+//          that goes on past the 8 is finished (32 tokens and more: summed) by
+//          add_range.
+//   zeros: 32 table rows per workgroup; rows without tokens are cleared (none of
+//          them when accumulating).
 template <typename G, typename O>
-__global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
-  __shared__ int start[kEmbedRows + 1];
-  const int64_t v0 = (int64_t)blockIdx.x * kEmbedRows;
+__device__ __forceinline__ void embed_sums(const EmbedGradArgs& a, int64_t wg) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slab = (int)(wg % a.slabs);
+  const int64_t at = (wg / a.slabs * (kThreads / 64) + wave) * kEmbedHeads;
+  if (at >= a.tokens) return;
+  const int s0 = (int)at, p = s0 + lane;
+  // 64 keys and token indices from s0; a head is a key that differs from the one before
+  const bool in = p < a.tokens;
+  const int pc = in ? p : a.tokens - 1;
+  const uint32_t key = a.keys[pc], idx = a.idx[pc], prev = a.keys[pc > 0 ? pc - 1 : 0];
+  const uint64_t heads = __ballot(p == 0 || !in || key != prev);       // a position past the end ends a range
+  const int c = slab * 512 + lane * 8;
+  const bool mine = c < a.width;
+  const int have = a.tokens - s0 < kEmbedHeads ? a.tokens - s0 : kEmbedHeads;
+  const uint32_t h8 = (uint32_t)heads & ((1u << have) - 1);
+  if (!h8) return;
+  const int first = __ffs(h8) - 1, last = 31 - __clz(h8);
+  // the last range's end: among the 64 keys, else by search
+  const uint64_t after = heads & ~((2ull << last) - 1);
+  const int e = after ? s0 + __ffsll((unsigned long long)after) - 1
+                      : s0 + 64 + wave_lower_bound(a.keys + s0 + 64, a.tokens - s0 - 64, (int64_t)__builtin_amdgcn_readlane((int)key, last) + 1);
+  const bool longer = e - s0 > kEmbedHeads;          // it goes on past the 8
+  const bool summed = longer && (e - (s0 + last) >= kRun || !a.vec_in);
+  const int stop = summed ? last : (longer ? kEmbedHeads : e - s0);    // positions [first, stop) are loaded here
+  Raw8<G> x[kEmbedHeads];
+  const bool direct = mine && a.vec_in;
+#pragma unroll
+  for (int u = 0; u < kEmbedHeads; ++u)
+    if (direct && u >= first && u < stop)
+      x[u].load(glob((const G*)a.grad) + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)idx, u) * a.ldg + c);
+  auto finish = [&](int l, float (&v)[8]) {          // write the row of the range that begins at position l
+    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, l);
+    if (!mine || k >= (uint32_t)a.rows || (int64_t)k == (int64_t)a.padding) return;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] *= a.scale;
+    gptr<O> out = glob((O*)a.out) + (int64_t)k * a.width + c;
+    if (a.accumulate) {
+      float o[8];
+      load8((gptr<const O>)out, a.vec_out, a.width - c, o);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += o[q];
+    }
+    store8(out, a.vec_out, a.width - c, v);
+  };
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  int head = first;
+#pragma unroll
+  for (int u = 0; u < kEmbedHeads; ++u) {
+    if (u < first || u >= stop) continue;
+    if (u > first && ((h8 >> u) & 1)) {
+      finish(head, v);
+      head = u;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = 0.f;
+    }
+    if (a.vec_in) {
+      x[u].add(v);
+    } else if (mine) {
+      float y[8];
+      load8(glob((const G*)a.grad) + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)idx, u) * a.ldg + c, false, a.width - c, y);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += y[q];
+    }
+  }
+  if (summed) {
+    if (stop > first) finish(head, v);
+    head = last;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = 0.f;
+    if (mine) add_range<G>(a, s0 + last, e, c, v);
+  } else if (longer && mine) {
+    add_tokens<G>(a, s0 + kEmbedHeads, e, c, v);
+  }
+  finish(head, v);
+}
+
+template <typename O>
+__device__ __forceinline__ void embed_zeros(const EmbedGradArgs& a, int64_t wg, int* start) {
+  const int64_t v0 = wg * kEmbedRows;
   const int wave = threadIdx.x >> 6;
   if (wave < 2) {
     const int at = wave_lower_bound(a.keys, a.tokens, wave ? v0 + kEmbedRows : v0);
     if ((threadIdx.x & 63) == 0) start[wave ? kEmbedRows : 0] = at;
   }
   __syncthreads();
-  if (threadIdx.x > 0 && threadIdx.x < kEmbedRows) {
-    const int64_t want = v0 + threadIdx.x;
-    int lo = start[0], hi = start[kEmbedRows];
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)a.keys[mid] < want) lo = mid + 1; else hi = mid;
+  const int lo0 = start[0], hi0 = start[kEmbedRows];
+  __syncthreads();
+  // start[r] becomes nonzero where row v0 + r has tokens: by marking the keys of a
+  // short range, by a search per row for a long one
+  if (threadIdx.x < kEmbedRows) {
+    int has = 0;
+    if (hi0 - lo0 > kThreads) {
+      const int64_t want = v0 + threadIdx.x;
+      int lo = lo0, hi = hi0;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)a.keys[mid] < want) lo = mid + 1; else hi = mid;
+      }
+      has = lo < hi0 && (int64_t)a.keys[lo] == want;
     }
-    start[threadIdx.x] = lo;
+    start[threadIdx.x] = has;
   }
   __syncthreads();
-  const int per = kThreads / a.tpr;                  // rows at a time
-  for (int r = threadIdx.x / a.tpr; r < kEmbedRows; r += per) {
+  if (hi0 - lo0 <= kThreads && (int)threadIdx.x < hi0 - lo0) start[(int64_t)a.keys[lo0 + threadIdx.x] - v0] = 1;
+  __syncthreads();
+  constexpr int E = 16 / (int)sizeof(O);             // elements per 16-byte store
+  for (int r = 0; r < kEmbedRows; ++r) {
     const int64_t v = v0 + r;
     if (v >= a.rows) return;
-    const int s = start[r], e = v == a.padding ? s : start[r + 1];
-    if (s == e && a.accumulate) continue;
+    if (start[r] && v != a.padding) continue;
     gptr<O> out = glob((O*)a.out) + v * a.width;
-    for (int c = (threadIdx.x & (a.tpr - 1)) * 8; c < a.width; c += a.tpr * 8) {
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (s != e) {
-        add_range<G>(a, s, e, c, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= a.scale;
-        if (a.accumulate) {
-          float o[8];
-          load8((gptr<const O>)out + c, a.vec_out, a.width - c, o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] += o[k];
-        }
-      }
-      store8(out + c, a.vec_out, a.width - c, x);
+    if (a.vec_out) {
+      for (int c = threadIdx.x * E; c < a.width; c += kThreads * E) *(gptr<u32x4_t>)(out + c) = u32x4_t{0u, 0u, 0u, 0u};
+    } else {
+      for (int c = threadIdx.x; c < a.width; c += kThreads) out[c] = O(0);
     }
   }
+}
+
+template <typename G, typename O>
+__global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
+  __shared__ int start[kEmbedRows + 1];
+  // workgroup b of n: ⌊(b + 1)·s/n⌋ > ⌊b·s/n⌋ picks s of them, evenly spread
+  const int64_t b = blockIdx.x, n = gridDim.x;
+  const int64_t before = b * a.seg_wg / n;
+  if ((b + 1) * a.seg_wg / n > before) embed_sums<G, O>(a, before);
+  else embed_zeros<O>(a, b - before, start);
 }
 
 // ---------------------------------------------------------------------------
@@ -1195,20 +1330,17 @@ int launch_embed(const EmbedArgs& a, void* stream) {
   if (a.f32) DMUON_LAUNCH(PH_EMBED, stream, k_embed<float>, grid, kThreads, 0, a);
   DMUON_LAUNCH(PH_EMBED, stream, k_embed<uint16_t>, grid, kThreads, 0, a);
 }
-template <int ITEMS>
-static int sort_block(const SortArgs& a, void* stream) {
-  static std::atomic<uint64_t> ready{0};
-  constexpr int lds = kScanThreads * ITEMS * 4;
-  int e = 0;
-  if (lds > 64 * 1024 && (e = raise_lds((const void*)k_sort_block<ITEMS>, lds, ready))) return e;
-  DMUON_LAUNCH(PH_EMBED_GRAD, stream, k_sort_block<ITEMS>, 1, kScanThreads, lds, a);
-}
-int launch_sort_block(const SortArgs& a, void* stream) {
-  if (a.tokens <= kScanThreads) return sort_block<1>(a, stream);
-  if (a.tokens <= 4 * kScanThreads) return sort_block<4>(a, stream);
-  if (a.tokens <= 8 * kScanThreads) return sort_block<8>(a, stream);
-  if (a.tokens <= 16 * kScanThreads) return sort_block<16>(a, stream);
-  return sort_block<32>(a, stream);
+int launch_sort_runs(const SortArgs& a, void* stream) {
+  const dim3 grid((unsigned)cdiv(a.tokens, kSortRun)), block(kScanThreads);
+  hipStream_t st = (hipStream_t)stream;
+  timing_before(PH_EMBED_GRAD, stream);
+  if (a.tokens <= kScanThreads) hipLaunchKernelGGL(k_sort_block<1>, grid, block, 0, st, a);
+  else if (a.tokens <= 4 * kScanThreads) hipLaunchKernelGGL(k_sort_block<4>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(k_sort_block<kSortRun / kScanThreads>, grid, block, 0, st, a);
+  if (a.tokens > kSortRun) hipLaunchKernelGGL(k_sort_merge, dim3((unsigned)cdiv(a.tokens, kThreads)), dim3(kThreads), 0, st, a);
+  const int e = (int)hipGetLastError();
+  timing_after(PH_EMBED_GRAD, stream);
+  return e;
 }
 int launch_sort_pass(const SortArgs& a, void* stream) {
   timing_before(PH_EMBED_GRAD, stream);
@@ -1226,7 +1358,7 @@ int launch_embed_run(const EmbedGradArgs& a, int level, void* stream) {
   DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<uint16_t, 0>), grid, kThreads, 0, a);
 }
 int launch_embed_grad(const EmbedGradArgs& a, void* stream) {
-  const unsigned grid = (unsigned)cdiv(a.rows, kEmbedRows);
+  const unsigned grid = (unsigned)(a.seg_wg + (a.accumulate ? 0 : cdiv(a.rows, kEmbedRows)));
   if (a.grad_f32) {
     if (a.out_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, float>), grid, kThreads, 0, a);
     DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, uint16_t>), grid, kThreads, 0, a);

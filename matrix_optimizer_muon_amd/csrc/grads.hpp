@@ -161,7 +161,8 @@ struct SortArgs {
   uint32_t* idx_out;
   uint32_t* hist;              // [256][blocks]
   int32_t blocks, shift;
-  int32_t key_bits, index_bits;  // one-workgroup sort: bits of a key and of a token index
+  int32_t key_bits;            // sort by runs: bits of a key
+  uint32_t* words;             // the sorted runs, where there are several
 };
 
 struct EmbedGradArgs {
@@ -175,7 +176,8 @@ struct EmbedGradArgs {
   int32_t vec_in, vec_out;
   float scale;
   void* out;
-  int32_t tpr;                 // threads per row (a power of two)
+  int32_t slabs;               // ceil(width / 512)
+  int64_t seg_wg;              // workgroups of the sums
   float* part[2];              // sums of whole aligned runs of 32 and 1024 equal keys
 };
 
@@ -195,7 +197,11 @@ struct CodecArgs {
 
 constexpr int kSortItems = 4096;         // per workgroup of a sort pass
 constexpr int kRun = 32;                 // sorted tokens per first-level sum, and those per second-level one
-constexpr int kSortBlockMax = 32768;     // tokens of the one-workgroup sort
+constexpr int kEmbedRows = 32;           // table rows per workgroup that clears rows
+constexpr int kEmbedHeads = 8;           // sorted positions per wave that sums ranges
+constexpr int kSortRunBits = 13;
+constexpr int kSortRun = 1 << kSortRunBits;            // tokens per run of the two-launch sort
+constexpr int kSortRunsMax = 65536;                    // tokens it takes
 
 int launch_pack(const PackArgs& a, int phase, void* stream);
 int launch_ce_scan(const CeScanArgs& a, void* stream);
@@ -204,7 +210,7 @@ int launch_ce_rows(const CeRowsArgs& a, void* stream);
 int launch_product(const ProductArgs& a, int phase, void* stream);
 int launch_join(const JoinArgs& a, int phase, void* stream);
 int launch_embed(const EmbedArgs& a, void* stream);
-int launch_sort_block(const SortArgs& a, void* stream);
+int launch_sort_runs(const SortArgs& a, void* stream);
 int launch_sort_pass(const SortArgs& a, void* stream);
 int launch_embed_run(const EmbedGradArgs& a, int level, void* stream);
 int launch_embed_grad(const EmbedGradArgs& a, void* stream);

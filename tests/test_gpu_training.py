@@ -368,6 +368,20 @@ def test_embedding_gradient_of_one_frequent_id(T):
     within(m.embedding_backward(ids, grad, 5), want, tol, "most")
 
 
+@pytest.mark.parametrize("T,V", [(1024, 9), (1025, 9), (4097, 300), (8192, 1000), (8193, 1000), (16385, 40000), (65536, 2000),
+                                 (65537, 2000), (9000, 524285), (9000, 524286), (9000, 524287), (9000, 600000)])
+def test_embedding_gradient_sorts(T, V):
+    """Token counts and table sizes at the borders of the sorts' variants; ids at both ends of the table and outside."""
+    m = mm()
+    g = gen(T + V)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ids[::5] = torch.randint(V - 2, V + 1, ids[::5].shape, generator=g, device="cuda")
+    ids[1::7] = torch.randint(-1, 2, ids[1::7].shape, generator=g, device="cuda")
+    grad = randn(g, T, 8)
+    want, tol = embed_reference(ids, grad, V, 1.0, None, torch.float32)
+    within(m.embedding_backward(ids, grad, V), want, tol)
+
+
 def test_embedding_gradient_accumulates_and_leaves_other_rows():
     m = mm()
     g = gen(3)
