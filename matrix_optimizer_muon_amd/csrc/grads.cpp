@@ -81,9 +81,14 @@ struct Carver {
 
 // K splits of a product with few tiles, so that all 256 CUs have work: whole
 // stages of 32, at least 8 of them per workgroup
-int pick_splits(int64_t tiles, int64_t k) {
-  const int64_t stages = cdiv(k, 32);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), stages / 8));
+int pick_splits(int64_t tiles, int tile, int64_t k) {
+  const int64_t stages = cdiv(k, 32), fill = tile == kTile ? 256 : 768;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(fill / std::max<int64_t>(tiles, 1), stages / 8));
+}
+
+// Edge of the product tiles: 256 (the step's core) or 128 (the small core).
+int pick_tile(int64_t rows, int64_t cols, int64_t k) {
+  return cdiv(rows, 256) * cdiv(cols, 256) < 256 || k < 1024 ? 128 : 256;
 }
 
 // May the core read this bf16 matrix K-major in place?  16-byte rows, and no tile
@@ -101,7 +106,8 @@ struct CePlan {
   bool f32, direct_w;
   int planes;
   int64_t T, D, V, ldd, piece, ldz;
-  int tiles_t, tiles_v, splits_h, splits_w;
+  int tile_z, tile_h, tile_w;            // tile edges: logits, hidden-state and weight gradient
+  int tiles_v, splits_h, splits_w;
   // workspace
   int32_t *rows, *pos, *tgt, *count;
   float *clse, *cg, *gmax, *zt, *part_h, *part_w;
@@ -125,11 +131,13 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   const int64_t n = cdiv(pl.V, std::min(piece, pl.V));
   pl.piece = std::min(round_up(cdiv(pl.V, n), kTile), round_up(pl.V, kTile));
   pl.ldz = round_up(std::min(pl.piece, pl.V), kLdAlign);
-  pl.tiles_t = (int)cdiv(pl.T, kTile);
-  pl.tiles_v = (int)cdiv(pl.V, kTile);
-  const int64_t td = cdiv(pl.D, kTile), piece_rows = std::min(pl.piece, pl.V);
-  pl.splits_h = pick_splits(pl.tiles_t * td, piece_rows);
-  pl.splits_w = pick_splits(cdiv(piece_rows, kTile) * td, pl.T);
+  const int64_t piece_rows = std::min(pl.piece, pl.V);
+  pl.tile_z = pick_tile(pl.T, piece_rows, pl.ldd * (pl.f32 ? 6 : 1));
+  pl.tile_h = pick_tile(pl.T, pl.D, piece_rows);
+  pl.tile_w = pick_tile(piece_rows, pl.D, pl.T);
+  pl.tiles_v = (int)cdiv(pl.V, pl.tile_z);
+  pl.splits_h = pick_splits(cdiv(pl.T, pl.tile_h) * cdiv(pl.D, pl.tile_h), pl.tile_h, piece_rows);
+  pl.splits_w = pick_splits(cdiv(piece_rows, pl.tile_w) * cdiv(pl.D, pl.tile_w), pl.tile_w, pl.T);
   Carver c{base};
   pl.rows = c.take<int32_t>(pl.T);
   pl.tgt = c.take<int32_t>(pl.T);
@@ -161,7 +169,7 @@ int check_ce(const dmuon_ce_problem* p, std::vector<Range>* rs) {
   if (p->vocab < 1 || p->vocab > kMaxRows) return fail(DMUON_E_SHAPE, "vocab must be in [1, 2^30]");
   if (p->ldh < p->width || p->ldw < p->width || p->ldh > kMaxStride || p->ldw > kMaxStride)
     return fail(DMUON_E_SHAPE, "ldh and ldw must be at least width");
-  if (cdiv(p->tokens, kTile) * cdiv(p->vocab, kTile) > INT32_MAX) return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
+  if (cdiv(p->tokens, 128) * cdiv(p->vocab, 128) > INT32_MAX) return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
   if (p->tokens > 0 && (!p->h || !p->targets)) return fail(DMUON_E_NULL, "h and targets must be set");
   if (!p->w) return fail(DMUON_E_NULL, "w must be set");
   if (rs) {
@@ -247,8 +255,9 @@ CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64
   g.v0 = (int32_t)v0;
   g.vrows = (int32_t)rows;
   g.tokens = (int32_t)pl.T;
-  g.tiles_v = (int32_t)cdiv(rows, kTile);
-  g.tiles_t = pl.tiles_t;
+  g.tile = pl.tile_z;
+  g.tiles_v = (int32_t)cdiv(rows, pl.tile_z);
+  g.tiles_t = (int32_t)cdiv(pl.T, pl.tile_z);
   g.count = pl.count;
   g.tgt = pl.tgt;
   return g;
@@ -268,7 +277,7 @@ int fill_zero(void* out, int32_t dtype, int64_t rows, int64_t cols, int phase, c
 // ---- weight gradient from a checkpoint ------------------------------------------
 struct WgradPlan {
   bool direct_g;
-  int planes, splits;
+  int planes, splits, tile;
   int64_t ldn, ldk, tiles_r, tiles_c;
   uint16_t *x, *g;
   float* part;
@@ -281,10 +290,11 @@ WgradPlan wgrad_plan(const dmuon_ckpt8_wgrad_problem& p, char* base) {
   pl.direct_g = p.grad_dtype == DMUON_BF16 && kmajor_in_place(p.grad_out, p.ldg, p.n);
   pl.ldn = round_up(p.n, kLdAlign);
   pl.ldk = round_up(p.k, kLdAlign);
-  pl.tiles_r = cdiv(p.n, kTile);
-  pl.tiles_c = cdiv(p.k, kTile);
-  const int64_t groups = p.offsets ? p.groups : 1;
-  pl.splits = pick_splits(pl.tiles_r * pl.tiles_c * groups, p.tokens / std::max<int64_t>(groups, 1));
+  const int64_t groups = p.offsets ? p.groups : 1, k = p.tokens / std::max<int64_t>(groups, 1);
+  pl.tile = pick_tile(p.n, p.k, k);
+  pl.tiles_r = cdiv(p.n, pl.tile);
+  pl.tiles_c = cdiv(p.k, pl.tile);
+  pl.splits = pick_splits(pl.tiles_r * pl.tiles_c * groups, pl.tile, k);
   Carver c{base};
   pl.x = c.take<uint16_t>(p.tokens * pl.ldk);
   if (!pl.direct_g) pl.g = c.take<uint16_t>(pl.planes * p.tokens * pl.ldn);
@@ -304,7 +314,7 @@ int check_wgrad(const dmuon_ckpt8_wgrad_problem* p, std::vector<Range>* rs) {
   if (p->reserved != 0) return fail(DMUON_E_SHAPE, "reserved must be 0");
   if (!p->offsets && p->groups > 1) return fail(DMUON_E_NULL, "offsets must be set for more than one group");
   const int64_t groups = p->offsets ? p->groups : 1;
-  if (cdiv(p->n, kTile) * cdiv(p->k, kTile) * std::max<int64_t>(groups, 1) > INT32_MAX / 256)
+  if (cdiv(p->n, 128) * cdiv(p->k, 128) * std::max<int64_t>(groups, 1) > INT32_MAX / 768)
     return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
   if (p->tokens > 0 && (!p->grad_out || !p->q || !p->exps)) return fail(DMUON_E_NULL, "grad_out, q and exps must be set");
   if (groups > 0 && !p->out) return fail(DMUON_E_NULL, "out must be set");
@@ -448,7 +458,6 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
     const CePlan pl = ce_plan(*p, true, (char*)workspace);
     if ((e = forced(env, -2))) return e;
     if ((e = ce_start(*p, pl, true, lse, grad_losses, nullptr, nullptr, env, stream))) return e;
-    const int64_t td = cdiv(pl.D, kTile);
     for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
       const int64_t rows = std::min(pl.piece, pl.V - v0);
       const uint16_t* w;
@@ -476,8 +485,9 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
         q.k = pl.T;
         q.count = pl.count;
         q.groups = 1;
-        q.tiles_r = (int32_t)cdiv(rows, kTile);
-        q.tiles_c = (int32_t)td;
+        q.tile = pl.tile_w;
+        q.tiles_r = (int32_t)cdiv(rows, q.tile);
+        q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
         q.splits = pl.splits_w;
         q.scale = pl.gmax;
         q.out = (char*)grad_w + v0 * pl.D * es;
@@ -517,8 +527,9 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
         q.k = rows;
         q.count = pl.count;
         q.groups = 1;
-        q.tiles_r = pl.tiles_t;
-        q.tiles_c = (int32_t)td;
+        q.tile = pl.tile_h;
+        q.tiles_r = (int32_t)cdiv(pl.T, q.tile);
+        q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
         q.splits = pl.splits_h;
         q.part = pl.part_h;
         q.ldp = (int32_t)pl.ldd;
@@ -782,6 +793,7 @@ int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* p, void* workspace, size_
     q.k = p->tokens;
     q.offsets = p->offsets;
     q.groups = (int32_t)groups;
+    q.tile = pl.tile;
     q.tiles_r = (int32_t)pl.tiles_r;
     q.tiles_c = (int32_t)pl.tiles_c;
     q.splits = pl.splits;

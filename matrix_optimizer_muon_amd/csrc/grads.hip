@@ -224,16 +224,124 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
 // ---------------------------------------------------------------------------
 // products on the core
 // ---------------------------------------------------------------------------
-// acc = Σ over the plane pairs of op, whose a and b point at plane 0
+// Small core: 128 × 128 per workgroup of 4 waves, 64 × 64 per wave, for products
+// whose tiles are few or whose K is short.  K is staged through LDS like the step's
+// core does (64-byte rows for row-major operands, 32 k-rows of 256 bytes for K-major
+// ones, the same swizzles), three stages of 16 KiB, so that three workgroups share a
+// CU: their waves are not in step, one's copies, prologue and epilogue run beside the
+// others' products.  One barrier per stage: a wave waits for its own share of stage
+// kt before it, so behind it the whole stage has landed and every wave is done with
+// stage kt − 1, whose slot stage kt + 2 takes.
+constexpr int kSmallStage = 2 * 128 * kRowBytes;        // 16 KiB
+constexpr int kSmallStages = 3;
+
 template <bool TA, bool TB>
+__device__ __forceinline__ void gemm_small(const Operands& op, char* smem, f32x16_t (&acc)[2][2]) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const __amdgpu_buffer_rsrc_t ra = range_rsrc(op.a, (int64_t)(op.rows_a < 128 ? op.rows_a : 128) * op.lda_b);
+  const __amdgpu_buffer_rsrc_t rb = range_rsrc(op.b, (int64_t)(op.rows_b < 128 ? op.rows_b : 128) * op.ldb_b);
+  // copies: wave w fills rows [32w, 32w + 32) of each operand, 16 rows (row-major) or
+  // 4 k-rows (K-major) per instruction; lane l lands at byte 16·l of its 1 KiB
+  int offa[2], offb[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = (wave * 2 + q) * 16 + (lane >> 2);
+    const int c = (lane & 3) ^ ((row >> 2) & 3);
+    const int kr = 4 * (wave * 2 + q) + (lane >> 4), un = lane & 15;
+    const int lun = (((un >> 1) ^ kmaj_swz(kr)) << 1) | (un & 1);
+    offa[q] = TA ? kr * op.lda_b + op.cola_b + lun * 16 : row * op.lda_b + c * 16;
+    offb[q] = TB ? kr * op.ldb_b + op.colb_b + lun * 16 : row * op.ldb_b + c * 16;
+  }
+  // fragments: 4 of 16 rows and 4 of 16 columns, all 32 k of a stage
+  int fa_off[4], fb_off[4], ta_off[4][2], tb_off[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ar = wr * 64 + 16 * i + (lane & 15), br = wc * 64 + 16 * i + (lane & 15), c = lane >> 4;
+    fa_off[i] = ar * kRowBytes + ((c ^ ((ar >> 2) & 3)) * 16);
+    fb_off[i] = 128 * kRowBytes + br * kRowBytes + ((c ^ ((br >> 2) & 3)) * 16);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int kr = 8 * (lane >> 4) + 4 * t + ((lane & 15) >> 2), sub = 4 * (lane & 3);
+      const int na = wr * 64 + 16 * i + sub, nb = wc * 64 + 16 * i + sub;
+      ta_off[i][t] = kr * 256 + (((na >> 4) ^ kmaj_swz(kr)) << 5) + ((2 * na) & 31);
+      tb_off[i][t] = 128 * kRowBytes + kr * 256 + (((nb >> 4) ^ kmaj_swz(kr)) << 5) + ((2 * nb) & 31);
+    }
+  }
+  auto kmaj_rsrc = [&](const char* p, int ld_b, int rows, int kt) {
+    const int left = rows - 32 * kt;
+    return range_rsrc(p + (int64_t)kt * 32 * ld_b, (int64_t)(left < 0 ? 0 : (left < 32 ? left : 32)) * ld_b);
+  };
+  auto issue = [&](int kt, int slot) {
+    char* base = smem + slot * kSmallStage;
+    const __amdgpu_buffer_rsrc_t sa = TA ? kmaj_rsrc(op.a, op.lda_b, op.rows_a, kt) : ra;
+    const __amdgpu_buffer_rsrc_t sb = TB ? kmaj_rsrc(op.b, op.ldb_b, op.rows_b, kt) : rb;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      char* da = base + (wave * 2 + q) * 1024;
+      char* db = da + 128 * kRowBytes;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sa, (__attribute__((address_space(3))) void*)da, 16,
+                                               offa[q] + (TA ? 0 : kt * kRowBytes), 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sb, (__attribute__((address_space(3))) void*)db, 16,
+                                               offb[q] + (TB ? 0 : kt * kRowBytes), 0, 0, 0);
+    }
+  };
+  const int KT = op.ktiles;
+  if (KT > 0) issue(0, 0);
+  if (KT > 1) issue(1, 1);
+  int slot = 0;
+#pragma unroll 1
+  for (int kt = 0; kt < KT; ++kt) {
+    if (kt + 1 < KT) DMUON_WAIT_VM(4);                   // own share of stage kt (4 copies per stage)
+    else DMUON_WAIT_VM(0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (kt + 2 < KT) issue(kt + 2, slot == 0 ? 2 : slot - 1);
+    const char* base = smem + slot * kSmallStage;
+    auto tr16 = [&](int off0, int off1) {
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(base + off0));
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(base + off1));
+      u32x4_t r;
+      r.x = (uint32_t)(uint16_t)lo.x | ((uint32_t)(uint16_t)lo.y << 16);
+      r.y = (uint32_t)(uint16_t)lo.z | ((uint32_t)(uint16_t)lo.w << 16);
+      r.z = (uint32_t)(uint16_t)hi.x | ((uint32_t)(uint16_t)hi.y << 16);
+      r.w = (uint32_t)(uint16_t)hi.z | ((uint32_t)(uint16_t)hi.w << 16);
+      return r;
+    };
+    u32x4_t fa[4], fb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fa[i] = TA ? tr16(ta_off[i][0], ta_off[i][1]) : *(const u32x4_t*)(base + fa_off[i]);
+      fb[i] = TB ? tr16(tb_off[i][0], tb_off[i][1]) : *(const u32x4_t*)(base + fb_off[i]);
+    }
+    static_for<4>([&](auto Sq) {
+      constexpr int qs = decltype(Sq)::value;
+      static_for<4>([&](auto Tq) {
+        constexpr int qt = decltype(Tq)::value;
+        mfma_quarter<2 * (qs & 1) + (qt & 1)>(acc[qs >> 1][qt >> 1], fa[qs], fb[qt]);
+      });
+    });
+    __builtin_amdgcn_sched_barrier(0);                   // the fragments are in registers before the next barrier
+    slot = slot == 2 ? 0 : slot + 1;
+  }
+  __syncthreads();                                       // LDS is free for the caller
+}
+
+// acc = Σ over the plane pairs of op, whose a and b point at plane 0
+template <typename S, bool TA, bool TB>
 __device__ __forceinline__ void gemm_planes(const Operands& op, int64_t a_plane, int64_t b_plane, const PlanePairs& pp,
-                                            char* smem, f32x16_t (&acc)[4][2]) {
-  if (pp.n == 1) {
-    gemm_mainloop<uint16_t, TA, TB>(op, smem, acc);
-    return;
+                                            char* smem, f32x16_t (&acc)[S::I][2]) {
+  constexpr bool large = S::I == 4;
+  if constexpr (large) {
+    if (pp.n == 1) {
+      gemm_mainloop<uint16_t, TA, TB>(op, smem, acc);
+      return;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < S::I; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -243,43 +351,58 @@ __device__ __forceinline__ void gemm_planes(const Operands& op, int64_t a_plane,
     Operands o = op;
     o.a += (int64_t)((pp.a >> (4 * p)) & 15) * a_plane * 2;
     o.b += (int64_t)((pp.b >> (4 * p)) & 15) * b_plane * 2;
-    gemm_mainloop<uint16_t, TA, TB, 0, 1>(o, smem, acc);
+    if constexpr (large) gemm_mainloop<uint16_t, TA, TB, 0, 1>(o, smem, acc);
+    else gemm_small<TA, TB>(o, smem, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < S::I; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) quarters_to_32x32(acc[i][j]);
 }
 
-// A tile whose lanes hold output rows (acc_col) and whose registers hold
-// consecutive output columns (acc_row + e) goes out through LDS as whole rows of
+// Tile shapes.  A workgroup computes rows (A's side) × columns (B's side) of a
+// product; a wave holds 32·I rows and 64 columns as I × 2 blocks of 32 × 32.
+//   Large: the step's core, 256 × 256 on 8 waves, one workgroup per CU;
+//   Small: 128 × 128 on 4 waves (gemm_small), three workgroups per CU.
+struct Large {
+  static constexpr int I = 4, WC = 4;                    // row blocks per wave, waves along the columns
+  static constexpr int M = 256, N = 256, Threads = 512, Lds = kGemmLds;
+};
+struct Small {
+  static constexpr int I = 2, WC = 2;
+  static constexpr int M = 128, N = 128, Threads = 256, Lds = kSmallStages * kSmallStage;
+};
+
+// A tile whose lanes hold output rows (the tile's columns) and whose registers hold
+// consecutive output columns (the tile's rows) goes out through LDS as whole rows of
 // 16-byte pieces.  f(i, j, r) is the value of register r of block (i, j).
 // Rows ≥ rows and columns ≥ cols are dropped; `vec` says that whole pieces may be
 // stored as such.
-template <typename F>
+template <typename S, typename F>
 __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
-  // 512-byte rows; 16-byte pieces XOR-swizzled by the row, so that the 32 rows one
-  // 8-byte write instruction touches fall in all banks
+  const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
+  // 16-byte pieces XOR-swizzled by the row, so that the 32 rows one 8-byte write
+  // instruction touches fall in all banks
+  constexpr int P = S::M / 8;                            // pieces per row
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < S::I; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int rq = 0; rq < 4; ++rq) {
         const int row = wc * 64 + j * 32 + r32;
-        const int piece = wr * 16 + i * 4 + rq;
+        const int piece = (wr * S::I + i) * 4 + rq;
         const uint2 v = make_uint2(pack_bf16x2(f(i, j, 4 * rq), f(i, j, 4 * rq + 1)),
                                    pack_bf16x2(f(i, j, 4 * rq + 2), f(i, j, 4 * rq + 3)));
-        *(uint2*)(smem + row * 512 + ((piece ^ (row & 31)) << 4) + h * 8) = v;
+        *(uint2*)(smem + row * (P * 16) + ((piece ^ (row & (P - 1) & 31)) << 4) + h * 8) = v;
       }
   __syncthreads();
 #pragma unroll 4
-  for (int q = 0; q < 16; ++q) {
-    const int id = tid + kGemmThreads * q;
-    const int row = id >> 5, piece = id & 31;
-    const u32x4_t v = *(const u32x4_t*)(smem + row * 512 + ((piece ^ (row & 31)) << 4));
+  for (int q = 0; q < S::N * P / S::Threads; ++q) {
+    const int id = tid + S::Threads * q;
+    const int row = id / P, piece = id % P;
+    const u32x4_t v = *(const u32x4_t*)(smem + row * (P * 16) + ((piece ^ (row & (P - 1) & 31)) << 4));
     const int left = cols - piece * 8;
     if (row >= rows || left <= 0) continue;
     gptr<uint16_t> d = glob(out) + (int64_t)row * ld + piece * 8;
@@ -294,32 +417,33 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, 
   }
   __syncthreads();
 }
-// fp32: 1 KiB rows, 128 of them at a time
-template <typename F>
+// fp32: half of the rows at a time
+template <typename S, typename F>
 __device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+  const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
+  constexpr int P = S::M / 4, R = S::N / 2;              // pieces per row, rows at a time
 #pragma unroll 1
   for (int hf = 0; hf < 2; ++hf) {
-    if ((wc >> 1) == hf) {
+    if (wc / (S::WC / 2) == hf) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int rq = 0; rq < 4; ++rq) {
-            const int row = (wc & 1) * 64 + j * 32 + r32;
-            const int piece = wr * 32 + i * 8 + rq * 2 + h;
-            *(float4*)(smem + row * 1024 + ((piece ^ (row & 31)) << 4)) =
+            const int row = wc % (S::WC / 2) * 64 + j * 32 + r32;
+            const int piece = (wr * S::I + i) * 8 + rq * 2 + h;
+            *(float4*)(smem + row * (P * 16) + ((piece ^ (row & 31)) << 4)) =
                 make_float4(f(i, j, 4 * rq), f(i, j, 4 * rq + 1), f(i, j, 4 * rq + 2), f(i, j, 4 * rq + 3));
           }
     }
     __syncthreads();
 #pragma unroll 4
-    for (int q = 0; q < 16; ++q) {
-      const int id = tid + kGemmThreads * q;
-      const int lr = id >> 6, piece = id & 63, row = hf * 128 + lr;
-      const f32x4_t v = *(const f32x4_t*)(smem + lr * 1024 + ((piece ^ (lr & 31)) << 4));
+    for (int q = 0; q < R * P / S::Threads; ++q) {
+      const int id = tid + S::Threads * q;
+      const int lr = id / P, piece = id % P, row = hf * R + lr;
+      const f32x4_t v = *(const f32x4_t*)(smem + lr * (P * 16) + ((piece ^ (lr & 31)) << 4));
       const int left = cols - piece * 4;
       if (row >= rows || left <= 0) continue;
       gptr<float> d = glob(out) + (int64_t)row * ld + piece * 4;
@@ -346,13 +470,13 @@ __device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int
 //   backward: dZ(t, v) = g_t·(exp(z − lse_t) − [v = target]), rounded to bf16 (one
 //             rounding; the matrix cores take bf16; fp32 operands: three planes).
 // ---------------------------------------------------------------------------
-template <bool BACKWARD, bool F32>
-__global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
+template <typename S, bool BACKWARD, bool F32>
+__global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   extern __shared__ __align__(16) char smem[];
   int tt, tv;
   band_tile(xcd_logical_block<64>(), g.tiles_t, g.tiles_v, tt, tv);
   const int count = *g.count;
-  const int row0 = tv * kTile, col0 = tt * kTile;   // vocabulary (in the piece), tokens
+  const int row0 = tv * S::M, col0 = tt * S::N;   // vocabulary (in the piece), tokens
   if (col0 >= count) return;
   Operands op;
   op.a = (const char*)(g.w + (int64_t)row0 * g.ldw);
@@ -363,13 +487,13 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
   op.rows_b = count - col0;
   op.cola_b = op.colb_b = 0;
   op.ktiles = g.kt;
-  f32x16_t acc[4][2];
-  gemm_planes<false, false>(op, g.w_plane, g.h_plane, g.pairs, smem, acc);
+  f32x16_t acc[S::I][2];
+  gemm_planes<S, false, false>(op, g.w_plane, g.h_plane, g.pairs, smem, acc);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
-  const int vleft = g.vrows - row0 - wr * 128 - h * 4;       // valid while register row < vleft
-  const bool ragged = g.vrows - row0 < kTile;
+  const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
+  const int vleft = g.vrows - row0 - wr * (32 * S::I) - h * 4;       // valid while register row < vleft
+  const bool ragged = g.vrows - row0 < S::M;
   // register row of the target of column j's token, or −1
   int want[2];
   float L[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
@@ -380,7 +504,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
     want[j] = -1;
     if (tok[j] < count) {
       const int y = g.tgt[tok[j]] - g.v0 - row0;
-      if (y >= 0 && y < kTile && g.tgt[tok[j]] >= 0 && (y >> 7) == wr && ((y >> 2) & 1) == h) want[j] = (y & 127) - 4 * h;
+      if (y >= 0 && y < S::M && g.tgt[tok[j]] >= 0 && y / (32 * S::I) == wr && ((y >> 2) & 1) == h) want[j] = y % (32 * S::I) - 4 * h;
       if constexpr (BACKWARD) {
         L[j] = g.clse[tok[j]];
         w[j] = g.cg[tok[j]] / *g.gmax;
@@ -390,12 +514,12 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
   auto reg_row = [](int i, int r) { return i * 32 + (r >> 2) * 8 + (r & 3); };
 
   if constexpr (!BACKWARD) {
-    CeStat* st = (CeStat*)smem;                              // [wave group][256]
+    CeStat* st = (CeStat*)smem;                              // [wave row][token of the tile]
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float m = -INFINITY, z = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           if (ragged && reg_row(i, r) >= vleft) acc[i][j][r] = -INFINITY;
@@ -406,26 +530,26 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
       const float m0 = m == -INFINITY ? 0.f : m;             // then s is 0, or NaN if a logit is
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s += __expf(acc[i][j][r] - m0);
       s += __shfl_xor(s, 32, 64);
-      if (h == 0) st[wr * kTile + wc * 64 + j * 32 + r32] = CeStat{m, s};
+      if (h == 0) st[wr * S::N + wc * 64 + j * 32 + r32] = CeStat{m, s};
       if (want[j] >= 0) g.zt[tok[j]] = z;
     }
     __syncthreads();
-    if (tid < kTile && col0 + tid < count) {
-      const CeStat a = st[tid], b = st[kTile + tid];
+    if (tid < S::N && col0 + tid < count) {
+      const CeStat a = st[tid], b = st[S::N + tid];
       const float m = fmaxf(a.m, b.m);
       const float sa = a.m == -INFINITY ? a.s : a.s * __expf(a.m - m);
       const float sb = b.m == -INFINITY ? b.s : b.s * __expf(b.m - m);
-      g.stats[(int64_t)(g.v0 / kTile + tv) * g.tokens + col0 + tid] = CeStat{m, sa + sb};
+      g.stats[(int64_t)(g.v0 / S::M + tv) * g.tokens + col0 + tid] = CeStat{m, sa + sb};
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           float p = __expf(acc[i][j][r] - L[j]);
@@ -439,16 +563,16 @@ __global__ __launch_bounds__(kGemmThreads) void k_ce_logits(CeLogitsArgs g) {
       // three planes: each stores what bf16 holds of the rest (exact differences)
 #pragma unroll 1
       for (int q = 0; q < kPlanes; ++q) {
-        store_tile(out + q * g.dz_plane, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
+        store_tile<S>(out + q * g.dz_plane, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < S::I; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] -= bf16_to_f32(f32_to_bf16(acc[i][j][r]));
       }
     } else {
-      store_tile(out, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
+      store_tile<S>(out, g.ldz, rows, cols, true, smem, [&](int i, int j, int r) { return acc[i][j][r]; });
     }
   }
 }
@@ -503,8 +627,8 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
 // partial sums for k_join; the hidden-state gradient adds up its vocabulary
 // pieces that way too.
 // ---------------------------------------------------------------------------
-template <bool TB>
-__global__ __launch_bounds__(kGemmThreads) void k_product(ProductArgs g) {
+template <typename S, bool TB>
+__global__ __launch_bounds__(S::Threads) void k_product(ProductArgs g) {
   extern __shared__ __align__(16) char smem[];
   int u = xcd_logical_block<64>();
   const int tiles = g.tiles_r * g.tiles_c;
@@ -515,7 +639,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_product(ProductArgs g) {
   int tr, tc;
   if (g.tiles_c <= g.tiles_r) band_tile(u, g.tiles_c, g.tiles_r, tc, tr);
   else band_tile(u, g.tiles_r, g.tiles_c, tr, tc);
-  const int row0 = tr * kTile, col0 = tc * kTile;
+  const int row0 = tr * S::N, col0 = tc * S::M;
   int rows = g.rows;
   int64_t k0 = 0, k1 = g.k;
   if (g.count) {
@@ -551,22 +675,22 @@ __global__ __launch_bounds__(kGemmThreads) void k_product(ProductArgs g) {
     op.colb_b = 0;
   }
   op.ktiles = (int)((k1 - k0 + 31) / 32);
-  f32x16_t acc[4][2];
-  gemm_planes<true, TB>(op, g.a_plane, g.b_plane, g.pairs, smem, acc);
+  f32x16_t acc[S::I][2];
+  gemm_planes<S, true, TB>(op, g.a_plane, g.b_plane, g.pairs, smem, acc);
 
   if (g.part) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wr = wave >> 2, wc = wave & 3, h = lane >> 5, r32 = lane & 31;
+    const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
     gptr<float> part = glob(g.part) + split * g.part_split + (int64_t)group * g.rows * g.ldp;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int row = row0 + wc * 64 + j * 32 + r32;
       if (row >= rows) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
         for (int rq = 0; rq < 4; ++rq) {
-          const int col = col0 + wr * 128 + i * 32 + rq * 8 + h * 4;
+          const int col = col0 + wr * (32 * S::I) + i * 32 + rq * 8 + h * 4;
           if (col >= g.ldp) continue;
           gptr<f32x4_t> p = (gptr<f32x4_t>)(part + (int64_t)row * g.ldp + col);
           f32x4_t v = {acc[i][j][4 * rq], acc[i][j][4 * rq + 1], acc[i][j][4 * rq + 2], acc[i][j][4 * rq + 3]};
@@ -583,10 +707,10 @@ __global__ __launch_bounds__(kGemmThreads) void k_product(ProductArgs g) {
   const int64_t at = ((int64_t)group * g.rows + row0) * g.cols + col0;
   const int rl = rows - row0, cl = g.cols - col0;
   if (g.out_f32)
-    store_tile((float*)g.out + at, g.cols, rl, cl, (g.cols & 3) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
+    store_tile<S>((float*)g.out + at, g.cols, rl, cl, (g.cols & 3) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
                [&](int i, int j, int r) { return acc[i][j][r] * s; });
   else
-    store_tile((uint16_t*)g.out + at, g.cols, rl, cl, (g.cols & 7) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
+    store_tile<S>((uint16_t*)g.out + at, g.cols, rl, cl, (g.cols & 7) == 0 && ((uintptr_t)g.out & 15) == 0, smem,
                [&](int i, int j, int r) { return acc[i][j][r] * s; });
 }
 
@@ -1028,14 +1152,16 @@ __device__ __forceinline__ int wave_lower_bound(const uint32_t* keys, int n, int
   return lo;
 }
 
-// One launch, two kinds of workgroups, interleaved so that both run all the time
-// (the sums wait on latency, the zeros on bandwidth):
+// One launch, two kinds of workgroups: the sums, which wait on latency, first, then
+// the zeros, which wait on bandwidth.  Zeros leave with nontemporal stores: with plain
+// ones the sums' loads waited behind them (8192 tokens into 32000 × 2048 bf16: 55 µs,
+// nontemporal 33 = 5 TB/s, either alone 20 to 24; interleaved 59, zeros first 57).
 //   sums:  one wave per 8 sorted positions and 512 columns.  It owns the ranges that
 //          begin there: the rows of their tokens among the 8 are loaded at once, added
 //          in order, and a range that ends is written (or added) to its row.  A range
 //          that goes on past the 8 is finished (32 tokens and more: summed) by
 //          add_range.
-//   zeros: 32 table rows per workgroup; rows without tokens are cleared (none of
+//   zeros: 16 table rows per workgroup; rows without tokens are cleared (none of
 //          them when accumulating).
 template <typename G, typename O>
 __device__ __forceinline__ void embed_sums(const EmbedGradArgs& a, int64_t wg) {
@@ -1151,7 +1277,8 @@ __device__ __forceinline__ void embed_zeros(const EmbedGradArgs& a, int64_t wg, 
     if (start[r] && v != a.padding) continue;
     gptr<O> out = glob((O*)a.out) + v * a.width;
     if (a.vec_out) {
-      for (int c = threadIdx.x * E; c < a.width; c += kThreads * E) *(gptr<u32x4_t>)(out + c) = u32x4_t{0u, 0u, 0u, 0u};
+      for (int c = threadIdx.x * E; c < a.width; c += kThreads * E)
+        __builtin_nontemporal_store(u32x4_t{0u, 0u, 0u, 0u}, (gptr<u32x4_t>)(out + c));
     } else {
       for (int c = threadIdx.x; c < a.width; c += kThreads) out[c] = O(0);
     }
@@ -1161,11 +1288,9 @@ __device__ __forceinline__ void embed_zeros(const EmbedGradArgs& a, int64_t wg, 
 template <typename G, typename O>
 __global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
   __shared__ int start[kEmbedRows + 1];
-  // workgroup b of n: ⌊(b + 1)·s/n⌋ > ⌊b·s/n⌋ picks s of them, evenly spread
-  const int64_t b = blockIdx.x, n = gridDim.x;
-  const int64_t before = b * a.seg_wg / n;
-  if ((b + 1) * a.seg_wg / n > before) embed_sums<G, O>(a, before);
-  else embed_zeros<O>(a, b - before, start);
+  const int64_t wg = blockIdx.x;
+  if (wg < a.seg_wg) embed_sums<G, O>(a, wg);
+  else embed_zeros<O>(a, wg - a.seg_wg, start);
 }
 
 // ---------------------------------------------------------------------------
@@ -1298,29 +1423,34 @@ int launch_pack(const PackArgs& a, int phase, void* stream) {
 int launch_ce_scan(const CeScanArgs& a, void* stream) {
   DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan, 1, kScanThreads, 0, a);
 }
-int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream) {
-  static std::atomic<uint64_t> ready[3];
-  const int v = backward ? (f32 ? 2 : 1) : 0;
-  const void* const kernels[3] = {(const void*)k_ce_logits<false, false>, (const void*)k_ce_logits<true, false>,
-                                  (const void*)k_ce_logits<true, true>};
-  const int e = raise_lds(kernels[v], kGemmLds, ready[v]);
+template <typename S, bool BACKWARD, bool F32>
+static int ce_logits(const CeLogitsArgs& a, void* stream) {
+  static std::atomic<uint64_t> ready{0};
+  const int e = raise_lds((const void*)k_ce_logits<S, BACKWARD, F32>, S::Lds, ready);
   if (e) return e;
-  const unsigned grid = (unsigned)(a.tiles_t * a.tiles_v);
-  if (!backward) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<false, false>), grid, kGemmThreads, kGemmLds, a);
-  if (f32) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<true, true>), grid, kGemmThreads, kGemmLds, a);
-  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<true, false>), grid, kGemmThreads, kGemmLds, a);
+  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<S, BACKWARD, F32>), (unsigned)(a.tiles_t * a.tiles_v), S::Threads, S::Lds, a);
+}
+int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream) {
+  if (a.tile == Large::M) {
+    if (!backward) return ce_logits<Large, false, false>(a, stream);
+    return f32 ? ce_logits<Large, true, true>(a, stream) : ce_logits<Large, true, false>(a, stream);
+  }
+  if (!backward) return ce_logits<Small, false, false>(a, stream);
+  return f32 ? ce_logits<Small, true, true>(a, stream) : ce_logits<Small, true, false>(a, stream);
 }
 int launch_ce_rows(const CeRowsArgs& a, void* stream) {
   DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
 }
-int launch_product(const ProductArgs& a, int phase, void* stream) {
-  static std::atomic<uint64_t> ready[2];
-  const void* const kernels[2] = {(const void*)k_product<true>, (const void*)k_product<false>};
-  const int e = raise_lds(kernels[a.b_rows ? 1 : 0], kGemmLds, ready[a.b_rows ? 1 : 0]);
+template <typename S, bool TB>
+static int product(const ProductArgs& a, int phase, void* stream) {
+  static std::atomic<uint64_t> ready{0};
+  const int e = raise_lds((const void*)k_product<S, TB>, S::Lds, ready);
   if (e) return e;
-  const unsigned grid = (unsigned)(a.tiles_r * a.tiles_c * a.groups * a.splits);
-  if (a.b_rows) DMUON_LAUNCH(phase, stream, k_product<false>, grid, kGemmThreads, kGemmLds, a);
-  DMUON_LAUNCH(phase, stream, k_product<true>, grid, kGemmThreads, kGemmLds, a);
+  DMUON_LAUNCH(phase, stream, (k_product<S, TB>), (unsigned)(a.tiles_r * a.tiles_c * a.groups * a.splits), S::Threads, S::Lds, a);
+}
+int launch_product(const ProductArgs& a, int phase, void* stream) {
+  if (a.tile == Large::M) return a.b_rows ? product<Large, false>(a, phase, stream) : product<Large, true>(a, phase, stream);
+  return a.b_rows ? product<Small, false>(a, phase, stream) : product<Small, true>(a, phase, stream);
 }
 int launch_join(const JoinArgs& a, int phase, void* stream) {
   DMUON_LAUNCH(phase, stream, k_join, stride_grid(a.rows * cdiv(a.cols, 8)), kThreads, 0, a);

@@ -74,6 +74,7 @@ struct CeLogitsArgs {
   int32_t kt;                  // stages of 32
   int32_t v0, vrows;           // the piece: first vocabulary row, rows
   int32_t tokens;              // compact rows at most
+  int32_t tile;                // 256 or 128: the tile's edge
   int32_t tiles_v, tiles_t;
   const int32_t* count;
   const int32_t* tgt;
@@ -114,6 +115,7 @@ struct ProductArgs {
   const int32_t* count;        // device bound of K (weight gradient) or of the rows (b_rows), or null
   const int32_t* offsets;      // K ranges of `groups` outputs, or null
   int32_t groups;
+  int32_t tile;                // 256 or 128: the tile's edge
   int32_t tiles_r, tiles_c, splits;
   const float* scale;          // device factor of the result, or null
   void* out;                   // final result: dense rows × cols per group
@@ -197,7 +199,7 @@ struct CodecArgs {
 
 constexpr int kSortItems = 4096;         // per workgroup of a sort pass
 constexpr int kRun = 32;                 // sorted tokens per first-level sum, and those per second-level one
-constexpr int kEmbedRows = 32;           // table rows per workgroup that clears rows
+constexpr int kEmbedRows = 16;           // table rows per workgroup that clears rows
 constexpr int kEmbedHeads = 8;           // sorted positions per wave that sums ranges
 constexpr int kSortRunBits = 13;
 constexpr int kSortRun = 1 << kSortRunBits;            // tokens per run of the two-launch sort
