@@ -52,19 +52,30 @@ __device__ __forceinline__ void load8(gptr<const float> p, bool vec, int left, f
 __device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
   return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
+// NT: nontemporal, for results that this library does not read again (the lookup of
+// 32768 tokens 85.6 → 83.6 µs, a checkpoint stored and read back 92 → 86)
+template <bool NT = false>
 __device__ __forceinline__ void store8(gptr<uint16_t> p, bool vec, int left, const float (&v)[8]) {
   if (vec) {
-    *(gptr<u32x4_t>)p = pack8(v);
+    if (NT) __builtin_nontemporal_store(pack8(v), (gptr<u32x4_t>)p);
+    else *(gptr<u32x4_t>)p = pack8(v);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (e < left) p[e] = f32_to_bf16(v[e]);
   }
 }
+template <bool NT = false>
 __device__ __forceinline__ void store8(gptr<float> p, bool vec, int left, const float (&v)[8]) {
   if (vec) {
-    ((gptr<f32x4_t>)p)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-    ((gptr<f32x4_t>)p)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    if (NT) {
+      __builtin_nontemporal_store(a, (gptr<f32x4_t>)p);
+      __builtin_nontemporal_store(b, (gptr<f32x4_t>)p + 1);
+    } else {
+      ((gptr<f32x4_t>)p)[0] = a;
+      ((gptr<f32x4_t>)p)[1] = b;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -377,7 +388,9 @@ struct Small {
 // consecutive output columns (the tile's rows) goes out through LDS as whole rows of
 // 16-byte pieces.  f(i, j, r) is the value of register r of block (i, j).
 // Rows ≥ rows and columns ≥ cols are dropped; `vec` says that whole pieces may be
-// stored as such.
+// stored as such.  The stores are nontemporal: with plain ones the experts' weight
+// gradients (738 MB of fp32) took 329 µs instead of 273, the cross-entropy gradients
+// of 2400 tokens 2.60 ms instead of 2.35.
 template <typename S, typename F>
 __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -407,7 +420,7 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, 
     if (row >= rows || left <= 0) continue;
     gptr<uint16_t> d = glob(out) + (int64_t)row * ld + piece * 8;
     if (vec && left >= 8) {
-      *(gptr<u32x4_t>)d = v;
+      __builtin_nontemporal_store(v, (gptr<u32x4_t>)d);
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -448,7 +461,7 @@ __device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int
       if (row >= rows || left <= 0) continue;
       gptr<float> d = glob(out) + (int64_t)row * ld + piece * 4;
       if (vec && left >= 4) {
-        *(gptr<f32x4_t>)d = v;
+        __builtin_nontemporal_store(v, (gptr<f32x4_t>)d);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -736,8 +749,8 @@ __global__ __launch_bounds__(kThreads) void k_join(JoinArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= s;
     }
-    if (a.out_f32) store8(glob((float*)a.out) + t * a.cols + c, vec, left, v);
-    else store8(glob((uint16_t*)a.out) + t * a.cols + c, vec, left, v);
+    if (a.out_f32) store8<true>(glob((float*)a.out) + t * a.cols + c, vec, left, v);
+    else store8<true>(glob((uint16_t*)a.out) + t * a.cols + c, vec, left, v);
   }
 }
 
@@ -760,7 +773,7 @@ __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= a.scale;
     }
-    store8(glob((T*)a.out) + t * a.width + c, a.vec, left, v);
+    store8<true>(glob((T*)a.out) + t * a.width + c, a.vec, left, v);
   }
 }
 
@@ -1342,7 +1355,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_quantize(CodecArgs a) {
     gptr<int8_t> d = glob(a.q) + r * a.cols + c;
     if (vec_q && left >= 8) {
       typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-      *(gptr<u32x2>)d = u32x2{w[0], w[1]};
+      __builtin_nontemporal_store(u32x2{w[0], w[1]}, (gptr<u32x2>)d);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -1352,7 +1365,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_quantize(CodecArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kThreads) void k_ckpt_read(CodecArgs a) {
   const int per = (a.cols + 7) >> 3;
   const int64_t n = a.rows * per, step = (int64_t)gridDim.x * kThreads;
@@ -1380,7 +1393,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_read(CodecArgs a) {
       const float x = __builtin_amdgcn_ldexpf((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), eb - 133);
       v[e] = eb == 255 ? __uint_as_float(0x7fc00000u) : x;
     }
-    store8(glob((T*)a.out) + r * a.ldo + c, a.vec && left >= 8, left, v);
+    store8<NT>(glob((T*)a.out) + r * a.ldo + c, a.vec && left >= 8, left, v);
   }
 }
 
@@ -1503,8 +1516,9 @@ int launch_ckpt_quantize(const CodecArgs& a, void* stream) {
 }
 int launch_ckpt_read(const CodecArgs& a, int phase, void* stream) {
   const unsigned grid = stride_grid(a.rows * cdiv(a.cols, 8));
-  if (a.f32) DMUON_LAUNCH(phase, stream, k_ckpt_read<float>, grid, kThreads, 0, a);
-  DMUON_LAUNCH(phase, stream, k_ckpt_read<uint16_t>, grid, kThreads, 0, a);
+  if (phase == PH_CKPT_WGRAD) DMUON_LAUNCH(phase, stream, (k_ckpt_read<uint16_t, false>), grid, kThreads, 0, a);   // an operand copy
+  if (a.f32) DMUON_LAUNCH(phase, stream, (k_ckpt_read<float, true>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(phase, stream, (k_ckpt_read<uint16_t, true>), grid, kThreads, 0, a);
 }
 
 }  // namespace dmuon
