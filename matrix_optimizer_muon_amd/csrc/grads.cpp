@@ -111,7 +111,8 @@ struct CePlan {
   // workspace
   int32_t *rows, *pos, *tgt, *count;
   float *clse, *cg, *gmax, *zt, *part_h, *part_w;
-  uint16_t *h, *w, *dz;
+  uint16_t *h, *hb, *w, *dz;
+  int64_t hb_plane;
   CeStat* stats;
   size_t bytes;
 };
@@ -143,6 +144,8 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   pl.tgt = c.take<int32_t>(pl.T);
   pl.count = c.take<int32_t>(1);
   pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
+  pl.hb_plane = round_up(pl.T, 16) * pl.ldd;
+  if (pl.tile_z == kTile) pl.hb = c.take<uint16_t>(pl.planes * pl.hb_plane);
   if (!pl.direct_w) pl.w = c.take<uint16_t>(pl.planes * piece_rows * pl.ldd);
   if (backward) {
     pl.pos = c.take<int32_t>(pl.T);
@@ -215,6 +218,13 @@ int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const f
   a.dst = pl.h;
   a.plane = pl.T * pl.ldd;
   a.ldd = (int32_t)pl.ldd;
+  if (pl.hb) {
+    PackArgs b = a;
+    b.dst = pl.hb;
+    b.plane = pl.hb_plane;
+    b.blocked = 1;
+    if ((e = go(env, PH_CE_PACK, stream, [&] { return launch_pack(b, PH_CE_PACK, stream); }))) return e;
+  }
   return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
 }
 
@@ -247,8 +257,8 @@ CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64
   g.w = w;
   g.w_plane = w_plane;
   g.ldw = ldw;
-  g.h = pl.h;
-  g.h_plane = pl.T * pl.ldd;
+  g.h = pl.hb ? pl.hb : pl.h;
+  g.h_plane = pl.hb ? pl.hb_plane : pl.T * pl.ldd;
   g.ldh = pl.ldd;
   g.pairs = plane_pairs(pl.planes, pl.planes);
   g.kt = (int32_t)(pl.ldd / 32);

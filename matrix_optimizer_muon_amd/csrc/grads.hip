@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
     const int c = (int)(id - r * per) * 8;
     const int64_t sr = a.gather ? (int64_t)a.gather[r] : r;
     const int left = a.cols - c;
-    gptr<uint16_t> d = glob(a.dst) + r * a.ldd + c;
+    gptr<uint16_t> d = glob(a.dst) + (a.blocked ? ((r >> 4) * (a.ldd >> 5) + (c >> 5)) * 512 + (((c >> 3) & 3) * 16 + (r & 15)) * 8 : r * a.ldd + c);
     float v[8];
     if (a.f32) {
       load8(glob((const float*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
@@ -235,6 +235,14 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
 // ---------------------------------------------------------------------------
 // products on the core
 // ---------------------------------------------------------------------------
+// Swizzle of the 64-byte rows of a row-major stage: 16-byte chunk c of row r sits at
+// chunk c ^ row_swz(r).  A 16-byte LDS read is served 16 lanes at a time, lanes 0–3,
+// 12–15 and 20–27 together (then 4–11, 16–19 and 28–31, and the same 32 lanes on): in
+// the fragments read here (lane l: row l & 15, chunk l >> 4) those are row quads 0 and 3
+// of one chunk and quads 1 and 2 of the next, which this order puts into four different
+// chunks, so all 64 banks serve a step.  (Quad order 0 1 2 3 counts a conflict per read.)
+__device__ __forceinline__ int row_swz(int r) { return (-(r >> 2)) & 3; }
+
 // Small core: 128 × 128 per workgroup of 4 waves, 64 × 64 per wave, for products
 // whose tiles are few or whose K is short.  K is staged through LDS like the step's
 // core does (64-byte rows for row-major operands, 32 k-rows of 256 bytes for K-major
@@ -259,7 +267,7 @@ __device__ __forceinline__ void gemm_small(const Operands& op, char* smem, f32x1
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int row = (wave * 2 + q) * 16 + (lane >> 2);
-    const int c = (lane & 3) ^ ((row >> 2) & 3);
+    const int c = (lane & 3) ^ row_swz(row);
     const int kr = 4 * (wave * 2 + q) + (lane >> 4), un = lane & 15;
     const int lun = (((un >> 1) ^ kmaj_swz(kr)) << 1) | (un & 1);
     offa[q] = TA ? kr * op.lda_b + op.cola_b + lun * 16 : row * op.lda_b + c * 16;
@@ -270,8 +278,8 @@ __device__ __forceinline__ void gemm_small(const Operands& op, char* smem, f32x1
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int ar = wr * 64 + 16 * i + (lane & 15), br = wc * 64 + 16 * i + (lane & 15), c = lane >> 4;
-    fa_off[i] = ar * kRowBytes + ((c ^ ((ar >> 2) & 3)) * 16);
-    fb_off[i] = 128 * kRowBytes + br * kRowBytes + ((c ^ ((br >> 2) & 3)) * 16);
+    fa_off[i] = ar * kRowBytes + ((c ^ row_swz(ar)) * 16);
+    fb_off[i] = 128 * kRowBytes + br * kRowBytes + ((c ^ row_swz(br)) * 16);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int kr = 8 * (lane >> 4) + 4 * t + ((lane & 15) >> 2), sub = 4 * (lane & 3);
@@ -340,44 +348,275 @@ __device__ __forceinline__ void gemm_small(const Operands& op, char* smem, f32x1
   __syncthreads();                                       // LDS is free for the caller
 }
 
-// acc = Σ over the plane pairs of op, whose a and b point at plane 0
-template <typename S, bool TA, bool TB>
-__device__ __forceinline__ void gemm_planes(const Operands& op, int64_t a_plane, int64_t b_plane, const PlanePairs& pp,
-                                            char* smem, f32x16_t (&acc)[S::I][2]) {
-  constexpr bool large = S::I == 4;
-  if constexpr (large) {
-    if (pp.n == 1) {
-      gemm_mainloop<uint16_t, TA, TB>(op, smem, acc);
-      return;
+// ---------------------------------------------------------------------------
+// Large core: 256 × 256 per workgroup of 8 waves, 128 × 64 per wave, 32-deep stages
+// through LDS, one barrier per stage.
+//
+// A wave multiplies the fragments of stage kt, which it read during stage kt − 1, and
+// reads those of stage kt + 1 in between: after the four MFMAs of a row fragment its
+// registers take the next stage's (the four column fragments have a second set).  So no
+// MFMA waits for LDS, and the barrier only orders the copies: before barrier kt every
+// wave has waited for its own share of stage kt + 1; behind it the stage is whole, and
+// stage kt − 1's slot is free (its fragments were multiplied before the barrier) for
+// the copies issued next.
+//
+// An operand is staged in one of three forms, each moved in whole 128-byte lines (the
+// 64-byte pieces of a 32-deep row-major stage cost 2.6 times as much per byte):
+//   kKMajor  k-rows of 512 bytes, four slots of 16 KiB, read with transposing loads;
+//   kRows    row-major, two stages at a time as 128-byte rows: three slots of 32 KiB;
+//   kBlocks  fragment order, blocks of 16 rows × 32 k ([row block][k block][lane][16
+//            bytes], lane l holding row l & 15 and k 8(l >> 4) … + 7): four slots of
+//            16 KiB, contiguous at both ends.
+// Stages past the last are issued with an empty range (no traffic), so that the counts
+// of copies in flight are the same throughout.
+// Measured against the step's core (two barriers per stage, two wave groups in turn) on
+// the products of the cross-entropy gradient at 8192 tokens × 16000 rows × 4096: see
+// k_ce_logits and k_product.
+// ---------------------------------------------------------------------------
+enum StageForm : int { kKMajor = 0, kRows = 1, kBlocks = 2 };
+typedef __attribute__((address_space(3))) char lds_char;
+constexpr int kSlot = kTile * kRowBytes;                // 16 KiB: one operand's stage
+constexpr int form_lds(int form) { return form == kRows ? 6 * kSlot : 4 * kSlot; }
+
+struct Side {
+  const char* p;                // kKMajor: k-row 0; kRows: first row of the tile; kBlocks: the tile's first block
+  int64_t pitch;                // bytes between k-rows, rows, or row blocks
+  int64_t extent;               // kKMajor: k-rows; kRows: rows from the tile's first; kBlocks: bytes from p
+  int col_b;                    // kKMajor: byte of the tile's first column in a k-row
+};
+
+// the copies of one operand and its fragments in LDS; N fragments of 16 rows per wave
+template <int FORM, int N>
+struct Stager {
+  Side s;
+  lds_char* lds;                                         // the operand's ring
+  int off[FORM == kRows ? 4 : 2];
+  int frag[FORM == kKMajor ? N : 2];                     // see read()
+  __amdgpu_buffer_rsrc_t whole;                          // kRows
+  int wave, lane;
+
+  __device__ __forceinline__ Stager(const Side& side, char* ring, int first) : s(side), lds((lds_char*)ring) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (FORM == kKMajor) {
+      const int ld = (int)s.pitch;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int kr = 2 * (wave * 2 + q) + (lane >> 5), un = lane & 31;
+        const int lun = (((un >> 1) ^ kmaj_swz(kr)) << 1) | (un & 1);
+        off[q] = kr * ld + s.col_b + lun * 16;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {                      // k-rows kr and kr + 4 share the swizzle
+        const int kr = 8 * (lane >> 4) + ((lane & 15) >> 2);
+        const int n = first + 16 * i + 4 * (lane & 3);
+        frag[i] = kr * 512 + (((n >> 4) ^ kmaj_swz(kr)) << 5) + ((2 * n) & 31);
+      }
+    } else if constexpr (FORM == kRows) {
+      // 8 rows of 128 bytes per instruction; 16-byte chunk c of row r at chunk
+      // c ^ ((r >> 1) & 7): the 16 lanes a 16-byte read serves together (see row_swz)
+      // then fall on 16 different chunks of the two row parities
+      const int ld = (int)s.pitch;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = (wave * 4 + q) * 8 + (lane >> 3);
+        off[q] = row * ld + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+      }
+      const int rows = (int)(s.extent < kTile ? s.extent : kTile);
+      whole = range_rsrc(s.p, (int64_t)rows * s.pitch);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = first + (lane & 15);
+        frag[h] = row * 128 + (((4 * h + (lane >> 4)) ^ ((row >> 1) & 7)) << 4);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) off[q] = lane * 16;
+      frag[0] = (first >> 4) * 1024 + lane * 16;
+      frag[1] = 0;
     }
   }
+  // LDS byte of stage kt's slot
+  __device__ __forceinline__ lds_char* slot(int kt) const {
+    if constexpr (FORM == kRows) return lds + (kt >> 1) % 3 * (2 * kSlot);
+    return lds + (kt & 3) * kSlot;
+  }
+  // copies into a slot: kKMajor and kBlocks two (every stage), kRows four (even stages only)
+  __device__ __forceinline__ void issue(lds_char* base, int kt, bool live) const {
+    typedef __attribute__((address_space(3))) void lds_void;
+    if constexpr (FORM == kRows) {
+      __amdgpu_buffer_rsrc_t r = whole;
+      if (!live) r = range_rsrc(nullptr, 0);
 #pragma unroll
-  for (int i = 0; i < S::I; ++i)
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + (wave * 4 + q) * 1024), 16, off[q] + kt * 64, 0, 0, 0);
+    } else if constexpr (FORM == kKMajor) {
+      int left = (int)s.extent - 32 * kt;
+      left = !live || left < 0 ? 0 : (left < 32 ? left : 32);
+      const __amdgpu_buffer_rsrc_t r = range_rsrc(s.p + (int64_t)kt * 32 * s.pitch, (int64_t)left * s.pitch);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + (wave * 2 + q) * 1024), 16, off[q], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t at = (wave * 2 + q) * s.pitch + (int64_t)kt * 1024;
+        const bool in = live && at + 1024 <= s.extent;
+        const __amdgpu_buffer_rsrc_t r = range_rsrc(in ? s.p + at : nullptr, 1024);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + (wave * 2 + q) * 1024), 16, off[q], 0, 0, 0);
+      }
+    }
+  }
+  // fragment I of a stage; half: which 64 bytes of a kRows row
+  template <int I>
+  __device__ __forceinline__ u32x4_t read(const lds_char* base, int half) const {
+    typedef const __attribute__((address_space(3))) u32x4_t lds_u32x4;
+    typedef __attribute__((address_space(3))) v4i16_t lds_v4i16;
+    if constexpr (FORM == kKMajor) {
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(base + frag[I]));
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(base + frag[I] + 4 * 512));
+      u32x4_t r;
+      r.x = (uint32_t)(uint16_t)lo.x | ((uint32_t)(uint16_t)lo.y << 16);
+      r.y = (uint32_t)(uint16_t)lo.z | ((uint32_t)(uint16_t)lo.w << 16);
+      r.z = (uint32_t)(uint16_t)hi.x | ((uint32_t)(uint16_t)hi.y << 16);
+      r.w = (uint32_t)(uint16_t)hi.z | ((uint32_t)(uint16_t)hi.w << 16);
+      return r;
+    } else if constexpr (FORM == kRows) {
+      return *(lds_u32x4*)(base + frag[half] + I * (16 * 128));
+    } else {
+      return *(lds_u32x4*)(base + frag[0] + I * 1024);
+    }
+  }
+};
+
+// One stage: copies into wa, wb and wr (a row-major operand's pair), the MFMAs on
+// fa / cur, and the next stage's fragments from na and nb.  The slots read and the slots
+// written are different ones; `restrict` tells the compiler, which would otherwise wait
+// for every copy in flight before a transposing read.
+template <int FA, int FB, bool EVEN>
+__device__ __forceinline__ void large_stage(const Stager<FA, 8>& a, const Stager<FB, 4>& b, const lds_char* __restrict__ na,
+                                            const lds_char* __restrict__ nb, lds_char* __restrict__ wa,
+                                            lds_char* __restrict__ wb, int kt, int KT, u32x4_t (&fa)[8], u32x4_t (&cur)[4],
+                                            u32x4_t (&nxt)[4], f32x16_t (&acc)[4][2]) {
+  // the copies after barrier kt: one stage (kt + 3) of the four-slot operands, then, at
+  // even kt, two stages (kt + 4, kt + 5) of the row-major one
+  if constexpr (FA != kRows) a.issue(wa, kt + 3, kt + 3 < KT);
+  if constexpr (FB != kRows) b.issue(wb, kt + 3, kt + 3 < KT);
+  if constexpr (EVEN && FA == kRows) a.issue(wa, kt + 4, kt + 4 < KT);
+  if constexpr (EVEN && FB == kRows) b.issue(wb, kt + 4, kt + 4 < KT);
+  __builtin_amdgcn_sched_barrier(0);
+  static_for<8>([&](auto Sq) {
+    constexpr int qs = decltype(Sq)::value;
+    static_for<4>([&](auto Tq) {
+      constexpr int qt = decltype(Tq)::value;
+      mfma_quarter<2 * (qs & 1) + (qt & 1)>(acc[qs >> 1][qt >> 1], fa[qs], cur[qt]);
+    });
+    fa[qs] = a.template read<qs>(na, EVEN ? 1 : 0);
+    if constexpr ((qs & 1) == 0) nxt[qs / 2] = b.template read<qs / 2>(nb, EVEN ? 1 : 0);
+    __builtin_amdgcn_sched_barrier(0);
+  });
+}
+
+// acc (quarter layout) += Σ over KT stages; FA and FB not both kRows (LDS)
+template <int FA, int FB>
+__device__ __forceinline__ void gemm_large(const Side& sa, const Side& sb, int KT, char* smem, f32x16_t (&acc)[4][2]) {
+  static_assert(!(FA == kRows && FB == kRows), "two row-major operands do not fit the LDS");
+  if (KT <= 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Stager<FA, 8> a(sa, smem, (wave >> 2) * 128);
+  const Stager<FB, 4> b(sb, smem + form_lds(FA), (wave & 3) * 64);
+  constexpr bool rows = FA == kRows || FB == kRows;
+  // in flight when stage kt + 1 has landed: without a row-major operand the four copies
+  // of one stage; with one, two of a four-slot stage and four of a row-major pair
+  constexpr int kInFlight = rows ? 6 : 4;
+  if constexpr (FA == kRows) a.issue(a.slot(0), 0, true);
+  if constexpr (FB == kRows) b.issue(b.slot(0), 0, true);
+  for (int st = 0; st < 3; ++st) {
+    if (st == 2) {
+      if constexpr (FA == kRows) a.issue(a.slot(2), 2, 2 < KT);
+      if constexpr (FB == kRows) b.issue(b.slot(2), 2, 2 < KT);
+    }
+    if constexpr (FA != kRows) a.issue(a.slot(st), st, st < KT);
+    if constexpr (FB != kRows) b.issue(b.slot(st), st, st < KT);
+  }
+  DMUON_WAIT_VM(8);                                      // own share of stage 0: 8 of the copies above come after it
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  u32x4_t fa[8], f0[4], f1[4];
+  static_for<8>([&](auto I) { fa[decltype(I)::value] = a.template read<decltype(I)::value>(a.slot(0), 0); });
+  static_for<4>([&](auto I) { f0[decltype(I)::value] = b.template read<decltype(I)::value>(b.slot(0), 0); });
+  auto stage = [&](auto Even, int kt) {
+    DMUON_WAIT_VM(kInFlight);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    large_stage<FA, FB, decltype(Even)::value>(a, b, a.slot(kt + 1), b.slot(kt + 1), a.slot(FA == kRows ? kt + 4 : kt + 3),
+                                               b.slot(FB == kRows ? kt + 4 : kt + 3), kt, KT, fa,
+                                               decltype(Even)::value ? f0 : f1, decltype(Even)::value ? f1 : f0, acc);
+  };
+  int kt = 0;
+#pragma unroll 1
+  for (; kt + 1 < KT; kt += 2) {
+    stage(std::true_type{}, kt);
+    stage(std::false_type{}, kt + 1);
+  }
+  if (kt < KT) stage(std::true_type{}, kt);
+  DMUON_WAIT_VM(0);                                      // the empty copies past the last stage write LDS too
+  __syncthreads();
+}
+
+template <int I>
+__device__ __forceinline__ void zero_acc(f32x16_t (&acc)[I][2]) {
+#pragma unroll
+  for (int i = 0; i < I; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+}
+
+// acc = Σ over the plane pairs of the operands, given at plane 0 (planes in elements)
+template <bool TA, bool TB>
+__device__ __forceinline__ void small_planes(const Operands& op, int64_t a_plane, int64_t b_plane, const PlanePairs& pp,
+                                             char* smem, f32x16_t (&acc)[2][2]) {
+  zero_acc(acc);
 #pragma unroll 1
   for (int p = 0; p < pp.n; ++p) {
     Operands o = op;
     o.a += (int64_t)((pp.a >> (4 * p)) & 15) * a_plane * 2;
     o.b += (int64_t)((pp.b >> (4 * p)) & 15) * b_plane * 2;
-    if constexpr (large) gemm_mainloop<uint16_t, TA, TB, 0, 1>(o, smem, acc);
-    else gemm_small<TA, TB>(o, smem, acc);
+    gemm_small<TA, TB>(o, smem, acc);
   }
 #pragma unroll
-  for (int i = 0; i < S::I; ++i)
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) quarters_to_32x32(acc[i][j]);
+}
+template <int FA, int FB>
+__device__ __forceinline__ void large_planes(const Side& sa, const Side& sb, int KT, int64_t a_plane, int64_t b_plane,
+                                             const PlanePairs& pp, char* smem, f32x16_t (&acc)[4][2]) {
+  zero_acc(acc);
+#pragma unroll 1
+  for (int p = 0; p < pp.n; ++p) {
+    Side x = sa, y = sb;
+    x.p += (int64_t)((pp.a >> (4 * p)) & 15) * a_plane * 2;
+    y.p += (int64_t)((pp.b >> (4 * p)) & 15) * b_plane * 2;
+    gemm_large<FA, FB>(x, y, KT, smem, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) quarters_to_32x32(acc[i][j]);
 }
 
 // Tile shapes.  A workgroup computes rows (A's side) × columns (B's side) of a
 // product; a wave holds 32·I rows and 64 columns as I × 2 blocks of 32 × 32.
-//   Large: the step's core, 256 × 256 on 8 waves, one workgroup per CU;
+//   Large: 256 × 256 on 8 waves (gemm_large), one workgroup per CU;
 //   Small: 128 × 128 on 4 waves (gemm_small), three workgroups per CU.
 struct Large {
   static constexpr int I = 4, WC = 4;                    // row blocks per wave, waves along the columns
-  static constexpr int M = 256, N = 256, Threads = 512, Lds = kGemmLds;
+  static constexpr int M = 256, N = 256, Threads = 512, Lds = form_lds(kRows) + form_lds(kBlocks);   // 160 KiB
 };
 struct Small {
   static constexpr int I = 2, WC = 2;
@@ -491,17 +730,25 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   const int count = *g.count;
   const int row0 = tv * S::M, col0 = tt * S::N;   // vocabulary (in the piece), tokens
   if (col0 >= count) return;
-  Operands op;
-  op.a = (const char*)(g.w + (int64_t)row0 * g.ldw);
-  op.b = (const char*)(g.h + (int64_t)col0 * g.ldh);
-  op.lda_b = (int)(g.ldw * 2);
-  op.ldb_b = (int)(g.ldh * 2);
-  op.rows_a = g.vrows - row0;
-  op.rows_b = count - col0;
-  op.cola_b = op.colb_b = 0;
-  op.ktiles = g.kt;
   f32x16_t acc[S::I][2];
-  gemm_planes<S, false, false>(op, g.w_plane, g.h_plane, g.pairs, smem, acc);
+  const char* wp = (const char*)(g.w + (int64_t)row0 * g.ldw);
+  if constexpr (S::I == 4) {
+    const int64_t at = (int64_t)(col0 / 16) * (g.ldh / 32) * 1024;       // H is in fragment order
+    const Side sa = {wp, g.ldw * 2, g.vrows - row0, 0};
+    const Side sb = {(const char*)g.h + at, (g.ldh / 32) * 1024, g.h_plane * 2 - at, 0};
+    large_planes<kRows, kBlocks>(sa, sb, g.kt, g.w_plane, g.h_plane, g.pairs, smem, acc);
+  } else {
+    Operands op;
+    op.a = wp;
+    op.b = (const char*)(g.h + (int64_t)col0 * g.ldh);
+    op.lda_b = (int)(g.ldw * 2);
+    op.ldb_b = (int)(g.ldh * 2);
+    op.rows_a = g.vrows - row0;
+    op.rows_b = count - col0;
+    op.cola_b = op.colb_b = 0;
+    op.ktiles = g.kt;
+    small_planes<false, false>(op, g.w_plane, g.h_plane, g.pairs, smem, acc);
+  }
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
@@ -666,30 +913,33 @@ __global__ __launch_bounds__(S::Threads) void k_product(ProductArgs g) {
     k1 = b < k0 ? k0 : (b < g.k ? b : g.k);
   }
   if (row0 >= rows) return;
-  if (g.splits > 1) {                    // whole stages per split
-    const int64_t st = (k1 - k0 + 31) / 32, per = (st + g.splits - 1) / g.splits;
-    const int64_t lo = k0 + per * split * 32, hi = lo + per * 32;
+  if (g.splits > 1) {                    // whole pairs of stages per split
+    const int64_t st = (k1 - k0 + 63) / 64, per = (st + g.splits - 1) / g.splits;
+    const int64_t lo = k0 + per * split * 64, hi = lo + per * 64;
     k1 = hi < k1 ? hi : k1;
     k0 = lo < k1 ? lo : k1;
   }
-  Operands op;
-  op.a = (const char*)(g.a + k0 * g.lda);
-  op.lda_b = (int)(g.lda * 2);
-  op.rows_a = (int)(k1 - k0);
-  op.cola_b = col0 * 2;
-  op.ldb_b = (int)(g.ldb * 2);
-  if (TB) {
-    op.b = (const char*)(g.b + k0 * g.ldb);
-    op.rows_b = (int)(k1 - k0);
-    op.colb_b = row0 * 2;
-  } else {
-    op.b = (const char*)(g.b + (int64_t)row0 * g.ldb + k0);
-    op.rows_b = rows - row0;
-    op.colb_b = 0;
-  }
-  op.ktiles = (int)((k1 - k0 + 31) / 32);
   f32x16_t acc[S::I][2];
-  gemm_planes<S, true, TB>(op, g.a_plane, g.b_plane, g.pairs, smem, acc);
+  const int kt = (int)((k1 - k0 + 31) / 32);
+  const char* ap = (const char*)(g.a + k0 * g.lda);
+  const char* bp = (const char*)(TB ? g.b + k0 * g.ldb : g.b + (int64_t)row0 * g.ldb + k0);
+  if constexpr (S::I == 4) {
+    const Side sa = {ap, g.lda * 2, k1 - k0, col0 * 2};
+    const Side sb = {bp, g.ldb * 2, TB ? k1 - k0 : (int64_t)(rows - row0), row0 * 2};
+    large_planes<kKMajor, TB ? kKMajor : kRows>(sa, sb, kt, g.a_plane, g.b_plane, g.pairs, smem, acc);
+  } else {
+    Operands op;
+    op.a = ap;
+    op.b = bp;
+    op.lda_b = (int)(g.lda * 2);
+    op.ldb_b = (int)(g.ldb * 2);
+    op.rows_a = (int)(k1 - k0);
+    op.rows_b = TB ? (int)(k1 - k0) : rows - row0;
+    op.cola_b = col0 * 2;
+    op.colb_b = TB ? row0 * 2 : 0;
+    op.ktiles = kt;
+    small_planes<true, TB>(op, g.a_plane, g.b_plane, g.pairs, smem, acc);
+  }
 
   if (g.part) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -39,6 +39,7 @@ struct PackArgs {
   uint16_t* dst;               // [plane][rows][ldd], columns cols … ldd − 1 zero
   int64_t plane;               // elements between planes
   int32_t ldd;                 // multiple of 64
+  int32_t blocked;             // 1: fragment order (rows padded to 16), 0: row-major
 };
 
 // ---- cross entropy ------------------------------------------------------------
