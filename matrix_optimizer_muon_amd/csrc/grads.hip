@@ -441,15 +441,17 @@ struct Stager {
     if constexpr (FORM == kRows) return lds + (kt >> 1) % 3 * (2 * kSlot);
     return lds + (kt & 3) * kSlot;
   }
-  // copies into a slot: kKMajor and kBlocks two (every stage), kRows four (even stages only)
-  __device__ __forceinline__ void issue(lds_char* base, int kt, bool live) const {
+  // two copies into a slot: a stage of kKMajor and kBlocks, one half of the rows of a
+  // pair of stages (the pair of the even stage kt) of kRows
+  __device__ __forceinline__ void issue(lds_char* base, int kt, bool live, int half = 0) const {
     typedef __attribute__((address_space(3))) void lds_void;
     if constexpr (FORM == kRows) {
       __amdgpu_buffer_rsrc_t r = whole;
       if (!live) r = range_rsrc(nullptr, 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + (wave * 4 + q) * 1024), 16, off[q] + kt * 64, 0, 0, 0);
+      for (int q = 0; q < 2; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + (wave * 4 + 2 * half + q) * 1024), 16,
+                                                 (half ? off[2 + q] : off[q]) + kt * 64, 0, 0, 0);
     } else if constexpr (FORM == kKMajor) {
       int left = (int)s.extent - 32 * kt;
       left = !live || left < 0 ? 0 : (left < 32 ? left : 32);
@@ -498,12 +500,13 @@ __device__ __forceinline__ void large_stage(const Stager<FA, 8>& a, const Stager
                                             const lds_char* __restrict__ nb, lds_char* __restrict__ wa,
                                             lds_char* __restrict__ wb, int kt, int KT, u32x4_t (&fa)[8], u32x4_t (&cur)[4],
                                             u32x4_t (&nxt)[4], f32x16_t (&acc)[4][2]) {
-  // the copies after barrier kt: one stage (kt + 3) of the four-slot operands, then, at
-  // even kt, two stages (kt + 4, kt + 5) of the row-major one
-  if constexpr (FA != kRows) a.issue(wa, kt + 3, kt + 3 < KT);
-  if constexpr (FB != kRows) b.issue(wb, kt + 3, kt + 3 < KT);
-  if constexpr (EVEN && FA == kRows) a.issue(wa, kt + 4, kt + 4 < KT);
-  if constexpr (EVEN && FB == kRows) b.issue(wb, kt + 4, kt + 4 < KT);
+  // the copies after barrier kt: one stage (kt + 3) of the four-slot operands, half of a
+  // pair (first the one of kt + 4, at odd kt the rest of it) of the row-major one
+  constexpr int pair = EVEN ? 4 : 3, half = EVEN ? 0 : 1;
+  if constexpr (FA == kRows) a.issue(wa, kt + pair, kt + pair < KT, half);
+  else a.issue(wa, kt + 3, kt + 3 < KT);
+  if constexpr (FB == kRows) b.issue(wb, kt + pair, kt + pair < KT, half);
+  else b.issue(wb, kt + 3, kt + 3 < KT);
   __builtin_amdgcn_sched_barrier(0);
   static_for<8>([&](auto Sq) {
     constexpr int qs = decltype(Sq)::value;
@@ -525,19 +528,21 @@ __device__ __forceinline__ void gemm_large(const Side& sa, const Side& sb, int K
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Stager<FA, 8> a(sa, smem, (wave >> 2) * 128);
   const Stager<FB, 4> b(sb, smem + form_lds(FA), (wave & 3) * 64);
-  constexpr bool rows = FA == kRows || FB == kRows;
-  // in flight when stage kt + 1 has landed: without a row-major operand the four copies
-  // of one stage; with one, two of a four-slot stage and four of a row-major pair
-  constexpr int kInFlight = rows ? 6 : 4;
-  if constexpr (FA == kRows) a.issue(a.slot(0), 0, true);
-  if constexpr (FB == kRows) b.issue(b.slot(0), 0, true);
+  // prologue: stages 0 to 2 (of a row-major operand the pairs 0, 1 and 2, 3), the order of
+  // the loop: 12 copies (stage 0 whole after the first 4 to 6, 8 or 6 behind it)
+  if constexpr (FA == kRows) { a.issue(a.slot(0), 0, true, 0); a.issue(a.slot(0), 0, true, 1); }
+  if constexpr (FB == kRows) { b.issue(b.slot(0), 0, true, 0); b.issue(b.slot(0), 0, true, 1); }
   for (int st = 0; st < 3; ++st) {
-    if (st == 2) {
-      if constexpr (FA == kRows) a.issue(a.slot(2), 2, 2 < KT);
-      if constexpr (FB == kRows) b.issue(b.slot(2), 2, 2 < KT);
-    }
     if constexpr (FA != kRows) a.issue(a.slot(st), st, st < KT);
     if constexpr (FB != kRows) b.issue(b.slot(st), st, st < KT);
+    if (st == 1) {
+      if constexpr (FA == kRows) a.issue(a.slot(2), 2, 2 < KT, 0);
+      if constexpr (FB == kRows) b.issue(b.slot(2), 2, 2 < KT, 0);
+    }
+    if (st == 2) {
+      if constexpr (FA == kRows) a.issue(a.slot(2), 2, 2 < KT, 1);
+      if constexpr (FB == kRows) b.issue(b.slot(2), 2, 2 < KT, 1);
+    }
   }
   DMUON_WAIT_VM(8);                                      // own share of stage 0: 8 of the copies above come after it
   __builtin_amdgcn_sched_barrier(0);
@@ -547,7 +552,7 @@ __device__ __forceinline__ void gemm_large(const Side& sa, const Side& sb, int K
   static_for<8>([&](auto I) { fa[decltype(I)::value] = a.template read<decltype(I)::value>(a.slot(0), 0); });
   static_for<4>([&](auto I) { f0[decltype(I)::value] = b.template read<decltype(I)::value>(b.slot(0), 0); });
   auto stage = [&](auto Even, int kt) {
-    DMUON_WAIT_VM(kInFlight);
+    DMUON_WAIT_VM(4);                                    // all but the last stage's copies: stage kt + 1 has landed
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
