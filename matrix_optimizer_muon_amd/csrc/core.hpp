@@ -214,10 +214,7 @@ struct DiagTerm {
   uint32_t a1, a2;   // bf16 bit patterns of α1, α2
 };
 
-// PART 1: the call adds to the accumulators as they are and leaves them in the
-// quarter layout, for a sum of several products (see gemm_planes of the training
-// gradients); 0: it starts from zero and ends in the 32×32 layout.
-template <typename T, bool TA = false, bool TB = false, int DIAG = 0, int PART = 0>
+template <typename T, bool TA = false, bool TB = false, int DIAG = 0>
 __device__ __forceinline__ void gemm_mainloop(const Operands& op, char* smem, f32x16_t (&acc)[4][2],
                                               const DiagTerm& dg = DiagTerm{0, 0u, 0u}) {
   static_assert(!(TA || TB) || sizeof(T) == 2, "K-major operands are bf16");
@@ -291,14 +288,12 @@ __device__ __forceinline__ void gemm_mainloop(const Operands& op, char* smem, f3
         }
       }
     }
-  if constexpr (PART == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  }
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   u32x4_t fa[2][4], fb[2][2];     // all fragments of one stage
   // K-major operands take a range per stage: exactly its 32 k-rows (fewer at the
@@ -482,7 +477,7 @@ __device__ __forceinline__ void gemm_mainloop(const Operands& op, char* smem, f3
     for (int kt = kb + nb < KT ? kb + nb : KT; kt < KT; ++kt) step(kt);
   }
   if (lead) __builtin_amdgcn_s_barrier();              // every wave passes 2·KT + 2 barriers
-  if constexpr (kQ && PART == 0) {
+  if constexpr (kQ) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -564,14 +559,17 @@ __device__ __forceinline__ void tri_tile(int u, int T, int& ti, int& tj) {
 // Runs of 64 suit the apply (two rounds of 8 × 4 tiles per XCD); the Gram and
 // the square (triangle tiles in bands of 4) measured faster with runs of 16.
 template <int RUN>
-__device__ __forceinline__ int xcd_logical_block() {
-  const int G = gridDim.x, b = blockIdx.x;
+__device__ __forceinline__ int xcd_logical_block(int b, int G) {
   constexpr int win = 8 * RUN;
   const int w = b / win;
   const int xcd = b & 7, slot = (b >> 3) - w * RUN;
   if ((w + 1) * win <= G) return w * win + xcd * RUN + slot;
   const int R = G - w * win, per = R >> 3, rem = R & 7;
   return w * win + (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + slot;
+}
+template <int RUN>
+__device__ __forceinline__ int xcd_logical_block() {
+  return xcd_logical_block<RUN>(blockIdx.x, gridDim.x);
 }
 
 }  // namespace dmuon

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <exception>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -79,16 +80,50 @@ struct Carver {
   }
 };
 
-// K splits of a product with few tiles, so that all 256 CUs have work: whole
-// stages of 32, at least 8 of them per workgroup
-int pick_splits(int64_t tiles, int tile, int64_t k) {
-  const int64_t stages = cdiv(k, 32), fill = tile == kTile ? 256 : 768;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(fill / std::max<int64_t>(tiles, 1), stages / 8));
+// Edge of a product's tiles and the K splits that share a tile's sum.
+struct Shape {
+  int tile, splits;
+};
+
+// rows × cols outputs, K of k and `pairs` plane products, `groups` of them.  The
+// large core (256², one workgroup per CU) does four times the work of the small
+// one (128², three per CU) in the same stage of 32 and loses only where there is
+// too little work to fill the CUs: it is taken from 14 of its stages per CU on.
+// Measured, checkpoint weight gradients [n, k] over T tokens, small against large,
+// each with its best split: 512² over 8192 (4 stages) 35.0 and 38.0 µs, 1536² over
+// 2048 (9) 40.0 and 41.0, 1024² over 8192 (16) 50.0 and 48.8, 2048² over 2048 (16)
+// 49.2 and 46.5, 4096×3584 over 512 (14) 39.0 and 30.8, 2048×1024 over 32768 (128)
+// 217 and 146, 4096² over 32768 1986 and 904.
+// The splits take the least of: rounds of workgroups × (stages of each + 6 for its
+// fill, drain and stores), plus the partial sums' way through memory and the join.
+// Measured, large, 2048² over 8192 tokens: 1, 2, 3, 4 and 8 splits take 152, 115,
+// 95, 88 and 109 µs; 2048×1024 over 32768: 4, 6, 8, 12 and 16 take 168, 165, 146,
+// 185 and 168.
+Shape pick_shape(int64_t rows, int64_t cols, int64_t k, int64_t pairs, int64_t groups) {
+  const int64_t stages = std::max<int64_t>(cdiv(k, 32), 1);
+  const bool large = cdiv(rows, 256) * cdiv(cols, 256) * groups * stages * pairs >= 14 * 256;
+  const int64_t tile = large ? 256 : 128, slots = large ? 256 : 512;
+  const int64_t tiles = std::max<int64_t>(cdiv(rows, tile) * cdiv(cols, tile) * groups, 1);
+  const double part = large ? 0.09 : 0.033;            // one partial tile, in stages
+  int best = 1;
+  double least = 0;
+  for (int64_t s = 1; s <= 64 && (s == 1 || (stages * pairs >= 8 * s && stages >= 2 * s && tiles * s <= 4 * slots)); ++s) {
+    const double cost = (double)cdiv(tiles * s, slots) * (double)(cdiv(stages, s) * pairs + 6) +
+                        (s > 1 ? 10 + part * (double)(tiles * s) : 0);
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = (int)s;
+    }
+  }
+  return {(int)tile, best};
 }
 
-// Edge of the product tiles: 256 (the step's core) or 128 (the small core).
-int pick_tile(int64_t rows, int64_t cols, int64_t k) {
-  return cdiv(rows, 256) * cdiv(cols, 256) < 256 || k < 1024 ? 128 : 256;
+// Edge of the logits' tiles, which have no splits.  Measured, forward over D
+// columns, small against large: 128 large tiles, D 1024 37.4 and 48.5 µs, D 4096 92
+// and 116; 256 large tiles, D 256 33.2 and 35.8, D 768 49.0 and 45.4, D 4096 165
+// and 131; 2048 large tiles, D 512 172 and 183, D 1024 306 and 273, D 4096 1284 and 883.
+int pick_logits_tile(int64_t tokens, int64_t vocab, int64_t k) {
+  return cdiv(tokens, 256) * cdiv(vocab, 256) >= 192 && k >= 768 ? 256 : 128;
 }
 
 // May the core read this bf16 matrix K-major in place?  16-byte rows, and no tile
@@ -106,8 +141,9 @@ struct CePlan {
   bool f32, direct_w;
   int planes;
   int64_t T, D, V, ldd, piece, ldz;
-  int tile_z, tile_h, tile_w;            // tile edges: logits, hidden-state and weight gradient
-  int tiles_v, splits_h, splits_w;
+  int tile_z, tiles_v;                   // logits
+  Shape sh, sw;                          // hidden-state and weight gradient
+  RowSpread spread;                      // of the hidden states' gradient
   // workspace
   int32_t *rows, *pos, *tgt, *count;
   float *clse, *cg, *gmax, *zt, *part_h, *part_w;
@@ -129,23 +165,29 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   // the piece: gradient logits of every token (backward) and the copy of W's rows
   const int64_t per_row = (backward ? pl.T * 2 * pl.planes : 0) + (pl.direct_w ? 0 : pl.ldd * 2 * pl.planes);
   int64_t piece = per_row ? std::max<int64_t>(kPieceBytes / per_row, 8 * kTile) : pl.V;
-  const int64_t n = cdiv(pl.V, std::min(piece, pl.V));
-  pl.piece = std::min(round_up(cdiv(pl.V, n), kTile), round_up(pl.V, kTile));
+  // equal pieces; where several fill the limit, of as many tile rows as make whole
+  // rounds of the weight gradient's tiles over the CUs
+  const int64_t n = cdiv(pl.V, std::min(piece, pl.V)), tiles_d = cdiv(pl.D, kTile);
+  pl.piece = round_up(cdiv(pl.V, n), kTile);
+  const int64_t whole = round_up(pl.piece, 256 / std::gcd(tiles_d, (int64_t)256) * kTile);
+  if (n > 1 && backward && whole <= piece) pl.piece = whole;
   pl.ldz = round_up(std::min(pl.piece, pl.V), kLdAlign);
   const int64_t piece_rows = std::min(pl.piece, pl.V);
-  pl.tile_z = pick_tile(pl.T, piece_rows, pl.ldd * (pl.f32 ? 6 : 1));
-  pl.tile_h = pick_tile(pl.T, pl.D, piece_rows);
-  pl.tile_w = pick_tile(piece_rows, pl.D, pl.T);
+  const int pairs = pl.f32 ? plane_pairs(pl.planes, pl.planes).n : 1;
+  pl.tile_z = pick_logits_tile(pl.T, piece_rows, pl.ldd * pairs);
   pl.tiles_v = (int)cdiv(pl.V, pl.tile_z);
-  pl.splits_h = pick_splits(cdiv(pl.T, pl.tile_h) * cdiv(pl.D, pl.tile_h), pl.tile_h, piece_rows);
-  pl.splits_w = pick_splits(cdiv(piece_rows, pl.tile_w) * cdiv(pl.D, pl.tile_w), pl.tile_w, pl.T);
+  pl.sh = pick_shape(pl.T, pl.D, piece_rows, pairs, 1);
+  const int64_t most = std::min<int64_t>(64, cdiv(piece_rows, 32) * pairs / 8);
+  pl.spread = {(int32_t)pl.T, (int32_t)cdiv(pl.T, pl.sh.tile), pl.sh.tile, pl.sh.splits, std::max(pl.sh.splits, (int32_t)most)};
+  pl.sw = pick_shape(piece_rows, pl.D, pl.T, pairs, 1);
   Carver c{base};
   pl.rows = c.take<int32_t>(pl.T);
   pl.tgt = c.take<int32_t>(pl.T);
   pl.count = c.take<int32_t>(1);
-  pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
+  // hidden states: the large logits read fragment order, the rest rows
   pl.hb_plane = round_up(pl.T, 16) * pl.ldd;
   if (pl.tile_z == kTile) pl.hb = c.take<uint16_t>(pl.planes * pl.hb_plane);
+  if (pl.tile_z != kTile || backward) pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
   if (!pl.direct_w) pl.w = c.take<uint16_t>(pl.planes * piece_rows * pl.ldd);
   if (backward) {
     pl.pos = c.take<int32_t>(pl.T);
@@ -153,8 +195,8 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
     pl.cg = c.take<float>(pl.T);
     pl.gmax = c.take<float>(1);
     pl.dz = c.take<uint16_t>(pl.planes * pl.T * pl.ldz);
-    pl.part_h = c.take<float>(pl.splits_h * pl.T * pl.ldd);
-    if (pl.splits_w > 1) pl.part_w = c.take<float>(pl.splits_w * piece_rows * pl.ldd);
+    pl.part_h = c.take<float>(pl.sh.splits * pl.T * pl.ldd);
+    if (pl.sw.splits > 1) pl.part_w = c.take<float>(pl.sw.splits * piece_rows * pl.ldd);
   } else {
     pl.zt = c.take<float>(pl.T);
     pl.stats = c.take<CeStat>((int64_t)pl.tiles_v * pl.T);
@@ -217,14 +259,9 @@ int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const f
   a.count = pl.count;
   a.dst = pl.h;
   a.plane = pl.T * pl.ldd;
+  a.blocks = pl.hb;
+  a.blocks_plane = pl.hb_plane;
   a.ldd = (int32_t)pl.ldd;
-  if (pl.hb) {
-    PackArgs b = a;
-    b.dst = pl.hb;
-    b.plane = pl.hb_plane;
-    b.blocked = 1;
-    if ((e = go(env, PH_CE_PACK, stream, [&] { return launch_pack(b, PH_CE_PACK, stream); }))) return e;
-  }
   return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
 }
 
@@ -257,8 +294,8 @@ CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64
   g.w = w;
   g.w_plane = w_plane;
   g.ldw = ldw;
-  g.h = pl.hb ? pl.hb : pl.h;
-  g.h_plane = pl.hb ? pl.hb_plane : pl.T * pl.ldd;
+  g.h = pl.tile_z == kTile ? pl.hb : pl.h;
+  g.h_plane = pl.tile_z == kTile ? pl.hb_plane : pl.T * pl.ldd;
   g.ldh = pl.ldd;
   g.pairs = plane_pairs(pl.planes, pl.planes);
   g.kt = (int32_t)(pl.ldd / 32);
@@ -287,7 +324,8 @@ int fill_zero(void* out, int32_t dtype, int64_t rows, int64_t cols, int phase, c
 // ---- weight gradient from a checkpoint ------------------------------------------
 struct WgradPlan {
   bool direct_g;
-  int planes, splits, tile;
+  int planes;
+  Shape shape;
   int64_t ldn, ldk, tiles_r, tiles_c;
   uint16_t *x, *g;
   float* part;
@@ -301,14 +339,13 @@ WgradPlan wgrad_plan(const dmuon_ckpt8_wgrad_problem& p, char* base) {
   pl.ldn = round_up(p.n, kLdAlign);
   pl.ldk = round_up(p.k, kLdAlign);
   const int64_t groups = p.offsets ? p.groups : 1, k = p.tokens / std::max<int64_t>(groups, 1);
-  pl.tile = pick_tile(p.n, p.k, k);
-  pl.tiles_r = cdiv(p.n, pl.tile);
-  pl.tiles_c = cdiv(p.k, pl.tile);
-  pl.splits = pick_splits(pl.tiles_r * pl.tiles_c * groups, pl.tile, k);
+  pl.shape = pick_shape(p.n, p.k, k, plane_pairs(1, pl.planes).n, groups);
+  pl.tiles_r = cdiv(p.n, pl.shape.tile);
+  pl.tiles_c = cdiv(p.k, pl.shape.tile);
   Carver c{base};
   pl.x = c.take<uint16_t>(p.tokens * pl.ldk);
   if (!pl.direct_g) pl.g = c.take<uint16_t>(pl.planes * p.tokens * pl.ldn);
-  if (pl.splits > 1) pl.part = c.take<float>(pl.splits * groups * p.n * pl.ldk);
+  if (pl.shape.splits > 1) pl.part = c.take<float>(pl.shape.splits * groups * p.n * pl.ldk);
   pl.bytes = c.off;
   return pl;
 }
@@ -495,10 +532,10 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
         q.k = pl.T;
         q.count = pl.count;
         q.groups = 1;
-        q.tile = pl.tile_w;
+        q.tile = pl.sw.tile;
         q.tiles_r = (int32_t)cdiv(rows, q.tile);
         q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
-        q.splits = pl.splits_w;
+        q.splits = pl.sw.splits;
         q.scale = pl.gmax;
         q.out = (char*)grad_w + v0 * pl.D * es;
         q.out_f32 = pl.f32;
@@ -537,13 +574,13 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
         q.k = rows;
         q.count = pl.count;
         q.groups = 1;
-        q.tile = pl.tile_h;
+        q.tile = pl.sh.tile;
         q.tiles_r = (int32_t)cdiv(pl.T, q.tile);
         q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
-        q.splits = pl.splits_h;
+        q.splits = pl.sh.splits;
+        q.spread = pl.spread;
         q.part = pl.part_h;
         q.ldp = (int32_t)pl.ldd;
-        q.part_split = pl.T * pl.ldd;
         q.add = v0 > 0;
         if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
       }
@@ -551,8 +588,8 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
     if (!grad_h) return DMUON_OK;
     JoinArgs j{};
     j.part = pl.part_h;
-    j.part_split = pl.T * pl.ldd;
-    j.splits = pl.splits_h;
+    j.count = pl.count;
+    j.spread = pl.spread;
     j.ldp = (int32_t)pl.ldd;
     j.pos = pl.pos;
     j.scale = pl.gmax;
@@ -803,10 +840,10 @@ int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* p, void* workspace, size_
     q.k = p->tokens;
     q.offsets = p->offsets;
     q.groups = (int32_t)groups;
-    q.tile = pl.tile;
+    q.tile = pl.shape.tile;
     q.tiles_r = (int32_t)pl.tiles_r;
     q.tiles_c = (int32_t)pl.tiles_c;
-    q.splits = pl.splits;
+    q.splits = pl.shape.splits;
     q.out = p->out;
     q.out_f32 = p->out_dtype == DMUON_F32;
     if (q.splits > 1) {

@@ -36,10 +36,11 @@ struct PackArgs {
   int64_t rows;                // destination rows (upper bound when count is set)
   const int32_t* gather;       // source row of destination row i, or null: i
   const int32_t* count;        // device row count, or null: rows
-  uint16_t* dst;               // [plane][rows][ldd], columns cols … ldd − 1 zero
+  uint16_t* dst;               // [plane][rows][ldd], columns cols … ldd − 1 zero; or null
   int64_t plane;               // elements between planes
+  uint16_t* blocks;            // the same in fragment order, rows padded to 16; or null
+  int64_t blocks_plane;
   int32_t ldd;                 // multiple of 64
-  int32_t blocked;             // 1: fragment order (rows padded to 16), 0: row-major
 };
 
 // ---- cross entropy ------------------------------------------------------------
@@ -103,6 +104,14 @@ struct CeRowsArgs {
 };
 
 // ---- gradient products --------------------------------------------------------
+// K splits of a product over the tokens that take part, whose number only the
+// device knows: the splits were planned for all rows, and the workgroups and the
+// partial sums of the tiles that no token reaches go to the others.
+struct RowSpread {
+  int32_t rows, tiles_r, tile; // rows planned for, their tiles, the tile's edge
+  int32_t splits, most;        // splits planned, splits at most
+};
+
 // C[row][col] = Σ_k B(k, row)·A(k, col): A's side is contiguous in the output.
 struct ProductArgs {
   const uint16_t* a;           // K-major: row k holds A(k, 0 …), [plane][…][lda]
@@ -118,6 +127,7 @@ struct ProductArgs {
   int32_t groups;
   int32_t tile;                // 256 or 128: the tile's edge
   int32_t tiles_r, tiles_c, splits;
+  RowSpread spread;            // with count and b_rows, instead of tiles_r, splits and part_split
   const float* scale;          // device factor of the result, or null
   void* out;                   // final result: dense rows × cols per group
   int32_t out_f32;
@@ -132,6 +142,8 @@ struct JoinArgs {
   const float* part;
   int64_t part_split;
   int32_t splits, ldp;
+  const int32_t* count;        // or null: the splits of `spread` for *count rows, back to back
+  RowSpread spread;
   const int32_t* pos;          // or null: t
   const float* scale;          // or null
   int64_t rows;

@@ -276,6 +276,17 @@ def test_ce_many_pieces():
     within(dw[rows], d.T @ hd, tol + 2.0 ** -8 * (d.T @ hd).abs(), "dw")
 
 
+@pytest.mark.parametrize("kept", [0, 1, 130, 256, 700, 2099])
+@pytest.mark.parametrize("D,V,dtype", [(200, 5000, torch.bfloat16), (520, 9000, torch.bfloat16), (136, 2500, torch.float32)])
+def test_ce_few_of_many_tokens(D, V, dtype, kept):
+    """Tiles and K splits are planned for every token; those that take part share them."""
+    T = 2100
+    h, w, y, gl = ce_inputs(T, D, V, dtype, 23, ignored=0.0)
+    out = torch.randperm(T, generator=gen(24), device="cuda")[kept:]
+    y[out] = IGNORE
+    check_ce(h, w, y, gl, f"{kept} of {T}")
+
+
 def test_ce_gradient_against_differences():
     """Directional derivatives of the fp64 loss: (L(+δ) − L(−δ))/2δ against ⟨grad, direction⟩ (fp32 gradients)."""
     m = mm()
