@@ -138,7 +138,7 @@ bool kmajor_in_place(const void* p, int64_t ld, int64_t cols) {
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 
 struct CePlan {
-  bool f32, direct_w;
+  bool f32, direct_w, few;
   int planes;
   int64_t T, D, V, ldd, piece, ldz;
   int tile_z, tiles_v;                   // logits
@@ -151,6 +151,7 @@ struct CePlan {
   int64_t hb_plane;
   CeStat* stats;
   size_t bytes;
+  bool hb_used() const { return few || tile_z == kTile; }       // the logits read fragment order
 };
 
 CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
@@ -161,7 +162,8 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   pl.D = p.width;
   pl.V = p.vocab;
   pl.ldd = round_up(pl.D, kLdAlign);
-  pl.direct_w = !pl.f32 && pl.D % kLdAlign == 0 && kmajor_in_place(p.w, p.ldw, pl.D);
+  pl.few = !backward && pl.T <= (pl.f32 ? kFewTokens : kFewTokens / 2);
+  pl.direct_w = pl.few || (!pl.f32 && pl.D % kLdAlign == 0 && kmajor_in_place(p.w, p.ldw, pl.D));
   // the piece: gradient logits of every token (backward) and the copy of W's rows
   const int64_t per_row = (backward ? pl.T * 2 * pl.planes : 0) + (pl.direct_w ? 0 : pl.ldd * 2 * pl.planes);
   int64_t piece = per_row ? std::max<int64_t>(kPieceBytes / per_row, 8 * kTile) : pl.V;
@@ -175,7 +177,7 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   const int64_t piece_rows = std::min(pl.piece, pl.V);
   const int pairs = pl.f32 ? plane_pairs(pl.planes, pl.planes).n : 1;
   pl.tile_z = pick_logits_tile(pl.T, piece_rows, pl.ldd * pairs);
-  pl.tiles_v = (int)cdiv(pl.V, pl.tile_z);
+  pl.tiles_v = (int)cdiv(pl.V, pl.few ? kFewRows : pl.tile_z);
   pl.sh = pick_shape(pl.T, pl.D, piece_rows, pairs, 1);
   const int64_t most = std::min<int64_t>(64, cdiv(piece_rows, 32) * pairs / 8);
   pl.spread = {(int32_t)pl.T, (int32_t)cdiv(pl.T, pl.sh.tile), pl.sh.tile, pl.sh.splits, std::max(pl.sh.splits, (int32_t)most)};
@@ -185,9 +187,9 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   pl.tgt = c.take<int32_t>(pl.T);
   pl.count = c.take<int32_t>(1);
   // hidden states: the large logits read fragment order, the rest rows
-  pl.hb_plane = round_up(pl.T, 16) * pl.ldd;
-  if (pl.tile_z == kTile) pl.hb = c.take<uint16_t>(pl.planes * pl.hb_plane);
-  if (pl.tile_z != kTile || backward) pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
+  pl.hb_plane = (pl.few ? few_tiles(pl.T) * 16 : round_up(pl.T, 16)) * pl.ldd;
+  if (pl.hb_used()) pl.hb = c.take<uint16_t>(pl.planes * pl.hb_plane);
+  if (backward || !pl.hb_used()) pl.h = c.take<uint16_t>(pl.planes * pl.T * pl.ldd);
   if (!pl.direct_w) pl.w = c.take<uint16_t>(pl.planes * piece_rows * pl.ldd);
   if (backward) {
     pl.pos = c.take<int32_t>(pl.T);
@@ -247,8 +249,6 @@ int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const f
   s.cg = pl.cg;
   s.count = pl.count;
   s.gmax = pl.gmax;
-  int e = go(env, PH_CE_PACK, stream, [&] { return launch_ce_scan(s, stream); });
-  if (e) return e;
   PackArgs a{};
   a.src = p.h;
   a.ld = p.ldh;
@@ -262,6 +262,9 @@ int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const f
   a.blocks = pl.hb;
   a.blocks_plane = pl.hb_plane;
   a.ldd = (int32_t)pl.ldd;
+  if (pl.few) return go(env, PH_CE_PACK, stream, [&] { return launch_ce_few_start(s, a, stream); });
+  int e = go(env, PH_CE_PACK, stream, [&] { return launch_ce_scan(s, stream); });
+  if (e) return e;
   return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
 }
 
@@ -294,8 +297,8 @@ CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64
   g.w = w;
   g.w_plane = w_plane;
   g.ldw = ldw;
-  g.h = pl.tile_z == kTile ? pl.hb : pl.h;
-  g.h_plane = pl.tile_z == kTile ? pl.hb_plane : pl.T * pl.ldd;
+  g.h = pl.hb_used() ? pl.hb : pl.h;
+  g.h_plane = pl.hb_used() ? pl.hb_plane : pl.T * pl.ldd;
   g.ldh = pl.ldd;
   g.pairs = plane_pairs(pl.planes, pl.planes);
   g.kt = (int32_t)(pl.ldd / 32);
@@ -458,7 +461,24 @@ int dmuon_linear_ce(const dmuon_ce_problem* p, float* losses, float* lse, void* 
     const CallEnv env = call_env();
     if ((e = forced(env, -2))) return e;
     if ((e = ce_start(*p, pl, false, nullptr, nullptr, losses, lse, env, stream))) return e;
-    for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
+    if (pl.few) {
+      CeFewArgs f{};
+      f.w = p->w;
+      f.ldw = p->ldw;
+      f.vec = ((uintptr_t)p->w & 15) == 0 && p->ldw * type_bytes(p->dtype) % 16 == 0;
+      f.width = (int32_t)pl.D;
+      f.vocab = (int32_t)pl.V;
+      f.tokens = (int32_t)pl.T;
+      f.kt = (int32_t)(pl.ldd / 32);
+      f.h = pl.hb;
+      f.h_plane = pl.hb_plane;
+      f.count = pl.count;
+      f.tgt = pl.tgt;
+      f.stats = pl.stats;
+      f.zt = pl.zt;
+      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_few(f, pl.f32, stream); }))) return e;
+    }
+    for (int64_t v0 = 0; v0 < pl.V && !pl.few; v0 += pl.piece) {
       const int64_t rows = std::min(pl.piece, pl.V - v0);
       const uint16_t* w;
       int64_t ldw, plane;

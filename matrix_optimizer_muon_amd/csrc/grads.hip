@@ -113,6 +113,34 @@ __device__ __forceinline__ void split3(float x, float (&p)[3]) {
 // rows lie together).  8192×4096 bf16, both copies: 32 µs; threads along a row and a
 // launch per copy took 20 + 62, most of it for 16-byte pieces of lines.
 // ---------------------------------------------------------------------------
+// columns c … c + 7 of destination row r, from source row sr
+__device__ __forceinline__ void pack_piece(const PackArgs& a, int64_t r, int64_t sr, int c, bool vec) {
+  const int left = a.cols - c;
+  const int64_t at = r * a.ldd + c;
+  const int64_t blk = ((r >> 4) * (a.ldd >> 5) + (c >> 5)) * 512 + (((c >> 3) & 3) * 16 + (r & 15)) * 8;
+  float v[8];
+  if (a.f32) {
+    load8(glob((const float*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
+    float p[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float s[3];
+      split3(v[e], s);
+      p[0][e] = s[0]; p[1][e] = s[1]; p[2][e] = s[2];
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) {
+      const u32x4_t w = pack8(p[q]);
+      if (a.dst) *(gptr<u32x4_t>)(glob(a.dst) + q * a.plane + at) = w;
+      if (a.blocks) *(gptr<u32x4_t>)(glob(a.blocks) + q * a.blocks_plane + blk) = w;
+    }
+  } else {
+    load8(glob((const uint16_t*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
+    const u32x4_t w = pack8(v);                     // bf16 → fp32 → bf16 is exact
+    if (a.dst) *(gptr<u32x4_t>)(glob(a.dst) + at) = w;
+    if (a.blocks) *(gptr<u32x4_t>)(glob(a.blocks) + blk) = w;
+  }
+}
 __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
   const int64_t rows = a.count ? (int64_t)*a.count : a.rows;
   const int lane = threadIdx.x & 63;
@@ -122,35 +150,8 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
   const uint32_t step = gridDim.x * (kThreads / 64);
   for (uint64_t u = (uint64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); u < n; u += step) {
     const uint32_t g = (uint32_t)u / per;
-    const int c = (int)((uint32_t)u - g * per) * 64 + (lane & 7) * 8;
     const int64_t r = (int64_t)g * 8 + (lane >> 3);
-    if (r >= rows) continue;
-    const int64_t sr = a.gather ? (int64_t)a.gather[r] : r;
-    const int left = a.cols - c;
-    const int64_t at = r * a.ldd + c;
-    const int64_t blk = ((r >> 4) * (a.ldd >> 5) + (c >> 5)) * 512 + (((c >> 3) & 3) * 16 + (r & 15)) * 8;
-    float v[8];
-    if (a.f32) {
-      load8(glob((const float*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
-      float p[3][8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float s[3];
-        split3(v[e], s);
-        p[0][e] = s[0]; p[1][e] = s[1]; p[2][e] = s[2];
-      }
-#pragma unroll
-      for (int q = 0; q < kPlanes; ++q) {
-        const u32x4_t w = pack8(p[q]);
-        if (a.dst) *(gptr<u32x4_t>)(glob(a.dst) + q * a.plane + at) = w;
-        if (a.blocks) *(gptr<u32x4_t>)(glob(a.blocks) + q * a.blocks_plane + blk) = w;
-      }
-    } else {
-      load8(glob((const uint16_t*)a.src) + sr * a.ld + c, vec && left >= 8, left, v);
-      const u32x4_t w = pack8(v);                   // bf16 → fp32 → bf16 is exact
-      if (a.dst) *(gptr<u32x4_t>)(glob(a.dst) + at) = w;
-      if (a.blocks) *(gptr<u32x4_t>)(glob(a.blocks) + blk) = w;
-    }
+    if (r < rows) pack_piece(a, r, a.gather ? (int64_t)a.gather[r] : r, (int)((uint32_t)u - g * per) * 64 + (lane & 7) * 8, vec);
   }
 }
 
@@ -860,41 +861,256 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
 }
 
 // ---------------------------------------------------------------------------
-// the tiles' statistics of each token joined: lse = M + log Σ s·exp(m − M),
-// loss = lse − z_target (NaN for a target outside the vocabulary).  16 tokens per
-// workgroup, 16 threads per token.
+// losses of at most 32 tokens (fp32: 64).  The bytes of W bound them, so W streams once from
+// memory into registers: a wave takes 16 vocabulary rows over all of D, the
+// fragments of U stages of 32 in flight while those before are multiplied, and the
+// hidden states come from the caches (64 KiB at 16 tokens × 2048).  W is read as it
+// is, of either type and any stride; fp32 values are split into planes in registers,
+// their leading product summed apart from the five corrections.
+// W's loads are nontemporal: with the caches full of another kernel's results, bf16,
+// 16 tokens × 2048 and a vocabulary of 32000, the call takes 43 µs, with plain loads 61.
+// The tiles of 128 against this, same state: bf16 × 4096, vocabulary 32000 and 128000:
+// 16 tokens 113 and 71, 268 and 240, 32 tokens 120 and 81, 262 and 284, 64 tokens 113
+// and 110, 262 and 363 (not taken); fp32 × 2048, 32000: 16 tokens 450 and 81 µs, 64
+// tokens 466 and 136 (the tiles need W as planes in memory first).
 // ---------------------------------------------------------------------------
+// The scan and the packing of so few tokens, in one launch: every wave finds the
+// tokens' places by itself with one ballot.
+__global__ __launch_bounds__(kThreads) void k_ce_few_start(CeScanArgs a, PackArgs p) {
+  __shared__ int place[kThreads / 64][kFewTokens];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool here = lane < a.tokens;
+  const int64_t y = load_index(a.targets, a.idx64, here ? lane : 0);
+  const bool part = here && y != a.ignore;
+  const uint64_t in = __ballot(part);
+  const int count = __popcll(in), i = __popcll(in & ((1ull << lane) - 1));
+  if (part) place[wave][i] = lane;
+  if (blockIdx.x == 0 && wave == 0) {
+    if (part) {
+      a.rows[i] = lane;
+      a.tgt[i] = y >= 0 && y < a.vocab ? (int32_t)y : -1;
+    } else if (here) {
+      a.losses[lane] = 0.f;
+      a.lse[lane] = 0.f;
+    }
+    if (lane == 0) *a.count = count;
+  }
+  __syncthreads();
+  const int per = p.ldd >> 6;
+  const int u = blockIdx.x * (kThreads / 64) + wave, g = u / per;
+  const int c = (u - g * per) * 64 + (lane & 7) * 8, r = g * 8 + (lane >> 3);
+  if (r >= count) return;
+  pack_piece(p, r, place[wave][r], c, (p.ld & 7) == 0 && ((uintptr_t)p.src & 15) == 0);
+}
+
+template <typename T>
+struct FewRaw;                           // 8 elements of a row of W as they were loaded
+template <>
+struct FewRaw<uint16_t> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = __builtin_nontemporal_load((gptr<const u32x4_t>)p); }
+  __device__ __forceinline__ void set(const float (&v)[8]) { u = pack8(v); }
+  __device__ __forceinline__ void planes(u32x4_t (&f)[1]) const { f[0] = u; }
+};
+template <>
+struct FewRaw<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(gptr<const float> p) {
+    a = __builtin_nontemporal_load((gptr<const f32x4_t>)p);
+    b = __builtin_nontemporal_load((gptr<const f32x4_t>)p + 1);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = f32x4_t{v[0], v[1], v[2], v[3]};
+    b = f32x4_t{v[4], v[5], v[6], v[7]};
+  }
+  __device__ __forceinline__ void planes(u32x4_t (&f)[kPlanes]) const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float p[kPlanes][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float s[3];
+      split3(v[e], s);
+      p[0][e] = s[0]; p[1][e] = s[1]; p[2][e] = s[2];
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) f[q] = pack8(p[q]);
+  }
+};
+
+__device__ __forceinline__ void mfma16(const u32x4_t& a, const u32x4_t& b, f32x4_t& c) {
+  bf16x8_t va, vb;
+  __builtin_memcpy(&va, &a, 16);
+  __builtin_memcpy(&vb, &b, 16);
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, vb, c, 0, 0, 0);
+}
+
+// T: W's type, NT: tiles of 16 tokens, U: stages in flight
+template <typename T, int NT, int U>
+__global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
+  constexpr int P = sizeof(T) == 4 ? kPlanes : 1, waves = kThreads / 64;
+  __shared__ CeStat part[waves][NT * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
+  const int v0 = (blockIdx.x * waves + wave) * 16;
+  const int row = v0 + n < g.vocab ? v0 + n : g.vocab - 1;               // a row of W, also past its end
+  const gptr<const T> w = glob((const T*)g.w) + (int64_t)row * g.ldw;
+  const gptr<const u32x4_t> h = (gptr<const u32x4_t>)glob(g.h) + n;       // fragment order: chunk c of stage k of tile j at 64·(j·kt + k) + 16·c
+  const int64_t plane = g.h_plane / 8;
+  const int full = g.vec ? g.width / 32 : 0;
+  f32x4_t acc[NT][P == 1 ? 1 : 2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int x = 0; x < (P == 1 ? 1 : 2); ++x) acc[j][x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // Chunk c (8 columns) of W's row and of the tokens, for lane group q.  A sum may
+  // take its K in any order: in the loop over whole stages a lane group takes the
+  // chunks 2q and 2q + 1 of a pair of bf16 stages, 32 bytes together, so that a pair of loads
+  // asks for whole lines (one stage after the other: 44 µs against 42.8 at 16 tokens).
+  auto chunk = [&](int k, int odd) { return P == 1 ? 4 * k + 2 * q + odd : 4 * (k + odd) + q; };
+  auto hidden = [&](int c, u32x4_t (&b)[NT][P]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int x = 0; x < P; ++x) b[j][x] = h[x * plane + (int64_t)j * g.kt * 64 + c * 16];
+  };
+  auto multiply = [&](const FewRaw<T>& raw, const u32x4_t (&b)[NT][P]) {
+    u32x4_t f[P];
+    raw.planes(f);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if constexpr (P == 1) {
+        mfma16(f[0], b[j][0], acc[j][0]);
+      } else {
+        mfma16(f[1], b[j][1], acc[j][1]);
+        mfma16(f[2], b[j][0], acc[j][1]);
+        mfma16(f[0], b[j][2], acc[j][1]);
+        mfma16(f[1], b[j][0], acc[j][1]);
+        mfma16(f[0], b[j][1], acc[j][1]);
+        mfma16(f[0], b[j][0], acc[j][0]);
+      }
+    }
+  };
+  FewRaw<T> cur[U], next[U];
+  u32x4_t hc[U][NT][P], hn[U][NT][P];
+  int k = 0;
+  if (full >= U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = chunk(u & ~1, u & 1);
+      cur[u].load(w + c * 8);
+      hidden(c, hc[u]);
+    }
+    for (; k + 2 * U <= full; k += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = chunk(k + U + (u & ~1), u & 1);
+        next[u].load(w + c * 8);
+        hidden(c, hn[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) multiply(cur[u], hc[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        cur[u] = next[u];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < P; ++x) hc[u][j][x] = hn[u][j][x];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) multiply(cur[u], hc[u]);
+    k += U;
+  }
+  const int last = (g.width + 31) / 32;
+  for (; k < last; ++k) {                 // the rest, and rows that are not 16-byte aligned
+    float x[8];
+    load8(w + k * 32 + q * 8, k < full, g.width - k * 32 - q * 8, x);
+    FewRaw<T> raw;
+    raw.set(x);
+    u32x4_t b[NT][P];
+    hidden(4 * k + q, b);
+    multiply(raw, b);
+  }
+
+  const int count = *g.count;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    f32x4_t z = acc[j][0];
+    if constexpr (P > 1) z += acc[j][P > 1 ? 1 : 0];
+    const float zr[4] = {z.x, z.y, z.z, z.w};
+    const int t = j * 16 + n;
+    const int want = t < count ? g.tgt[t] - v0 - 4 * q : -1;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (v0 + 4 * q + r < g.vocab) m = fmaxf(m, zr[r]);
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    const float m0 = m == -INFINITY ? 0.f : m;               // then s is 0, or NaN if a logit is
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (v0 + 4 * q + r < g.vocab) {
+        s += __expf(zr[r] - m0);
+        if (r == want) g.zt[t] = zr[r];
+      }
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (q == 0) part[wave][t] = CeStat{m, s};
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < NT * 16 && t < count) {
+    float m = part[0][t].m, s = 0.f;
+#pragma unroll
+    for (int x = 1; x < waves; ++x) m = fmaxf(m, part[x][t].m);
+#pragma unroll
+    for (int x = 0; x < waves; ++x) s += part[x][t].m == -INFINITY ? part[x][t].s : part[x][t].s * __expf(part[x][t].m - m);
+    g.stats[(int64_t)blockIdx.x * g.tokens + t] = CeStat{m, s};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the tiles' statistics of each token joined: lse = M + log Σ s·exp(m − M),
+// loss = lse − z_target (NaN for a target outside the vocabulary).  TOK tokens per
+// workgroup: 16, or 4 where the tokens are few and their entries many (16 tokens ×
+// 500 entries: ROWS_US).
+// ---------------------------------------------------------------------------
+// (m, s) joined with another pair; a NaN in s stays
+__device__ __forceinline__ void join_stat(CeStat& a, CeStat b) {
+  const float m = fmaxf(a.m, b.m);
+  a.s = (a.m == -INFINITY ? a.s : a.s * __expf(a.m - m)) + (b.m == -INFINITY ? b.s : b.s * __expf(b.m - m));
+  a.m = m;
+}
+template <int TOK>
 __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
-  __shared__ CeStat part[16][17];
+  constexpr int per = kThreads / TOK, waves = kThreads / 64;
+  __shared__ CeStat part[waves][TOK];
   const int count = *a.count;
-  const int i0 = blockIdx.x * 16;
+  const int i0 = blockIdx.x * TOK;
   if (i0 >= count) return;
-  const int ti = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int ti = threadIdx.x % TOK, k = threadIdx.x / TOK;
   const int i = i0 + ti;
-  float M = -INFINITY, S = 0.f;
+  CeStat all = {-INFINITY, 0.f};
   if (i < count) {
-    for (int v = k; v < a.tiles_v; v += 64) {
+    for (int v = k; v < a.tiles_v; v += 4 * per) {
       CeStat x[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        x[u] = v + 16 * u < a.tiles_v ? a.stats[(int64_t)(v + 16 * u) * a.tokens + i] : CeStat{-INFINITY, 0.f};
-      const float m = fmaxf(fmaxf(fmaxf(x[0].m, x[1].m), fmaxf(x[2].m, x[3].m)), M);
-      float s = M == -INFINITY ? S : S * __expf(M - m);
+        x[u] = v + per * u < a.tiles_v ? a.stats[(int64_t)(v + per * u) * a.tokens + i] : CeStat{-INFINITY, 0.f};
+      const float m = fmaxf(fmaxf(fmaxf(x[0].m, x[1].m), fmaxf(x[2].m, x[3].m)), all.m);
+      float s = all.m == -INFINITY ? all.s : all.s * __expf(all.m - m);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        s += x[u].m == -INFINITY ? x[u].s : x[u].s * __expf(x[u].m - m);    // a NaN in s stays
-      M = m;
-      S = s;
+      for (int u = 0; u < 4; ++u) s += x[u].m == -INFINITY ? x[u].s : x[u].s * __expf(x[u].m - m);
+      all = CeStat{m, s};
     }
   }
-  part[k][ti] = CeStat{M, S};
+#pragma unroll
+  for (int o = TOK; o < 64; o <<= 1) join_stat(all, CeStat{__shfl_xor(all.m, o, 64), __shfl_xor(all.s, o, 64)});
+  if ((threadIdx.x & 63) < TOK) part[threadIdx.x >> 6][ti] = all;
   __syncthreads();
-  if (threadIdx.x < 16 && i < count) {
-    float m = -INFINITY;
-    for (int q = 0; q < 16; ++q) m = fmaxf(m, part[q][ti].m);
-    float s = 0.f;
-    for (int q = 0; q < 16; ++q) s += part[q][ti].m == -INFINITY ? part[q][ti].s : part[q][ti].s * __expf(part[q][ti].m - m);
-    const float lse = m + logf(s);
+  if (threadIdx.x < TOK && i < count) {
+    for (int q = 1; q < waves; ++q) join_stat(all, part[q][ti]);
+    const float lse = all.m + logf(all.s);
     const int t = a.rows[i];
     a.lse[t] = lse;
     a.losses[t] = a.tgt[i] >= 0 ? lse - a.zt[i] : __uint_as_float(0x7fc00000u);
@@ -1715,10 +1931,10 @@ static int raise_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready
   return e;
 }
 
-#define DMUON_LAUNCH(phase, stream, kernel, grid, block, lds, args)                            \
+#define DMUON_LAUNCH(phase, stream, kernel, grid, block, lds, ...)                             \
   do {                                                                                         \
     timing_before(phase, stream);                                                              \
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, (hipStream_t)(stream), args);     \
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, (hipStream_t)(stream), __VA_ARGS__); \
     const int err_ = (int)hipGetLastError();                                                   \
     timing_after(phase, stream);                                                               \
     return err_;                                                                               \
@@ -1745,8 +1961,23 @@ int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream)
   if (!backward) return ce_logits<Small, false, false>(a, stream);
   return f32 ? ce_logits<Small, true, true>(a, stream) : ce_logits<Small, true, false>(a, stream);
 }
+int launch_ce_few_start(const CeScanArgs& a, const PackArgs& p, void* stream) {
+  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_few_start, (unsigned)cdiv(cdiv(a.tokens, 8) * (p.ldd / 64), kThreads / 64), kThreads, 0, a, p);
+}
+int launch_ce_few(const CeFewArgs& a, int f32, void* stream) {
+  const unsigned grid = (unsigned)cdiv(a.vocab, kFewRows);
+  const int nt = few_tiles(a.tokens);
+  if (f32) {
+    if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 1, 2>), grid, kThreads, 0, a);
+    if (nt == 2) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 2, 2>), grid, kThreads, 0, a);
+    DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 4, 2>), grid, kThreads, 0, a);
+  }
+  if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 1, 8>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 2, 8>), grid, kThreads, 0, a);
+}
 int launch_ce_rows(const CeRowsArgs& a, void* stream) {
-  DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
+  if (a.tokens <= kFewTokens) DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows<4>, (unsigned)cdiv(a.tokens, 4), kThreads, 0, a);
+  DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows<16>, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
 }
 template <typename S, bool TB>
 static int product(const ProductArgs& a, int phase, void* stream) {

@@ -92,6 +92,24 @@ struct CeLogitsArgs {
   int32_t ldz;
 };
 
+// losses of few tokens: W in place, hidden states in fragment order
+constexpr int kFewTokens = 64; // fp32; bf16 half of them
+constexpr int kFewRows = 64;   // vocabulary rows per workgroup and statistics entry
+inline int few_tiles(int64_t tokens) { return tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4; }
+struct CeFewArgs {
+  const void* w;
+  int64_t ldw;
+  int32_t vec;                 // W's rows are 16-byte aligned
+  int32_t width, vocab, tokens;
+  int32_t kt;                  // stages of 32 per row of h
+  const uint16_t* h;           // [plane][tile of 16 tokens][stage][512]
+  int64_t h_plane;
+  const int32_t* count;
+  const int32_t* tgt;
+  CeStat* stats;               // [64 vocabulary rows][tokens]
+  float* zt;
+};
+
 struct CeRowsArgs {
   const CeStat* stats;
   const float* zt;
@@ -221,6 +239,8 @@ constexpr int kSortRunsMax = 65536;                    // tokens it takes
 int launch_pack(const PackArgs& a, int phase, void* stream);
 int launch_ce_scan(const CeScanArgs& a, void* stream);
 int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream);
+int launch_ce_few_start(const CeScanArgs& a, const PackArgs& p, void* stream);
+int launch_ce_few(const CeFewArgs& a, int f32, void* stream);
 int launch_ce_rows(const CeRowsArgs& a, void* stream);
 int launch_product(const ProductArgs& a, int phase, void* stream);
 int launch_join(const JoinArgs& a, int phase, void* stream);

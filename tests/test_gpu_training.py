@@ -276,6 +276,17 @@ def test_ce_many_pieces():
     within(dw[rows], d.T @ hd, tol + 2.0 ** -8 * (d.T @ hd).abs(), "dw")
 
 
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 49, 64, 65])
+@pytest.mark.parametrize("D,V,shift", [(32, 64, 0), (264, 1000, 0), (333, 65, 0), (2056, 130, 0), (320, 700, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_ce_few_tokens(T, D, V, shift, dtype):
+    """Widths and vocabularies around the fragments' sizes, rows off the 16-byte grid."""
+    h, w, y, gl = ce_inputs(T, D + shift, V, dtype, 100 + T)
+    if T > 1:
+        y[T // 2] = V + 3                                        # no target: NaN loss, lse as ever
+    check_ce(h[:, shift:], w[:, shift:], y, gl, f"{T} tokens")
+
+
 @pytest.mark.parametrize("kept", [0, 1, 130, 256, 700, 2099])
 @pytest.mark.parametrize("D,V,dtype", [(200, 5000, torch.bfloat16), (520, 9000, torch.bfloat16), (136, 2500, torch.float32)])
 def test_ce_few_of_many_tokens(D, V, dtype, kept):
