@@ -689,9 +689,11 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t ld, int rows, 
   }
   __syncthreads();
 }
-// fp32: half of the rows at a time
-template <typename S, typename F>
-__device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f) {
+// fp32: half of the rows at a time.  PART: a partial sum, which is read again soon
+// (plain stores) and may `add` to what is there.
+template <typename S, bool PART = false, typename F>
+__device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int cols, bool vec, char* smem, F f,
+                                           bool add = false) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
   constexpr int P = S::M / 4, R = S::N / 2;              // pieces per row, rows at a time
@@ -715,11 +717,14 @@ __device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int
     for (int q = 0; q < R * P / S::Threads; ++q) {
       const int id = tid + S::Threads * q;
       const int lr = id / P, piece = id % P, row = hf * R + lr;
-      const f32x4_t v = *(const f32x4_t*)(smem + lr * (P * 16) + ((piece ^ (lr & 31)) << 4));
+      f32x4_t v = *(const f32x4_t*)(smem + lr * (P * 16) + ((piece ^ (lr & 31)) << 4));
       const int left = cols - piece * 4;
       if (row >= rows || left <= 0) continue;
       gptr<float> d = glob(out) + (int64_t)row * ld + piece * 4;
-      if (vec && left >= 4) {
+      if (PART) {                                        // whole pieces: ld is a multiple of 64
+        if (add) v += *(gptr<f32x4_t>)d;
+        *(gptr<f32x4_t>)d = v;
+      } else if (vec && left >= 4) {
         __builtin_nontemporal_store(v, (gptr<f32x4_t>)d);
       } else {
 #pragma unroll
@@ -1195,28 +1200,8 @@ __global__ __launch_bounds__(S::Threads) void k_product(ProductArgs g) {
   }
 
   if (g.part) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wr = wave / S::WC, wc = wave % S::WC, h = lane >> 5, r32 = lane & 31;
-    gptr<float> part = glob(g.part) + split * part_split + (int64_t)group * g.rows * g.ldp;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = row0 + wc * 64 + j * 32 + r32;
-      if (row >= rows) continue;
-#pragma unroll
-      for (int i = 0; i < S::I; ++i)
-#pragma unroll
-        for (int rq = 0; rq < 4; ++rq) {
-          const int col = col0 + wr * (32 * S::I) + i * 32 + rq * 8 + h * 4;
-          if (col >= g.ldp) continue;
-          gptr<f32x4_t> p = (gptr<f32x4_t>)(part + (int64_t)row * g.ldp + col);
-          f32x4_t v = {acc[i][j][4 * rq], acc[i][j][4 * rq + 1], acc[i][j][4 * rq + 2], acc[i][j][4 * rq + 3]};
-          if (g.add) {
-            const f32x4_t o = *p;
-            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-          }
-          *p = v;
-        }
-    }
+    store_tile<S, true>(g.part + split * part_split + ((int64_t)group * g.rows + row0) * g.ldp + col0, g.ldp, rows - row0, g.ldp - col0,
+                        true, smem, [&](int i, int j, int r) { return acc[i][j][r]; }, g.add);
     return;
   }
   const float s = g.scale ? *g.scale : 1.f;
