@@ -167,6 +167,7 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   // the piece: gradient logits of every token (backward) and the copy of W's rows
   const int64_t per_row = (backward ? pl.T * 2 * pl.planes : 0) + (pl.direct_w ? 0 : pl.ldd * 2 * pl.planes);
   int64_t piece = per_row ? std::max<int64_t>(kPieceBytes / per_row, 8 * kTile) : pl.V;
+  if (backward) piece = std::min(piece, kMaxLd);       // also the rows' stride of the gradient logits
   // equal pieces; where several fill the limit, of as many tile rows as make whole
   // rounds of the weight gradient's tiles over the CUs
   const int64_t n = cdiv(pl.V, std::min(piece, pl.V)), tiles_d = cdiv(pl.D, kTile);

@@ -2,8 +2,10 @@
 // over a large vocabulary, embedding lookup and its gradient, activation
 // checkpoints in 8 bits and the weight gradient computed from them.
 //
-// Every matrix product runs on the step's bf16 contraction core (core.hpp).  fp32
-// operands enter it as three bf16 planes whose sum is the fp32 value.
+// The matrix products run on two contraction cores of this file, built from the step's
+// parts (core.hpp): 256 × 256 tiles where there is work to fill every CU, 128 × 128
+// tiles elsewhere.  fp32 operands enter them as three bf16 planes whose sum is the fp32
+// value.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
@@ -161,9 +163,10 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
 // places come from ballots and one scan over (row of 1024 tokens, wave).
 // Forward: tokens whose target is not ignore_index (the others get loss and lse
 // 0).  Backward: those whose target also lies in the vocabulary and whose weight
-// is not zero.  The largest |weight| goes out too: dZ uses weights relative to it
-// and the products' epilogues multiply it back, so that a uniform weight leaves
-// p − δ unscaled when it is rounded to bf16 and tiny weights do not underflow.
+// is not zero.  The largest finite |weight| (1 if there is none) goes out too: dZ uses
+// weights relative to it and the products' epilogues multiply it back, so that a
+// uniform weight leaves p − δ unscaled when it is rounded to bf16 and tiny weights do
+// not underflow.
 // Latency bound: 4 µs for 8192 tokens (a walk over one range per thread: 39).
 // ---------------------------------------------------------------------------
 constexpr int kScanThreads = 1024;
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
     for (int k = 0; k < kScanRows; ++k) {
       const bool part = y[k] != a.ignore && (!a.backward || (y[k] >= 0 && y[k] < a.vocab && !(g[k] == 0.f)));
       in[k] = __ballot(part);
-      if (part) gm = fmaxf(gm, fabsf(g[k]));
+      if (part && fabsf(g[k]) < INFINITY) gm = fmaxf(gm, fabsf(g[k]));
       if (lane == 0) place[k * waves + wave] = __popcll(in[k]);
     }
     __syncthreads();
@@ -243,12 +246,12 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < waves; ++w) gm = fmaxf(gm, wave_max[w]);
-    *a.gmax = gm;
+    *a.gmax = gm > 0.f ? gm : 1.f;
   }
 }
 
 // ---------------------------------------------------------------------------
-// products on the core
+// the two cores of the products
 // ---------------------------------------------------------------------------
 // Swizzle of the 64-byte rows of a row-major stage: 16-byte chunk c of row r sits at
 // chunk c ^ row_swz(r).  A 16-byte LDS read is served 16 lanes at a time, lanes 0–3,
@@ -384,9 +387,10 @@ __device__ __forceinline__ void gemm_small(const Operands& op, char* smem, f32x1
 //            16 KiB, contiguous at both ends.
 // Stages past the last are issued with an empty range (no traffic), so that the counts
 // of copies in flight are the same throughout.
-// Measured against the step's core (two barriers per stage, two wave groups in turn) on
-// the products of the cross-entropy gradient at 8192 tokens × 16000 rows × 4096: see
-// k_ce_logits and k_product.
+// What bounds it is the way from L2 into LDS: at 8192 tokens × 16000 rows × 4096 the
+// weight gradient takes 797 µs (the step's core, two barriers per stage and two wave
+// groups in turn, 907), without its copies 580, without its LDS reads 624, and 4 waves of
+// 128 × 128, which read LDS a third less, 870.
 // ---------------------------------------------------------------------------
 enum StageForm : int { kKMajor = 0, kRows = 1, kBlocks = 2 };
 typedef __attribute__((address_space(3))) char lds_char;

@@ -206,6 +206,25 @@ def test_ce_gradient_weights_of_any_magnitude(scale):
     check_ce(h, w, y, gl * scale, f"{scale}")
 
 
+def test_ce_gradient_weights_that_are_not_finite():
+    """An infinite or NaN weight reaches its own token's gradient and the vocabulary
+    rows (all of them: every row takes part in every token), no other token's."""
+    m = mm()
+    h, w, y, gl = ce_inputs(40, 64, 300, torch.bfloat16, 31, ignored=0.0)
+    _, lse = m.linear_cross_entropy(h, w, y)
+    for bad in (math.inf, -math.inf, math.nan):
+        g = gl.clone()
+        g[7] = bad
+        dh, dw = m.linear_cross_entropy_backward(h, w, y, lse, g)
+        ref = ce_reference(h, w, y, torch.where(g.isfinite(), g, 0.0), lse)
+        keep = torch.arange(40, device="cuda") != 7
+        within(dh[keep], ref["dh"][keep], ref["tol_h"][keep], f"dh beside {bad}")
+        assert not dh[7].isfinite().any() and not dw.isfinite().any()
+        only = torch.full_like(gl, bad)
+        dh, dw = m.linear_cross_entropy_backward(h, w, y, lse, only)
+        assert not dh.isfinite().any() and not dw.isfinite().any()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_ce_strides_and_alignment(dtype):
     """Strided rows, rows off the 16-byte grid, and a view whose last row ends the

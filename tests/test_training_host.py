@@ -102,6 +102,12 @@ def test_ce_workspace_keeps_no_logits():
     assert 0 < small < 1 << 16
 
 
+def test_ce_pieces_of_a_huge_vocabulary():
+    """One token: the gradient logits' rows stay short enough for 32-bit offsets (2^20
+    of 2 bytes), though 256 MiB would hold 2^27 of them."""
+    assert ce_size(ce(tokens=1, width=64, vocab=1 << 27, ldh=64, ldw=64), 1)[1] < 1 << 26
+
+
 @pytest.mark.parametrize("point", ["plan", "ce_pack"])
 def test_forced_failure_before_the_first_launch(point, monkeypatch):
     monkeypatch.setenv("DMUON_TEST_FAIL_AT", point)
