@@ -805,29 +805,41 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   }
   auto reg_row = [](int i, int r) { return i * 32 + (r >> 2) * 8 + (r & 3); };
 
+  constexpr float kLog2e = 1.44269504088896341f;
   if constexpr (!BACKWARD) {
     CeStat* st = (CeStat*)smem;                              // [wave row][token of the tile]
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float m = -INFINITY, z = 0.f;
+      if (ragged) {
+#pragma unroll
+        for (int i = 0; i < S::I; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (reg_row(i, r) >= vleft) acc[i][j][r] = -INFINITY;
+      }
+      float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (ragged && reg_row(i, r) >= vleft) acc[i][j][r] = -INFINITY;
-          m = fmaxf(m, acc[i][j][r]);
-          if (reg_row(i, r) == want[j]) z = acc[i][j][r];
-        }
+        for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 32, 64));
-      const float m0 = m == -INFINITY ? 0.f : m;             // then s is 0, or NaN if a logit is
+      const float m0 = m == -INFINITY ? 0.f : m * kLog2e;    // then s is 0, or NaN if a logit is
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s += __expf(acc[i][j][r] - m0);
+        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -m0));
       s += __shfl_xor(s, 32, 64);
       if (h == 0) st[wr * S::N + wc * 64 + j * 32 + r32] = CeStat{m, s};
-      if (want[j] >= 0) g.zt[tok[j]] = z;
+      if (__any(want[j] >= 0)) {                             // few tiles hold a token's target
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::I; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (reg_row(i, r) == want[j]) z = acc[i][j][r];
+        if (want[j] >= 0) g.zt[tok[j]] = z;
+      }
     }
     __syncthreads();
     if (tid < S::N && col0 + tid < count) {
@@ -839,16 +851,31 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+      const float l2 = L[j] * kLog2e;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float p = __expf(acc[i][j][r] - L[j]);
-          if (reg_row(i, r) == want[j]) p -= 1.f;
-          p *= w[j];
-          acc[i][j][r] = ragged && reg_row(i, r) >= vleft ? 0.f : p;
-        }
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -l2));
+      if (__any(want[j] >= 0)) {
+#pragma unroll
+        for (int i = 0; i < S::I; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (reg_row(i, r) == want[j]) acc[i][j][r] -= 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < S::I; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= w[j];
+      if (ragged) {
+#pragma unroll
+        for (int i = 0; i < S::I; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (reg_row(i, r) >= vleft) acc[i][j][r] = 0.f;
+      }
+    }
     uint16_t* out = g.dz + (int64_t)col0 * g.ldz + row0;
     const int rows = count - col0, cols = g.ldz - row0;
     if constexpr (F32) {
