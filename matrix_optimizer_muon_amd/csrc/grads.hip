@@ -1881,7 +1881,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_quantize(CodecArgs a) {
     gptr<int8_t> d = glob(a.q) + r * a.cols + c;
     if (vec_q && left >= 8) {
       typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-      __builtin_nontemporal_store(u32x2{w[0], w[1]}, (gptr<u32x2>)d);
+      *(gptr<u32x2>)d = u32x2{w[0], w[1]};         // nontemporal: as fast, but reading 90 MB back takes 55 µs instead of 42
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
