@@ -559,17 +559,14 @@ __device__ __forceinline__ void tri_tile(int u, int T, int& ti, int& tj) {
 // Runs of 64 suit the apply (two rounds of 8 × 4 tiles per XCD); the Gram and
 // the square (triangle tiles in bands of 4) measured faster with runs of 16.
 template <int RUN>
-__device__ __forceinline__ int xcd_logical_block(int b, int G) {
+__device__ __forceinline__ int xcd_logical_block() {
+  const int G = gridDim.x, b = blockIdx.x;
   constexpr int win = 8 * RUN;
   const int w = b / win;
   const int xcd = b & 7, slot = (b >> 3) - w * RUN;
   if ((w + 1) * win <= G) return w * win + xcd * RUN + slot;
   const int R = G - w * win, per = R >> 3, rem = R & 7;
   return w * win + (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + slot;
-}
-template <int RUN>
-__device__ __forceinline__ int xcd_logical_block() {
-  return xcd_logical_block<RUN>(blockIdx.x, gridDim.x);
 }
 
 }  // namespace dmuon

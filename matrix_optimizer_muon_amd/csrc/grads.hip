@@ -740,6 +740,16 @@ __device__ __forceinline__ void store_tile(float* out, int64_t ld, int rows, int
   }
 }
 
+// The map of xcd_logical_block<64> over the first G workgroups of a launch, G known on
+// the device only; the others have nothing to do.
+__device__ __forceinline__ int live_block(int G) {
+  constexpr int run = 64, win = 8 * run;
+  const int b = blockIdx.x, w = b / win, xcd = b & 7, slot = (b >> 3) - w * run;
+  if ((w + 1) * win <= G) return w * win + xcd * run + slot;
+  const int left = G - w * win, per = left >> 3, rem = left & 7;
+  return w * win + (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + slot;
+}
+
 // ---------------------------------------------------------------------------
 // logits tiles, 256 vocabulary rows × 256 tokens: z(v, t) = Σ_d W(v, d)·H(t, d).
 // W is the core's A operand, so a lane's registers hold vocabulary entries of one
@@ -760,7 +770,7 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   const int tiles_t = (count + S::N - 1) / S::N, live = tiles_t * g.tiles_v;
   if ((int)blockIdx.x >= live) return;
   int tt, tv;
-  band_tile(xcd_logical_block<64>(blockIdx.x, live), tiles_t, g.tiles_v, tt, tv);
+  band_tile(live_block(live), tiles_t, g.tiles_v, tt, tv);
   const int row0 = tv * S::M, col0 = tt * S::N;   // vocabulary (in the piece), tokens
   f32x16_t acc[S::I][2];
   const char* wp = (const char*)(g.w + (int64_t)row0 * g.ldw);
@@ -1188,7 +1198,7 @@ __global__ __launch_bounds__(S::Threads) void k_product(ProductArgs g) {
   }
   const int tiles = tiles_r * g.tiles_c, live = tiles * g.groups * splits;
   if ((int)blockIdx.x >= live) return;
-  int u = xcd_logical_block<64>(blockIdx.x, live);
+  int u = live_block(live);
   const int split = u / (tiles * g.groups);
   u -= split * tiles * g.groups;
   const int group = u / tiles;
