@@ -699,6 +699,36 @@ def test_graph_replays():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,D,V,dtype", [(20, 264, 1000, torch.bfloat16), (40, 100, 700, torch.float32),
+                                         (2100, 520, 9000, torch.bfloat16), (2100, 136, 2500, torch.float32)])
+def test_graph_replays_with_other_tokens_taking_part(T, D, V, dtype):
+    """A captured loss and gradient: how many tokens count is read on the device, from
+    all of them to none."""
+    m = mm()
+    h, w, y, gl = ce_inputs(T, D, V, dtype, 51, ignored=0.0)
+    all_y = y.clone()
+
+    def run():
+        losses, lse = m.linear_cross_entropy(h, w, y)
+        return [losses, lse, *m.linear_cross_entropy_backward(h, w, y, lse, gl)]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for kept in (T // 3, 0, T, 1):
+        y.copy_(all_y)
+        y[kept:] = IGNORE
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, want):
+            assert torch.equal(a, b), kept
+        assert not held[2][kept:].any() and not held[0][kept:].any()
+
+
 @pytest.mark.parametrize("phase", ["ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec", "ckpt_wgrad"])
 def test_forced_failures(phase, monkeypatch):
     calls = one_of_each()
