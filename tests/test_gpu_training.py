@@ -295,6 +295,14 @@ def test_ce_many_pieces():
     within(dw[rows], d.T @ hd, tol + 2.0 ** -8 * (d.T @ hd).abs(), "dw")
 
 
+@pytest.mark.parametrize("T,D,V,dtype", [(2001, 800, 6500, torch.bfloat16), (1999, 780, 6501, torch.bfloat16),
+                                         (2049, 1024, 6400, torch.bfloat16), (2001, 136, 6500, torch.float32)])
+def test_ce_large_tiles(T, D, V, dtype):
+    """Enough work for the 256 × 256 tiles in the logits and in both products."""
+    h, w, y, gl = ce_inputs(T, D, V, dtype, 60)
+    check_ce(h, w, y, gl, f"{T}x{D}x{V}")
+
+
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 49, 64, 65])
 @pytest.mark.parametrize("D,V,shift", [(32, 64, 0), (264, 1000, 0), (333, 65, 0), (2056, 130, 0), (320, 700, 1)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -590,6 +598,34 @@ def test_wgrad_groups(offsets):
     got = m.checkpoint_wgrad(grad, q, b, offsets=at, out_dtype=torch.float32)
     within(got, want, tol)
     assert torch.equal(m.checkpoint_wgrad(grad, q, b, offsets=at, out_dtype=torch.bfloat16), got.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,N,K,gdt,odt", [(3001, 1500, 1700, torch.bfloat16, torch.float32), (2999, 1501, 1703, torch.bfloat16, torch.bfloat16),
+                                           (500, 4000, 4100, torch.bfloat16, torch.bfloat16), (1100, 1500, 1700, torch.float32, torch.float32)])
+def test_wgrad_large_tiles(T, N, K, gdt, odt):
+    """Enough work for the 256 × 256 tiles, with K splits and without."""
+    m = mm()
+    g = gen(T + N + K)
+    x, grad = randn(g, T, K), randn(g, T, N).to(gdt)
+    q, b = m.checkpoint_quantize(x)
+    want, tol = wgrad_reference(grad, q, b, odt)
+    within(m.checkpoint_wgrad(grad, q, b, out_dtype=odt), want, tol)
+
+
+def test_wgrad_large_tiles_in_groups():
+    """Uneven and empty groups whose rows start and end inside stages; rows outside hold NaN."""
+    m = mm()
+    g = gen(77)
+    T, N, K = 3001, 1496, 1704
+    offsets = [3, 700, 700, 701, 1900, 2990]
+    x, grad = randn(g, T, K), randn(g, T, N).to(torch.bfloat16)
+    for gone in (slice(0, 3), slice(2990, T)):
+        grad[gone] = math.nan
+        x[gone] = math.inf
+    q, b = m.checkpoint_quantize(x)
+    want, tol = wgrad_reference(grad, q, b, torch.float32, offsets)
+    at = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    within(m.checkpoint_wgrad(grad, q, b, offsets=at, out_dtype=torch.float32), want, tol)
 
 
 def test_wgrad_offsets_out_of_range_are_clamped():
