@@ -1,6 +1,6 @@
 // Device code shared by the HIP sources for gfx950 (MI355X): small conversions,
-// range-checked buffer access and the matrix-core contraction core that every
-// product of the library runs on, with its tile orders.
+// range-checked buffer access, and the step's matrix-core contraction core with its
+// tile orders, parts of which the training gradients' cores use too.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -319,7 +319,7 @@ __device__ __forceinline__ void gemm_mainloop(const Operands& op, char* smem, f3
                                                offb[q] + (TB ? 0 : kt * kRowBytes), 0, 0, 0);
     }
   };
-  const int KT = op.ktiles;
+  const int KT = op.ktiles;        // ≥ 2 (leading dims are multiples of 64 elements)
   const bool lead = wr == 1;       // group 1 runs one phase ahead of group 0
 
   // Memory phase of stage kt.  Every wave waited for its own share of stage kt
