@@ -728,6 +728,7 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     a.grad_f32 = grad_dtype == DMUON_F32;
     a.out_f32 = out_dtype == DMUON_F32;
     a.accumulate = accumulate;
+    a.zero_rows = (int32_t)std::clamp<int64_t>(32768 / (width * type_bytes(out_dtype)), kEmbedRows, kThreads);
     a.vec_in = rows16(grad_out, ldg, width, type_bytes(grad_dtype));
     a.vec_out = rows16(grad_table, width, width, type_bytes(out_dtype));
     a.scale = scale;

@@ -1725,8 +1725,9 @@ __device__ __forceinline__ int wave_lower_bound(const uint32_t* keys, int n, int
 //          in order, and a range that ends is written (or added) to its row.  A range
 //          that goes on past the 8 is finished (32 tokens and more: summed) by
 //          add_range.
-//   zeros: 16 table rows per workgroup; rows without tokens are cleared (none of
-//          them when accumulating).
+//   zeros: 16 to 256 table rows per workgroup, 32 KiB where they are short (92945 × 64
+//          bf16, 14976 tokens: 15 µs, 16 rows each 30); those without tokens are cleared (none of them
+//          when accumulating).
 template <typename G, typename O>
 __device__ __forceinline__ void embed_sums(const EmbedGradArgs& a, int64_t wg) {
   const int lane = threadIdx.x & 63;
@@ -1807,18 +1808,19 @@ __device__ __forceinline__ void embed_sums(const EmbedGradArgs& a, int64_t wg) {
 
 template <typename O>
 __device__ __forceinline__ void embed_zeros(const EmbedGradArgs& a, int64_t wg, int* start) {
-  const int64_t v0 = wg * kEmbedRows;
+  const int n = a.zero_rows;
+  const int64_t v0 = wg * n;
   const int wave = threadIdx.x >> 6;
   if (wave < 2) {
-    const int at = wave_lower_bound(a.keys, a.tokens, wave ? v0 + kEmbedRows : v0);
-    if ((threadIdx.x & 63) == 0) start[wave ? kEmbedRows : 0] = at;
+    const int at = wave_lower_bound(a.keys, a.tokens, wave ? v0 + n : v0);
+    if ((threadIdx.x & 63) == 0) start[wave ? n : 0] = at;
   }
   __syncthreads();
-  const int lo0 = start[0], hi0 = start[kEmbedRows];
+  const int lo0 = start[0], hi0 = start[n];
   __syncthreads();
   // start[r] becomes nonzero where row v0 + r has tokens: by marking the keys of a
   // short range, by a search per row for a long one
-  if (threadIdx.x < kEmbedRows) {
+  if ((int)threadIdx.x < n) {
     int has = 0;
     if (hi0 - lo0 > kThreads) {
       const int64_t want = v0 + threadIdx.x;
@@ -1835,23 +1837,20 @@ __device__ __forceinline__ void embed_zeros(const EmbedGradArgs& a, int64_t wg, 
   if (hi0 - lo0 <= kThreads && (int)threadIdx.x < hi0 - lo0) start[(int64_t)a.keys[lo0 + threadIdx.x] - v0] = 1;
   __syncthreads();
   constexpr int E = 16 / (int)sizeof(O);             // elements per 16-byte store
-  for (int r = 0; r < kEmbedRows; ++r) {
-    const int64_t v = v0 + r;
-    if (v >= a.rows) return;
-    if (start[r] && v != a.padding) continue;
-    gptr<O> out = glob((O*)a.out) + v * a.width;
-    if (a.vec_out) {
-      for (int c = threadIdx.x * E; c < a.width; c += kThreads * E)
-        __builtin_nontemporal_store(u32x4_t{0u, 0u, 0u, 0u}, (gptr<u32x4_t>)(out + c));
-    } else {
-      for (int c = threadIdx.x; c < a.width; c += kThreads) out[c] = O(0);
-    }
+  const int per = a.vec_out ? a.width / E : a.width;     // stores per row
+  const int rows = a.rows - v0 < n ? (int)(a.rows - v0) : n;
+  for (int q = threadIdx.x; q < rows * per; q += kThreads) {
+    const int r = q / per, c = q - r * per;
+    if (start[r] && v0 + r != a.padding) continue;
+    gptr<O> out = glob((O*)a.out) + (v0 + r) * a.width;
+    if (a.vec_out) __builtin_nontemporal_store(u32x4_t{0u, 0u, 0u, 0u}, (gptr<u32x4_t>)(out + c * E));
+    else out[c] = O(0);
   }
 }
 
 template <typename G, typename O>
 __global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
-  __shared__ int start[kEmbedRows + 1];
+  __shared__ int start[kThreads + 1];
   const int64_t wg = blockIdx.x;
   if (wg < a.seg_wg) embed_sums<G, O>(a, wg);
   else embed_zeros<O>(a, wg - a.seg_wg, start);
@@ -2068,7 +2067,7 @@ int launch_embed_run(const EmbedGradArgs& a, int level, void* stream) {
   DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_run<uint16_t, 0>), grid, kThreads, 0, a);
 }
 int launch_embed_grad(const EmbedGradArgs& a, void* stream) {
-  const unsigned grid = (unsigned)(a.seg_wg + (a.accumulate ? 0 : cdiv(a.rows, kEmbedRows)));
+  const unsigned grid = (unsigned)(a.seg_wg + (a.accumulate ? 0 : cdiv(a.rows, a.zero_rows)));
   if (a.grad_f32) {
     if (a.out_f32) DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, float>), grid, kThreads, 0, a);
     DMUON_LAUNCH(PH_EMBED_GRAD, stream, (k_embed_grad<float, uint16_t>), grid, kThreads, 0, a);

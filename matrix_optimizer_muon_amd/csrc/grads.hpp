@@ -207,6 +207,7 @@ struct EmbedGradArgs {
   int64_t ldg;
   int32_t grad_f32, out_f32, accumulate;
   int32_t vec_in, vec_out;
+  int32_t zero_rows;           // table rows per workgroup that clears rows
   float scale;
   void* out;
   int32_t slabs;               // ceil(width / 512)
@@ -230,7 +231,7 @@ struct CodecArgs {
 
 constexpr int kSortItems = 4096;         // per workgroup of a sort pass
 constexpr int kRun = 32;                 // sorted tokens per first-level sum, and those per second-level one
-constexpr int kEmbedRows = 16;           // table rows per workgroup that clears rows
+constexpr int kEmbedRows = 16;           // table rows per workgroup that clears rows, at least (kThreads at most)
 constexpr int kEmbedHeads = 8;           // sorted positions per wave that sums ranges
 constexpr int kSortRunBits = 13;
 constexpr int kSortRun = 1 << kSortRunBits;            // tokens per run of the two-launch sort
