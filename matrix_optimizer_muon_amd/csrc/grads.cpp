@@ -648,7 +648,10 @@ int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const 
     a.tokens = tokens;
     a.rows = rows;
     a.width = (int32_t)width;
-    a.vec = rows16(table, ldt, width, es) && rows16(out, width, width, es);
+    // elements of a row that one thread moves: 8, or what the alignment allows
+    const uint64_t align = (uint64_t)(uintptr_t)table | (uint64_t)(uintptr_t)out | (uint64_t)(ldt * es) | (uint64_t)(width * es);
+    a.unit = rows16(table, ldt, width, es) && rows16(out, width, width, es) ? 8
+             : align % (2 * es) ? 1 : align % (4 * es) ? 2 : 4;
     a.table = table;
     a.ldt = ldt;
     a.out = out;

@@ -1309,20 +1309,44 @@ __global__ __launch_bounds__(kThreads) void k_join(JoinArgs a) {
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_embed(EmbedArgs a) {
-  const int per = (a.width + 7) >> 3;
+  const int per = a.width >> 3;
   const int64_t n = a.tokens * per, step = (int64_t)gridDim.x * kThreads;
   for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < n; q += step) {
     const int64_t t = q / per;
     const int c = (int)(q - t * per) * 8;
-    const int left = a.width - c;
     const int64_t id = load_index(a.ids, a.idx64, t);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (id >= 0 && id < a.rows) {
-      load8(glob((const T*)a.table) + id * a.ldt + c, a.vec, left, v);
+      load8(glob((const T*)a.table) + id * a.ldt + c, true, 8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= a.scale;
     }
-    store8<true>(glob((T*)a.out) + t * a.width + c, a.vec, left, v);
+    store8<true>(glob((T*)a.out) + t * a.width + c, true, 8, v);
+  }
+}
+
+// Rows without 16-byte pieces of 8 elements: N elements per thread, the largest unit
+// that the rows' alignment allows, so that a wave still covers whole lines (25472 tokens
+// × 684 fp32: 23 µs, bf16 16; eight elements one by one per thread 62 and 39).
+template <typename T, int N>
+__global__ __launch_bounds__(kThreads) void k_embed_units(EmbedArgs a) {
+  typedef T unit __attribute__((ext_vector_type(N)));
+  const int per = a.width / N;
+  const int64_t n = a.tokens * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < n; q += step) {
+    const int64_t t = q / per;
+    const int c = (int)(q - t * per) * N;
+    const int64_t id = load_index(a.ids, a.idx64, t);
+    unit u = {};
+    if (id >= 0 && id < a.rows) {
+      u = *(gptr<const unit>)(glob((const T*)a.table) + id * a.ldt + c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if constexpr (sizeof(T) == 4) u[e] *= a.scale;
+        else u[e] = f32_to_bf16(bf16_to_f32(u[e]) * a.scale);
+      }
+    }
+    __builtin_nontemporal_store(u, (gptr<unit>)(glob((T*)a.out) + t * a.width + c));
   }
 }
 
@@ -2034,10 +2058,16 @@ int launch_product(const ProductArgs& a, int phase, void* stream) {
 int launch_join(const JoinArgs& a, int phase, void* stream) {
   DMUON_LAUNCH(phase, stream, k_join, stride_grid(a.rows * cdiv(a.cols, 8)), kThreads, 0, a);
 }
+template <typename T>
+static int embed_rows(const EmbedArgs& a, void* stream) {
+  const unsigned grid = stride_grid(a.tokens * cdiv(a.width, a.unit));
+  if (a.unit == 8) DMUON_LAUNCH(PH_EMBED, stream, k_embed<T>, grid, kThreads, 0, a);
+  if (a.unit == 4) DMUON_LAUNCH(PH_EMBED, stream, (k_embed_units<T, 4>), grid, kThreads, 0, a);
+  if (a.unit == 2) DMUON_LAUNCH(PH_EMBED, stream, (k_embed_units<T, 2>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_EMBED, stream, (k_embed_units<T, 1>), grid, kThreads, 0, a);
+}
 int launch_embed(const EmbedArgs& a, void* stream) {
-  const unsigned grid = stride_grid(a.tokens * cdiv(a.width, 8));
-  if (a.f32) DMUON_LAUNCH(PH_EMBED, stream, k_embed<float>, grid, kThreads, 0, a);
-  DMUON_LAUNCH(PH_EMBED, stream, k_embed<uint16_t>, grid, kThreads, 0, a);
+  return a.f32 ? embed_rows<float>(a, stream) : embed_rows<uint16_t>(a, stream);
 }
 int launch_sort_runs(const SortArgs& a, void* stream) {
   const dim3 grid((unsigned)cdiv(a.tokens, kSortRun)), block(kScanThreads);

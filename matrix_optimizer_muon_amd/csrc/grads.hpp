@@ -177,7 +177,7 @@ struct EmbedArgs {
   int32_t f32;                 // table and out
   int64_t tokens, rows;
   int32_t width;
-  int32_t vec;                 // rows are 16-byte aligned multiples of 8 elements
+  int32_t unit;                // elements a thread moves at a time: 8 (16-byte rows), 4, 2 or 1
   const void* table;
   int64_t ldt;
   void* out;

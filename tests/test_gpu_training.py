@@ -371,6 +371,23 @@ def test_embedding_lookup(T, V, D, dtype):
     assert torch.equal(m.embedding(ids.view(1, -1, 1).clamp(0, V - 1), table), table[ids.clamp(0, V - 1)].view(1, -1, 1, D + 8))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,ld,shift", [(12, 12, 0), (684, 684, 0), (4, 20, 4), (20, 24, 2), (6, 8, 2), (2, 2, 0), (8, 9, 0), (9, 16, 0), (16, 24, 4)])
+def test_embedding_lookup_alignments(D, ld, shift, dtype):
+    """Rows that allow 8, 4, 2 or 1 elements at a time, by their width, stride and start."""
+    m = mm()
+    g = gen(D + ld)
+    flat = randn(g, 500 * ld + shift).to(dtype)
+    table = flat[shift:].view(500, ld)[:, :D]
+    ids = torch.randint(-1, 501, (3000,), generator=g, device="cuda")
+    want = torch.where(((ids >= 0) & (ids < 500))[:, None], table[ids.clamp(0, 499)].float() * 0.75, 0.0).to(dtype)
+    assert torch.equal(m.embedding(ids, table, scale=0.75), want)
+    room = torch.full((3000 * D + 8,), 5.0, device="cuda").to(dtype)      # an output off the grid, its surroundings kept
+    out = room[shift:shift + 3000 * D].view(3000, D)
+    assert torch.equal(m.embedding(ids, table, scale=0.75, out=out), want)
+    assert (room[:shift] == 5).all() and (room[shift + 3000 * D:] == 5).all()
+
+
 def embed_reference(ids, grad, V, scale, pad, out):
     use = (ids >= 0) & (ids < V)
     if pad is not None:
