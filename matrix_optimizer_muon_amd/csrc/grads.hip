@@ -761,9 +761,11 @@ __device__ __forceinline__ int live_block(int G) {
 //             target's logit;
 //   backward: dZ(t, v) = g_t·(exp(z − lse_t) − [v = target]), rounded to bf16 (one
 //             rounding; the matrix cores take bf16; fp32 operands: three planes).
-// The exponentials are 2^(z·log₂e − lse·log₂e), one fused multiply-add and one
-// instruction; the target's entry is looked for only in parts of a tile that hold
-// one (6% of them at 128000 words).  Bound by the product (see the large core): 4096 tokens × 4096, vocabulary
+// The exponentials are 2^((z − largest)·log₂e) and 2^((z − lse)·log₂e), the difference
+// first: it is exact where the two are close, so that the largest logit's own term is 1
+// and a certain token's probability too, whatever their size (one fused multiply-add,
+// z·log₂e − lse·log₂e, is off by lse·2⁻²⁴ in the exponent).  The target's entry is looked
+// for only in parts of a tile that hold one (6% of them at 128000 words).  Bound by the product (see the large core): 4096 tokens × 4096, vocabulary
 // 32000, forward 870 µs = 1.23 PFLOP/s; 8192 × 4096 and 16384 rows, backward 867 µs =
 // 1.27; of a tile's 109 µs about 10 are prologue and epilogue, which nothing overlaps.
 // ---------------------------------------------------------------------------
@@ -839,12 +841,12 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 32, 64));
-      const float m0 = m == -INFINITY ? 0.f : m * kLog2e;    // then s is 0, or NaN if a logit is
+      const float m0 = m == -INFINITY ? 0.f : m;             // then s is 0, or NaN if a logit is
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -m0));
+        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - m0) * kLog2e);
       s += __shfl_xor(s, 32, 64);
       if (h == 0) st[wr * S::N + wc * 64 + j * 32 + r32] = CeStat{m, s};
       if (__any(want[j] >= 0)) {                             // few tiles hold a token's target
@@ -868,11 +870,10 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float l2 = L[j] * kLog2e;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -l2));
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_amdgcn_exp2f((acc[i][j][r] - L[j]) * kLog2e);
       if (__any(want[j] >= 0)) {
 #pragma unroll
         for (int i = 0; i < S::I; ++i)
@@ -1123,7 +1124,8 @@ __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
 
 // ---------------------------------------------------------------------------
 // the tiles' statistics of each token joined: lse = M + log Σ s·exp(m − M),
-// loss = lse − z_target (NaN for a target outside the vocabulary).  TOK tokens per
+// loss = (M − z_target) + log Σ … (NaN for a target outside the vocabulary): neither
+// term is negative, and the logarithm keeps its digits beside a large M.  TOK tokens per
 // workgroup: 16, or 4 where the tokens are few and their entries many (16 tokens: 500
 // entries 5.6 and 3.2 µs, 2000 entries 17.8 and 5.9).
 // ---------------------------------------------------------------------------
@@ -1162,10 +1164,10 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
   __syncthreads();
   if (threadIdx.x < TOK && i < count) {
     for (int q = 1; q < waves; ++q) join_stat(all, part[q][ti]);
-    const float lse = all.m + logf(all.s);
+    const float ls = logf(all.s);                            // ≥ 0: the largest logit's own term is 1
     const int t = a.rows[i];
-    a.lse[t] = lse;
-    a.losses[t] = a.tgt[i] >= 0 ? lse - a.zt[i] : __uint_as_float(0x7fc00000u);
+    a.lse[t] = all.m + ls;
+    a.losses[t] = a.tgt[i] >= 0 ? (all.m - a.zt[i]) + ls : __uint_as_float(0x7fc00000u);
   }
 }
 
