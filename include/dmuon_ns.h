@@ -322,6 +322,9 @@ int dmuon_adamw_step(const dmuon_adamw_tensor* tensors, int32_t n_tensors, const
 
 typedef enum { DMUON_I32 = 0, DMUON_I64 = 1 } dmuon_index_dtype;
 
+/* A target that lies in another shard of the vocabulary (see below). */
+#define DMUON_TARGET_ELSEWHERE (-2147483647 - 1)
+
 /* Softmax cross entropy of `tokens` hidden states against a vocabulary:
  *   z(t, v) = Σ_d h(t, d)·w(v, d)
  *   lse(t) = log Σ_v exp z(t, v),   loss(t) = lse(t) − z(t, target(t))
@@ -332,8 +335,16 @@ typedef enum { DMUON_I32 = 0, DMUON_I64 = 1 } dmuon_index_dtype;
  *   w            device [vocab, width], row stride ldw
  *   targets      device [tokens]; a token whose target equals ignore_index has
  *                loss 0, lse 0 and no part in any gradient, whatever its hidden
- *                state holds; any other target outside [0, vocab) gives a loss of
- *                NaN and no gradient
+ *                state holds; one of DMUON_TARGET_ELSEWHERE (unless that is
+ *                ignore_index) has no target among these rows: its loss is its lse,
+ *                and the backward pass has the softmax term of its gradients; any
+ *                other target outside [0, vocab) gives a loss of NaN and no gradient
+ * A vocabulary in shards: each shard's call gets its rows of w and the targets
+ * shifted by its first row, DMUON_TARGET_ELSEWHERE where they fall outside (a
+ * target that is only shifted has no gradient there).  With the calls' results,
+ *   lse = log Σ exp lse_shard,   loss = lse − Σ (lse_shard − loss_shard),
+ * and the backward calls get the joined lse: grad_h is the sum of theirs, grad_w
+ * their rows.
  * 0 ≤ tokens ≤ 2^24, 1 ≤ width ≤ 65536, 1 ≤ vocab ≤ 2^30. */
 typedef struct {
   int64_t tokens, width, vocab;
@@ -358,8 +369,8 @@ int dmuon_linear_ce(const dmuon_ce_problem* problem, float* losses, float* lse, 
 
 /* With dz(t, v) = grad_losses(t)·(exp(z(t, v) − lse(t)) − [v = target(t)]):
  *   grad_h = dz·w  [tokens, width],   grad_w = dzᵀ·h  [vocab, width]
- * lse: as dmuon_linear_ce returned it (or the joined value of a sharded
- * vocabulary).  grad_losses: device fp32 [tokens], for a mean 1/n at every token;
+ * (−[…] is absent for DMUON_TARGET_ELSEWHERE.)  lse: as dmuon_linear_ce returned it, or
+ * the joined value of a vocabulary in shards.  grad_losses: device fp32 [tokens], for a mean 1/n at every token;
  * a token whose value is 0 is treated as ignored.  grad_h, grad_w: device, dense,
  * of the problem's dtype, fully written; NULL where not wanted.  For bf16, dz is
  * rounded to bf16 once (relative to the largest finite |grad_losses|). */

@@ -18,14 +18,14 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding as _b
-from .training import (checkpoint_dequantize, checkpoint_quantize, checkpoint_wgrad, embedding,  # noqa: F401
+from .training import (TARGET_ELSEWHERE, checkpoint_dequantize, checkpoint_quantize, checkpoint_wgrad, embedding,  # noqa: F401
                        embedding_backward, linear_cross_entropy, linear_cross_entropy_backward)
 from .workloads import HYPER  # noqa: F401
 
 __all__ = ["muon_step", "muon_step_workspace_size", "adamw_step", "MuonStep", "AdamwStep",
            "ns_batched", "lpt_assign", "gemm_nt",
            "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
-           "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize", "checkpoint_wgrad",
+           "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize", "checkpoint_wgrad", "TARGET_ELSEWHERE",
            "phase_timing", "phase_timing_read", "abi_version", "load_library", "HYPER"]
 
 QUINTIC = (HYPER["a"], HYPER["b"], HYPER["c"])

@@ -18,6 +18,8 @@
 namespace dmuon {
 namespace {
 
+static_assert(kElsewhere == DMUON_TARGET_ELSEWHERE, "the kernels' value is the header's");
+
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;    // rows of one cross-entropy or wgrad call
 constexpr int64_t kMaxIds = (int64_t)1 << 30;       // ids of one embedding call
 constexpr int64_t kMaxWidth = 65536;

@@ -162,8 +162,8 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
 // workgroup walks the tokens 8192 at a time, the loads of a step issued together:
 // places come from ballots and one scan over (row of 1024 tokens, wave).
 // Forward: tokens whose target is not ignore_index (the others get loss and lse
-// 0).  Backward: those whose target also lies in the vocabulary and whose weight
-// is not zero.  The largest finite |weight| (1 if there is none) goes out too: dZ uses
+// 0).  Backward: those whose target also lies in the vocabulary, or in another shard of
+// it (kElsewhere: a row of probabilities without a target), and whose weight is not zero.  The largest finite |weight| (1 if there is none) goes out too: dZ uses
 // weights relative to it and the products' epilogues multiply it back, so that a
 // uniform weight leaves p − δ unscaled when it is rounded to bf16 and tiny weights do
 // not underflow.
@@ -171,6 +171,11 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kScanThreads = 1024;
 constexpr int kScanRows = 8;
+__device__ __forceinline__ bool in_vocab(int64_t y, int32_t vocab) { return y >= 0 && y < vocab; }
+// what the list keeps of a target: a vocabulary row, kTgtElsewhere or kTgtNone
+__device__ __forceinline__ int32_t list_target(int64_t y, int32_t vocab) {
+  return in_vocab(y, vocab) ? (int32_t)y : y == kElsewhere ? kTgtElsewhere : kTgtNone;
+}
 __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
   constexpr int waves = kScanThreads / 64, parts = kScanRows * waves;      // 128 partial counts
   __shared__ int place[parts];
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
     uint64_t in[kScanRows];
 #pragma unroll
     for (int k = 0; k < kScanRows; ++k) {
-      const bool part = y[k] != a.ignore && (!a.backward || (y[k] >= 0 && y[k] < a.vocab && !(g[k] == 0.f)));
+      const bool part = y[k] != a.ignore && (!a.backward || ((in_vocab(y[k], a.vocab) || y[k] == kElsewhere) && !(g[k] == 0.f)));
       in[k] = __ballot(part);
       if (part && fabsf(g[k]) < INFINITY) gm = fmaxf(gm, fabsf(g[k]));
       if (lane == 0) place[k * waves + wave] = __popcll(in[k]);
@@ -225,7 +230,7 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
       if (a.backward) a.pos[t] = part ? i : -1;
       if (part) {
         a.rows[i] = (int32_t)t;
-        a.tgt[i] = y[k] >= 0 && y[k] < a.vocab ? (int32_t)y[k] : -1;
+        a.tgt[i] = list_target(y[k], a.vocab);
         if (a.backward) {
           a.clse[i] = l[k];
           a.cg[i] = g[k];
@@ -941,7 +946,7 @@ __global__ __launch_bounds__(kThreads) void k_ce_few_start(CeScanArgs a, PackArg
   if (blockIdx.x == 0 && wave == 0) {
     if (part) {
       a.rows[i] = lane;
-      a.tgt[i] = y >= 0 && y < a.vocab ? (int32_t)y : -1;
+      a.tgt[i] = list_target(y, a.vocab);
     } else if (here) {
       a.losses[lane] = 0.f;
       a.lse[lane] = 0.f;
@@ -1124,8 +1129,9 @@ __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
 
 // ---------------------------------------------------------------------------
 // the tiles' statistics of each token joined: lse = M + log Σ s·exp(m − M),
-// loss = (M − z_target) + log Σ … (NaN for a target outside the vocabulary): neither
-// term is negative, and the logarithm keeps its digits beside a large M.  TOK tokens per
+// loss = (M − z_target) + log Σ …: neither term is negative, and the logarithm keeps its
+// digits beside a large M (a target in another shard: the lse; one outside the
+// vocabulary: NaN).  TOK tokens per
 // workgroup: 16, or 4 where the tokens are few and their entries many (16 tokens: 500
 // entries 5.6 and 3.2 µs, 2000 entries 17.8 and 5.9).
 // ---------------------------------------------------------------------------
@@ -1166,8 +1172,9 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
     for (int q = 1; q < waves; ++q) join_stat(all, part[q][ti]);
     const float ls = logf(all.s);                            // ≥ 0: the largest logit's own term is 1
     const int t = a.rows[i];
+    const int y = a.tgt[i];
     a.lse[t] = all.m + ls;
-    a.losses[t] = a.tgt[i] >= 0 ? (all.m - a.zt[i]) + ls : __uint_as_float(0x7fc00000u);
+    a.losses[t] = y >= 0 ? (all.m - a.zt[i]) + ls : y == kTgtElsewhere ? all.m + ls : __uint_as_float(0x7fc00000u);
   }
 }
 

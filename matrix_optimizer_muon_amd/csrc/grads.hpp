@@ -44,6 +44,9 @@ struct PackArgs {
 };
 
 // ---- cross entropy ------------------------------------------------------------
+constexpr int64_t kElsewhere = INT32_MIN;    // DMUON_TARGET_ELSEWHERE
+constexpr int32_t kTgtNone = -1;             // compact targets that are no vocabulary row
+constexpr int32_t kTgtElsewhere = -2;
 struct CeScanArgs {
   const void* targets;
   int32_t idx64;
@@ -56,7 +59,7 @@ struct CeScanArgs {
   float* lse;
   int32_t* rows;               // token of compact row i
   int32_t* pos;                // compact row of token t, or −1
-  int32_t* tgt;                // target of compact row i (−1: outside the vocabulary)
+  int32_t* tgt;                // target of compact row i, kTgtElsewhere or kTgtNone
   float* clse;                 // backward: lse of compact row i
   float* cg;                   // backward: gradient weight of compact row i
   int32_t* count;              // number of compact rows

@@ -21,8 +21,9 @@ from . import _binding as _b
 
 __all__ = ["linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
            "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize",
-           "checkpoint_wgrad"]
+           "checkpoint_wgrad", "TARGET_ELSEWHERE"]
 
+TARGET_ELSEWHERE = -2 ** 31     # a target that lies in another shard of the vocabulary
 CKPT_BLOCK = 32          # columns that share one exponent byte
 
 
@@ -175,8 +176,12 @@ def linear_cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, st
     bf16 or both fp32; targets: int64 or int32 of h's leading shape.  Returns
     (losses, lse), fp32 of that shape: lse is the log-sum-exp of the token's
     logits, losses = lse − the target's logit.  Tokens whose target is
-    ``ignore_index`` have loss and lse 0; another target outside the vocabulary
-    gives NaN.
+    ``ignore_index`` have loss and lse 0; a target of ``TARGET_ELSEWHERE`` gives the
+    lse as the loss, another one outside the vocabulary NaN.
+
+    A vocabulary in shards: call each with its rows of w and the targets shifted by
+    its first row, ``TARGET_ELSEWHERE`` where that is not one of its rows.  Then lse
+    is the logsumexp of the shards' and the loss lse − Σ (lse_shard − loss_shard).
     """
     import torch
     prob = _ce_problem(h, w, targets, ignore_index)
@@ -193,7 +198,9 @@ def linear_cross_entropy_backward(h, w, targets, lse, grad_losses, *, ignore_ind
                                   need_h=True, need_w=True, workspace=None, stream=None):
     """Gradients of ``linear_cross_entropy`` with respect to h and w.
 
-    lse: as ``linear_cross_entropy`` returned it; grad_losses: fp32 of the same
+    lse: as ``linear_cross_entropy`` returned it (of a vocabulary in shards: the
+    joined one, with each shard's targets as there; grad_h is then the sum of the
+    shards' results); grad_losses: fp32 of the same
     shape, the gradient of each token's loss (for a mean, 1/n everywhere); a token
     whose entry is 0 is left out like an ignored one.  Returns (grad_h, grad_w) in
     h's dtype, dense, of h's and w's shape; ``grad_h`` / ``grad_w`` name tensors to
