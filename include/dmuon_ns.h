@@ -312,7 +312,9 @@ int dmuon_adamw_step(const dmuon_adamw_tensor* tensors, int32_t n_tensors, const
  * table take these gradients as given (embeddings and lm_head on an AdamW route);
  * the operators are this library's own.  Types: bf16 or fp32; bf16 products run on
  * the bf16 matrix cores with fp32 accumulation; fp32 operands enter them as three
- * bf16 terms whose sum is the fp32 value, so fp32 products keep fp32 accuracy.
+ * bf16 terms whose sum is the fp32 value, so fp32 products keep fp32 accuracy
+ * (an infinity times a finite number is as in fp32; two infinities give NaN).
+ * Logits of -inf have probability 0, one of +inf makes its token's lse NaN.
  * Matrices are row-major with the last dim contiguous; a row stride (ld*, in
  * elements) may exceed the row.  Outputs are dense.  Every sum has a fixed order.
  * Alignment never matters for correctness: 16-byte aligned rows are read in place

@@ -95,16 +95,19 @@ __device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t 
 
 // x = hi + mid + lo, each a bf16 value: hi is x rounded to bf16 (cut off where
 // rounding would overflow), mid the rest rounded, lo the rest of that: 24 bits.
-// An infinity or NaN sits in hi alone.
+// An infinity or NaN sits in lo alone: lo meets only the other side's hi (plane_pairs),
+// which is 0 for a 0 only, so that an infinity times another finite number stays one
+// (in hi it would meet the mid and lo of that number, which may be 0: NaN).  Two
+// infinities meet each other's hi = 0 and give NaN.
 __device__ __forceinline__ void split3(float x, float (&p)[3]) {
   const bool special = (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
   float hi = bf16_to_f32(f32_to_bf16(x));
   if ((__float_as_uint(hi) & 0x7f800000u) == 0x7f800000u && !special) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
   const float r = x - hi;
   const float mid = bf16_to_f32(f32_to_bf16(r));
-  p[0] = hi;
+  p[0] = special ? 0.f : hi;
   p[1] = special ? 0.f : mid;
-  p[2] = special ? 0.f : bf16_to_f32(f32_to_bf16(r - mid));
+  p[2] = special ? x : bf16_to_f32(f32_to_bf16(r - mid));
 }
 
 // ---------------------------------------------------------------------------
