@@ -316,7 +316,8 @@ int dmuon_adamw_step(const dmuon_adamw_tensor* tensors, int32_t n_tensors, const
  * (an infinity times a finite number is as in fp32; two infinities give NaN).
  * Logits of -inf have probability 0, one of +inf makes its token's lse NaN.
  * Matrices are row-major with the last dim contiguous; a row stride (ld*, in
- * elements) may exceed the row.  Outputs are dense.  Every sum has a fixed order.
+ * elements) may exceed the row, and a matrix ends within 2^48 bytes of its start.
+ * Outputs are dense.  Every sum has a fixed order.
  * Alignment never matters for correctness: 16-byte aligned rows are read in place
  * or with 16-byte accesses, other rows are copied or read element by element.
  * Data on the device is not validated on the host; what an id, target or offset

@@ -26,6 +26,7 @@ constexpr int64_t kMaxWidth = 65536;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // vocabulary, table rows
 constexpr int64_t kMaxLd = (int64_t)1 << 20;        // row strides the kernels take in place
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxExtent = (int64_t)1 << 48;    // bytes of a strided matrix: the largest dense one (2^30 × 65536 fp32)
 
 // C entry bodies: nothing thrown on the host (an allocation that fails) leaves them
 template <typename F>
@@ -56,6 +57,10 @@ bool index_type(int32_t t) { return t == DMUON_I32 || t == DMUON_I64; }
 
 void add_range(std::vector<Range>& rs, const void* p, int64_t bytes, bool ro) {
   if (p && bytes > 0) rs.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, ro});
+}
+// rows × cols elements of es bytes at a stride of ld (≥ cols, checked before) end within kMaxExtent
+bool spans(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  return rows <= 1 || ld <= (kMaxExtent / es - cols) / (rows - 1);
 }
 int64_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
   return rows > 0 ? ((rows - 1) * ld + cols) * es : 0;
@@ -219,11 +224,13 @@ int check_ce(const dmuon_ce_problem* p, std::vector<Range>* rs) {
   if (p->vocab < 1 || p->vocab > kMaxRows) return fail(DMUON_E_SHAPE, "vocab must be in [1, 2^30]");
   if (p->ldh < p->width || p->ldw < p->width || p->ldh > kMaxStride || p->ldw > kMaxStride)
     return fail(DMUON_E_SHAPE, "ldh and ldw must be at least width");
+  const int64_t es = type_bytes(p->dtype);
+  if (!spans(p->tokens, p->width, p->ldh, es) || !spans(p->vocab, p->width, p->ldw, es))
+    return fail(DMUON_E_SHAPE, "h and w must end within 2^48 bytes");
   if (cdiv(p->tokens, 128) * cdiv(p->vocab, 128) > INT32_MAX) return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
   if (p->tokens > 0 && (!p->h || !p->targets)) return fail(DMUON_E_NULL, "h and targets must be set");
   if (!p->w) return fail(DMUON_E_NULL, "w must be set");
   if (rs) {
-    const int64_t es = type_bytes(p->dtype);
     add_range(*rs, p->h, strided_bytes(p->tokens, p->width, p->ldh, es), true);
     add_range(*rs, p->w, strided_bytes(p->vocab, p->width, p->ldw, es), true);
     add_range(*rs, p->targets, p->tokens * (p->index_dtype == DMUON_I64 ? 8 : 4), true);
@@ -363,6 +370,7 @@ int check_wgrad(const dmuon_ckpt8_wgrad_problem* p, std::vector<Range>* rs) {
   if (p->tokens < 0 || p->tokens > kMaxTokens) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^24]");
   if (p->n < 1 || p->n > kMaxWidth || p->k < 1 || p->k > kMaxWidth) return fail(DMUON_E_SHAPE, "n and k must be in [1, 65536]");
   if (p->ldg < p->n || p->ldg > kMaxStride) return fail(DMUON_E_SHAPE, "ldg must be at least n");
+  if (!spans(p->tokens, p->n, p->ldg, type_bytes(p->grad_dtype))) return fail(DMUON_E_SHAPE, "grad_out must end within 2^48 bytes");
   if (p->groups < 0 || p->groups > (1 << 20)) return fail(DMUON_E_SHAPE, "groups must be in [0, 2^20]");
   if (p->reserved != 0) return fail(DMUON_E_SHAPE, "reserved must be 0");
   if (!p->offsets && p->groups > 1) return fail(DMUON_E_NULL, "offsets must be set for more than one group");
@@ -632,6 +640,7 @@ int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const 
     int e = check_embed_sizes(tokens, rows, width);
     if (e) return e;
     if (ldt < width || ldt > kMaxStride) return fail(DMUON_E_SHAPE, "ldt must be at least width");
+    if (!spans(rows, width, ldt, type_bytes(dtype))) return fail(DMUON_E_SHAPE, "table must end within 2^48 bytes");
     if (!std::isfinite(scale)) return fail(DMUON_E_CFG, "scale must be finite");
     if (tokens == 0) return DMUON_OK;
     if (!ids || !out || (rows > 0 && !table)) return fail(DMUON_E_NULL, "ids, table and out must be set");
@@ -683,6 +692,7 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     int e = check_embed_sizes(tokens, rows, width);
     if (e) return e;
     if (ldg < width || ldg > kMaxStride) return fail(DMUON_E_SHAPE, "ldg must be at least width");
+    if (!spans(tokens, width, ldg, type_bytes(grad_dtype))) return fail(DMUON_E_SHAPE, "grad_out must end within 2^48 bytes");
     if (!std::isfinite(scale)) return fail(DMUON_E_CFG, "scale must be finite");
     if (accumulate != 0 && accumulate != 1) return fail(DMUON_E_CFG, "accumulate must be 0 or 1");
     if (rows == 0) return DMUON_OK;
@@ -754,6 +764,7 @@ int dmuon_ckpt8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     int e = check_codec(rows, cols, dtype);
     if (e) return e;
     if (ldx < cols || ldx > kMaxStride) return fail(DMUON_E_SHAPE, "ldx must be at least cols");
+    if (!spans(rows, cols, ldx, type_bytes(dtype))) return fail(DMUON_E_SHAPE, "x must end within 2^48 bytes");
     if (rows * cols == 0) return DMUON_OK;
     if (!x || !q || !exps) return fail(DMUON_E_NULL, "x, q and exps must be set");
     const int64_t es = type_bytes(dtype), blocks = cdiv(cols, 32);
