@@ -348,7 +348,9 @@ typedef enum { DMUON_I32 = 0, DMUON_I64 = 1 } dmuon_index_dtype;
  *   lse = log Σ exp lse_shard,   loss = lse − Σ (lse_shard − loss_shard),
  * and the backward calls get the joined lse: grad_h is the sum of theirs, grad_w
  * their rows.
- * 0 ≤ tokens ≤ 2^24, 1 ≤ width ≤ 65536, 1 ≤ vocab ≤ 2^30. */
+ * 0 ≤ tokens ≤ 2^24, 1 ≤ width ≤ 65536, 1 ≤ vocab ≤ 2^30; tokens × vocab < 2^45, and
+ * for the backward pass tokens × width < 2^39 (a launch holds fewer than 2^32
+ * threads), both counted in tiles. */
 typedef struct {
   int64_t tokens, width, vocab;
   int32_t dtype;
@@ -394,7 +396,9 @@ int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const 
  * padding_id (−1: none) contribute nothing.  grad_out: device [tokens, width], row
  * stride ldg, grad_dtype.  grad_table: device [rows, width], out_dtype, fully
  * written; with accumulate = 1 the sum is added to what it holds (for a table tied
- * to the head) and rows without tokens are left as they are. */
+ * to the head) and rows without tokens are left as they are.  A launch holds a wave
+ * per 8 tokens and 512 columns and 256 threads per 16 to 256 rows, together fewer
+ * than 2^32 threads (tokens < 2^29 at up to 512 columns); larger calls are refused. */
 int dmuon_embedding_backward_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t* bytes);
 int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t tokens, const void* grad_out,
                              int64_t ldg, int32_t grad_dtype, int64_t rows, int64_t width, float scale,

@@ -28,6 +28,9 @@ constexpr int64_t kMaxLd = (int64_t)1 << 20;        // row strides the kernels t
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxExtent = (int64_t)1 << 48;    // bytes of a strided matrix: the largest dense one (2^30 × 65536 fp32)
 
+// A launch takes fewer than 2^32 threads.
+bool launchable(int64_t workgroups, int64_t threads) { return workgroups < ((int64_t)1 << 32) / threads; }
+
 // C entry bodies: nothing thrown on the host (an allocation that fails) leaves them
 template <typename F>
 int guarded(F&& f) {
@@ -169,12 +172,15 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   pl.D = p.width;
   pl.V = p.vocab;
   pl.ldd = round_up(pl.D, kLdAlign);
-  pl.few = !backward && pl.T <= (pl.f32 ? kFewTokens : kFewTokens / 2);
+  pl.few = !backward && pl.T <= (pl.f32 ? kFewTokens : kFewTokens / 2) && launchable(cdiv(pl.V, kFewRows), kThreads);
   pl.direct_w = pl.few || (!pl.f32 && pl.D % kLdAlign == 0 && kmajor_in_place(p.w, p.ldw, pl.D));
   // the piece: gradient logits of every token (backward) and the copy of W's rows
   const int64_t per_row = (backward ? pl.T * 2 * pl.planes : 0) + (pl.direct_w ? 0 : pl.ldd * 2 * pl.planes);
   int64_t piece = per_row ? std::max<int64_t>(kPieceBytes / per_row, 8 * kTile) : pl.V;
   if (backward) piece = std::min(piece, kMaxLd);       // also the rows' stride of the gradient logits
+  // and what one launch of the logits' tiles takes, of either size: whole tiles of 256, 63 at least
+  const int64_t most_tiles = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads, a tile of 128 rows each
+  piece = std::min(piece, most_tiles / cdiv(pl.T, 128) * 128 / kTile * kTile);
   // equal pieces; where several fill the limit, of as many tile rows as make whole
   // rounds of the weight gradient's tiles over the CUs
   const int64_t n = cdiv(pl.V, std::min(piece, pl.V)), tiles_d = cdiv(pl.D, kTile);
@@ -215,7 +221,7 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
   return pl;
 }
 
-int check_ce(const dmuon_ce_problem* p, std::vector<Range>* rs) {
+int check_ce(const dmuon_ce_problem* p, bool backward, std::vector<Range>* rs) {
   if (!p) return fail(DMUON_E_NULL, "problem is NULL");
   if (!float_type(p->dtype)) return fail(DMUON_E_DTYPE, "dtype must be DMUON_F32 or DMUON_BF16");
   if (!index_type(p->index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
@@ -227,7 +233,11 @@ int check_ce(const dmuon_ce_problem* p, std::vector<Range>* rs) {
   const int64_t es = type_bytes(p->dtype);
   if (!spans(p->tokens, p->width, p->ldh, es) || !spans(p->vocab, p->width, p->ldw, es))
     return fail(DMUON_E_SHAPE, "h and w must end within 2^48 bytes");
-  if (cdiv(p->tokens, 128) * cdiv(p->vocab, 128) > INT32_MAX) return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
+  if (cdiv(p->tokens, 128) * cdiv(p->vocab, 128) > INT32_MAX) return fail(DMUON_E_SHAPE, "tokens × vocab is too large");
+  // the hidden states' gradient in one launch (of the large tiles, at such a size; the
+  // logits and the weight gradient go by pieces that fit)
+  if (backward && !launchable(cdiv(p->tokens, 256) * cdiv(p->width, 256), 512))
+    return fail(DMUON_E_SHAPE, "tokens × width is too large for one launch");
   if (p->tokens > 0 && (!p->h || !p->targets)) return fail(DMUON_E_NULL, "h and targets must be set");
   if (!p->w) return fail(DMUON_E_NULL, "w must be set");
   if (rs) {
@@ -422,8 +432,22 @@ int check_embed_sizes(int64_t tokens, int64_t rows, int64_t width) {
   if (tokens < 0 || tokens > kMaxIds) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^30]");
   if (rows < 0 || rows > kMaxRows) return fail(DMUON_E_SHAPE, "rows must be in [0, 2^30]");
   if (width < 1 || width > kMaxWidth) return fail(DMUON_E_SHAPE, "width must be in [1, 65536]");
-  if (cdiv(tokens, kEmbedHeads * (kThreads / 64)) * cdiv(width, 512) + cdiv(rows, kEmbedRows) > INT32_MAX)
-    return fail(DMUON_E_SHAPE, "too many workgroups in one launch");
+  return DMUON_OK;
+}
+
+// table rows per workgroup that clears rows, and workgroups of the sums
+int64_t embed_zero_rows(int64_t width, int64_t es) {
+  return std::clamp<int64_t>(32768 / (width * es), kEmbedRows, kThreads);
+}
+int64_t embed_sum_groups(int64_t tokens, int64_t width) { return cdiv(tokens, kEmbedHeads * (kThreads / 64)) * cdiv(width, 512); }
+
+// the gradient's largest launches: the sums with the rows that are cleared (counted for
+// an fp32 table), and the run sums, a workgroup per 32 tokens
+int check_embed_grad(int64_t tokens, int64_t rows, int64_t width) {
+  int e = check_embed_sizes(tokens, rows, width);
+  if (e) return e;
+  if (!launchable(embed_sum_groups(tokens, width) + cdiv(rows, embed_zero_rows(width, 4)), kThreads))
+    return fail(DMUON_E_SHAPE, "tokens × width or rows × width is too large for one launch");
   return DMUON_OK;
 }
 
@@ -449,7 +473,7 @@ int dmuon_linear_ce_workspace_size(const dmuon_ce_problem* p, int32_t backward, 
   return guarded([&]() -> int {
     if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
     if (backward != 0 && backward != 1) return fail(DMUON_E_CFG, "backward must be 0 or 1");
-    int e = check_ce(p, nullptr);
+    int e = check_ce(p, backward != 0, nullptr);
     if (e) return e;
     *bytes = p->tokens ? ce_plan(*p, backward != 0, nullptr).bytes : 0;
     return DMUON_OK;
@@ -460,7 +484,7 @@ int dmuon_linear_ce(const dmuon_ce_problem* p, float* losses, float* lse, void* 
                     void* stream) {
   return guarded([&]() -> int {
     std::vector<Range> rs;
-    int e = check_ce(p, &rs);
+    int e = check_ce(p, false, &rs);
     if (e) return e;
     if (p->tokens == 0) return DMUON_OK;
     if (!losses || !lse) return fail(DMUON_E_NULL, "losses and lse must be set");
@@ -517,7 +541,7 @@ int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const 
                              void* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> int {
     std::vector<Range> rs;
-    int e = check_ce(p, &rs);
+    int e = check_ce(p, true, &rs);
     if (e) return e;
     if (!grad_h && !grad_w) return DMUON_OK;
     if (p->tokens > 0 && (!lse || !grad_losses)) return fail(DMUON_E_NULL, "lse and grad_losses must be set");
@@ -674,7 +698,7 @@ int dmuon_embedding(const void* ids, int32_t index_dtype, int64_t tokens, const 
 int dmuon_embedding_backward_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t* bytes) {
   return guarded([&]() -> int {
     if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
-    int e = check_embed_sizes(tokens, rows, width);
+    int e = check_embed_grad(tokens, rows, width);
     if (e) return e;
     *bytes = tokens && rows ? embed_plan(tokens, rows, width, nullptr).bytes : 0;
     return DMUON_OK;
@@ -689,7 +713,7 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     if (!index_type(index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
     if (!float_type(grad_dtype) || !float_type(out_dtype))
       return fail(DMUON_E_DTYPE, "grad_dtype and out_dtype must be DMUON_F32 or DMUON_BF16");
-    int e = check_embed_sizes(tokens, rows, width);
+    int e = check_embed_grad(tokens, rows, width);
     if (e) return e;
     if (ldg < width || ldg > kMaxStride) return fail(DMUON_E_SHAPE, "ldg must be at least width");
     if (!spans(tokens, width, ldg, type_bytes(grad_dtype))) return fail(DMUON_E_SHAPE, "grad_out must end within 2^48 bytes");
@@ -743,13 +767,13 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
     a.grad_f32 = grad_dtype == DMUON_F32;
     a.out_f32 = out_dtype == DMUON_F32;
     a.accumulate = accumulate;
-    a.zero_rows = (int32_t)std::clamp<int64_t>(32768 / (width * type_bytes(out_dtype)), kEmbedRows, kThreads);
+    a.zero_rows = (int32_t)embed_zero_rows(width, type_bytes(out_dtype));
     a.vec_in = rows16(grad_out, ldg, width, type_bytes(grad_dtype));
     a.vec_out = rows16(grad_table, width, width, type_bytes(out_dtype));
     a.scale = scale;
     a.out = grad_table;
     a.slabs = (int32_t)cdiv(width, 512);
-    a.seg_wg = cdiv(tokens, kEmbedHeads * (kThreads / 64)) * a.slabs;
+    a.seg_wg = embed_sum_groups(tokens, width);
     for (int l = 0; l < 2; ++l) a.part[l] = pl.part[l];
     int64_t span = kRun;
     for (int l = 0; l < 2 && span <= tokens; ++l, span *= kRun)

@@ -70,3 +70,30 @@ def test_sizes_at_the_limits_have_a_workspace(backward, dtype):
     for kw in (dict(tokens=1 << 24), dict(tokens=1 << 24, n=65536, ldg=65536, k=65536), dict(tokens=1 << 24, offsets=at(6), groups=1 << 20)):
         p = wg(grad_dtype=dtype, **kw)
         assert B.lib().dmuon_ckpt8_wgrad_workspace_size(ctypes.byref(p), ctypes.byref(out)) == 0 and 0 < out.value < 1 << 55
+
+
+def test_launches_of_the_table_gradient_hold_fewer_than_2_32_threads(stop):
+    """Refused before anything is enqueued; they were accepted and failed at a launch
+    behind the sort."""
+    need = ctypes.c_size_t(0)
+    for tokens, rows, width, rc in ((1 << 29, 100, 8, SHAPE), ((1 << 29) - 64, 100, 8, HIP), (1 << 28, 100, 1024, SHAPE),
+                                    ((1 << 28) - 256, 100, 1024, HIP), (1 << 22, 100, 65536, SHAPE), (1000, 1 << 30, 64, HIP),
+                                    (1000, 1 << 28, 65536, SHAPE)):
+        got = embed_bwd(tokens=tokens, rows=rows, width=width, ldg=width, ids=1 << 40, g=1 << 50, out=1 << 52, ws=1 << 55, nbytes=1 << 50)
+        assert got == rc, (tokens, rows, width)
+        size = B.lib().dmuon_embedding_backward_workspace_size(tokens, rows, width, ctypes.byref(need))
+        assert (size == SHAPE) == (rc == SHAPE)
+    # the lookup's launch walks over its rows and takes them all
+    assert embed(tokens=1 << 30, rows=1 << 30, width=8, ids=1 << 40, table=1 << 50, out=1 << 52) == HIP
+
+
+def test_launches_of_the_cross_entropy_hold_fewer_than_2_32_threads(stop):
+    p = ce(tokens=1 << 24, width=32768, ldh=32768, ldw=32768, vocab=100, h=1 << 46, w=1 << 50, targets=1 << 51)
+    far = dict(lse=1 << 52, ws=1 << 56, nbytes=1 << 54)
+    assert ce_bwd(p, gl=1 << 53, gh=1 << 54, gw=1 << 55, **far) == SHAPE
+    assert ce_size(p, 1)[0] == SHAPE and ce_size(p, 0)[0] == 0
+    assert ce_fwd(p, losses=1 << 53, **far) == HIP
+    # few tokens: a workgroup per 64 words up to 2^30 − 64 of them, then tiles of 128
+    # (8 bytes of statistics per token and either)
+    few, tiles = ce_size(ce(tokens=1, vocab=(1 << 30) - 64))[1], ce_size(ce(tokens=1, vocab=1 << 30))[1]
+    assert few > (1 << 27) - 64 and tiles < (1 << 26) + (1 << 16)
