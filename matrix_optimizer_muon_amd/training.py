@@ -9,8 +9,11 @@
 
 The functions marshal arguments only and enqueue on ``stream`` (the current
 stream when None); results are allocated on it.  They take part in no autograd
-graph: a caller wires them into its backward pass.  Gradients come in the layout
-``muon_step`` and ``adamw_step`` read (dense, bf16 or fp32).
+graph: a caller wires them into its backward pass, for instance as the two halves
+of a ``torch.autograd.Function``.  ``linear_cross_entropy`` and ``embedding`` refuse
+inputs that require gradients where autograd records (outside ``torch.no_grad()``
+and a Function's ``forward``), since their results would drop them.  Gradients come
+in the layout ``muon_step`` and ``adamw_step`` read (dense, bf16 or fp32).
 """
 from __future__ import annotations
 
@@ -29,6 +32,17 @@ CKPT_BLOCK = 32          # columns that share one exponent byte
 
 def _ptr(t):
     return ctypes.c_void_p(None if t is None else t.data_ptr())
+
+
+def _no_graph(call, **tensors):
+    """Refuse inputs whose gradients autograd expects to flow through this call."""
+    import torch
+    if not torch.is_grad_enabled():
+        return
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.requires_grad:
+            raise ValueError(f"{name} requires gradients, which {call} does not record: call it under torch.no_grad() or in "
+                             f"a torch.autograd.Function and pass the gradients on with {call}_backward, or detach {name}")
 
 
 def _gpu(t, what):
@@ -184,6 +198,7 @@ def linear_cross_entropy(h, w, targets, *, ignore_index=-100, workspace=None, st
     is the logsumexp of the shards' and the loss lse − Σ (lse_shard − loss_shard).
     """
     import torch
+    _no_graph("linear_cross_entropy", h=h, w=w)
     prob = _ce_problem(h, w, targets, ignore_index)
     with _on(stream, h, w, targets) as on:
         losses = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
@@ -233,6 +248,7 @@ def embedding(ids, table, *, scale=1.0, out=None, stream=None):
     ids: int64 or int32 of any shape; table: [rows, width] (rows may be strided).
     """
     import torch
+    _no_graph("embedding", table=table)
     _dense(ids, "ids")
     if isinstance(table, torch.Tensor) and table.dim() != 2:
         raise ValueError("table must be 2-D (rows, width)")
