@@ -105,6 +105,19 @@ class Ckpt8WgradProblem(ctypes.Structure):
 _lib = None
 
 
+def _check_library(L):
+    """The library is of this ABI and whole: entry points were added without a new number,
+    so an older build may lack some."""
+    missing = [name for name in EXPORTED if not hasattr(L, name)]
+    if "dmuon_abi_version" not in missing:
+        L.dmuon_abi_version.restype = ctypes.c_int32
+        L.dmuon_abi_version.argtypes = []
+        if L.dmuon_abi_version() != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} has ABI {L.dmuon_abi_version()}, expected {ABI_VERSION}: rebuild it")
+    if missing:
+        raise RuntimeError(f"{LIB_PATH} lacks {', '.join(missing[:3])}{' …' if len(missing) > 3 else ''}: rebuild it")
+
+
 def lib():
     """Load libdmuon_ns.so (built in-tree); raise if it is missing."""
     global _lib
@@ -113,6 +126,7 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built: run `python -m matrix_optimizer_muon_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
+    _check_library(L)
     vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
     P = ctypes.POINTER
@@ -145,19 +159,9 @@ def lib():
     L.dmuon_ckpt8_wgrad.argtypes = [P(Ckpt8WgradProblem), vp, sz, vp]
     L.dmuon_last_error.restype = ctypes.c_char_p
     L.dmuon_last_error.argtypes = []
-    L.dmuon_abi_version.restype = i32
-    for name in ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_muon_step",
-                 "dmuon_muon_step_prepare", "dmuon_muon_step_run", "dmuon_muon_step_noalloc",
-                 "dmuon_ns_batched_workspace_size", "dmuon_ns_batched", "dmuon_lpt_assign",
-                 "dmuon_adamw_step_workspace_size", "dmuon_adamw_step",
-                 "dmuon_gemm_nt", "dmuon_phase_timing", "dmuon_phase_timing_read",
-                 "dmuon_linear_ce_workspace_size", "dmuon_linear_ce", "dmuon_linear_ce_backward",
-                 "dmuon_embedding", "dmuon_embedding_backward_workspace_size",
-                 "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
-                 "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad"]:
-        getattr(L, name).restype = ctypes.c_int
-    if L.dmuon_abi_version() != ABI_VERSION:
-        raise RuntimeError(f"{LIB_PATH} has ABI {L.dmuon_abi_version()}, expected {ABI_VERSION}: rebuild it")
+    for name in EXPORTED:
+        if name != "dmuon_last_error":
+            getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
 
