@@ -410,8 +410,8 @@ int dmuon_embedding_backward(const void* ids, int32_t index_dtype, int64_t token
  * byte: b is the biased fp32 exponent of their largest magnitude, or one more where
  * that would round to 128 (not past 254, where q saturates at ±127), and
  * q = rint(x·2^(133 − b)), half to even.  So every value is kept to within half a
- * step 2^(b − 134), at most 2^−7 of the block's largest.  Blocks below 2^−126 become
- * zeros (b = 0); a block with an infinity or NaN reads back as NaN throughout
+ * step, 2^(b − 134), or a step where q saturates, either way at most 1/127.5 of the
+ * block's largest.  Blocks below 2^−126 become zeros (b = 0); a block with an infinity or NaN reads back as NaN throughout
  * (b = 255).  Every value is exact in bf16.
  * x: device [rows, cols], row stride ldx; q: device int8 [rows, cols]; exps: device
  * uint8 [rows, ceil(cols/32)]; out: device [rows, cols].  rows ≤ 2^30, cols ≤ 65536. */
@@ -429,7 +429,7 @@ int dmuon_ckpt8_dequantize(const int8_t* q, const uint8_t* exps, int64_t rows, i
  * out is [groups, n, k] and group g sums the rows offsets(g) … offsets(g + 1) − 1
  * (the tokens of one expert; an empty group gives zeros); rows outside every group
  * are not used.  Offsets are clamped to [0, tokens], a falling one makes an empty
- * group.  groups ≤ 2^20 (ignored without offsets). */
+ * group.  groups ≤ 2^20 (without offsets 0 or 1: more are refused). */
 typedef struct {
   int64_t tokens, n, k;
   int32_t grad_dtype;

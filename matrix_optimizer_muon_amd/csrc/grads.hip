@@ -1897,9 +1897,10 @@ __global__ __launch_bounds__(kThreads) void k_embed_grad(EmbedGradArgs a) {
 // byte and the value q·2^(b − 133).  b is the biased fp32 exponent of the block's
 // largest magnitude (one more where that would round to 128, unless b = 254, where
 // q saturates at 127), so that q = rint(x·2^(133 − b)) has |q| ≤ 127 and every
-// value is kept to within 2^(b − 134), half a step.  A block whose largest
-// magnitude is below 2^−126 becomes zeros (b = 0); a block that holds an infinity
-// or NaN reads back as NaN (b = 255).  q·2^(b − 133) is exact in bf16.
+// value is kept to within 2^(b − 134), half a step, or a step where q saturates (at
+// most 1/127.5 of the block's largest).  A block whose largest magnitude is below 2^−126
+// becomes zeros (b = 0); a block that holds an infinity or NaN reads back as NaN
+// (b = 255).  q·2^(b − 133) is exact in bf16.
 // Four threads share a block, 8 columns each.  Bound by memory: 8192 × 11008 bf16 stored
 // in 50 µs (5.4 TB/s), read back in 40 (6.8 TB/s, what was just stored from the caches).
 // ---------------------------------------------------------------------------

@@ -311,8 +311,9 @@ def checkpoint_quantize(x, *, out=None, stream=None):
     """An activation kept in 8 bits: (q, exps), int8 of x's shape and uint8 [..., ceil(columns / 32)].
 
     x: [..., columns], bf16 or fp32.  x ≈ q·2^(exps − 133) with one exponent per 32
-    columns of a row, every value to within half a step (at most 2^−7 of the
-    block's largest).  A block with an infinity or NaN reads back as NaN.
+    columns of a row, every value to within 1/127.5 of the block's largest (half a
+    step; a step for the last values below 2^128).  A block with an infinity or NaN
+    reads back as NaN.
     ``out``: a (q, exps) pair to write.
     """
     import torch
