@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <exception>
 #include <numeric>
 #include <string>
 #include <vector>
@@ -31,14 +30,15 @@ constexpr int64_t kMaxExtent = (int64_t)1 << 48;    // bytes of a strided matrix
 // A launch takes fewer than 2^32 threads.
 bool launchable(int64_t workgroups, int64_t threads) { return workgroups < ((int64_t)1 << 32) / threads; }
 
-// C entry bodies: nothing thrown on the host (an allocation that fails) leaves them
+// C entry bodies: nothing thrown on the host leaves them.  Where an allocation failed the
+// message must not need one: it fits a string's own 15 bytes.
 template <typename F>
 int guarded(F&& f) {
   clear_error();
   try {
     return f();
-  } catch (const std::exception& e) {
-    return fail(DMUON_E_HIP, std::string("host error: ") + e.what());
+  } catch (...) {
+    return fail(DMUON_E_HIP, "out of memory");
   }
 }
 
