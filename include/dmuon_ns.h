@@ -378,7 +378,10 @@ int dmuon_linear_ce(const dmuon_ce_problem* problem, float* losses, float* lse, 
  * the joined value of a vocabulary in shards.  grad_losses: device fp32 [tokens], for a mean 1/n at every token;
  * a token whose value is 0 is treated as ignored.  grad_h, grad_w: device, dense,
  * of the problem's dtype, fully written; NULL where not wanted.  For bf16, dz is
- * rounded to bf16 once (relative to the largest finite |grad_losses|). */
+ * rounded to bf16 once (relative to the largest finite |grad_losses|): the gradients
+ * are about 0.002 of their norm away from exact ones, where their own rounding to
+ * bf16 alone makes 0.0017.  fp32 copies of h and w give fp32 gradients instead, for
+ * about six times the products. */
 int dmuon_linear_ce_backward(const dmuon_ce_problem* problem, const float* lse, const float* grad_losses,
                              void* grad_h, void* grad_w, void* workspace, size_t workspace_bytes,
                              void* stream);

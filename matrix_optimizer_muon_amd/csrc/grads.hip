@@ -170,7 +170,8 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackArgs a) {
 // weights relative to it and the products' epilogues multiply it back, so that a
 // uniform weight leaves p − δ unscaled when it is rounded to bf16 and tiny weights do
 // not underflow.
-// Latency bound: 4 µs for 8192 tokens (a walk over one range per thread: 39).
+// Latency bound: forward 5.6 µs for 4096 tokens, backward 8.7 for 8192 (a walk over one
+// range per thread: 39).
 // ---------------------------------------------------------------------------
 constexpr int kScanThreads = 1024;
 constexpr int kScanRows = 8;
@@ -768,14 +769,18 @@ __device__ __forceinline__ int live_block(int G) {
 //   forward:  per tile and token the largest logit and Σ exp(z − largest), and the
 //             target's logit;
 //   backward: dZ(t, v) = g_t·(exp(z − lse_t) − [v = target]), rounded to bf16 (one
-//             rounding; the matrix cores take bf16; fp32 operands: three planes).
+//             rounding, at most 2⁻⁸ of each entry: the matrix cores take bf16, and a
+//             second plane would double both products; fp32 operands: three planes).
+//             The gradients are then 0.0018 to 0.0023 of their norm away from the
+//             64-bit ones, their own rounding to bf16 alone 0.0017; in fp32 4·10⁻⁷.
 // The exponentials are 2^((z − largest)·log₂e) and 2^((z − lse)·log₂e), the difference
 // first: it is exact where the two are close, so that the largest logit's own term is 1
 // and a certain token's probability too, whatever their size (one fused multiply-add,
 // z·log₂e − lse·log₂e, is off by lse·2⁻²⁴ in the exponent).  The target's entry is looked
 // for only in parts of a tile that hold one (6% of them at 128000 words).  Bound by the product (see the large core): 4096 tokens × 4096, vocabulary
-// 32000, forward 870 µs = 1.23 PFLOP/s; 8192 × 4096 and 16384 rows, backward 867 µs =
-// 1.27; of a tile's 109 µs about 10 are prologue and epilogue, which nothing overlaps.
+// 32000, forward: the whole call 870 µs = 1.23 PFLOP/s (the kernel under the profiler, at
+// other clocks, 875 to 1210); 8192 × 4096 and 16384 rows, backward: 850 to 890 µs on
+// average = 1.23 to 1.29.  Of a tile's 109 µs about 10 are prologue and epilogue, which nothing overlaps.
 // ---------------------------------------------------------------------------
 template <typename S, bool BACKWARD, bool F32>
 __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
@@ -929,11 +934,14 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
 // is, of either type and any stride; fp32 values are split into planes in registers,
 // their leading product summed apart from the five corrections.
 // W's loads are nontemporal: with the caches full of another kernel's results, bf16,
-// 16 tokens × 2048 and a vocabulary of 32000, the call takes 43 µs, with plain loads 61.
-// The tiles of 128 against this, same state: bf16 × 4096, vocabulary 32000 and 128000:
-// 16 tokens 113 and 71, 268 and 240, 32 tokens 120 and 81, 262 and 284, 64 tokens 113
-// and 110, 262 and 363 (not taken); fp32 × 2048, 32000: 16 tokens 450 and 81 µs, 64
-// tokens 466 and 136 (the tiles need W as planes in memory first).
+// 16 tokens × 2048 and a vocabulary of 32000, the call takes 42 µs, with plain loads 61.
+// The tiles of 128 against this, bf16, behind another kernel's results: 16 tokens × 4096,
+// vocabulary 8000 75 and 41 µs, 32000 129 and 71, 128000 281 and 242; 32 tokens 76 and 47,
+// 130 and 82, 292 and 284.  Called back to back, 32 tokens: 63 and 43, 75 and 78, 224 and
+// 282: there the tiles win from a W of about 256 MB on (at 16 tokens from 1 GB, 221 and
+// 238), which is not taken: a loss follows the model that made its hidden states.  64
+// tokens behind a full cache 113 and 110, 262 and 363 (not taken).  fp32 × 2048, 32000:
+// 16 tokens 405 and 75 µs, 64 tokens 421 and 135 (the tiles need W as planes first).
 // ---------------------------------------------------------------------------
 // The scan and the packing of so few tokens, in one launch: every wave finds the
 // tokens' places by itself with one ballot.
@@ -1191,10 +1199,10 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
 // and planned splits of 2, 160 of 256 workgroups had work, and the gradient took 644
 // µs over the vocabulary of 50257 against 435 with the splits spread over them.
 // Bound by the core: 8192 tokens × 4096 and 16384 vocabulary rows, weight gradient
-// 828 µs = 1.33 PFLOP/s, hidden states 851 = 1.29; 8192 × 4096 × 11008 from a
-// checkpoint 560 to 600 µs, 688 tiles in three rounds of 256 CUs.  Short K is bound by
-// the stores: 64 experts of 1408 × 2048 over 250 tokens each, 738 MB of fp32, 200 to
-// 245 µs.
+// 815 to 850 µs = 1.32 PFLOP/s, hidden states 840 to 870 = 1.29; 8192 × 4096 × 11008 from
+// a checkpoint 630 to 670, at best 600, 688 tiles in three rounds of 256 CUs.  Short K is
+// bound by the stores: 64 experts of 1408 × 2048 over 250 tokens each, 738 MB of fp32,
+// 240 to 270 µs, at best 219 (averages of runs under the profiler, at its clocks).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int row_splits(int rows, const RowSpread& p) {
   if (rows <= 0) return 1;
