@@ -50,7 +50,7 @@
  *   call return DMUON_E_HIP at a named point as a failed HIP call would:
  *   "plan" (before anything is enqueued), "table" (the table copy) or a phase
  *   name ("ingest", "norm", "gram", "square", "apply", "update", "adamw", or one of
- *   the training gradients' phases 8 to 15 below: that phase's first launch, the
+ *   the phases 8 to 19 below: that phase's first launch, the
  *   earlier launches being enqueued).
  * - DMUON_DEBUG_SYNC (environment, for debugging; set and not "0") waits for
  *   each launch to finish before the next is enqueued, so a call returns only
@@ -451,6 +451,69 @@ int dmuon_ckpt8_wgrad_workspace_size(const dmuon_ckpt8_wgrad_problem* problem, s
 int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* problem, void* workspace, size_t workspace_bytes,
                       void* stream);
 
+/* ---- log probabilities ----------------------------------------------------
+ * What policy-gradient training and distillation read of a model, and its gradients.
+ * Types, strides, alignment and determinism as for the training gradients above. */
+
+/* Rows of logits in memory.  With x(t, v) = scale·z(t, v):
+ *   lse(t) = log Σ_v exp x(t, v),   logprob(t) = x(t, target(t)) − lse(t),
+ *   entropy(t) = −Σ_v p(t, v)·log p(t, v),   p = exp(x − lse)
+ * and the `top` largest x of each row as their indices and log probabilities, largest
+ * first, equal ones by rising index.
+ *   dtype        dmuon_dtype of the logits (and their gradient)
+ *   index_dtype  dmuon_index_dtype of targets
+ *   logits       device [tokens, vocab], row stride ld
+ *   targets      device [tokens], or NULL: no row has a target and none is ignored.  A
+ *                row whose target equals ignore_index has logprob, entropy and lse 0, ids
+ *                −1 with log probability 0 and no gradient, and its logits are not read;
+ *                one of DMUON_TARGET_ELSEWHERE (unless that is ignore_index) has the
+ *                log probability −lse and the gradient without its target's term; any
+ *                other target outside [0, vocab) gives a log probability of NaN and no
+ *                gradient
+ *   scale        in [2^-20, 2^20]: 1/temperature
+ *   top          0 … 128, at most vocab (dmuon_logprobs alone)
+ * Logits of -inf have probability 0; in a row of nothing else lse and the log
+ * probabilities are -inf, and the entropy and the gradient 0.  A NaN or +inf makes the
+ * row's lse, log probabilities, entropy and gradient NaN; among the alternatives NaN
+ * stands with -inf.  scale·z must stay within fp32.
+ * Columns in shards: each shard's call gets its columns and the shifted targets as in
+ * dmuon_ce_problem; with p_s = exp(lse_s − lse),
+ *   lse = log Σ exp lse_s,   logprob = Σ (logprob_s + lse_s) − lse,
+ *   entropy = lse − Σ p_s·(lse_s − entropy_s),
+ * and the backward calls get the joined lse and entropy.
+ * 0 ≤ tokens ≤ 2^24, 1 ≤ vocab ≤ 2^22, fewer than 2^32 threads in a launch: 256 (64 for
+ * short rows) per row and 8192 columns of the gradient, or 131072 of the others. */
+typedef struct {
+  int64_t tokens, vocab;
+  int32_t dtype;
+  int32_t index_dtype;
+  const void* logits;
+  int64_t ld;
+  const void* targets;
+  int64_t ignore_index;
+  float scale;
+  int32_t top;
+} dmuon_logprobs_problem;
+
+/* Bytes of workspace of dmuon_logprobs (host only, no HIP call; 0 where a workgroup
+ * takes a whole row: then the workspace may be NULL). */
+int dmuon_logprobs_workspace_size(const dmuon_logprobs_problem* problem, size_t* bytes);
+
+/* logprobs (NULL without targets), entropy, lse: device fp32 [tokens]; top_ids: device
+ * int64 [tokens, top], top_logprobs: device fp32 [tokens, top] (not read for top = 0). */
+int dmuon_logprobs(const dmuon_logprobs_problem* problem, float* logprobs, float* entropy, float* lse, int64_t* top_ids,
+                   float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream);
+
+/* With g, e the gradients of logprob and entropy (device fp32 [tokens], either may be
+ * NULL; a row where both are 0 has none) and l = x − lse:
+ *   grad_logits(t, v) = scale·(g(t)·([v = target(t)] − p) − e(t)·p·(l + entropy(t)))
+ * lse, entropy: as dmuon_logprobs wrote them (entropy is read with grad_entropy only).
+ * grad_logits: device [tokens, vocab], row stride ld_grad, of the logits' dtype; it may
+ * be the logits themselves, with their stride. */
+int dmuon_logprobs_backward(const dmuon_logprobs_problem* problem, const float* lse, const float* entropy,
+                            const float* grad_logprobs, const float* grad_entropy, void* grad_logits, int64_t ld_grad,
+                            void* stream);
+
 /* Plain NT product C = A·Bᵀ on the matrix-core kernel the step uses (a test hook
  * for the contraction core).  A: M×K (lda elements per row), B: N×K (ldb), both
  * dtype (bf16 or fp32), device; C: M×N fp32 (ldc), device.  lda and ldb must be
@@ -503,7 +566,8 @@ int dmuon_debug_slice_buffers(const dmuon_tensor* tensors, int32_t n_tensors, co
  * copies), 1 norm finalize, 2 Gram, 3 square+poly, 4 apply, 5 update (k = 0
  * only), 6 gemm_nt, 7 adamw, and of the training gradients 8 ce_pack (list of
  * tokens, operand copies), 9 ce_logits, 10 ce_rows (losses), 11 ce_grads (the two
- * products), 12 embed, 13 embed_grad (sort and sums), 14 ckpt_codec, 15 ckpt_wgrad. */
+ * products), 12 embed, 13 embed_grad (sort and sums), 14 ckpt_codec, 15 ckpt_wgrad, then
+ * 16 logprobs, 17 logprobs_grad, 18 grad_norm, 19 grad_clip. */
 int dmuon_phase_timing(int32_t enable);
 int dmuon_phase_timing_read(double* ms, int64_t* count, int32_t n);
 

@@ -32,7 +32,7 @@ PREC = {"bf16": 0, "f32": 1}
 I32, I64 = 0, 1
 PHASES = ["ingest", "norm", "gram", "square", "apply", "update", "gemm_nt", "adamw",
           "ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec",
-          "ckpt_wgrad"]
+          "ckpt_wgrad", "logprobs", "logprobs_grad", "grad_norm", "grad_clip"]
 EXPORTED = ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_muon_step",
             "dmuon_muon_step_prepare", "dmuon_muon_step_run", "dmuon_muon_step_noalloc",
             "dmuon_ns_batched_workspace_size",
@@ -42,7 +42,8 @@ EXPORTED = ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_m
             "dmuon_linear_ce_workspace_size", "dmuon_linear_ce", "dmuon_linear_ce_backward",
             "dmuon_embedding", "dmuon_embedding_backward_workspace_size",
             "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
-            "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad"]
+            "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad",
+            "dmuon_logprobs_workspace_size", "dmuon_logprobs", "dmuon_logprobs_backward"]
 ABI_VERSION = 5
 
 
@@ -102,6 +103,13 @@ class Ckpt8WgradProblem(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("reserved", ctypes.c_int32), ("out", ctypes.c_void_p)]
 
 
+class LogprobsProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("index_dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("targets", ctypes.c_void_p), ("ignore_index", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("top", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -157,6 +165,9 @@ def lib():
     L.dmuon_ckpt8_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, vp]
     L.dmuon_ckpt8_wgrad_workspace_size.argtypes = [P(Ckpt8WgradProblem), P(sz)]
     L.dmuon_ckpt8_wgrad.argtypes = [P(Ckpt8WgradProblem), vp, sz, vp]
+    L.dmuon_logprobs_workspace_size.argtypes = [P(LogprobsProblem), P(sz)]
+    L.dmuon_logprobs.argtypes = [P(LogprobsProblem), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dmuon_logprobs_backward.argtypes = [P(LogprobsProblem), vp, vp, vp, vp, vp, i64, vp]
     L.dmuon_last_error.restype = ctypes.c_char_p
     L.dmuon_last_error.argtypes = []
     for name in EXPORTED:

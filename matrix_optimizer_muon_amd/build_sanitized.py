@@ -16,8 +16,8 @@ import sys
 
 from . import build as _build
 
-HOST_SOURCES = ["abi.cpp", "grads.cpp", "lpt.cpp"]
-KERNEL_SOURCES = ["kernels.hip", "grads.hip"]
+HOST_SOURCES = [s for s in _build.SOURCES if s.endswith(".cpp")]
+KERNEL_SOURCES = [s for s in _build.SOURCES if s.endswith(".hip")]
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer"]
 
 

@@ -110,7 +110,8 @@ static uint32_t fnv1a(const char* p, size_t n) {
 // is skipped on a stream under graph capture, where it is not allowed.
 static const char* const kPhaseNames[PH_TOTAL] = {
     "ingest",  "norm",      "gram",    "square",   "apply", "update",     "gemm_nt",    "adamw",
-    "ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec", "ckpt_wgrad"};
+    "ce_pack", "ce_logits", "ce_rows", "ce_grads", "embed", "embed_grad", "ckpt_codec", "ckpt_wgrad",
+    "logprobs", "logprobs_grad", "grad_norm", "grad_clip"};
 const char* phase_name(int phase) { return kPhaseNames[phase]; }
 CallEnv call_env() {
   CallEnv f;

@@ -13,85 +13,10 @@
 #include <mutex>
 
 #include "core.hpp"
+#include "elements.hpp"
 #include "grads.hpp"
 
 namespace dmuon {
-
-// ---------------------------------------------------------------------------
-// small helpers
-// ---------------------------------------------------------------------------
-// 8 consecutive elements as fp32: 16-byte loads where `vec`, else element by
-// element with zeros from column `left` on
-__device__ __forceinline__ void unpack8(const u32x4_t& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(gptr<const uint16_t> p, bool vec, int left, float (&v)[8]) {
-  if (vec) {
-    const u32x4_t u = *(gptr<const u32x4_t>)p;
-    unpack8(u, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? bf16_to_f32(p[e]) : 0.f;
-  }
-}
-__device__ __forceinline__ void load8(gptr<const float> p, bool vec, int left, float (&v)[8]) {
-  if (vec) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4_t a = ((gptr<const f32x4_t>)p)[h];
-      v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.f;
-  }
-}
-__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
-  return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-}
-// NT: nontemporal, for results that this library does not read again (the lookup of
-// 32768 tokens 85.6 → 83.6 µs, a checkpoint stored and read back 92 → 86)
-template <bool NT = false>
-__device__ __forceinline__ void store8(gptr<uint16_t> p, bool vec, int left, const float (&v)[8]) {
-  if (vec) {
-    if (NT) __builtin_nontemporal_store(pack8(v), (gptr<u32x4_t>)p);
-    else *(gptr<u32x4_t>)p = pack8(v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) p[e] = f32_to_bf16(v[e]);
-  }
-}
-template <bool NT = false>
-__device__ __forceinline__ void store8(gptr<float> p, bool vec, int left, const float (&v)[8]) {
-  if (vec) {
-    const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-    if (NT) {
-      __builtin_nontemporal_store(a, (gptr<f32x4_t>)p);
-      __builtin_nontemporal_store(b, (gptr<f32x4_t>)p + 1);
-    } else {
-      ((gptr<f32x4_t>)p)[0] = a;
-      ((gptr<f32x4_t>)p)[1] = b;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) p[e] = v[e];
-  }
-}
-
-// An int32 or int64 index, as its dwords and without a branch, so that several
-// loads of a thread are in flight together.
-__device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t i) {
-  const gptr<const int32_t> q = glob((const int32_t*)p) + (i << idx64);
-  const int32_t lo = q[0], hi = q[idx64];
-  return (int64_t)(((uint64_t)(uint32_t)(idx64 ? hi : lo >> 31) << 32) | (uint32_t)lo);
-}
 
 // x = hi + mid + lo, each a bf16 value: hi is x rounded to bf16 (cut off where
 // rounding would overflow), mid the rest rounded, lo the rest of that: 24 bits.
@@ -1996,12 +1921,6 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_read(CodecArgs a) {
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-// Workgroups of a grid-stride kernel: enough to fill 256 CUs several times over
-static unsigned stride_grid(int64_t items) {
-  const int64_t wg = cdiv(items, kThreads);
-  return (unsigned)(wg < 1 ? 1 : (wg < 16384 ? wg : 16384));
-}
-
 // Dynamic LDS limit of a kernel, raised once per device (first calls may come from
 // several threads); `ready` holds one bit per device.
 static int raise_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
@@ -2016,15 +1935,6 @@ static int raise_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready
   if (e == 0 && bit) ready.fetch_or(bit, std::memory_order_release);
   return e;
 }
-
-#define DMUON_LAUNCH(phase, stream, kernel, grid, block, lds, ...)                             \
-  do {                                                                                         \
-    timing_before(phase, stream);                                                              \
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, (hipStream_t)(stream), __VA_ARGS__); \
-    const int err_ = (int)hipGetLastError();                                                   \
-    timing_after(phase, stream);                                                               \
-    return err_;                                                                               \
-  } while (0)
 
 int launch_pack(const PackArgs& a, int phase, void* stream) {
   DMUON_LAUNCH(phase, stream, k_pack, stride_grid(round_up(a.rows, 8) * (a.ldd / 8)), kThreads, 0, a);

@@ -36,7 +36,11 @@ enum Phase : int {
   PH_EMBED_GRAD = 13,  // token sort and the table's gradient
   PH_CKPT_CODEC = 14,  // 8-bit activation checkpoints: store, read back
   PH_CKPT_WGRAD = 15,  // weight gradient from a checkpoint
-  PH_TOTAL = 16
+  PH_LOGPROBS = 16,    // log probabilities from logits: entropies, alternatives
+  PH_LOGPROBS_GRAD = 17,  // and their gradient
+  PH_GRAD_NORM = 18,   // sums of squares of many gradients
+  PH_GRAD_CLIP = 19,   // the clipped gradients
+  PH_TOTAL = 20
 };
 
 // One tensor (2-D = batch 1, or 3-D batch of slices) as the kernels see it.

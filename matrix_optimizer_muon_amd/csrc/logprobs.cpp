@@ -1,0 +1,174 @@
+// C entry points of the log probabilities from logits in memory, with entropies and
+// alternatives, and of their gradient.
+#include <cmath>
+#include <vector>
+
+#include "entry.hpp"
+#include "grads.hpp"
+#include "logprobs.hpp"
+
+namespace dmuon {
+namespace {
+
+constexpr int64_t kMaxVocab = (int64_t)1 << 22;     // words of a row of logits
+constexpr int64_t kMaxKeys = 6144;                  // candidates of a row's pieces together, in the joining workgroup's LDS
+static_assert(kMaxVocab <= kMaxKeys / kTopMost * kPieceMost, "the largest vocabulary in pieces that can be joined");
+
+struct RowsPlan {
+  int64_t piece, pieces;
+  RowStat* stats;
+  uint64_t* cand;
+  size_t bytes;
+};
+
+// Columns per workgroup.  A row is one piece unless it is too long for a workgroup or the
+// rows are too few to fill the card.
+RowsPlan rows_plan(const dmuon_logprobs_problem& p, char* base) {
+  RowsPlan pl{};
+  int64_t n = std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
+  if (p.top == 0 && p.vocab <= kWaveRow) n = 1;
+  n = std::max<int64_t>({n, cdiv(p.vocab, kPieceMost), 1});
+  pl.piece = round_up(cdiv(p.vocab, n), 8);
+  pl.pieces = cdiv(p.vocab, pl.piece);
+  if (pl.pieces == 1) return pl;
+  Carver c{base};
+  pl.stats = c.take<RowStat>(p.tokens * pl.pieces);
+  if (p.top) pl.cand = c.take<uint64_t>(p.tokens * pl.pieces * p.top);
+  pl.bytes = c.off;
+  return pl;
+}
+
+int check_rows(const dmuon_logprobs_problem* p, bool backward) {
+  if (!p) return fail(DMUON_E_NULL, "problem is NULL");
+  if (!float_type(p->dtype)) return fail(DMUON_E_DTYPE, "dtype must be DMUON_F32 or DMUON_BF16");
+  if (!index_type(p->index_dtype)) return fail(DMUON_E_DTYPE, "index_dtype must be DMUON_I32 or DMUON_I64");
+  if (p->tokens < 0 || p->tokens > kMaxTokens) return fail(DMUON_E_SHAPE, "tokens must be in [0, 2^24]");
+  if (p->vocab < 1 || p->vocab > kMaxVocab) return fail(DMUON_E_SHAPE, "vocab must be in [1, 2^22]");
+  if (p->ld < p->vocab || p->ld > kMaxStride) return fail(DMUON_E_SHAPE, "ld must be at least vocab");
+  if (!spans(p->tokens, p->vocab, p->ld, type_bytes(p->dtype))) return fail(DMUON_E_SHAPE, "logits must end within 2^48 bytes");
+  if (!(p->scale >= 0x1p-20f && p->scale <= 0x1p20f)) return fail(DMUON_E_CFG, "scale must be in [2^-20, 2^20]");
+  if (!backward && (p->top < 0 || p->top > kTopMost || p->top > p->vocab))
+    return fail(DMUON_E_CFG, "top must be in [0, 128] and at most vocab");
+  if (p->tokens > 0 && !p->logits) return fail(DMUON_E_NULL, "logits must be set");
+  if (p->tokens > 0) {
+    const int64_t work = backward ? p->tokens * cdiv(p->vocab, kThreads * kGradUnits * 8) : p->tokens * rows_plan(*p, nullptr).pieces;
+    if (!launchable(work, kThreads)) return fail(DMUON_E_SHAPE, "tokens × vocab is too large for one launch");
+  }
+  return DMUON_OK;
+}
+
+void rows_ranges(const dmuon_logprobs_problem& p, bool logits, std::vector<Range>& rs) {
+  if (logits) add_range(rs, p.logits, strided_bytes(p.tokens, p.vocab, p.ld, type_bytes(p.dtype)), true);
+  add_range(rs, p.targets, p.tokens * (p.index_dtype == DMUON_I64 ? 8 : 4), true);
+}
+
+}  // namespace
+}  // namespace dmuon
+
+using namespace dmuon;
+
+extern "C" {
+
+int dmuon_logprobs_workspace_size(const dmuon_logprobs_problem* p, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
+    int e = check_rows(p, false);
+    if (e) return e;
+    *bytes = p->tokens ? rows_plan(*p, nullptr).bytes : 0;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_logprobs(const dmuon_logprobs_problem* p, float* logprobs, float* entropy, float* lse, int64_t* top_ids,
+                   float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int e = check_rows(p, false);
+    if (e) return e;
+    if (p->tokens == 0) return DMUON_OK;
+    if (!entropy || !lse) return fail(DMUON_E_NULL, "entropy and lse must be set");
+    if (!logprobs != !p->targets) return fail(DMUON_E_NULL, "logprobs and targets must be set together");
+    if (p->top && (!top_ids || !top_logprobs)) return fail(DMUON_E_NULL, "top_ids and top_logprobs must be set");
+    std::vector<Range> rs;
+    rows_ranges(*p, true, rs);
+    add_range(rs, logprobs, p->tokens * 4, false);
+    add_range(rs, entropy, p->tokens * 4, false);
+    add_range(rs, lse, p->tokens * 4, false);
+    add_range(rs, top_ids, p->tokens * p->top * 8, false);
+    add_range(rs, top_logprobs, p->tokens * p->top * 4, false);
+    if ((e = check_alias(rs))) return e;
+    const size_t need = rows_plan(*p, nullptr).bytes;
+    if (need && (e = check_ws(workspace, workspace_bytes, need, rs))) return e;
+    const RowsPlan pl = rows_plan(*p, (char*)workspace);
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    LogprobsArgs a{};
+    a.logits = p->logits;
+    a.ld = p->ld;
+    a.rows = p->tokens;
+    a.vocab = (int32_t)p->vocab;
+    a.top = p->top;
+    a.piece = (int32_t)pl.piece;
+    a.pieces = (int32_t)pl.pieces;
+    a.scale = p->scale;
+    a.targets = p->targets;
+    a.idx64 = p->index_dtype == DMUON_I64;
+    a.ignore = p->ignore_index;
+    a.logprobs = logprobs;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.stats = pl.stats;
+    a.cand = pl.cand;
+    const int f32 = p->dtype == DMUON_F32;
+    if ((e = go(env, PH_LOGPROBS, stream, [&] { return launch_logprobs(a, f32, stream); }))) return e;
+    if (a.pieces == 1) return DMUON_OK;
+    return go(env, PH_LOGPROBS, stream, [&] { return launch_logprobs_join(a, f32, stream); });
+  });
+}
+
+int dmuon_logprobs_backward(const dmuon_logprobs_problem* p, const float* lse, const float* entropy, const float* grad_logprobs,
+                            const float* grad_entropy, void* grad_logits, int64_t ld_grad, void* stream) {
+  return guarded([&]() -> int {
+    int e = check_rows(p, true);
+    if (e) return e;
+    if (ld_grad < p->vocab || ld_grad > kMaxStride) return fail(DMUON_E_SHAPE, "ld_grad must be at least vocab");
+    const int64_t es = type_bytes(p->dtype);
+    if (!spans(p->tokens, p->vocab, ld_grad, es)) return fail(DMUON_E_SHAPE, "grad_logits must end within 2^48 bytes");
+    if (p->tokens == 0) return DMUON_OK;
+    if (!lse || !grad_logits) return fail(DMUON_E_NULL, "lse and grad_logits must be set");
+    if (!grad_logprobs && !grad_entropy) return fail(DMUON_E_NULL, "grad_logprobs or grad_entropy must be set");
+    if (grad_logprobs && !p->targets) return fail(DMUON_E_NULL, "grad_logprobs needs targets");
+    if (grad_entropy && !entropy) return fail(DMUON_E_NULL, "grad_entropy needs entropy");
+    const bool in_place = grad_logits == p->logits && ld_grad == p->ld;
+    std::vector<Range> rs;
+    rows_ranges(*p, !in_place, rs);
+    add_range(rs, lse, p->tokens * 4, true);
+    if (grad_entropy) add_range(rs, entropy, p->tokens * 4, true);
+    add_range(rs, grad_logprobs, p->tokens * 4, true);
+    add_range(rs, grad_entropy, p->tokens * 4, true);
+    add_range(rs, grad_logits, strided_bytes(p->tokens, p->vocab, ld_grad, es), false);
+    if ((e = check_alias(rs))) return e;
+    const CallEnv env = call_env();
+    if ((e = forced(env, -2))) return e;
+    LogprobsGradArgs a{};
+    a.logits = p->logits;
+    a.ld = p->ld;
+    a.rows = p->tokens;
+    a.vocab = (int32_t)p->vocab;
+    a.pieces = p->vocab <= kGradWave ? 1 : (int32_t)cdiv(p->vocab, kThreads * kGradUnits * 8);
+    a.scale = p->scale;
+    a.targets = p->targets;
+    a.idx64 = p->index_dtype == DMUON_I64;
+    a.ignore = p->ignore_index;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.grad_logprobs = grad_logprobs;
+    a.grad_entropy = grad_entropy;
+    a.out = grad_logits;
+    a.ldo = ld_grad;
+    return go(env, PH_LOGPROBS_GRAD, stream, [&] { return launch_logprobs_grad(a, p->dtype == DMUON_F32, stream); });
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,562 @@
+// HIP kernels of log probabilities from logits in memory for gfx950 (MI355X): the given
+// token's log probability, the entropy and the most likely alternatives of every row, and
+// the gradient.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "core.hpp"
+#include "elements.hpp"
+#include "grads.hpp"
+#include "logprobs.hpp"
+
+namespace dmuon {
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kNan = __builtin_nanf("");
+
+// ---------------------------------------------------------------------------
+// units of a row: 8 consecutive elements (or one), as they were loaded.  A row starts at
+// any element, so the 16-byte accesses are of types aligned to one element only.
+// ---------------------------------------------------------------------------
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
+template <typename T, int UNIT>
+struct Unit;
+template <>
+struct Unit<uint16_t, 8> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = *(gptr<const u32x4_any>)p; }
+  __device__ __forceinline__ void values(float (&v)[8]) const { unpack8(u, v); }
+};
+template <>
+struct Unit<float, 8> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(gptr<const float> p) {
+    a = ((gptr<const f32x4_any>)p)[0];
+    b = ((gptr<const f32x4_any>)p)[1];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <typename T>
+struct Unit<T, 1> {
+  T x;
+  __device__ __forceinline__ void load(gptr<const T> p) { x = *p; }
+  __device__ __forceinline__ void values(float (&v)[1]) const { v[0] = value(x); }
+  static __device__ __forceinline__ float value(uint16_t b) { return bf16_to_f32(b); }
+  static __device__ __forceinline__ float value(float f) { return f; }
+};
+__device__ __forceinline__ float element(gptr<const uint16_t> p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float element(gptr<const float> p) { return *p; }
+
+// unit j of a piece of len elements, −∞ past its end
+template <typename T, int UNIT>
+__device__ __forceinline__ void edge_unit(gptr<const T> row, int j, int len, float (&v)[UNIT]) {
+#pragma unroll
+  for (int e = 0; e < UNIT; ++e) v[e] = j * UNIT + e < len ? element(row + j * UNIT + e) : -INFINITY;
+}
+template <typename T, int UNIT>
+__device__ __forceinline__ void any_unit(gptr<const T> row, int j, int len, float (&v)[UNIT]) {
+  if ((j + 1) * UNIT <= len) {
+    Unit<T, UNIT> x;
+    x.load(row + j * UNIT);
+    x.values(v);
+  } else {
+    edge_unit<T, UNIT>(row, j, len, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// one pass over a row: with m the largest logit so far,
+//   s = Σ e^{c(z − m)},   u = Σ (z − m)·e^{c(z − m)}   (c: the scale)
+// and both multiplied by e^{c(m − m')} when m grows to m' (u first becomes
+// Σ (z − m')·…, that is u + (m − m')·s).  m starts at the lowest finite value, so that no
+// difference is −∞ − −∞: a logit of −∞ has e = 0, and its difference is kept finite for
+// the product 0·(z − m).  A NaN reaches s through its e.
+// ---------------------------------------------------------------------------
+constexpr float kFar = -1e30f;           // a difference whose exponential is 0
+
+struct Running {
+  float m, s, u;
+  __device__ __forceinline__ void grow(float to, float c2) {
+    const float d = m - to;
+    const float a = __builtin_amdgcn_exp2f(d * c2);
+    u = a * fmaf(fmaxf(d, kFar), s, u);
+    s *= a;
+    m = to;
+  }
+  template <int N>
+  __device__ __forceinline__ float add(const float (&v)[N], float c2) {        // returns the largest of v
+    float most = v[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) most = fmaxf(most, v[e]);
+    if (most > m) grow(most, c2);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float d = v[e] - m;
+      const float p = __builtin_amdgcn_exp2f(d * c2);
+      s += p;
+      u = fmaf(p, fmaxf(d, kFar), u);
+    }
+    return most;
+  }
+};
+
+// the statistics of all lanes of a wave, in every lane
+__device__ __forceinline__ void join_wave(Running& r, float c2) {
+  float m = r.m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  r.grow(m, c2);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    r.s += __shfl_xor(r.s, o, 64);
+    r.u += __shfl_xor(r.u, o, 64);
+  }
+}
+
+// A finished row.  Where no logit is finite (s = 0: all are −∞) lse and every log
+// probability are −∞ and the entropy is 0.
+struct Row {
+  float m, log_s, lse, entropy, scale;
+  __device__ __forceinline__ Row(const Running& r, float c) : m(r.m), scale(c) {
+    const bool none = r.s == 0.f;
+    log_s = none ? 0.f : logf(r.s);
+    lse = none ? -INFINITY : fmaf(r.m, c, log_s);
+    entropy = none ? 0.f : log_s - r.u * c / r.s;
+  }
+  // (z − m)·c − log s: neither term is positive, and the logarithm keeps its digits
+  // beside a large m
+  __device__ __forceinline__ float log_p(float z) const { return (z - m) * scale - log_s; }
+};
+
+// Keys order by value, then by lower index: the value's bits as a whole number in the
+// high half, ~index in the low one.  NaN counts as −∞, −0 as 0.  No key is 0.
+__device__ __forceinline__ float rankable(float z) { return fmaxf(z, -INFINITY) + 0.f; }
+__device__ __forceinline__ uint64_t key_of(float z, int32_t index) {
+  const uint32_t b = __float_as_uint(z);
+  return ((uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t b = (uint32_t)(key >> 32);
+  return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ int32_t key_index(uint64_t key) { return (int32_t)~(uint32_t)key; }
+
+// what a row's target asks for
+enum : int { kIgnored, kInside, kShard, kOutside };
+__device__ __forceinline__ int target_kind(int64_t y, int64_t ignore, int32_t vocab) {
+  return y == ignore ? kIgnored : y >= 0 && y < vocab ? kInside : y == kElsewhere ? kShard : kOutside;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, int64_t y, int kind, const Row& r) {
+  a.lse[row] = r.lse;
+  a.entropy[row] = r.entropy;
+  if (!a.targets) return;
+  a.logprobs[row] = kind == kInside ? r.log_p(element(glob((const T*)a.logits) + row * a.ld + y)) : kind == kShard ? -r.lse : kNan;
+}
+
+// ---------------------------------------------------------------------------
+// the k largest of a piece.  The k-th largest of the threads' maxima, tau, is not above
+// the k-th largest element, so only groups whose maximum (kept in LDS by the first pass)
+// reaches tau are read again, and few elements do.  If more than the list holds are
+// greater than tau, the k-th largest of those it took becomes the new tau (it is greater:
+// each round drops at least the rest of the list).  Elements equal to tau are needed
+// where fewer than k are greater; where many are (equal logits, words masked out by −∞)
+// the first of them in order are looked for.  Places come from counting the greater keys:
+// keys are distinct, so the result does not depend on the list's order.
+// ---------------------------------------------------------------------------
+constexpr int kStrict = 768, kTies = 256;
+
+struct TopShared {
+  float group[kGroups][kThreads];        // largest of each thread's groups
+  uint16_t flag[kGroups * kThreads];     // groups to read again
+  uint64_t list[kStrict + kTies];
+  __attribute__((aligned(16))) float most[kThreads];   // each thread's largest
+  int flags, strict, ties, wave[kThreads / 64];
+  float tau;
+};
+
+// the number of keys greater than `key` in list[0, n)
+__device__ __forceinline__ int places_above(const uint64_t* list, int n, uint64_t key) {
+  int r = 0;
+  for (int i = 0; i < n; ++i) r += list[i] > key;
+  return r;
+}
+
+// emit(place, key) for the min(k, len) largest of the piece; returns their number
+template <typename T, int UNIT, typename F>
+__device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int len, int first, int k, int groups, F emit) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int want = k < len ? k : len;
+  float mine = -INFINITY;
+  for (int g = 0; g < groups; ++g) mine = fmaxf(mine, sh.group[g][tid]);
+  sh.most[tid] = mine;
+  __syncthreads();
+  int above = 0;
+  for (int i = 0; i < kThreads; i += 4) {
+    const f32x4_t o = *(const f32x4_t*)&sh.most[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) above += o[e] > mine || (o[e] == mine && i + e < tid);
+  }
+  if (above == k - 1) sh.tau = mine;
+  __syncthreads();
+  int strict, ties;
+  float tau;
+  for (;;) {
+    tau = sh.tau;
+    if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
+    __syncthreads();
+    for (int g = 0; g < groups; ++g)
+      if (sh.group[g][tid] >= tau) sh.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
+    __syncthreads();
+    const int units = sh.flags * kGroupUnits;
+    for (int w = tid; w < units; w += kThreads) {
+      const int f = sh.flag[w / kGroupUnits];
+      const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
+      if (j * UNIT >= len) continue;
+      float v[UNIT];
+      any_unit<T, UNIT>(row, j, len, v);
+#pragma unroll
+      for (int e = 0; e < UNIT; ++e) {
+        const float z = rankable(v[e]);
+        const int at = j * UNIT + e;
+        if (z > tau) {
+          const int i = atomicAdd(&sh.strict, 1);
+          if (i < kStrict) sh.list[i] = key_of(z, first + at);
+        } else if (z == tau && at < len) {
+          const int i = atomicAdd(&sh.ties, 1);
+          if (i < kTies) sh.list[kStrict + i] = key_of(z, first + at);
+        }
+      }
+    }
+    __syncthreads();
+    strict = sh.strict;
+    ties = sh.ties;
+    if (strict <= kStrict) break;
+    for (int i = tid; i < kStrict; i += kThreads)
+      if (places_above(sh.list, kStrict, sh.list[i]) == k - 1) sh.tau = key_value(sh.list[i]);
+    __syncthreads();
+  }
+  if (strict >= want) {
+    ties = 0;
+  } else if (ties > kTies) {
+    const int need = want - strict;
+    int have = 0;
+    for (int base = 0; have < need && base * 8 < len; base += kThreads) {
+      float v[8];
+      any_unit<T, 8>(row, base + tid, len, v);
+      uint32_t in = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) in |= (uint32_t)(rankable(v[e]) == tau && (base + tid) * 8 + e < len) << e;
+      int incl = __popc(in);
+      const int n = incl;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 63) sh.wave[wave] = incl;
+      __syncthreads();
+      int at = have + incl - n, all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 64; ++w) {
+        if (w < wave) at += sh.wave[w];
+        all += sh.wave[w];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (in >> e & 1) {
+          if (at < need) sh.list[kStrict + at] = key_of(tau, first + (base + tid) * 8 + e);
+          ++at;
+        }
+      have += all;
+      __syncthreads();
+    }
+    ties = need;
+  }
+  // one list: the ties behind the others
+  const int n = strict + ties;
+  uint64_t moved = 0;
+  if (tid < ties) moved = sh.list[kStrict + tid];
+  __syncthreads();
+  if (tid < ties) sh.list[strict + tid] = moved;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = sh.list[i];
+    const int place = places_above(sh.list, n, key);
+    if (place < want) emit(place, key);
+  }
+  return want;
+}
+
+// ---------------------------------------------------------------------------
+// G threads per row (or piece of one): a wave where rows are short, else a workgroup.
+// Memory bound: a thread has kGroupUnits loads of 16 bytes in flight.
+// ---------------------------------------------------------------------------
+template <typename T, int G, bool TOP, int UNIT>
+__global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
+  __shared__ Running part[kThreads / 64];
+  const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const uint32_t id = blockIdx.x * (kThreads / G) + (G == 64 ? threadIdx.x >> 6 : 0);
+  const int64_t row = id / (uint32_t)a.pieces;
+  const int piece = (int)(id - (uint32_t)row * a.pieces);
+  if (row >= a.rows) return;                             // only where a wave has its own row
+  const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
+  const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
+  if (kind == kIgnored) {
+    if (piece == 0) {
+      if (tid == 0) a.logprobs[row] = a.entropy[row] = a.lse[row] = 0.f;
+      for (int i = tid; i < a.top; i += G) {
+        a.top_ids[row * a.top + i] = -1;
+        a.top_logprobs[row * a.top + i] = 0.f;
+      }
+    }
+    return;
+  }
+  const int first = piece * a.piece;
+  const int len = a.vocab - first < a.piece ? a.vocab - first : a.piece;
+  const gptr<const T> src = glob((const T*)a.logits) + row * a.ld + first;
+  const float c2 = a.scale * kLog2e;
+  constexpr int B = sizeof(T) == 2 || UNIT == 1 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
+  const int groups = (len + G * kGroupUnits * UNIT - 1) / (G * kGroupUnits * UNIT);
+  Running r = {kLowest, 0.f, 0.f};
+  extern __shared__ __align__(16) char top_smem[];
+  TopShared& sh = *(TopShared*)top_smem;
+  for (int g = 0; g < groups; ++g) {
+    float most = -INFINITY;
+    if ((g + 1) * G * kGroupUnits * UNIT <= len) {
+#pragma unroll
+      for (int b = 0; b < kGroupUnits; b += B) {
+        Unit<T, UNIT> x[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) x[k].load(src + (int64_t)((g * kGroupUnits + b + k) * G + tid) * UNIT);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          float v[UNIT];
+          x[k].values(v);
+          const float o = r.add(v, c2);
+          if (TOP) most = fmaxf(most, o);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kGroupUnits; ++k) {
+        const int j = (g * kGroupUnits + k) * G + tid;
+        if (j * UNIT >= len) break;
+        float v[UNIT];
+        any_unit<T, UNIT>(src, j, len, v);
+        const float o = r.add(v, c2);
+        if (TOP) most = fmaxf(most, o);
+      }
+    }
+    if (TOP) sh.group[g][tid] = rankable(most);
+  }
+  join_wave(r, c2);
+  if constexpr (G > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = r;
+    __syncthreads();
+    Running all = part[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) {
+      Running o = part[w];
+      const float m = fmaxf(all.m, o.m);
+      all.grow(m, c2);
+      o.grow(m, c2);
+      all.s += o.s;
+      all.u += o.u;
+    }
+    r = all;
+  }
+  const Row done(r, a.scale);
+  if (tid == 0) {
+    if (a.pieces == 1) write_row<T>(a, row, y, kind, done);
+    else a.stats[row * a.pieces + piece] = RowStat{r.m, r.s, r.u};
+  }
+  if constexpr (TOP) {
+    if (a.pieces == 1) {
+      select_top<T, UNIT>(sh, src, len, first, a.top, groups, [&](int place, uint64_t key) {
+        a.top_ids[row * a.top + place] = key_index(key);
+        a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
+      });
+    } else {
+      uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
+      const int n = select_top<T, UNIT>(sh, src, len, first, a.top, groups, [&](int place, uint64_t key) { out[place] = key; });
+      for (int i = n + tid; i < a.top; i += kThreads) out[i] = 0;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the pieces of a row joined: statistics by one wave, then the k largest of the pieces'
+// sorted candidates, all in LDS, by the same rule as in a piece.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
+  extern __shared__ __align__(16) char join_smem[];
+  __shared__ Running whole;
+  __shared__ uint64_t most[kThreads], list[kStrict], tau_key;
+  __shared__ int count;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
+  const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
+  if (kind == kIgnored) return;                          // written by the first piece's workgroup
+  const float c2 = a.scale * kLog2e;
+  if (tid < 64) {
+    Running r = {kLowest, 0.f, 0.f};
+    if (tid < a.pieces) {
+      const RowStat s = a.stats[row * a.pieces + tid];
+      r.m = s.m;
+      r.s = s.s;
+      r.u = s.u;
+    }
+    join_wave(r, c2);
+    if (tid == 0) {
+      whole = r;
+      write_row<T>(a, row, y, kind, Row(r, a.scale));
+    }
+  }
+  if (a.top == 0) return;
+  uint64_t* keys = (uint64_t*)join_smem;
+  const int n = a.pieces * a.top;
+  uint64_t mine = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = a.cand[row * n + i];
+    keys[i] = key;
+    mine = key > mine ? key : mine;
+  }
+  most[tid] = mine;
+  __syncthreads();
+  const Row done(whole, a.scale);
+  int above = 0;
+  for (int i = 0; i < kThreads; ++i) above += most[i] > mine || (most[i] == mine && i < tid);
+  if (above == a.top - 1) tau_key = mine;
+  __syncthreads();
+  for (;;) {
+    const uint64_t tau = tau_key;
+    if (tid == 0) count = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads)
+      if (keys[i] >= tau && keys[i] != 0) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kStrict) list[at] = keys[i];
+      }
+    __syncthreads();
+    const int have = count;
+    if (have <= kStrict) {
+      for (int i = tid; i < have; i += kThreads) {
+        const int place = places_above(list, have, list[i]);
+        if (place < a.top) {
+          a.top_ids[row * a.top + place] = key_index(list[i]);
+          a.top_logprobs[row * a.top + place] = done.log_p(key_value(list[i]));
+        }
+      }
+      return;
+    }
+    for (int i = tid; i < kStrict; i += kThreads)
+      if (places_above(list, kStrict, list[i]) == a.top - 1) tau_key = list[i];
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the gradient, element by element: with l = c·z − lse and p = e^l,
+//   dz = c·(g·[v = target] − p·(g + h·(l + H)))     (g, h: of the log probability, the entropy)
+// l is kept from −200 on (e^−200 is 0 in fp32), so that 0·−∞ does not arise.  Rows that
+// take no part are zeros and their logits are not read.  Memory bound.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void store_unit(gptr<uint16_t> p, const float (&v)[8]) {
+  __builtin_nontemporal_store(pack8(v), (gptr<u32x4_any>)p);
+}
+__device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[8]) {
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
+  __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, (gptr<f32x4_any>)p + 1);
+}
+__device__ __forceinline__ void store_element(gptr<uint16_t> p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ void store_element(gptr<float> p, float v) { *p = v; }
+
+template <typename T, int G>
+__global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) {
+  const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const uint32_t id = blockIdx.x * (kThreads / G) + (G == 64 ? threadIdx.x >> 6 : 0);
+  const int64_t row = id / (uint32_t)a.pieces;
+  const int piece = (int)(id - (uint32_t)row * a.pieces);
+  if (row >= a.rows) return;
+  const int j0 = piece * G * kGradUnits + tid;           // this thread's units: j0 + k·G
+  const gptr<const T> src = glob((const T*)a.logits) + row * a.ld;
+  const gptr<T> dst = glob((T*)a.out) + row * a.ldo;
+  const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
+  const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kShard;
+  float g = a.grad_logprobs ? a.grad_logprobs[row] : 0.f;
+  float h = a.grad_entropy ? a.grad_entropy[row] : 0.f;
+  const float lse = a.lse[row];
+  const float entropy = a.grad_entropy ? a.entropy[row] : 0.f;
+  const bool takes_part = kind != kIgnored && kind != kOutside && !(g == 0.f && h == 0.f) && !(lse == -INFINITY);
+  if (lse != lse) g = kNan;
+  const int target = kind == kInside ? (int)y : -1;
+#pragma unroll
+  for (int k = 0; k < kGradUnits; ++k) {
+    const int j = j0 + k * G;
+    if (j * 8 >= a.vocab) break;
+    float v[8];
+    if (takes_part) {
+      any_unit<T, 8>(src, j, a.vocab, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float l = fmaxf(fmaf(v[e], a.scale, -lse), -200.f);
+        const float p = __builtin_amdgcn_exp2f(l * kLog2e);
+        const float d = -p * fmaf(h, l + entropy, g);
+        v[e] = a.scale * (j * 8 + e == target ? d + g : d);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    if ((j + 1) * 8 <= a.vocab) {
+      store_unit(dst + j * 8, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j * 8 + e < a.vocab) store_element(dst + j * 8 + e, v[e]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+template <typename T>
+static int logprobs(const LogprobsArgs& a, void* stream) {
+  const int64_t work = a.rows * a.pieces;
+  if (a.top) {
+    if (a.vocab < kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, true, 1>), (unsigned)work, kThreads, sizeof(TopShared), a);
+    DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, true, 8>), (unsigned)work, kThreads, sizeof(TopShared), a);
+  }
+  if (a.vocab <= kWaveRow) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, 64, false, 8>), (unsigned)cdiv(work, kThreads / 64), kThreads, 0, a);
+  DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, false, 8>), (unsigned)work, kThreads, 0, a);
+}
+int launch_logprobs(const LogprobsArgs& a, int f32, void* stream) { return f32 ? logprobs<float>(a, stream) : logprobs<uint16_t>(a, stream); }
+int launch_logprobs_join(const LogprobsArgs& a, int f32, void* stream) {
+  const unsigned lds = (unsigned)(a.pieces * a.top * sizeof(uint64_t));
+  if (f32) DMUON_LAUNCH(PH_LOGPROBS, stream, k_logprobs_join<float>, (unsigned)a.rows, kThreads, lds, a);
+  DMUON_LAUNCH(PH_LOGPROBS, stream, k_logprobs_join<uint16_t>, (unsigned)a.rows, kThreads, lds, a);
+}
+template <typename T>
+static int logprobs_grad(const LogprobsGradArgs& a, void* stream) {
+  const int64_t work = a.rows * a.pieces;
+  if (a.vocab <= kGradWave) DMUON_LAUNCH(PH_LOGPROBS_GRAD, stream, (k_logprobs_grad<T, 64>), (unsigned)cdiv(work, kThreads / 64), kThreads, 0, a);
+  DMUON_LAUNCH(PH_LOGPROBS_GRAD, stream, (k_logprobs_grad<T, kThreads>), (unsigned)work, kThreads, 0, a);
+}
+int launch_logprobs_grad(const LogprobsGradArgs& a, int f32, void* stream) {
+  return f32 ? logprobs_grad<float>(a, stream) : logprobs_grad<uint16_t>(a, stream);
+}
+
+}  // namespace dmuon

@@ -1,0 +1,70 @@
+// Arguments of the log-probability kernels (logprobs.hip), shared with their entry
+// points (logprobs.cpp).  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.hpp"
+
+namespace dmuon {
+
+constexpr int kTopMost = 128;            // alternatives per row
+constexpr int kGroupUnits = 8;           // units of 8 elements that a thread takes together
+constexpr int kGroups = 8;               // such groups per thread at most
+constexpr int kPieceMost = kThreads * kGroupUnits * 8 * kGroups;     // 131072 columns per workgroup
+constexpr int kPieceLeast = kThreads * 8;                            // 2048
+constexpr int kPiecesMost = 64;          // pieces of one row (a wave joins them)
+constexpr int kWaveRow = 64 * kGroupUnits * 8;       // 4096: rows up to this, without alternatives, take one wave each
+constexpr int kGradUnits = 4;            // units of 8 elements per thread of the gradient
+constexpr int kGradWave = 64 * kGradUnits * 8;       // 2048: rows up to this take one wave each
+
+// Σ exp(scale·(z − m)) and Σ (z − m)·exp(scale·(z − m)) of a row's piece, m its largest logit
+struct RowStat {
+  float m, s, u;
+};
+
+struct LogprobsArgs {
+  const void* logits;          // rows × vocab, row stride ld
+  int64_t ld;
+  int64_t rows;
+  int32_t vocab;
+  int32_t top;                 // alternatives, 0: none
+  int32_t piece, pieces;       // columns per workgroup, workgroups per row
+  float scale;
+  const void* targets;         // or null: every row takes part, none has a target
+  int32_t idx64;
+  int64_t ignore;
+  float* logprobs;             // null without targets
+  float* entropy;
+  float* lse;
+  int64_t* top_ids;            // [rows][top]
+  float* top_logprobs;
+  // where pieces > 1
+  RowStat* stats;              // [rows][pieces]
+  uint64_t* cand;              // [rows][pieces][top], best first, 0 where there are fewer
+};
+
+struct LogprobsGradArgs {
+  const void* logits;
+  int64_t ld;
+  int64_t rows;
+  int32_t vocab;
+  int32_t pieces;              // workgroups (or waves) per row
+  float scale;
+  const void* targets;         // or null
+  int32_t idx64;
+  int64_t ignore;
+  const float* lse;
+  const float* entropy;        // with grad_entropy
+  const float* grad_logprobs;  // or null
+  const float* grad_entropy;   // or null
+  void* out;                   // rows × vocab, row stride ldo
+  int64_t ldo;
+};
+
+int launch_logprobs(const LogprobsArgs& a, int f32, void* stream);
+int launch_logprobs_join(const LogprobsArgs& a, int f32, void* stream);
+int launch_logprobs_grad(const LogprobsGradArgs& a, int f32, void* stream);
+
+}  // namespace dmuon

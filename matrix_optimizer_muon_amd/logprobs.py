@@ -1,0 +1,112 @@
+"""Log probabilities of given tokens with entropies, and their gradients (see include/dmuon_ns.h).
+
+    token_logprobs(logits, targets, top=20)              # from logits: also the alternatives
+    token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_entropy)
+
+Calls, streams and autograd as in ``training``: the functions record nothing, and the
+forward ones refuse inputs that require gradients where autograd records.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+from . import _binding as _b
+from .training import _dense, _float_code, _index_code, _matrix, _no_graph, _on, _ptr, _ws_args
+
+__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_backward"]
+
+
+class TokenLogprobs(NamedTuple):
+    """Per token: ``logprobs`` of its target, ``entropy`` and ``lse`` of its scaled logits
+    (fp32), and with alternatives ``top_ids`` (int64) and ``top_logprobs`` (fp32) [..., top].
+    What was not asked for is None."""
+    logprobs: Optional[object]
+    entropy: object
+    lse: object
+    top_ids: Optional[object] = None
+    top_logprobs: Optional[object] = None
+
+
+def _rows_problem(logits, targets, scale, top, ignore_index):
+    tokens, vocab, ld = _matrix(logits, "logits")
+    icode = _b.I64
+    if targets is not None:
+        _dense(targets, "targets", None, logits.shape[:-1])
+        icode = _index_code(targets, "targets")
+    return _b.LogprobsProblem(tokens, vocab, _float_code(logits.dtype, "logits"), icode, logits.data_ptr(), ld,
+                              None if targets is None else targets.data_ptr(), int(ignore_index), float(scale), int(top))
+
+
+def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100, workspace=None, stream=None):
+    """Log probabilities of given tokens, entropies and the most likely alternatives.
+
+    logits: [..., vocab], bf16 or fp32 (rows may be strided); targets: int64 or int32 of
+    the leading shape, or None for the distributions alone.  The logits are multiplied by
+    ``scale`` (1/temperature).  Returns a ``TokenLogprobs``.  Tokens whose target is
+    ``ignore_index`` have zeros (ids -1); ``TARGET_ELSEWHERE`` gives -lse, another target
+    outside the vocabulary NaN.  ``top`` (up to 128) alternatives come largest first, equal
+    logits by rising id.
+
+    A vocabulary in shards: call each with its columns and the shifted targets,
+    ``TARGET_ELSEWHERE`` where that is not one of its columns.  Then lse is the logsumexp of
+    the shards', the log probability sum(logprobs_s + lse_s) - lse, the entropy
+    lse - sum(exp(lse_s - lse)*(lse_s - entropy_s)).
+    """
+    import torch
+    _no_graph("token_logprobs", logits=logits)
+    prob = _rows_problem(logits, targets, scale, top, ignore_index)
+    need = ctypes.c_size_t(0)
+    _b.check(_b.lib().dmuon_logprobs_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
+    shape, dev = logits.shape[:-1], logits.device
+    with _on(stream, logits, targets) as on:
+        new = lambda *more, dtype=torch.float32: torch.empty((*shape, *more), dtype=dtype, device=dev)  # noqa: E731
+        logprobs = None if targets is None else new()
+        entropy, lse = new(), new()
+        ids, best = (new(top, dtype=torch.int64), new(top)) if top else (None, None)
+        ws = on.workspace(workspace, need.value, dev)
+        _b.check(_b.lib().dmuon_logprobs(ctypes.byref(prob), _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(ids), _ptr(best),
+                                         *_ws_args(ws), on.handle))
+    return TokenLogprobs(logprobs, entropy, lse, ids, best)
+
+
+def _check_row_grads(shape, lse, entropy, grad_logprobs, grad_entropy):
+    import torch
+    _dense(lse, "lse", torch.float32, shape)
+    if grad_logprobs is None and grad_entropy is None:
+        raise ValueError("grad_logprobs or grad_entropy must be given")
+    if grad_logprobs is not None:
+        _dense(grad_logprobs, "grad_logprobs", torch.float32, shape)
+    if grad_entropy is not None:
+        _dense(grad_entropy, "grad_entropy", torch.float32, shape)
+        if entropy is None:
+            raise ValueError("grad_entropy needs entropy")
+        _dense(entropy, "entropy", torch.float32, shape)
+
+
+def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_entropy=None, *, scale=1.0, ignore_index=-100,
+                            out=None, stream=None):
+    """The gradient of ``token_logprobs`` with respect to the logits.
+
+    lse, entropy: as ``token_logprobs`` returned them (of a vocabulary in shards: the
+    joined ones); grad_logprobs, grad_entropy: fp32 of the same shape, the gradients of
+    each token's log probability and entropy (either may be None).  Returns a dense tensor
+    of the logits' shape and type, or writes ``out``, which may have strided rows and may be
+    ``logits`` itself.
+    """
+    import torch
+    prob = _rows_problem(logits, targets, scale, 0, ignore_index)
+    _check_row_grads(logits.shape[:-1], lse, entropy, grad_logprobs, grad_entropy)
+    if grad_logprobs is not None and targets is None:
+        raise ValueError("grad_logprobs needs targets")
+    ld = prob.vocab
+    if out is not None:
+        if out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out must have the logits' shape and type")
+        ld = _matrix(out, "out")[2]
+    with _on(stream, logits, targets, lse, entropy, grad_logprobs, grad_entropy, out) as on:
+        if out is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _b.check(_b.lib().dmuon_logprobs_backward(ctypes.byref(prob), _ptr(lse), _ptr(entropy), _ptr(grad_logprobs),
+                                                  _ptr(grad_entropy), _ptr(out), ld, on.handle))
+    return out
