@@ -514,6 +514,19 @@ int dmuon_logprobs_backward(const dmuon_logprobs_problem* problem, const float* 
                             const float* grad_logprobs, const float* grad_entropy, void* grad_logits, int64_t ld_grad,
                             void* stream);
 
+/* The same log probabilities and entropies from hidden states: z = h·wᵀ of a
+ * dmuon_ce_problem (its sizes, targets and shards; scale as above), in pieces of the
+ * vocabulary and never kept.  logprobs, entropy, lse: device fp32 [tokens].
+ * Backward: grad_h = dz·w and grad_w = dzᵀ·h with dz the gradient of z above; either may be
+ * NULL.  For bf16, dz is rounded to bf16 once, relative to the largest finite weight, as
+ * in dmuon_linear_ce_backward. */
+int dmuon_linear_logprobs_workspace_size(const dmuon_ce_problem* problem, int32_t backward, size_t* bytes);
+int dmuon_linear_logprobs(const dmuon_ce_problem* problem, float scale, float* logprobs, float* entropy, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int dmuon_linear_logprobs_backward(const dmuon_ce_problem* problem, float scale, const float* lse, const float* entropy,
+                                   const float* grad_logprobs, const float* grad_entropy, void* grad_h, void* grad_w,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Plain NT product C = A·Bᵀ on the matrix-core kernel the step uses (a test hook
  * for the contraction core).  A: M×K (lda elements per row), B: N×K (ldb), both
  * dtype (bf16 or fp32), device; C: M×N fp32 (ldc), device.  lda and ldb must be

@@ -18,7 +18,8 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding as _b
-from .logprobs import TokenLogprobs, token_logprobs, token_logprobs_backward  # noqa: F401
+from .logprobs import (TokenLogprobs, linear_token_logprobs, linear_token_logprobs_backward, token_logprobs,  # noqa: F401
+                       token_logprobs_backward)
 from .training import (TARGET_ELSEWHERE, checkpoint_dequantize, checkpoint_quantize, checkpoint_wgrad, embedding,  # noqa: F401
                        embedding_backward, linear_cross_entropy, linear_cross_entropy_backward)
 from .workloads import HYPER  # noqa: F401
@@ -27,7 +28,8 @@ __all__ = ["muon_step", "muon_step_workspace_size", "adamw_step", "MuonStep", "A
            "ns_batched", "lpt_assign", "gemm_nt",
            "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
            "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize", "checkpoint_wgrad", "TARGET_ELSEWHERE",
-           "TokenLogprobs", "token_logprobs", "token_logprobs_backward",
+           "TokenLogprobs", "token_logprobs", "token_logprobs_backward", "linear_token_logprobs",
+           "linear_token_logprobs_backward",
            "phase_timing", "phase_timing_read", "abi_version", "load_library", "HYPER"]
 
 QUINTIC = (HYPER["a"], HYPER["b"], HYPER["c"])

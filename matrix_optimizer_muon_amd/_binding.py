@@ -43,7 +43,8 @@ EXPORTED = ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_m
             "dmuon_embedding", "dmuon_embedding_backward_workspace_size",
             "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
             "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad",
-            "dmuon_logprobs_workspace_size", "dmuon_logprobs", "dmuon_logprobs_backward"]
+            "dmuon_logprobs_workspace_size", "dmuon_logprobs", "dmuon_logprobs_backward",
+            "dmuon_linear_logprobs_workspace_size", "dmuon_linear_logprobs", "dmuon_linear_logprobs_backward"]
 ABI_VERSION = 5
 
 
@@ -168,6 +169,9 @@ def lib():
     L.dmuon_logprobs_workspace_size.argtypes = [P(LogprobsProblem), P(sz)]
     L.dmuon_logprobs.argtypes = [P(LogprobsProblem), vp, vp, vp, vp, vp, vp, sz, vp]
     L.dmuon_logprobs_backward.argtypes = [P(LogprobsProblem), vp, vp, vp, vp, vp, i64, vp]
+    L.dmuon_linear_logprobs_workspace_size.argtypes = [P(CeProblem), i32, P(sz)]
+    L.dmuon_linear_logprobs.argtypes = [P(CeProblem), f32, vp, vp, vp, vp, sz, vp]
+    L.dmuon_linear_logprobs_backward.argtypes = [P(CeProblem), f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.dmuon_last_error.restype = ctypes.c_char_p
     L.dmuon_last_error.argtypes = []
     for name in EXPORTED:

@@ -50,6 +50,9 @@ inline bool float_type(int32_t t) { return t == DMUON_F32 || t == DMUON_BF16; }
 inline int64_t type_bytes(int32_t t) { return t == DMUON_F32 ? 4 : 2; }
 inline bool index_type(int32_t t) { return t == DMUON_I32 || t == DMUON_I64; }
 
+// scale of the logits that log probabilities are taken of
+inline bool logit_scale(float s) { return s >= 0x1p-20f && s <= 0x1p20f; }
+
 inline void add_range(std::vector<Range>& rs, const void* p, int64_t bytes, bool ro) {
   if (p && bytes > 0) rs.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, ro});
 }

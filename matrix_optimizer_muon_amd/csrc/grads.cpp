@@ -73,7 +73,15 @@ bool kmajor_in_place(const void* p, int64_t ld, int64_t cols) {
   return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && ld <= kMaxLd && (ld == cols || cols % kTile == 0);
 }
 
-// ---- cross entropy ------------------------------------------------------------
+// ---- cross entropy, log probabilities with entropies ----------------------------
+// What the log probabilities have beside a loss and its gradient.
+struct Entropies {
+  float scale;
+  float* entropy;                        // forward
+  const float* entropy_in;               // backward, with grad_entropy
+  const float* grad_entropy;             // or null
+};
+
 // Bytes of gradient logits (and operand copies of W) that one piece of the
 // vocabulary may take.
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
@@ -87,15 +95,16 @@ struct CePlan {
   RowSpread spread;                      // of the hidden states' gradient
   // workspace
   int32_t *rows, *pos, *tgt, *count;
-  float *clse, *cg, *gmax, *zt, *part_h, *part_w;
+  float *clse, *cg, *ce, *cent, *gmax, *zt, *part_h, *part_w;
   uint16_t *h, *hb, *w, *dz;
   int64_t hb_plane;
   CeStat* stats;
+  CeStatU* stats_u;
   size_t bytes;
   bool hb_used() const { return few || tile_z == kTile; }       // the logits read fragment order
 };
 
-CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
+CePlan ce_plan(const dmuon_ce_problem& p, bool backward, bool entropies, char* base) {
   CePlan pl{};
   pl.f32 = p.dtype == DMUON_F32;
   pl.planes = pl.f32 ? kPlanes : 1;
@@ -140,13 +149,18 @@ CePlan ce_plan(const dmuon_ce_problem& p, bool backward, char* base) {
     pl.pos = c.take<int32_t>(pl.T);
     pl.clse = c.take<float>(pl.T);
     pl.cg = c.take<float>(pl.T);
+    if (entropies) {
+      pl.ce = c.take<float>(pl.T);
+      pl.cent = c.take<float>(pl.T);
+    }
     pl.gmax = c.take<float>(1);
     pl.dz = c.take<uint16_t>(pl.planes * pl.T * pl.ldz);
     pl.part_h = c.take<float>(pl.sh.splits * pl.T * pl.ldd);
     if (pl.sw.splits > 1) pl.part_w = c.take<float>(pl.sw.splits * piece_rows * pl.ldd);
   } else {
     pl.zt = c.take<float>(pl.T);
-    pl.stats = c.take<CeStat>((int64_t)pl.tiles_v * pl.T);
+    if (entropies) pl.stats_u = c.take<CeStatU>((int64_t)pl.tiles_v * pl.T);
+    else pl.stats = c.take<CeStat>((int64_t)pl.tiles_v * pl.T);
   }
   pl.bytes = c.off;
   return pl;
@@ -181,7 +195,7 @@ int check_ce(const dmuon_ce_problem* p, bool backward, std::vector<Range>* rs) {
 
 // the compact list of tokens and the operand copy of their hidden states
 int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const float* lse_in, const float* grad_losses,
-             float* losses, float* lse, const CallEnv& env, void* stream) {
+             float* losses, float* lse, const Entropies* ent, const CallEnv& env, void* stream) {
   CeScanArgs s{};
   s.targets = p.targets;
   s.idx64 = p.index_dtype == DMUON_I64;
@@ -193,6 +207,13 @@ int ce_start(const dmuon_ce_problem& p, const CePlan& pl, bool backward, const f
   s.lse_in = lse_in;
   s.losses = losses;
   s.lse = lse;
+  if (ent) {
+    s.entropy = ent->entropy;
+    s.grad_entropy = ent->grad_entropy;
+    s.entropy_in = ent->entropy_in;
+    s.ce = pl.ce;
+    s.cent = pl.cent;
+  }
   s.rows = pl.rows;
   s.pos = pl.pos;
   s.tgt = pl.tgt;
@@ -243,8 +264,13 @@ int ce_piece(const dmuon_ce_problem& p, const CePlan& pl, int64_t v0, int64_t ro
   return go(env, PH_CE_PACK, stream, [&] { return launch_pack(a, PH_CE_PACK, stream); });
 }
 
-CeLogitsArgs logits_args(const CePlan& pl, const uint16_t* w, int64_t ldw, int64_t w_plane, int64_t v0, int64_t rows) {
+CeLogitsArgs logits_args(const CePlan& pl, const Entropies* ent, const uint16_t* w, int64_t ldw, int64_t w_plane, int64_t v0, int64_t rows) {
   CeLogitsArgs g{};
+  g.with_entropy = ent != nullptr;
+  g.scale = ent ? ent->scale : 1.f;
+  g.stats_u = pl.stats_u;
+  g.ce = pl.ce;
+  g.cent = pl.cent;
   g.w = w;
   g.w_plane = w_plane;
   g.ldw = ldw;
@@ -273,6 +299,203 @@ int fill_zero(void* out, int32_t dtype, int64_t rows, int64_t cols, int phase, c
   j.out = out;
   j.out_f32 = dtype == DMUON_F32;
   return go(env, phase, stream, [&] { return launch_join(j, phase, stream); });
+}
+
+int ce_size(const dmuon_ce_problem* p, bool backward, bool entropies, size_t* bytes) {
+  if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
+  int e = check_ce(p, backward, nullptr);
+  if (e) return e;
+  *bytes = p->tokens ? ce_plan(*p, backward, entropies, nullptr).bytes : 0;
+  return DMUON_OK;
+}
+
+int ce_forward(const dmuon_ce_problem* p, const Entropies* ent, float* losses, float* lse, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  std::vector<Range> rs;
+  int e = check_ce(p, false, &rs);
+  if (e) return e;
+  if (p->tokens == 0) return DMUON_OK;
+  if (!losses || !lse || (ent && !ent->entropy))
+    return fail(DMUON_E_NULL, ent ? "logprobs, entropy and lse must be set" : "losses and lse must be set");
+  add_range(rs, losses, p->tokens * 4, false);
+  add_range(rs, lse, p->tokens * 4, false);
+  if (ent) add_range(rs, ent->entropy, p->tokens * 4, false);
+  if ((e = check_alias(rs))) return e;
+  if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, false, ent != nullptr, nullptr).bytes, rs))) return e;
+  const CePlan pl = ce_plan(*p, false, ent != nullptr, (char*)workspace);
+  const CallEnv env = call_env();
+  if ((e = forced(env, -2))) return e;
+  if ((e = ce_start(*p, pl, false, nullptr, nullptr, losses, lse, ent, env, stream))) return e;
+  if (pl.few) {
+    CeFewArgs f{};
+    f.w = p->w;
+    f.ldw = p->ldw;
+    f.vec = ((uintptr_t)p->w & 15) == 0 && p->ldw * type_bytes(p->dtype) % 16 == 0;
+    f.width = (int32_t)pl.D;
+    f.vocab = (int32_t)pl.V;
+    f.tokens = (int32_t)pl.T;
+    f.kt = (int32_t)(pl.ldd / 32);
+    f.h = pl.hb;
+    f.h_plane = pl.hb_plane;
+    f.count = pl.count;
+    f.tgt = pl.tgt;
+    f.stats = pl.stats;
+    f.zt = pl.zt;
+    f.with_entropy = ent != nullptr;
+    f.scale = ent ? ent->scale : 1.f;
+    f.stats_u = pl.stats_u;
+    if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_few(f, pl.f32, stream); }))) return e;
+  }
+  for (int64_t v0 = 0; v0 < pl.V && !pl.few; v0 += pl.piece) {
+    const int64_t rows = std::min(pl.piece, pl.V - v0);
+    const uint16_t* w;
+    int64_t ldw, plane;
+    if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
+    CeLogitsArgs g = logits_args(pl, ent, w, ldw, plane, v0, rows);
+    g.stats = pl.stats;
+    g.zt = pl.zt;
+    if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 0, pl.f32, stream); }))) return e;
+  }
+  CeRowsArgs r{};
+  r.stats = pl.stats;
+  r.zt = pl.zt;
+  r.tgt = pl.tgt;
+  r.rows = pl.rows;
+  r.count = pl.count;
+  r.tokens = (int32_t)pl.T;
+  r.tiles_v = pl.tiles_v;
+  r.losses = losses;
+  r.lse = lse;
+  r.stats_u = pl.stats_u;
+  r.entropy = ent ? ent->entropy : nullptr;
+  return go(env, PH_CE_ROWS, stream, [&] { return launch_ce_rows(r, stream); });
+}
+
+int ce_backward(const dmuon_ce_problem* p, const Entropies* ent, const float* lse, const float* grad_losses, void* grad_h,
+                void* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
+  std::vector<Range> rs;
+  int e = check_ce(p, true, &rs);
+  if (e) return e;
+  if (!grad_h && !grad_w) return DMUON_OK;
+  if (p->tokens > 0 && ent) {
+    if (!lse) return fail(DMUON_E_NULL, "lse must be set");
+    if (!grad_losses && !ent->grad_entropy) return fail(DMUON_E_NULL, "grad_logprobs or grad_entropy must be set");
+    if (ent->grad_entropy && !ent->entropy_in) return fail(DMUON_E_NULL, "grad_entropy needs entropy");
+  } else if (p->tokens > 0 && (!lse || !grad_losses)) {
+    return fail(DMUON_E_NULL, "lse and grad_losses must be set");
+  }
+  const int64_t es = type_bytes(p->dtype);
+  add_range(rs, lse, p->tokens * 4, true);
+  add_range(rs, grad_losses, p->tokens * 4, true);
+  if (ent) {
+    if (ent->grad_entropy) add_range(rs, ent->entropy_in, p->tokens * 4, true);
+    add_range(rs, ent->grad_entropy, p->tokens * 4, true);
+  }
+  add_range(rs, grad_h, p->tokens * p->width * es, false);
+  add_range(rs, grad_w, p->vocab * p->width * es, false);
+  if ((e = check_alias(rs))) return e;
+  const CallEnv env = call_env();
+  if (p->tokens == 0) {
+    if ((e = forced(env, -2))) return e;
+    return grad_w ? fill_zero(grad_w, p->dtype, p->vocab, p->width, PH_CE_GRADS, env, stream) : DMUON_OK;
+  }
+  if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, true, ent != nullptr, nullptr).bytes, rs))) return e;
+  const CePlan pl = ce_plan(*p, true, ent != nullptr, (char*)workspace);
+  if ((e = forced(env, -2))) return e;
+  if ((e = ce_start(*p, pl, true, lse, grad_losses, nullptr, nullptr, ent, env, stream))) return e;
+  for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
+    const int64_t rows = std::min(pl.piece, pl.V - v0);
+    const uint16_t* w;
+    int64_t ldw, plane;
+    if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
+    CeLogitsArgs g = logits_args(pl, ent, w, ldw, plane, v0, rows);
+    g.clse = pl.clse;
+    g.cg = pl.cg;
+    g.gmax = pl.gmax;
+    g.dz = pl.dz;
+    g.dz_plane = pl.T * pl.ldz;
+    g.ldz = (int32_t)pl.ldz;
+    if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 1, pl.f32, stream); }))) return e;
+    if (grad_w) {
+      ProductArgs q{};
+      q.a = pl.h;
+      q.a_plane = pl.T * pl.ldd;
+      q.lda = pl.ldd;
+      q.b = pl.dz;
+      q.b_plane = g.dz_plane;
+      q.ldb = pl.ldz;
+      q.pairs = plane_pairs(pl.planes, pl.planes);
+      q.rows = (int32_t)rows;
+      q.cols = (int32_t)pl.D;
+      q.k = pl.T;
+      q.count = pl.count;
+      q.groups = 1;
+      q.tile = pl.sw.tile;
+      q.tiles_r = (int32_t)cdiv(rows, q.tile);
+      q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
+      q.splits = pl.sw.splits;
+      q.scale = pl.gmax;
+      q.out = (char*)grad_w + v0 * pl.D * es;
+      q.out_f32 = pl.f32;
+      if (q.splits > 1) {
+        q.part = pl.part_w;
+        q.ldp = (int32_t)pl.ldd;
+        q.part_split = rows * pl.ldd;
+      }
+      if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
+      if (q.splits > 1) {
+        JoinArgs j{};
+        j.part = q.part;
+        j.part_split = q.part_split;
+        j.splits = q.splits;
+        j.ldp = q.ldp;
+        j.scale = pl.gmax;
+        j.rows = rows;
+        j.cols = (int32_t)pl.D;
+        j.out = q.out;
+        j.out_f32 = pl.f32;
+        if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); }))) return e;
+      }
+    }
+    if (grad_h) {
+      ProductArgs q{};
+      q.a = w;
+      q.a_plane = plane;
+      q.lda = ldw;
+      q.b = pl.dz;
+      q.b_plane = g.dz_plane;
+      q.ldb = pl.ldz;
+      q.pairs = plane_pairs(pl.planes, pl.planes);
+      q.b_rows = 1;
+      q.rows = (int32_t)pl.T;
+      q.cols = (int32_t)pl.D;
+      q.k = rows;
+      q.count = pl.count;
+      q.groups = 1;
+      q.tile = pl.sh.tile;
+      q.tiles_r = (int32_t)cdiv(pl.T, q.tile);
+      q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
+      q.splits = pl.sh.splits;
+      q.spread = pl.spread;
+      q.part = pl.part_h;
+      q.ldp = (int32_t)pl.ldd;
+      q.add = v0 > 0;
+      if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
+    }
+  }
+  if (!grad_h) return DMUON_OK;
+  JoinArgs j{};
+  j.part = pl.part_h;
+  j.count = pl.count;
+  j.spread = pl.spread;
+  j.ldp = (int32_t)pl.ldd;
+  j.pos = pl.pos;
+  j.scale = pl.gmax;
+  j.rows = pl.T;
+  j.cols = (int32_t)pl.D;
+  j.out = grad_h;
+  j.out_f32 = pl.f32;
+  return go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); });
 }
 
 // ---- weight gradient from a checkpoint ------------------------------------------
@@ -402,188 +625,46 @@ extern "C" {
 
 int dmuon_linear_ce_workspace_size(const dmuon_ce_problem* p, int32_t backward, size_t* bytes) {
   return guarded([&]() -> int {
-    if (!bytes) return fail(DMUON_E_NULL, "bytes is NULL");
-    if (backward != 0 && backward != 1) return fail(DMUON_E_CFG, "backward must be 0 or 1");
-    int e = check_ce(p, backward != 0, nullptr);
-    if (e) return e;
-    *bytes = p->tokens ? ce_plan(*p, backward != 0, nullptr).bytes : 0;
-    return DMUON_OK;
+    if (bytes && backward != 0 && backward != 1) return fail(DMUON_E_CFG, "backward must be 0 or 1");
+    return ce_size(p, backward != 0, false, bytes);
   });
 }
 
 int dmuon_linear_ce(const dmuon_ce_problem* p, float* losses, float* lse, void* workspace, size_t workspace_bytes,
                     void* stream) {
-  return guarded([&]() -> int {
-    std::vector<Range> rs;
-    int e = check_ce(p, false, &rs);
-    if (e) return e;
-    if (p->tokens == 0) return DMUON_OK;
-    if (!losses || !lse) return fail(DMUON_E_NULL, "losses and lse must be set");
-    add_range(rs, losses, p->tokens * 4, false);
-    add_range(rs, lse, p->tokens * 4, false);
-    if ((e = check_alias(rs))) return e;
-    if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, false, nullptr).bytes, rs))) return e;
-    const CePlan pl = ce_plan(*p, false, (char*)workspace);
-    const CallEnv env = call_env();
-    if ((e = forced(env, -2))) return e;
-    if ((e = ce_start(*p, pl, false, nullptr, nullptr, losses, lse, env, stream))) return e;
-    if (pl.few) {
-      CeFewArgs f{};
-      f.w = p->w;
-      f.ldw = p->ldw;
-      f.vec = ((uintptr_t)p->w & 15) == 0 && p->ldw * type_bytes(p->dtype) % 16 == 0;
-      f.width = (int32_t)pl.D;
-      f.vocab = (int32_t)pl.V;
-      f.tokens = (int32_t)pl.T;
-      f.kt = (int32_t)(pl.ldd / 32);
-      f.h = pl.hb;
-      f.h_plane = pl.hb_plane;
-      f.count = pl.count;
-      f.tgt = pl.tgt;
-      f.stats = pl.stats;
-      f.zt = pl.zt;
-      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_few(f, pl.f32, stream); }))) return e;
-    }
-    for (int64_t v0 = 0; v0 < pl.V && !pl.few; v0 += pl.piece) {
-      const int64_t rows = std::min(pl.piece, pl.V - v0);
-      const uint16_t* w;
-      int64_t ldw, plane;
-      if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
-      CeLogitsArgs g = logits_args(pl, w, ldw, plane, v0, rows);
-      g.stats = pl.stats;
-      g.zt = pl.zt;
-      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 0, pl.f32, stream); }))) return e;
-    }
-    CeRowsArgs r{};
-    r.stats = pl.stats;
-    r.zt = pl.zt;
-    r.tgt = pl.tgt;
-    r.rows = pl.rows;
-    r.count = pl.count;
-    r.tokens = (int32_t)pl.T;
-    r.tiles_v = pl.tiles_v;
-    r.losses = losses;
-    r.lse = lse;
-    return go(env, PH_CE_ROWS, stream, [&] { return launch_ce_rows(r, stream); });
-  });
+  return guarded([&]() -> int { return ce_forward(p, nullptr, losses, lse, workspace, workspace_bytes, stream); });
 }
 
 int dmuon_linear_ce_backward(const dmuon_ce_problem* p, const float* lse, const float* grad_losses, void* grad_h,
                              void* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> int {
-    std::vector<Range> rs;
-    int e = check_ce(p, true, &rs);
-    if (e) return e;
-    if (!grad_h && !grad_w) return DMUON_OK;
-    if (p->tokens > 0 && (!lse || !grad_losses)) return fail(DMUON_E_NULL, "lse and grad_losses must be set");
-    const int64_t es = type_bytes(p->dtype);
-    add_range(rs, lse, p->tokens * 4, true);
-    add_range(rs, grad_losses, p->tokens * 4, true);
-    add_range(rs, grad_h, p->tokens * p->width * es, false);
-    add_range(rs, grad_w, p->vocab * p->width * es, false);
-    if ((e = check_alias(rs))) return e;
-    const CallEnv env = call_env();
-    if (p->tokens == 0) {
-      if ((e = forced(env, -2))) return e;
-      return grad_w ? fill_zero(grad_w, p->dtype, p->vocab, p->width, PH_CE_GRADS, env, stream) : DMUON_OK;
-    }
-    if ((e = check_ws(workspace, workspace_bytes, ce_plan(*p, true, nullptr).bytes, rs))) return e;
-    const CePlan pl = ce_plan(*p, true, (char*)workspace);
-    if ((e = forced(env, -2))) return e;
-    if ((e = ce_start(*p, pl, true, lse, grad_losses, nullptr, nullptr, env, stream))) return e;
-    for (int64_t v0 = 0; v0 < pl.V; v0 += pl.piece) {
-      const int64_t rows = std::min(pl.piece, pl.V - v0);
-      const uint16_t* w;
-      int64_t ldw, plane;
-      if ((e = ce_piece(*p, pl, v0, rows, &w, &ldw, &plane, env, stream))) return e;
-      CeLogitsArgs g = logits_args(pl, w, ldw, plane, v0, rows);
-      g.clse = pl.clse;
-      g.cg = pl.cg;
-      g.gmax = pl.gmax;
-      g.dz = pl.dz;
-      g.dz_plane = pl.T * pl.ldz;
-      g.ldz = (int32_t)pl.ldz;
-      if ((e = go(env, PH_CE_LOGITS, stream, [&] { return launch_ce_logits(g, 1, pl.f32, stream); }))) return e;
-      if (grad_w) {
-        ProductArgs q{};
-        q.a = pl.h;
-        q.a_plane = pl.T * pl.ldd;
-        q.lda = pl.ldd;
-        q.b = pl.dz;
-        q.b_plane = g.dz_plane;
-        q.ldb = pl.ldz;
-        q.pairs = plane_pairs(pl.planes, pl.planes);
-        q.rows = (int32_t)rows;
-        q.cols = (int32_t)pl.D;
-        q.k = pl.T;
-        q.count = pl.count;
-        q.groups = 1;
-        q.tile = pl.sw.tile;
-        q.tiles_r = (int32_t)cdiv(rows, q.tile);
-        q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
-        q.splits = pl.sw.splits;
-        q.scale = pl.gmax;
-        q.out = (char*)grad_w + v0 * pl.D * es;
-        q.out_f32 = pl.f32;
-        if (q.splits > 1) {
-          q.part = pl.part_w;
-          q.ldp = (int32_t)pl.ldd;
-          q.part_split = rows * pl.ldd;
-        }
-        if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
-        if (q.splits > 1) {
-          JoinArgs j{};
-          j.part = q.part;
-          j.part_split = q.part_split;
-          j.splits = q.splits;
-          j.ldp = q.ldp;
-          j.scale = pl.gmax;
-          j.rows = rows;
-          j.cols = (int32_t)pl.D;
-          j.out = q.out;
-          j.out_f32 = pl.f32;
-          if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); }))) return e;
-        }
-      }
-      if (grad_h) {
-        ProductArgs q{};
-        q.a = w;
-        q.a_plane = plane;
-        q.lda = ldw;
-        q.b = pl.dz;
-        q.b_plane = g.dz_plane;
-        q.ldb = pl.ldz;
-        q.pairs = plane_pairs(pl.planes, pl.planes);
-        q.b_rows = 1;
-        q.rows = (int32_t)pl.T;
-        q.cols = (int32_t)pl.D;
-        q.k = rows;
-        q.count = pl.count;
-        q.groups = 1;
-        q.tile = pl.sh.tile;
-        q.tiles_r = (int32_t)cdiv(pl.T, q.tile);
-        q.tiles_c = (int32_t)cdiv(pl.D, q.tile);
-        q.splits = pl.sh.splits;
-        q.spread = pl.spread;
-        q.part = pl.part_h;
-        q.ldp = (int32_t)pl.ldd;
-        q.add = v0 > 0;
-        if ((e = go(env, PH_CE_GRADS, stream, [&] { return launch_product(q, PH_CE_GRADS, stream); }))) return e;
-      }
-    }
-    if (!grad_h) return DMUON_OK;
-    JoinArgs j{};
-    j.part = pl.part_h;
-    j.count = pl.count;
-    j.spread = pl.spread;
-    j.ldp = (int32_t)pl.ldd;
-    j.pos = pl.pos;
-    j.scale = pl.gmax;
-    j.rows = pl.T;
-    j.cols = (int32_t)pl.D;
-    j.out = grad_h;
-    j.out_f32 = pl.f32;
-    return go(env, PH_CE_GRADS, stream, [&] { return launch_join(j, PH_CE_GRADS, stream); });
+    return ce_backward(p, nullptr, lse, grad_losses, grad_h, grad_w, workspace, workspace_bytes, stream);
+  });
+}
+
+int dmuon_linear_logprobs_workspace_size(const dmuon_ce_problem* p, int32_t backward, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (bytes && backward != 0 && backward != 1) return fail(DMUON_E_CFG, "backward must be 0 or 1");
+    return ce_size(p, backward != 0, true, bytes);
+  });
+}
+
+int dmuon_linear_logprobs(const dmuon_ce_problem* p, float scale, float* logprobs, float* entropy, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    if (!logit_scale(scale)) return fail(DMUON_E_CFG, "scale must be in [2^-20, 2^20]");
+    const Entropies ent = {scale, entropy, nullptr, nullptr};
+    return ce_forward(p, &ent, logprobs, lse, workspace, workspace_bytes, stream);
+  });
+}
+
+int dmuon_linear_logprobs_backward(const dmuon_ce_problem* p, float scale, const float* lse, const float* entropy,
+                                   const float* grad_logprobs, const float* grad_entropy, void* grad_h, void* grad_w,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    if (!logit_scale(scale)) return fail(DMUON_E_CFG, "scale must be in [2^-20, 2^20]");
+    const Entropies ent = {scale, nullptr, entropy, grad_entropy};
+    return ce_backward(p, &ent, lse, grad_logprobs, grad_h, grad_w, workspace, workspace_bytes, stream);
   });
 }
 

@@ -105,6 +105,9 @@ __device__ __forceinline__ bool in_vocab(int64_t y, int32_t vocab) { return y >=
 __device__ __forceinline__ int32_t list_target(int64_t y, int32_t vocab) {
   return in_vocab(y, vocab) ? (int32_t)y : y == kElsewhere ? kTgtElsewhere : kTgtNone;
 }
+// ENT: log probabilities with entropies, whose gradient has a weight for each; a row of
+// nothing but −∞ (lse −∞) has no gradient.
+template <bool ENT>
 __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
   constexpr int waves = kScanThreads / 64, parts = kScanRows * waves;      // 128 partial counts
   __shared__ int place[parts];
@@ -115,7 +118,7 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
   int base = 0;
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kScanRows * kScanThreads) {
     int64_t y[kScanRows];
-    float g[kScanRows], l[kScanRows];
+    float g[kScanRows], l[kScanRows], ge[ENT ? kScanRows : 1], en[ENT ? kScanRows : 1];
 #pragma unroll
     for (int k = 0; k < kScanRows; ++k) {
       const int64_t t = t0 + k * kScanThreads + tid;
@@ -123,17 +126,24 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
       y[k] = load_index(a.targets, a.idx64, u);
       g[k] = l[k] = 0.f;
       if (a.backward) {
-        g[k] = glob(a.grad_losses)[u];
+        if (!ENT || a.grad_losses) g[k] = glob(a.grad_losses)[u];
         l[k] = glob(a.lse_in)[u];
+        if constexpr (ENT) {
+          ge[k] = a.grad_entropy ? glob(a.grad_entropy)[u] : 0.f;
+          en[k] = a.grad_entropy ? glob(a.entropy_in)[u] : 0.f;
+        }
       }
       if (t >= a.tokens) y[k] = a.ignore;
     }
     uint64_t in[kScanRows];
 #pragma unroll
     for (int k = 0; k < kScanRows; ++k) {
-      const bool part = y[k] != a.ignore && (!a.backward || ((in_vocab(y[k], a.vocab) || y[k] == kElsewhere) && !(g[k] == 0.f)));
+      const bool some = ENT ? !(g[k] == 0.f && ge[ENT ? k : 0] == 0.f) && !(l[k] == -INFINITY) : !(g[k] == 0.f);
+      const bool part = y[k] != a.ignore && (!a.backward || ((in_vocab(y[k], a.vocab) || y[k] == kElsewhere) && some));
       in[k] = __ballot(part);
       if (part && fabsf(g[k]) < INFINITY) gm = fmaxf(gm, fabsf(g[k]));
+      if constexpr (ENT)
+        if (a.backward && part && fabsf(ge[k]) < INFINITY) gm = fmaxf(gm, fabsf(ge[k]));
       if (lane == 0) place[k * waves + wave] = __popcll(in[k]);
     }
     __syncthreads();
@@ -163,10 +173,15 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
         if (a.backward) {
           a.clse[i] = l[k];
           a.cg[i] = g[k];
+          if constexpr (ENT) {
+            a.ce[i] = ge[k];
+            a.cent[i] = en[k];
+          }
         }
       } else if (!a.backward) {
         a.losses[t] = 0.f;
         a.lse[t] = 0.f;
+        if constexpr (ENT) a.entropy[t] = 0.f;
       }
     }
     base = total;
@@ -707,7 +722,29 @@ __device__ __forceinline__ int live_block(int G) {
 // other clocks, 875 to 1210); 8192 × 4096 and 16384 rows, backward: 850 to 890 µs on
 // average = 1.23 to 1.29.  Of a tile's 109 µs about 10 are prologue and epilogue, which nothing overlaps.
 // ---------------------------------------------------------------------------
-template <typename S, bool BACKWARD, bool F32>
+// ENT: log probabilities with entropies, of x = scale·z.
+//   forward:  also Σ (x − largest)·exp(x − largest); the entropy is the logarithm of the
+//             sum of exponentials minus the quotient of the two sums, neither of which cancels;
+//   backward: dZ(t, v) = scale·(g_t·([v = target] − p) − e_t·p·(l + entropy_t)), l = x − lse_t,
+//             p = exp l, l kept from −200 on (p is 0 there) so that 0·−∞ does not arise.
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kFar = -1e30f;               // a difference whose exponential is 0
+// (m, s) joined with another pair; a NaN in s stays
+__device__ __forceinline__ void join_stat(CeStat& a, CeStat b) {
+  const float m = fmaxf(a.m, b.m);
+  a.s = (a.m == -INFINITY ? a.s : a.s * __expf(a.m - m)) + (b.m == -INFINITY ? b.s : b.s * __expf(b.m - m));
+  a.m = m;
+}
+// ... with u = Σ (x − m)·e^(x − m), which becomes Σ (x − m')·… for another m' first
+__device__ __forceinline__ void join_stat(CeStatU& a, CeStatU b) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = a.m == -INFINITY ? 0.f : a.m - m, db = b.m == -INFINITY ? 0.f : b.m - m;
+  const float fa = __expf(da), fb = __expf(db);
+  a.u = fa * fmaf(fmaxf(da, kFar), a.s, a.u) + fb * fmaf(fmaxf(db, kFar), b.s, b.u);
+  a.s = a.s * fa + b.s * fb;
+  a.m = m;
+}
+template <typename S, bool BACKWARD, bool F32, bool ENT>
 __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   extern __shared__ __align__(16) char smem[];
   // the order is laid over the tiles that tokens reach, so that every XCD gets its
@@ -744,7 +781,7 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
   const bool ragged = g.vrows - row0 < S::M;
   // register row of the target of column j's token, or −1
   int want[2];
-  float L[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+  float L[2] = {0.f, 0.f}, w[2] = {0.f, 0.f}, we[2] = {0.f, 0.f}, H[2] = {0.f, 0.f};
   int tok[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -756,14 +793,27 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
       if constexpr (BACKWARD) {
         L[j] = g.clse[tok[j]];
         w[j] = g.cg[tok[j]] / *g.gmax;
+        if constexpr (ENT) {
+          w[j] *= g.scale;
+          we[j] = g.ce[tok[j]] / *g.gmax * g.scale;
+          H[j] = g.cent[tok[j]];
+        }
       }
     }
   }
   auto reg_row = [](int i, int r) { return i * 32 + (r >> 2) * 8 + (r & 3); };
 
-  constexpr float kLog2e = 1.44269504088896341f;
+  using Stat = std::conditional_t<ENT, CeStatU, CeStat>;
+  if constexpr (ENT && !BACKWARD) {
+#pragma unroll
+    for (int i = 0; i < S::I; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= g.scale;
+  }
   if constexpr (!BACKWARD) {
-    CeStat* st = (CeStat*)smem;                              // [wave row][token of the tile]
+    Stat* st = (Stat*)smem;                                  // [wave row][token of the tile]
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (ragged) {
@@ -780,13 +830,21 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
         for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       const float m0 = m == -INFINITY ? 0.f : m;             // then s is 0, or NaN if a logit is
-      float s = 0.f;
+      float s = 0.f, u = 0.f;
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((acc[i][j][r] - m0) * kLog2e);
+        for (int r = 0; r < 16; ++r) {
+          const float d = acc[i][j][r] - m0, p = __builtin_amdgcn_exp2f(d * kLog2e);
+          s += p;
+          if constexpr (ENT) u = fmaf(p, fmaxf(d, kFar), u);
+        }
       s += __shfl_xor(s, 32, 64);
-      if (h == 0) st[wr * S::N + wc * 64 + j * 32 + r32] = CeStat{m, s};
+      if constexpr (ENT) u += __shfl_xor(u, 32, 64);
+      if (h == 0) {
+        if constexpr (ENT) st[wr * S::N + wc * 64 + j * 32 + r32] = CeStatU{m, s, u};
+        else st[wr * S::N + wc * 64 + j * 32 + r32] = CeStat{m, s};
+      }
       if (__any(want[j] >= 0)) {                             // few tiles hold a token's target
         float z = 0.f;
 #pragma unroll
@@ -799,11 +857,18 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
     }
     __syncthreads();
     if (tid < S::N && col0 + tid < count) {
-      const CeStat a = st[tid], b = st[S::N + tid];
-      const float m = fmaxf(a.m, b.m);
-      const float sa = a.m == -INFINITY ? a.s : a.s * __expf(a.m - m);
-      const float sb = b.m == -INFINITY ? b.s : b.s * __expf(b.m - m);
-      g.stats[(int64_t)(g.v0 / S::M + tv) * g.tokens + col0 + tid] = CeStat{m, sa + sb};
+      const int64_t at = (int64_t)(g.v0 / S::M + tv) * g.tokens + col0 + tid;
+      if constexpr (ENT) {
+        CeStatU a = st[tid];
+        join_stat(a, st[S::N + tid]);
+        g.stats_u[at] = a;
+      } else {
+        const CeStat a = st[tid], b = st[S::N + tid];
+        const float m = fmaxf(a.m, b.m);
+        const float sa = a.m == -INFINITY ? a.s : a.s * __expf(a.m - m);
+        const float sb = b.m == -INFINITY ? b.s : b.s * __expf(b.m - m);
+        g.stats[at] = CeStat{m, sa + sb};
+      }
     }
   } else {
 #pragma unroll
@@ -811,18 +876,28 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
 #pragma unroll
       for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_amdgcn_exp2f((acc[i][j][r] - L[j]) * kLog2e);
+        for (int r = 0; r < 16; ++r) {
+          if constexpr (ENT) {
+            float l = fmaf(acc[i][j][r], g.scale, -L[j]);
+            l = l < -200.f ? -200.f : l;                     // a NaN stays
+            acc[i][j][r] = -__builtin_amdgcn_exp2f(l * kLog2e) * fmaf(we[j], l + H[j], w[j]);
+          } else {
+            acc[i][j][r] = __builtin_amdgcn_exp2f((acc[i][j][r] - L[j]) * kLog2e);
+          }
+        }
       if (__any(want[j] >= 0)) {
 #pragma unroll
         for (int i = 0; i < S::I; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (reg_row(i, r) == want[j]) acc[i][j][r] -= 1.f;
+            if (reg_row(i, r) == want[j]) acc[i][j][r] += ENT ? w[j] : -1.f;
       }
+      if constexpr (!ENT) {
 #pragma unroll
-      for (int i = 0; i < S::I; ++i)
+        for (int i = 0; i < S::I; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] *= w[j];
+          for (int r = 0; r < 16; ++r) acc[i][j][r] *= w[j];
+      }
       if (ragged) {
 #pragma unroll
         for (int i = 0; i < S::I; ++i)
@@ -886,6 +961,7 @@ __global__ __launch_bounds__(kThreads) void k_ce_few_start(CeScanArgs a, PackArg
     } else if (here) {
       a.losses[lane] = 0.f;
       a.lse[lane] = 0.f;
+      if (a.entropy) a.entropy[lane] = 0.f;
     }
     if (lane == 0) *a.count = count;
   }
@@ -939,10 +1015,11 @@ __device__ __forceinline__ void mfma16(const u32x4_t& a, const u32x4_t& b, f32x4
 }
 
 // T: W's type, NT: tiles of 16 tokens, U: stages in flight
-template <typename T, int NT, int U>
+template <typename T, int NT, int U, bool ENT>
 __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
   constexpr int P = sizeof(T) == 4 ? kPlanes : 1, waves = kThreads / 64;
-  __shared__ CeStat part[waves][NT * 16];
+  using Stat = std::conditional_t<ENT, CeStatU, CeStat>;
+  __shared__ Stat part[waves][NT * 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
   const int v0 = (blockIdx.x * waves + wave) * 16;
   const int row = v0 + n < g.vocab ? v0 + n : g.vocab - 1;               // a row of W, also past its end
@@ -1031,10 +1108,11 @@ __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
   for (int j = 0; j < NT; ++j) {
     f32x4_t z = acc[j][0];
     if constexpr (P > 1) z += acc[j][P > 1 ? 1 : 0];
+    if constexpr (ENT) z *= g.scale;
     const float zr[4] = {z.x, z.y, z.z, z.w};
     const int t = j * 16 + n;
     const int want = t < count ? g.tgt[t] - v0 - 4 * q : -1;
-    float m = -INFINITY, s = 0.f;
+    float m = -INFINITY, s = 0.f, u = 0.f;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (v0 + 4 * q + r < g.vocab) m = fmaxf(m, zr[r]);
@@ -1044,16 +1122,31 @@ __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (v0 + 4 * q + r < g.vocab) {
-        s += __expf(zr[r] - m0);
+        const float p = __expf(zr[r] - m0);
+        s += p;
+        if constexpr (ENT) u = fmaf(p, fmaxf(zr[r] - m0, kFar), u);
         if (r == want) g.zt[t] = zr[r];
       }
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
-    if (q == 0) part[wave][t] = CeStat{m, s};
+    if constexpr (ENT) {
+      u += __shfl_xor(u, 16, 64);
+      u += __shfl_xor(u, 32, 64);
+      if (q == 0) part[wave][t] = CeStatU{m, s, u};
+    } else {
+      if (q == 0) part[wave][t] = CeStat{m, s};
+    }
   }
   __syncthreads();
   const int t = threadIdx.x;
-  if (t < NT * 16 && t < count) {
+  if constexpr (ENT) {
+    if (t < NT * 16 && t < count) {
+      CeStatU all = part[0][t];
+#pragma unroll
+      for (int x = 1; x < waves; ++x) join_stat(all, part[x][t]);
+      g.stats_u[(int64_t)blockIdx.x * g.tokens + t] = all;
+    }
+  } else if (t < NT * 16 && t < count) {
     float m = part[0][t].m, s = 0.f;
 #pragma unroll
     for (int x = 1; x < waves; ++x) m = fmaxf(m, part[x][t].m);
@@ -1071,23 +1164,29 @@ __global__ __launch_bounds__(kThreads) void k_ce_few(CeFewArgs g) {
 // workgroup: 16, or 4 where the tokens are few and their entries many (16 tokens: 500
 // entries 5.6 and 3.2 µs, 2000 entries 17.8 and 5.9).
 // ---------------------------------------------------------------------------
-// (m, s) joined with another pair; a NaN in s stays
-__device__ __forceinline__ void join_stat(CeStat& a, CeStat b) {
-  const float m = fmaxf(a.m, b.m);
-  a.s = (a.m == -INFINITY ? a.s : a.s * __expf(a.m - m)) + (b.m == -INFINITY ? b.s : b.s * __expf(b.m - m));
-  a.m = m;
-}
-template <int TOK>
+template <int TOK, bool ENT>
 __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
   constexpr int per = kThreads / TOK, waves = kThreads / 64;
-  __shared__ CeStat part[waves][TOK];
+  using Stat = std::conditional_t<ENT, CeStatU, CeStat>;
+  __shared__ Stat part[waves][TOK];
   const int count = *a.count;
   const int i0 = blockIdx.x * TOK;
   if (i0 >= count) return;
   const int ti = threadIdx.x % TOK, k = threadIdx.x / TOK;
   const int i = i0 + ti;
-  CeStat all = {-INFINITY, 0.f};
-  if (i < count) {
+  Stat all = {-INFINITY, 0.f};
+  if constexpr (ENT) {
+    if (i < count) {
+      for (int v = k; v < a.tiles_v; v += 4 * per) {
+        CeStatU x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          x[u] = v + per * u < a.tiles_v ? a.stats_u[(int64_t)(v + per * u) * a.tokens + i] : CeStatU{-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) join_stat(all, x[u]);
+      }
+    }
+  } else if (i < count) {
     for (int v = k; v < a.tiles_v; v += 4 * per) {
       CeStat x[4];
 #pragma unroll
@@ -1101,7 +1200,10 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
     }
   }
 #pragma unroll
-  for (int o = TOK; o < 64; o <<= 1) join_stat(all, CeStat{__shfl_xor(all.m, o, 64), __shfl_xor(all.s, o, 64)});
+  for (int o = TOK; o < 64; o <<= 1) {
+    if constexpr (ENT) join_stat(all, CeStatU{__shfl_xor(all.m, o, 64), __shfl_xor(all.s, o, 64), __shfl_xor(all.u, o, 64)});
+    else join_stat(all, CeStat{__shfl_xor(all.m, o, 64), __shfl_xor(all.s, o, 64)});
+  }
   if ((threadIdx.x & 63) < TOK) part[threadIdx.x >> 6][ti] = all;
   __syncthreads();
   if (threadIdx.x < TOK && i < count) {
@@ -1110,6 +1212,12 @@ __global__ __launch_bounds__(kThreads) void k_ce_rows(CeRowsArgs a) {
     const int t = a.rows[i];
     const int y = a.tgt[i];
     a.lse[t] = all.m + ls;
+    if constexpr (ENT) {                                     // nothing but −∞: no entropy
+      const bool none = all.s == 0.f;
+      a.entropy[t] = none ? 0.f : ls - all.u / all.s;
+      a.losses[t] = y >= 0 ? (none ? -INFINITY : (a.zt[i] - all.m) - ls) : y == kTgtElsewhere ? -(all.m + ls) : __uint_as_float(0x7fc00000u);
+      return;
+    }
     a.losses[t] = y >= 0 ? (all.m - a.zt[i]) + ls : y == kTgtElsewhere ? all.m + ls : __uint_as_float(0x7fc00000u);
   }
 }
@@ -1940,41 +2048,49 @@ int launch_pack(const PackArgs& a, int phase, void* stream) {
   DMUON_LAUNCH(phase, stream, k_pack, stride_grid(round_up(a.rows, 8) * (a.ldd / 8)), kThreads, 0, a);
 }
 int launch_ce_scan(const CeScanArgs& a, void* stream) {
-  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan, 1, kScanThreads, 0, a);
+  if (a.entropy || a.ce) DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan<true>, 1, kScanThreads, 0, a);
+  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_scan<false>, 1, kScanThreads, 0, a);
 }
-template <typename S, bool BACKWARD, bool F32>
+template <typename S, bool BACKWARD, bool F32, bool ENT>
 static int ce_logits(const CeLogitsArgs& a, void* stream) {
   static std::atomic<uint64_t> ready{0};
-  const int e = raise_lds((const void*)k_ce_logits<S, BACKWARD, F32>, S::Lds, ready);
+  const int e = raise_lds((const void*)k_ce_logits<S, BACKWARD, F32, ENT>, S::Lds, ready);
   if (e) return e;
-  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<S, BACKWARD, F32>), (unsigned)(a.tiles_t * a.tiles_v), S::Threads, S::Lds, a);
+  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_logits<S, BACKWARD, F32, ENT>), (unsigned)(a.tiles_t * a.tiles_v), S::Threads, S::Lds, a);
+}
+template <typename S, bool ENT>
+static int ce_logits_of(const CeLogitsArgs& a, int backward, int f32, void* stream) {
+  if (!backward) return ce_logits<S, false, false, ENT>(a, stream);
+  return f32 ? ce_logits<S, true, true, ENT>(a, stream) : ce_logits<S, true, false, ENT>(a, stream);
 }
 int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream) {
-  if (a.tile == Large::M) {
-    if (!backward) return ce_logits<Large, false, false>(a, stream);
-    return f32 ? ce_logits<Large, true, true>(a, stream) : ce_logits<Large, true, false>(a, stream);
-  }
-  if (!backward) return ce_logits<Small, false, false>(a, stream);
-  return f32 ? ce_logits<Small, true, true>(a, stream) : ce_logits<Small, true, false>(a, stream);
+  if (a.tile == Large::M) return a.with_entropy ? ce_logits_of<Large, true>(a, backward, f32, stream) : ce_logits_of<Large, false>(a, backward, f32, stream);
+  return a.with_entropy ? ce_logits_of<Small, true>(a, backward, f32, stream) : ce_logits_of<Small, false>(a, backward, f32, stream);
 }
 int launch_ce_few_start(const CeScanArgs& a, const PackArgs& p, void* stream) {
   DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_few_start, (unsigned)cdiv(cdiv(a.tokens, 8) * (p.ldd / 64), kThreads / 64), kThreads, 0, a, p);
 }
-int launch_ce_few(const CeFewArgs& a, int f32, void* stream) {
+template <bool ENT>
+static int ce_few(const CeFewArgs& a, int f32, void* stream) {
   const unsigned grid = (unsigned)cdiv(a.vocab, kFewRows);
   const int nt = few_tiles(a.tokens);
   if (f32) {
-    if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 1, 2>), grid, kThreads, 0, a);
-    if (nt == 2) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 2, 2>), grid, kThreads, 0, a);
-    DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 4, 2>), grid, kThreads, 0, a);
+    if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 1, 2, ENT>), grid, kThreads, 0, a);
+    if (nt == 2) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 2, 2, ENT>), grid, kThreads, 0, a);
+    DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<float, 4, 2, ENT>), grid, kThreads, 0, a);
   }
-  if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 1, 8>), grid, kThreads, 0, a);
-  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 2, 8>), grid, kThreads, 0, a);
+  if (nt == 1) DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 1, 8, ENT>), grid, kThreads, 0, a);
+  DMUON_LAUNCH(PH_CE_LOGITS, stream, (k_ce_few<uint16_t, 2, 8, ENT>), grid, kThreads, 0, a);
 }
-int launch_ce_rows(const CeRowsArgs& a, void* stream) {
-  if (a.tokens <= kFewTokens) DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows<4>, (unsigned)cdiv(a.tokens, 4), kThreads, 0, a);
-  DMUON_LAUNCH(PH_CE_ROWS, stream, k_ce_rows<16>, (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
+int launch_ce_few(const CeFewArgs& a, int f32, void* stream) {
+  return a.with_entropy ? ce_few<true>(a, f32, stream) : ce_few<false>(a, f32, stream);
 }
+template <bool ENT>
+static int ce_rows(const CeRowsArgs& a, void* stream) {
+  if (a.tokens <= kFewTokens) DMUON_LAUNCH(PH_CE_ROWS, stream, (k_ce_rows<4, ENT>), (unsigned)cdiv(a.tokens, 4), kThreads, 0, a);
+  DMUON_LAUNCH(PH_CE_ROWS, stream, (k_ce_rows<16, ENT>), (unsigned)cdiv(a.tokens, 16), kThreads, 0, a);
+}
+int launch_ce_rows(const CeRowsArgs& a, void* stream) { return a.entropy ? ce_rows<true>(a, stream) : ce_rows<false>(a, stream); }
 template <typename S, bool TB>
 static int product(const ProductArgs& a, int phase, void* stream) {
   static std::atomic<uint64_t> ready{0};

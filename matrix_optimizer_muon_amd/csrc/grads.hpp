@@ -57,17 +57,27 @@ struct CeScanArgs {
   const float* lse_in;         // backward
   float* losses;               // forward: zeroed where ignored
   float* lse;
+  float* entropy;              // the same, or null
+  const float* grad_entropy;   // backward of the log probabilities: or null
+  const float* entropy_in;     // with grad_entropy
   int32_t* rows;               // token of compact row i
   int32_t* pos;                // compact row of token t, or −1
   int32_t* tgt;                // target of compact row i, kTgtElsewhere or kTgtNone
   float* clse;                 // backward: lse of compact row i
   float* cg;                   // backward: gradient weight of compact row i
+  float* ce;                   // ... of its entropy
+  float* cent;                 // its entropy
   int32_t* count;              // number of compact rows
   float* gmax;                 // backward: largest |weight|
 };
 
 struct CeStat {
   float m, s;                  // largest logit, Σ exp(z − m)
+};
+
+// with entropies also Σ (x − m)·exp(x − m), x the scaled logits
+struct CeStatU {
+  float m, s, u;
 };
 
 struct CeLogitsArgs {
@@ -86,6 +96,12 @@ struct CeLogitsArgs {
   // forward
   CeStat* stats;               // [vocabulary tile][tokens]
   float* zt;                   // target's logit
+  // log probabilities with entropies: the logits' scale and these statistics instead
+  int32_t with_entropy;
+  float scale;
+  CeStatU* stats_u;
+  const float* ce;             // backward: weights of the entropies, and the entropies
+  const float* cent;
   // backward
   const float* clse;
   const float* cg;
@@ -111,6 +127,9 @@ struct CeFewArgs {
   const int32_t* tgt;
   CeStat* stats;               // [64 vocabulary rows][tokens]
   float* zt;
+  int32_t with_entropy;
+  float scale;
+  CeStatU* stats_u;
 };
 
 struct CeRowsArgs {
@@ -120,8 +139,10 @@ struct CeRowsArgs {
   const int32_t* rows;
   const int32_t* count;
   int32_t tokens, tiles_v;
-  float* losses;
+  float* losses;               // or the log probabilities
   float* lse;
+  const CeStatU* stats_u;      // with entropies, instead of stats
+  float* entropy;
 };
 
 // ---- gradient products --------------------------------------------------------

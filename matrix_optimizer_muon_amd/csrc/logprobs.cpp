@@ -46,7 +46,7 @@ int check_rows(const dmuon_logprobs_problem* p, bool backward) {
   if (p->vocab < 1 || p->vocab > kMaxVocab) return fail(DMUON_E_SHAPE, "vocab must be in [1, 2^22]");
   if (p->ld < p->vocab || p->ld > kMaxStride) return fail(DMUON_E_SHAPE, "ld must be at least vocab");
   if (!spans(p->tokens, p->vocab, p->ld, type_bytes(p->dtype))) return fail(DMUON_E_SHAPE, "logits must end within 2^48 bytes");
-  if (!(p->scale >= 0x1p-20f && p->scale <= 0x1p20f)) return fail(DMUON_E_CFG, "scale must be in [2^-20, 2^20]");
+  if (!logit_scale(p->scale)) return fail(DMUON_E_CFG, "scale must be in [2^-20, 2^20]");
   if (!backward && (p->top < 0 || p->top > kTopMost || p->top > p->vocab))
     return fail(DMUON_E_CFG, "top must be in [0, 128] and at most vocab");
   if (p->tokens > 0 && !p->logits) return fail(DMUON_E_NULL, "logits must be set");

@@ -495,12 +495,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const gptr<T> dst = glob((T*)a.out) + row * a.ldo;
   const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
   const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kShard;
-  float g = a.grad_logprobs ? a.grad_logprobs[row] : 0.f;
-  float h = a.grad_entropy ? a.grad_entropy[row] : 0.f;
+  const float g = a.grad_logprobs ? a.grad_logprobs[row] : 0.f;
+  const float h = a.grad_entropy ? a.grad_entropy[row] : 0.f;
   const float lse = a.lse[row];
   const float entropy = a.grad_entropy ? a.entropy[row] : 0.f;
   const bool takes_part = kind != kIgnored && kind != kOutside && !(g == 0.f && h == 0.f) && !(lse == -INFINITY);
-  if (lse != lse) g = kNan;
   const int target = kind == kInside ? (int)y : -1;
 #pragma unroll
   for (int k = 0; k < kGradUnits; ++k) {
@@ -511,7 +510,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
       any_unit<T, 8>(src, j, a.vocab, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float l = fmaxf(fmaf(v[e], a.scale, -lse), -200.f);
+        float l = fmaf(v[e], a.scale, -lse);
+        l = l < -200.f ? -200.f : l;                     // a NaN stays
         const float p = __builtin_amdgcn_exp2f(l * kLog2e);
         const float d = -p * fmaf(h, l + entropy, g);
         v[e] = a.scale * (j * 8 + e == target ? d + g : d);

@@ -2,6 +2,8 @@
 
     token_logprobs(logits, targets, top=20)              # from logits: also the alternatives
     token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_entropy)
+    linear_token_logprobs(h, w, targets)                 # from hidden states, logits not kept
+    linear_token_logprobs_backward(h, w, targets, lse, entropy, grad_logprobs, grad_entropy)
 
 Calls, streams and autograd as in ``training``: the functions record nothing, and the
 forward ones refuse inputs that require gradients where autograd records.
@@ -12,9 +14,10 @@ import ctypes
 from typing import NamedTuple, Optional
 
 from . import _binding as _b
-from .training import _dense, _float_code, _index_code, _matrix, _no_graph, _on, _ptr, _ws_args
+from .training import _ce_problem, _dense, _float_code, _index_code, _matrix, _no_graph, _on, _ptr, _ws_args
 
-__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_backward"]
+__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_backward", "linear_token_logprobs",
+           "linear_token_logprobs_backward"]
 
 
 class TokenLogprobs(NamedTuple):
@@ -110,3 +113,55 @@ def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_e
         _b.check(_b.lib().dmuon_logprobs_backward(ctypes.byref(prob), _ptr(lse), _ptr(entropy), _ptr(grad_logprobs),
                                                   _ptr(grad_entropy), _ptr(out), ld, on.handle))
     return out
+
+
+def _linear_workspace(prob, backward, workspace, on, device):
+    need = ctypes.c_size_t(0)
+    _b.check(_b.lib().dmuon_linear_logprobs_workspace_size(ctypes.byref(prob), backward, ctypes.byref(need)))
+    return on.workspace(workspace, need.value, device)
+
+
+def linear_token_logprobs(h, w, targets, *, scale=1.0, ignore_index=-100, workspace=None, stream=None):
+    """Log probabilities of given tokens and entropies of a vocabulary, logits not kept.
+
+    h, w, targets, ``ignore_index`` and shards of the vocabulary as in
+    ``linear_cross_entropy``; the logits h·wᵀ are multiplied by ``scale``.  Returns a
+    ``TokenLogprobs`` without alternatives, its values as those of ``token_logprobs``.
+    """
+    import torch
+    _no_graph("linear_token_logprobs", h=h, w=w)
+    prob = _ce_problem(h, w, targets, ignore_index)
+    with _on(stream, h, w, targets) as on:
+        logprobs, entropy, lse = (torch.empty(targets.shape, dtype=torch.float32, device=h.device) for _ in range(3))
+        ws = _linear_workspace(prob, 0, workspace, on, h.device)
+        _b.check(_b.lib().dmuon_linear_logprobs(ctypes.byref(prob), float(scale), _ptr(logprobs), _ptr(entropy), _ptr(lse),
+                                                *_ws_args(ws), on.handle))
+    return TokenLogprobs(logprobs, entropy, lse)
+
+
+def linear_token_logprobs_backward(h, w, targets, lse, entropy, grad_logprobs, grad_entropy=None, *, scale=1.0,
+                                   ignore_index=-100, grad_h=None, grad_w=None, need_h=True, need_w=True, workspace=None,
+                                   stream=None):
+    """Gradients of ``linear_token_logprobs`` with respect to h and w.
+
+    lse, entropy, grad_logprobs and grad_entropy as in ``token_logprobs_backward``; grad_h,
+    grad_w, ``need_h`` and ``need_w`` as in ``linear_cross_entropy_backward``.
+    """
+    import torch
+    prob = _ce_problem(h, w, targets, ignore_index)
+    _check_row_grads(targets.shape, lse, entropy, grad_logprobs, grad_entropy)
+    for t, what, like, need in ((grad_h, "grad_h", h, need_h), (grad_w, "grad_w", w, need_w)):
+        if t is not None and not need:
+            raise ValueError(f"{what} is given but not needed")
+        if t is not None:
+            _dense(t, what, like.dtype, like.shape)
+    with _on(stream, h, w, targets, lse, entropy, grad_logprobs, grad_entropy, grad_h, grad_w) as on:
+        if need_h and grad_h is None:
+            grad_h = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        if need_w and grad_w is None:
+            grad_w = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+        ws = _linear_workspace(prob, 1, workspace, on, h.device)
+        _b.check(_b.lib().dmuon_linear_logprobs_backward(ctypes.byref(prob), float(scale), _ptr(lse), _ptr(entropy),
+                                                         _ptr(grad_logprobs), _ptr(grad_entropy), _ptr(grad_h), _ptr(grad_w),
+                                                         *_ws_args(ws), on.handle))
+    return grad_h, grad_w

@@ -135,3 +135,64 @@ def test_python_refusals():
         with torch.no_grad():
             assert "GPU tensor" in refusal(call)
     assert "torch.Tensor" in refusal(lambda: mm.token_logprobs([1.0], y))
+
+
+# ---- from hidden states -----------------------------------------------------------
+def ce(**kw):
+    d = dict(tokens=64, width=128, vocab=1000, dtype=B.BF16, index_dtype=B.I64, h=at(1), ldh=128, w=at(2), ldw=128, targets=at(3),
+             ignore_index=-100)
+    d.update(kw)
+    return B.CeProblem(*[d[n] for n, _ in B.CeProblem._fields_])
+
+
+def lsize(p, backward=0):
+    out = ctypes.c_size_t(0)
+    rc = B.lib().dmuon_linear_logprobs_workspace_size(ctypes.byref(p), backward, ctypes.byref(out))
+    return rc, out.value
+
+
+def lfwd(p, scale=1.0, lp=at(4), H=at(5), lse=at(6), ws=WS, nbytes=1 << 39):
+    return B.lib().dmuon_linear_logprobs(ctypes.byref(p), scale, vp(lp), vp(H), vp(lse), vp(ws), nbytes, None)
+
+
+def lbwd(p, scale=1.0, lse=at(6), H=at(5), g=at(7), e=at(8), gh=at(9), gw=at(10), ws=WS, nbytes=1 << 39):
+    return B.lib().dmuon_linear_logprobs_backward(ctypes.byref(p), scale, vp(lse), vp(H), vp(g), vp(e), vp(gh), vp(gw), vp(ws),
+                                                  nbytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=7), -4), (dict(index_dtype=5), -4), (dict(tokens=-1), -3), (dict(tokens=(1 << 24) + 1), -3), (dict(width=0, ldh=0, ldw=0), -3),
+    (dict(vocab=0), -3), (dict(ldh=127), -3), (dict(ldw=127), -3), (dict(h=None), -1), (dict(w=None), -1), (dict(targets=None), -1),
+    (dict(tokens=1 << 24, vocab=1 << 30), -3)])
+def test_linear_refusals(kw, code):
+    assert lfwd(ce(**kw)) == code and lbwd(ce(**kw)) == code
+
+
+def test_linear_refusals_of_outputs():
+    p = ce()
+    assert lfwd(p) == -8 and lbwd(p) == -8
+    for s in (0.0, -1.0, math.inf, math.nan, 2.0 ** -21, 2.0 ** 21):
+        assert lfwd(p, s) == -5 and lbwd(p, s) == -5
+    assert lfwd(p, lp=None) == -1 and lfwd(p, H=None) == -1 and lfwd(p, lse=None) == -1
+    assert lfwd(p, H=at(4)) == -7 and lfwd(p, H=at(1)) == -7
+    assert lbwd(p, lse=None) == -1 and lbwd(p, H=None) == -1 and lbwd(p, g=None, e=None) == -1
+    assert lbwd(p, g=None) == -8 and lbwd(p, e=None, H=None) == -8 and lbwd(p, gh=None) == -8
+    assert lbwd(p, gh=None, gw=None) == 0
+    assert lbwd(p, gh=at(8)) == -7 and lbwd(p, gw=at(5)) == -7
+    for call, n in ((lfwd, lsize(p)[1]), (lbwd, lsize(p, 1)[1])):
+        assert n > 0 and call(p, nbytes=n) == -8
+        assert call(p, nbytes=n - 1) == -6 and call(p, ws=None) == -6 and call(p, ws=WS + 8) == -6 and call(p, ws=at(1)) == -7
+    assert lsize(p, 2)[0] == -5
+    assert B.lib().dmuon_linear_logprobs_workspace_size(ctypes.byref(p), 0, None) == -1
+    none = ce(tokens=0, h=None, targets=None)
+    assert lsize(none) == (0, 0) and lfwd(none, lp=None, H=None, lse=None, ws=None) == 0
+    assert lbwd(none, lse=None, H=None, g=None, e=None, gw=None, ws=None) == -8     # accepted
+
+
+def test_linear_python_refusals():
+    h, w, y, g = torch.zeros(4, 8), torch.zeros(5, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
+    assert "GPU tensor" in refusal(lambda: mm.linear_token_logprobs(h, w, y))
+    assert "GPU tensor" in refusal(lambda: mm.linear_token_logprobs_backward(h, w, y, g, g, g))
+    leaf = h.clone().requires_grad_()
+    assert refusal(lambda: mm.linear_token_logprobs(leaf, w, y)).startswith("h requires gradients")
+    assert refusal(lambda: mm.linear_token_logprobs(h, w.clone().requires_grad_(), y)).startswith("w requires gradients")
