@@ -527,6 +527,49 @@ int dmuon_linear_logprobs_backward(const dmuon_ce_problem* problem, float scale,
                                    const float* grad_logprobs, const float* grad_entropy, void* grad_h, void* grad_w,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- gradient norm and clipping -------------------------------------------
+ * The global 2-norm over many gradients and the gradients scaled down to it, between the
+ * backward pass and the steps:
+ *   norm = √(Σ_i Σ_e g_i(e)²),   c = min(1, max_norm/(norm + eps)),   out_i = c·g_i
+ * Squares and sums are in 64 bits (nothing overflows or vanishes; a norm beyond fp32 is
+ * infinite), c·g is rounded to fp32 and to out's type.  Where the norm is not finite, c is
+ * 1: the gradients pass as they are, and the norm says so. */
+
+/* One gradient of any shape, dense, numel ≥ 0 elements (0: skipped).
+ *   grad        device, dtype (bf16 or fp32)
+ *   out         device, out_dtype: the clipped gradient, for instance inside a packed
+ *               reduce buffer; grad itself to clip in place (then the types agree, and
+ *               nothing is written where c is 1); NULL where only the norm is wanted
+ * out must overlap no other buffer (DMUON_E_ALIAS).  Alignment never matters.  At most
+ * 2^41 elements in all. */
+typedef struct {
+  int64_t numel;
+  int32_t dtype;
+  int32_t out_dtype;
+  const void* grad;
+  void* out;
+} dmuon_grad_tensor;
+
+/* Bytes of workspace of the calls below (host only, no HIP call). */
+int dmuon_grad_workspace_size(const dmuon_grad_tensor* tensors, int32_t n_tensors, size_t* bytes);
+
+/* Writes the tables of these tensors into the workspace; the runs launch the kernels
+ * that read them.  As for dmuon_muon_step_prepare: one prepare serves any number of runs
+ * with the same tensors, and a run on a workspace that holds another table changes
+ * nothing.  Runs that overlap on different streams need a workspace each. */
+int dmuon_grad_prepare(const dmuon_grad_tensor* tensors, int32_t n_tensors, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* norm: device fp32, one value (0 without elements). */
+int dmuon_grad_norm_run(const dmuon_grad_tensor* tensors, int32_t n_tensors, float* norm, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* measure = 1: computes and writes norm, then clips.  measure = 0: clips by the norm it
+ * reads (of gradients on several owners: the root of the sum of their squares).  max_norm,
+ * eps ≥ 0, finite.  Every tensor has an out. */
+int dmuon_grad_clip_run(const dmuon_grad_tensor* tensors, int32_t n_tensors, float max_norm, float eps, int32_t measure,
+                        float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Plain NT product C = A·Bᵀ on the matrix-core kernel the step uses (a test hook
  * for the contraction core).  A: M×K (lda elements per row), B: N×K (ldb), both
  * dtype (bf16 or fp32), device; C: M×N fp32 (ldc), device.  lda and ldb must be

@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _binding as _b
+from .clip import ClipGradNorm, clip_grad_norm, grad_norm  # noqa: F401
 from .logprobs import (TokenLogprobs, linear_token_logprobs, linear_token_logprobs_backward, token_logprobs,  # noqa: F401
                        token_logprobs_backward)
 from .training import (TARGET_ELSEWHERE, checkpoint_dequantize, checkpoint_quantize, checkpoint_wgrad, embedding,  # noqa: F401
@@ -29,7 +30,7 @@ __all__ = ["muon_step", "muon_step_workspace_size", "adamw_step", "MuonStep", "A
            "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
            "embedding_backward", "checkpoint_quantize", "checkpoint_dequantize", "checkpoint_wgrad", "TARGET_ELSEWHERE",
            "TokenLogprobs", "token_logprobs", "token_logprobs_backward", "linear_token_logprobs",
-           "linear_token_logprobs_backward",
+           "linear_token_logprobs_backward", "ClipGradNorm", "clip_grad_norm", "grad_norm",
            "phase_timing", "phase_timing_read", "abi_version", "load_library", "HYPER"]
 
 QUINTIC = (HYPER["a"], HYPER["b"], HYPER["c"])

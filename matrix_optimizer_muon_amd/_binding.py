@@ -44,7 +44,8 @@ EXPORTED = ["dmuon_muon_step_workspace_size", "dmuon_muon_step_groups", "dmuon_m
             "dmuon_embedding_backward", "dmuon_ckpt8_quantize", "dmuon_ckpt8_dequantize",
             "dmuon_ckpt8_wgrad_workspace_size", "dmuon_ckpt8_wgrad",
             "dmuon_logprobs_workspace_size", "dmuon_logprobs", "dmuon_logprobs_backward",
-            "dmuon_linear_logprobs_workspace_size", "dmuon_linear_logprobs", "dmuon_linear_logprobs_backward"]
+            "dmuon_linear_logprobs_workspace_size", "dmuon_linear_logprobs", "dmuon_linear_logprobs_backward",
+            "dmuon_grad_workspace_size", "dmuon_grad_prepare", "dmuon_grad_norm_run", "dmuon_grad_clip_run"]
 ABI_VERSION = 5
 
 
@@ -111,6 +112,11 @@ class LogprobsProblem(ctypes.Structure):
                 ("scale", ctypes.c_float), ("top", ctypes.c_int32)]
 
 
+class GradTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -172,6 +178,10 @@ def lib():
     L.dmuon_linear_logprobs_workspace_size.argtypes = [P(CeProblem), i32, P(sz)]
     L.dmuon_linear_logprobs.argtypes = [P(CeProblem), f32, vp, vp, vp, vp, sz, vp]
     L.dmuon_linear_logprobs_backward.argtypes = [P(CeProblem), f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dmuon_grad_workspace_size.argtypes = [P(GradTensor), i32, P(sz)]
+    L.dmuon_grad_prepare.argtypes = [P(GradTensor), i32, vp, sz, vp]
+    L.dmuon_grad_norm_run.argtypes = [P(GradTensor), i32, vp, vp, sz, vp]
+    L.dmuon_grad_clip_run.argtypes = [P(GradTensor), i32, f32, f32, i32, vp, vp, sz, vp]
     L.dmuon_last_error.restype = ctypes.c_char_p
     L.dmuon_last_error.argtypes = []
     for name in EXPORTED:

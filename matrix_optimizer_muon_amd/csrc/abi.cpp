@@ -139,7 +139,7 @@ int settle(const CallEnv& f, void* stream, const char* what) {
   return DMUON_OK;
 }
 
-static int write_table(void* dst, const std::vector<char>& host, void* stream, const CallEnv& fa) {
+int write_table(void* dst, const std::vector<char>& host, void* stream, const CallEnv& fa) {
   int e = forced(fa, -1);
   if (e) return e;
   e = launch_write_table(dst, host.data(), host.size(), stream);

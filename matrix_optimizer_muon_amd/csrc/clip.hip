@@ -1,0 +1,187 @@
+// HIP kernels of the global norm over many gradients and of clipping by it, for gfx950
+// (MI355X).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "clip.hpp"
+#include "core.hpp"
+#include "elements.hpp"
+
+namespace dmuon {
+
+// ---------------------------------------------------------------------------
+// the list of tensors: a workgroup takes a contiguous range of chunks, found with a search
+// of 64 probes a step, and walks the tensors it meets.  f(problem, first element, end).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int first_problem(const ClipTable& tab, int chunk) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = tab.n;                                 // the last p with chunk0[p] ≤ chunk lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 63) >> 6;
+    const int i = lane * step;
+    const bool in = i < n && tab.chunk0[lo + i] <= chunk;
+    const int k = (__popcll(__ballot(in)) - 1) * step;
+    lo += k;
+    n = n - k < step ? n - k : step;
+  }
+  return lo;
+}
+
+// false: the workspace holds another table
+template <typename F>
+__device__ __forceinline__ bool walk(const ClipTable& tab, F f) {
+  int c = (int)((int64_t)blockIdx.x * tab.chunks / tab.groups);
+  const int end = (int)((int64_t)(blockIdx.x + 1) * tab.chunks / tab.groups);
+  if (tab.probs[0].tag != tab.tag) return false;
+  for (int p = first_problem(tab, c); c < end; ++p) {
+    const ClipProblem& P = tab.probs[p];
+    if (P.tag != tab.tag) return false;
+    const int base = tab.chunk0[p], next = tab.chunk0[p + 1];
+    const int stop = next < end ? next : end;
+    const int64_t e0 = (int64_t)(c - base) * kClipChunk, e1 = (int64_t)(stop - base) * kClipChunk;
+    f(P, e0, e1 < P.numel ? e1 : P.numel);
+    c = stop;
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// sums of squares in 64 bits: a square of an fp32 value is exact there, nothing overflows or
+// vanishes, and the order is fixed.  Memory bound.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ double sum_workgroup(double v, double* shared) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (shared[0] + shared[1]) + (shared[2] + shared[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void add_squares(gptr<const T> p, int64_t e0, int64_t e1, double (&sum)[2]) {
+  constexpr int B = sizeof(T) == 2 ? 8 : 4;              // loads in flight
+  const int64_t units = (e1 - e0) >> 3;
+  int64_t j = threadIdx.x;
+  auto add = [&](const Unit<T, 8>& x) {
+    float v[8];
+    x.values(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e & 1] = fma((double)v[e], (double)v[e], sum[e & 1]);
+  };
+  for (; j + (B - 1) * kThreads < units; j += B * kThreads) {
+    Unit<T, 8> x[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) x[k].load(p + e0 + (j + k * kThreads) * 8);
+#pragma unroll
+    for (int k = 0; k < B; ++k) add(x[k]);
+  }
+  for (; j < units; j += kThreads) {
+    Unit<T, 8> x;
+    x.load(p + e0 + j * 8);
+    add(x);
+  }
+  const int64_t e = e0 + units * 8 + threadIdx.x;        // at most 7 elements at a tensor's end
+  if (e < e1) {
+    const double v = element(p + e);
+    sum[0] = fma(v, v, sum[0]);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_norm(ClipTable tab) {
+  __shared__ double shared[kThreads / 64];
+  double sum[2] = {0.0, 0.0};
+  const bool ok = walk(tab, [&](const ClipProblem& P, int64_t e0, int64_t e1) {
+    if (P.f32) add_squares(glob((const float*)P.grad), e0, e1, sum);
+    else add_squares(glob((const uint16_t*)P.grad), e0, e1, sum);
+  });
+  const double all = sum_workgroup(sum[0] + sum[1], shared);
+  if (ok && threadIdx.x == 0) tab.part[blockIdx.x] = all;
+}
+
+// the norm of all partial sums, the same bits wherever it is computed
+__device__ __forceinline__ float joined_norm(const ClipTable& tab, double* shared) {
+  double v[kClipGroups / kThreads];
+#pragma unroll
+  for (int k = 0; k < kClipGroups / kThreads; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    v[k] = i < tab.groups ? tab.part[i] : 0.0;
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < kClipGroups / kThreads; ++k) sum += v[k];
+  return (float)sqrt(sum_workgroup(sum, shared));
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_norm_join(ClipTable tab, float* norm) {
+  __shared__ double shared[kThreads / 64];
+  if (tab.n > 0 && tab.probs[0].tag != tab.tag) return;  // no tensors: 0
+  const float n = joined_norm(tab, shared);
+  if (threadIdx.x == 0) *norm = n;
+}
+
+// ---------------------------------------------------------------------------
+// out = c·g, c = min(1, max_norm/(norm + eps)), 1 where the norm is not finite: one
+// rounding to fp32 and one to the output's type.  Every workgroup joins the partial sums
+// for itself (16 KiB from the caches) instead of waiting for another launch.  A range is
+// walked backwards: its end is what the sums left in the caches.  In place nothing is
+// written where c is 1.
+// ---------------------------------------------------------------------------
+template <typename T, typename O>
+__device__ __forceinline__ void scale_range(gptr<const T> p, gptr<O> out, int64_t e0, int64_t e1, float c) {
+  constexpr int B = 4;
+  const int64_t units = (e1 - e0) >> 3;
+  const int64_t tail = e0 + units * 8 + threadIdx.x;
+  if (tail < e1) store_element(out + tail, element(p + tail) * c);
+  auto put = [&](const Unit<T, 8>& x, int64_t at) {
+    float v[8];
+    x.values(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= c;
+    store_unit(out + at, v);
+  };
+  int64_t j = units - 1 - threadIdx.x;
+  for (; j - (B - 1) * kThreads >= 0; j -= B * kThreads) {
+    Unit<T, 8> x[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) x[k].load(p + e0 + (j - k * kThreads) * 8);
+#pragma unroll
+    for (int k = 0; k < B; ++k) put(x[k], e0 + (j - k * kThreads) * 8);
+  }
+  for (; j >= 0; j -= kThreads) {
+    Unit<T, 8> x;
+    x.load(p + e0 + j * 8);
+    put(x, e0 + j * 8);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable tab, ClipScalars s) {
+  __shared__ double shared[kThreads / 64];
+  if (tab.probs[0].tag != tab.tag) return;
+  const float norm = s.measured ? joined_norm(tab, shared) : *s.norm;
+  if (s.measured && blockIdx.x == 0 && threadIdx.x == 0) *s.norm = norm;
+  const double quotient = (double)s.max_norm / ((double)norm + (double)s.eps);
+  const float c = !(fabsf(norm) < INFINITY) || !(quotient < 1.0) ? 1.f : (float)quotient;
+  walk(tab, [&](const ClipProblem& P, int64_t e0, int64_t e1) {
+    if (P.out == P.grad && c == 1.f) return;
+    if (P.f32) {
+      if (P.out_f32) scale_range(glob((const float*)P.grad), glob((float*)P.out), e0, e1, c);
+      else scale_range(glob((const float*)P.grad), glob((uint16_t*)P.out), e0, e1, c);
+    } else {
+      if (P.out_f32) scale_range(glob((const uint16_t*)P.grad), glob((float*)P.out), e0, e1, c);
+      else scale_range(glob((const uint16_t*)P.grad), glob((uint16_t*)P.out), e0, e1, c);
+    }
+  });
+}
+
+int launch_grad_norm(const ClipTable& tab, void* stream) {
+  DMUON_LAUNCH(PH_GRAD_NORM, stream, k_grad_norm, (unsigned)tab.groups, kThreads, 0, tab);
+}
+int launch_grad_norm_join(const ClipTable& tab, float* norm, void* stream) {
+  DMUON_LAUNCH(PH_GRAD_NORM, stream, k_grad_norm_join, 1, kThreads, 0, tab, norm);
+}
+int launch_grad_clip(const ClipTable& tab, const ClipScalars& s, void* stream) {
+  DMUON_LAUNCH(PH_GRAD_CLIP, stream, k_grad_clip, (unsigned)tab.groups, kThreads, 0, tab, s);
+}
+
+}  // namespace dmuon

@@ -83,6 +83,53 @@ __device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t 
 }
 
 // ---------------------------------------------------------------------------
+// units: 8 consecutive elements (or one) as they were loaded, from any element on, so that
+// rows of every alignment move 16 bytes at a time: the types are aligned to one element only.
+// ---------------------------------------------------------------------------
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
+template <typename T, int UNIT>
+struct Unit;
+template <>
+struct Unit<uint16_t, 8> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = *(gptr<const u32x4_any>)p; }
+  __device__ __forceinline__ void values(float (&v)[8]) const { unpack8(u, v); }
+};
+template <>
+struct Unit<float, 8> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(gptr<const float> p) {
+    a = ((gptr<const f32x4_any>)p)[0];
+    b = ((gptr<const f32x4_any>)p)[1];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <typename T>
+struct Unit<T, 1> {
+  T x;
+  __device__ __forceinline__ void load(gptr<const T> p) { x = *p; }
+  __device__ __forceinline__ void values(float (&v)[1]) const { v[0] = value(x); }
+  static __device__ __forceinline__ float value(uint16_t b) { return bf16_to_f32(b); }
+  static __device__ __forceinline__ float value(float f) { return f; }
+};
+__device__ __forceinline__ float element(gptr<const uint16_t> p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float element(gptr<const float> p) { return *p; }
+__device__ __forceinline__ void store_unit(gptr<uint16_t> p, const float (&v)[8]) {
+  __builtin_nontemporal_store(pack8(v), (gptr<u32x4_any>)p);
+}
+__device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[8]) {
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
+  __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, (gptr<f32x4_any>)p + 1);
+}
+__device__ __forceinline__ void store_element(gptr<uint16_t> p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ void store_element(gptr<float> p, float v) { *p = v; }
+
+// ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 // Workgroups of a grid-stride kernel: enough to fill 256 CUs several times over

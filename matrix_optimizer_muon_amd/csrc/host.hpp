@@ -28,6 +28,7 @@ CallEnv call_env();
 int forced(const CallEnv& f, int where);
 int settle(const CallEnv& f, void* stream, const char* what);
 const char* phase_name(int phase);
+int write_table(void* dst, const std::vector<char>& host, void* stream, const CallEnv& f);
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
