@@ -25,7 +25,7 @@ struct RowsPlan {
 // rows are too few to fill the card.
 RowsPlan rows_plan(const dmuon_logprobs_problem& p, char* base) {
   RowsPlan pl{};
-  int64_t n = std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
+  int64_t n = p.tokens >= 1024 ? 1 : std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
   if (p.top == 0 && p.vocab <= kWaveRow) n = 1;
   n = std::max<int64_t>({n, cdiv(p.vocab, kPieceMost), 1});
   pl.piece = round_up(cdiv(p.vocab, n), 8);

@@ -100,17 +100,20 @@ struct Row {
   __device__ __forceinline__ float log_p(float z) const { return (z - m) * scale - log_s; }
 };
 
+// ordered bits: rise with the value
+__device__ __forceinline__ uint32_t ordered(float z) {
+  const uint32_t b = __float_as_uint(z);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
 // Keys order by value, then by lower index: the value's bits as a whole number in the
 // high half, ~index in the low one.  NaN counts as −∞, −0 as 0.  No key is 0.
 __device__ __forceinline__ float rankable(float z) { return fmaxf(z, -INFINITY) + 0.f; }
-__device__ __forceinline__ uint64_t key_of(float z, int32_t index) {
-  const uint32_t b = __float_as_uint(z);
-  return ((uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32) | (uint32_t)~index;
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-  const uint32_t b = (uint32_t)(key >> 32);
-  return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
-}
+__device__ __forceinline__ uint64_t key_of(float z, int32_t index) { return (uint64_t)ordered(z) << 32 | (uint32_t)~index; }
+__device__ __forceinline__ float key_value(uint64_t key) { return from_ordered((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int32_t key_index(uint64_t key) { return (int32_t)~(uint32_t)key; }
 
 // what a row's target asks for
@@ -129,84 +132,94 @@ __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, in
 
 // ---------------------------------------------------------------------------
 // the k largest of a piece.  The k-th largest of the threads' maxima, tau, is not above
-// the k-th largest element, so only groups whose maximum (kept in LDS by the first pass)
-// reaches tau are read again, and few elements do.  If more than the list holds are
+// the k-th largest element, and few elements reach it.  Every wave finds it by itself, bit
+// by bit from ballots over the 256 maxima.  If more elements than the list holds are
 // greater than tau, the k-th largest of those it took becomes the new tau (it is greater:
-// each round drops at least the rest of the list).  Elements equal to tau are needed
-// where fewer than k are greater; where many are (equal logits, words masked out by −∞)
-// the first of them in order are looked for.  Places come from counting the greater keys:
+// each round drops at least the rest of the list).  Elements equal to tau are needed where
+// fewer than k are greater; where many are (equal logits, words masked out by −∞) the
+// first of them in order are looked for.  Places come from counting the greater keys:
 // keys are distinct, so the result does not depend on the list's order.
 // ---------------------------------------------------------------------------
-constexpr int kStrict = 768, kTies = 256;
+constexpr int kStrict = 512, kTies = 256;
 
 struct TopShared {
-  float group[kGroups][kThreads];        // largest of each thread's groups
-  uint16_t flag[kGroups * kThreads];     // groups to read again
-  uint64_t list[kStrict + kTies];
-  __attribute__((aligned(16))) float most[kThreads];   // each thread's largest
+  alignas(16) uint64_t list[kStrict + kTies];
+  float most[kThreads];                  // each thread's largest
   int flags, strict, ties, wave[kThreads / 64];
   float tau;
 };
+struct GroupShared {
+  float group[kGroups][kThreads];        // largest of each thread's groups
+  uint16_t flag[kGroups * kThreads];     // groups to read again
+};
+
+// the k-th largest of 256 values in LDS, in every lane (k ≤ 256)
+template <typename T>
+__device__ __forceinline__ float kth_of_threads(const float* most, int k) {
+  constexpr int N = kThreads / 64, low = sizeof(T) == 2 ? 16 : 0;     // bf16: 16 bits tell the values apart
+  const int lane = threadIdx.x & 63;
+  uint32_t key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) key[i] = ordered(most[lane + 64 * i]) >> low;
+  uint32_t t = 0;
+#pragma unroll
+  for (int b = 31 - low; b >= 0; --b) {
+    const uint32_t c = t | 1u << b;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= c));
+    if (n >= k) t = c;
+  }
+  t = __builtin_amdgcn_readfirstlane(t);
+  return from_ordered(low ? t << 16 | (t & 0x8000u ? 0u : 0xffffu) : t);
+}
 
 // the number of keys greater than `key` in list[0, n)
 __device__ __forceinline__ int places_above(const uint64_t* list, int n, uint64_t key) {
   int r = 0;
-  for (int i = 0; i < n; ++i) r += list[i] > key;
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    ulonglong2 o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = *(const ulonglong2*)(list + i + 2 * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r += (o[u].x > key) + (o[u].y > key);
+  }
+  for (; i < n; ++i) r += list[i] > key;
   return r;
 }
 
-// emit(place, key) for the min(k, len) largest of the piece; returns their number
-template <typename T, int UNIT, typename F>
-__device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int len, int first, int k, int groups, F emit) {
+__device__ __forceinline__ void put_candidate(TopShared& sh, float raw, float tau, bool inside, int index) {
+  const float z = rankable(raw);
+  if (z > tau) {
+    const int i = atomicAdd(&sh.strict, 1);
+    if (i < kStrict) sh.list[i] = key_of(z, index);
+  } else if (z == tau && inside) {
+    const int i = atomicAdd(&sh.ties, 1);
+    if (i < kTies) sh.list[kStrict + i] = key_of(z, index);
+  }
+}
+
+// emit(place, key) for the min(k, len) largest of the piece, whose threads' maxima are in
+// sh.most and whose counters are 0 (behind a barrier); returns their number.  gather(tau)
+// puts the piece's elements from tau on into the list.
+template <typename T, typename G, typename F>
+__device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int len, int first, int k, G gather, F emit) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int want = k < len ? k : len;
-  float mine = -INFINITY;
-  for (int g = 0; g < groups; ++g) mine = fmaxf(mine, sh.group[g][tid]);
-  sh.most[tid] = mine;
-  __syncthreads();
-  int above = 0;
-  for (int i = 0; i < kThreads; i += 4) {
-    const f32x4_t o = *(const f32x4_t*)&sh.most[i];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) above += o[e] > mine || (o[e] == mine && i + e < tid);
-  }
-  if (above == k - 1) sh.tau = mine;
-  __syncthreads();
+  float tau = kth_of_threads<T>(sh.most, k);
   int strict, ties;
-  float tau;
   for (;;) {
-    tau = sh.tau;
-    if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
-    __syncthreads();
-    for (int g = 0; g < groups; ++g)
-      if (sh.group[g][tid] >= tau) sh.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
-    __syncthreads();
-    const int units = sh.flags * kGroupUnits;
-    for (int w = tid; w < units; w += kThreads) {
-      const int f = sh.flag[w / kGroupUnits];
-      const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
-      if (j * UNIT >= len) continue;
-      float v[UNIT];
-      any_unit<T, UNIT>(row, j, len, v);
-#pragma unroll
-      for (int e = 0; e < UNIT; ++e) {
-        const float z = rankable(v[e]);
-        const int at = j * UNIT + e;
-        if (z > tau) {
-          const int i = atomicAdd(&sh.strict, 1);
-          if (i < kStrict) sh.list[i] = key_of(z, first + at);
-        } else if (z == tau && at < len) {
-          const int i = atomicAdd(&sh.ties, 1);
-          if (i < kTies) sh.list[kStrict + i] = key_of(z, first + at);
-        }
-      }
-    }
+    gather(tau);
     __syncthreads();
     strict = sh.strict;
     ties = sh.ties;
     if (strict <= kStrict) break;
     for (int i = tid; i < kStrict; i += kThreads)
       if (places_above(sh.list, kStrict, sh.list[i]) == k - 1) sh.tau = key_value(sh.list[i]);
+    __syncthreads();
+    tau = sh.tau;
+    if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
     __syncthreads();
   }
   if (strict >= want) {
@@ -246,13 +259,14 @@ __device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int 
     }
     ties = need;
   }
-  // one list: the ties behind the others
+  if (ties > 0) {                        // one list: the ties behind the others
+    uint64_t moved = 0;
+    if (tid < ties) moved = sh.list[kStrict + tid];
+    __syncthreads();
+    if (tid < ties) sh.list[strict + tid] = moved;
+    __syncthreads();
+  }
   const int n = strict + ties;
-  uint64_t moved = 0;
-  if (tid < ties) moved = sh.list[kStrict + tid];
-  __syncthreads();
-  if (tid < ties) sh.list[strict + tid] = moved;
-  __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = sh.list[i];
     const int place = places_above(sh.list, n, key);
@@ -263,9 +277,15 @@ __device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int 
 
 // ---------------------------------------------------------------------------
 // G threads per row (or piece of one): a wave where rows are short, else a workgroup.
-// Memory bound: a thread has kGroupUnits loads of 16 bytes in flight.
+// Memory bound: a thread has kGroupUnits loads of 16 bytes in flight.  With alternatives,
+// pieces of up to 2048 stay in registers, 8 elements per thread (kShort; kNarrow, for
+// vocabularies below that, takes them 256 apart, so that as many threads as possible hold
+// a maximum); of longer ones (kLong) the maxima of each thread's groups stay in LDS, and
+// only groups that reach tau are read again.
 // ---------------------------------------------------------------------------
-template <typename T, int G, bool TOP, int UNIT>
+enum : int { kNoTop, kLong, kShort, kNarrow };
+
+template <typename T, int G, int TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
   __shared__ Running part[kThreads / 64];
   const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
@@ -289,39 +309,59 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
   const int len = a.vocab - first < a.piece ? a.vocab - first : a.piece;
   const gptr<const T> src = glob((const T*)a.logits) + row * a.ld + first;
   const float c2 = a.scale * kLog2e;
-  constexpr int B = sizeof(T) == 2 || UNIT == 1 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
-  const int groups = (len + G * kGroupUnits * UNIT - 1) / (G * kGroupUnits * UNIT);
   Running r = {kLowest, 0.f, 0.f};
   extern __shared__ __align__(16) char top_smem[];
   TopShared& sh = *(TopShared*)top_smem;
-  for (int g = 0; g < groups; ++g) {
-    float most = -INFINITY;
-    if ((g + 1) * G * kGroupUnits * UNIT <= len) {
+  GroupShared& groups = *(GroupShared*)(top_smem + sizeof(TopShared));
+  float most = -INFINITY;                                // of this thread
+  float held[8];                                         // kShort, kNarrow: its elements
+  constexpr int B = sizeof(T) == 2 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
+  const int ngroups = (len + G * kGroupUnits * 8 - 1) / (G * kGroupUnits * 8);
+  if constexpr (TOP == kShort) {
+    any_unit<T, 8>(src, tid, len, held);
+    most = r.add(held, c2);
+  } else if constexpr (TOP == kNarrow) {
 #pragma unroll
-      for (int b = 0; b < kGroupUnits; b += B) {
-        Unit<T, UNIT> x[B];
+    for (int e = 0; e < 8; ++e) held[e] = e * kThreads + tid < len ? element(src + e * kThreads + tid) : -INFINITY;
+    most = r.add(held, c2);
+  } else {
+    for (int g = 0; g < ngroups; ++g) {
+      float top = -INFINITY;
+      if ((g + 1) * G * kGroupUnits * 8 <= len) {
 #pragma unroll
-        for (int k = 0; k < B; ++k) x[k].load(src + (int64_t)((g * kGroupUnits + b + k) * G + tid) * UNIT);
+        for (int b = 0; b < kGroupUnits; b += B) {
+          Unit<T, 8> x[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-          float v[UNIT];
-          x[k].values(v);
+          for (int k = 0; k < B; ++k) x[k].load(src + (int64_t)((g * kGroupUnits + b + k) * G + tid) * 8);
+#pragma unroll
+          for (int k = 0; k < B; ++k) {
+            float v[8];
+            x[k].values(v);
+            const float o = r.add(v, c2);
+            if (TOP) top = fmaxf(top, o);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kGroupUnits; ++k) {
+          const int j = (g * kGroupUnits + k) * G + tid;
+          if (j * 8 >= len) break;
+          float v[8];
+          any_unit<T, 8>(src, j, len, v);
           const float o = r.add(v, c2);
-          if (TOP) most = fmaxf(most, o);
+          if (TOP) top = fmaxf(top, o);
         }
       }
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < kGroupUnits; ++k) {
-        const int j = (g * kGroupUnits + k) * G + tid;
-        if (j * UNIT >= len) break;
-        float v[UNIT];
-        any_unit<T, UNIT>(src, j, len, v);
-        const float o = r.add(v, c2);
-        if (TOP) most = fmaxf(most, o);
+      if (TOP) {
+        top = rankable(top);
+        groups.group[g][tid] = top;
+        most = fmaxf(most, top);
       }
     }
-    if (TOP) sh.group[g][tid] = rankable(most);
+  }
+  if constexpr (TOP) {
+    sh.most[tid] = rankable(most);
+    if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
   }
   join_wave(r, c2);
   if constexpr (G > 64) {
@@ -346,14 +386,37 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
     else a.stats[row * a.pieces + piece] = RowStat{r.m, r.s, r.u};
   }
   if constexpr (TOP) {
+    auto gather = [&](float tau) {
+      if constexpr (TOP == kLong) {
+        for (int g = 0; g < ngroups; ++g)
+          if (groups.group[g][tid] >= tau) groups.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
+        __syncthreads();
+        const int units = sh.flags * kGroupUnits;
+        for (int w = tid; w < units; w += kThreads) {
+          const int f = groups.flag[w / kGroupUnits];
+          const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
+          if (j * 8 >= len) continue;
+          float v[8];
+          any_unit<T, 8>(src, j, len, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) put_candidate(sh, v[e], tau, j * 8 + e < len, first + j * 8 + e);
+        }
+      } else if (sh.most[tid] >= tau) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int at = TOP == kShort ? tid * 8 + e : e * kThreads + tid;
+          put_candidate(sh, held[e], tau, at < len, first + at);
+        }
+      }
+    };
     if (a.pieces == 1) {
-      select_top<T, UNIT>(sh, src, len, first, a.top, groups, [&](int place, uint64_t key) {
+      select_top(sh, src, len, first, a.top, gather, [&](int place, uint64_t key) {
         a.top_ids[row * a.top + place] = key_index(key);
         a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
       });
     } else {
       uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
-      const int n = select_top<T, UNIT>(sh, src, len, first, a.top, groups, [&](int place, uint64_t key) { out[place] = key; });
+      const int n = select_top(sh, src, len, first, a.top, gather, [&](int place, uint64_t key) { out[place] = key; });
       for (int i = n + tid; i < a.top; i += kThreads) out[i] = 0;
     }
   }
@@ -367,7 +430,9 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   extern __shared__ __align__(16) char join_smem[];
   __shared__ Running whole;
-  __shared__ uint64_t most[kThreads], list[kStrict], tau_key;
+  __shared__ alignas(16) uint64_t list[kStrict];
+  __shared__ float most[kThreads];
+  __shared__ uint64_t next_tau;
   __shared__ int count;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
@@ -393,24 +458,20 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   uint64_t* keys = (uint64_t*)join_smem;
   const int n = a.pieces * a.top;
   uint64_t mine = 0;
+#pragma unroll 8
   for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = a.cand[row * n + i];
     keys[i] = key;
     mine = key > mine ? key : mine;
   }
-  most[tid] = mine;
+  most[tid] = mine ? key_value(mine) : -INFINITY;
+  if (tid == 0) count = 0;
   __syncthreads();
   const Row done(whole, a.scale);
-  int above = 0;
-  for (int i = 0; i < kThreads; ++i) above += most[i] > mine || (most[i] == mine && i < tid);
-  if (above == a.top - 1) tau_key = mine;
-  __syncthreads();
+  uint64_t tau = key_of(kth_of_threads<T>(most, a.top), -1);       // the least key of that value
   for (;;) {
-    const uint64_t tau = tau_key;
-    if (tid == 0) count = 0;
-    __syncthreads();
     for (int i = tid; i < n; i += kThreads)
-      if (keys[i] >= tau && keys[i] != 0) {
+      if (keys[i] >= tau) {
         const int at = atomicAdd(&count, 1);
         if (at < kStrict) list[at] = keys[i];
       }
@@ -427,7 +488,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
       return;
     }
     for (int i = tid; i < kStrict; i += kThreads)
-      if (places_above(list, kStrict, list[i]) == a.top - 1) tau_key = list[i];
+      if (places_above(list, kStrict, list[i]) == a.top - 1) next_tau = list[i];
+    __syncthreads();
+    tau = next_tau;
+    if (tid == 0) count = 0;
     __syncthreads();
   }
 }
@@ -490,13 +554,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
 // ---------------------------------------------------------------------------
 template <typename T>
 static int logprobs(const LogprobsArgs& a, void* stream) {
-  const int64_t work = a.rows * a.pieces;
+  const unsigned work = (unsigned)(a.rows * a.pieces);
+  constexpr unsigned few = sizeof(TopShared), all = sizeof(TopShared) + sizeof(GroupShared);
   if (a.top) {
-    if (a.vocab < kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, true, 1>), (unsigned)work, kThreads, sizeof(TopShared), a);
-    DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, true, 8>), (unsigned)work, kThreads, sizeof(TopShared), a);
+    if (a.vocab < kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kNarrow>), work, kThreads, few, a);
+    if (a.piece <= kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kShort>), work, kThreads, few, a);
+    DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kLong>), work, kThreads, all, a);
   }
-  if (a.vocab <= kWaveRow) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, 64, false, 8>), (unsigned)cdiv(work, kThreads / 64), kThreads, 0, a);
-  DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, false, 8>), (unsigned)work, kThreads, 0, a);
+  if (a.vocab <= kWaveRow) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, 64, kNoTop>), (unsigned)cdiv(work, kThreads / 64), kThreads, 0, a);
+  DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kNoTop>), work, kThreads, 0, a);
 }
 int launch_logprobs(const LogprobsArgs& a, int f32, void* stream) { return f32 ? logprobs<float>(a, stream) : logprobs<uint16_t>(a, stream); }
 int launch_logprobs_join(const LogprobsArgs& a, int f32, void* stream) {

@@ -31,6 +31,12 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[object] = None
 
 
+def _three(shape, device):
+    """Three fp32 results of one allocation."""
+    import torch
+    return torch.empty((3, *shape), dtype=torch.float32, device=device).unbind(0)
+
+
 def _rows_problem(logits, targets, scale, top, ignore_index):
     tokens, vocab, ld = _matrix(logits, "logits")
     icode = _b.I64
@@ -63,13 +69,16 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100,
     _b.check(_b.lib().dmuon_logprobs_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
     shape, dev = logits.shape[:-1], logits.device
     with _on(stream, logits, targets) as on:
-        new = lambda *more, dtype=torch.float32: torch.empty((*shape, *more), dtype=dtype, device=dev)  # noqa: E731
-        logprobs = None if targets is None else new()
-        entropy, lse = new(), new()
-        ids, best = (new(top, dtype=torch.int64), new(top)) if top else (None, None)
-        ws = on.workspace(workspace, need.value, dev)
+        logprobs, entropy, lse = _three(shape, dev)
+        if targets is None:
+            logprobs = None
+        ids = best = None
+        if top:
+            ids = torch.empty((*shape, top), dtype=torch.int64, device=dev)
+            best = torch.empty((*shape, top), dtype=torch.float32, device=dev)
+        ws = _ws_args(on.workspace(workspace, need.value, dev)) if need.value else (None, 0)
         _b.check(_b.lib().dmuon_logprobs(ctypes.byref(prob), _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(ids), _ptr(best),
-                                         *_ws_args(ws), on.handle))
+                                         *ws, on.handle))
     return TokenLogprobs(logprobs, entropy, lse, ids, best)
 
 
@@ -128,11 +137,10 @@ def linear_token_logprobs(h, w, targets, *, scale=1.0, ignore_index=-100, worksp
     ``linear_cross_entropy``; the logits h·wᵀ are multiplied by ``scale``.  Returns a
     ``TokenLogprobs`` without alternatives, its values as those of ``token_logprobs``.
     """
-    import torch
     _no_graph("linear_token_logprobs", h=h, w=w)
     prob = _ce_problem(h, w, targets, ignore_index)
     with _on(stream, h, w, targets) as on:
-        logprobs, entropy, lse = (torch.empty(targets.shape, dtype=torch.float32, device=h.device) for _ in range(3))
+        logprobs, entropy, lse = _three(targets.shape, h.device)
         ws = _linear_workspace(prob, 0, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_logprobs(ctypes.byref(prob), float(scale), _ptr(logprobs), _ptr(entropy), _ptr(lse),
                                                 *_ws_args(ws), on.handle))
