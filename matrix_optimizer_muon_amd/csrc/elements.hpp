@@ -95,6 +95,8 @@ template <>
 struct Unit<uint16_t, 8> {
   u32x4_t u;
   __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = *(gptr<const u32x4_any>)p; }
+  __device__ __forceinline__ void set(const float (&v)[8]) { u = pack8(v); }
+  __device__ __forceinline__ void clear() { u = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }     // −∞
   __device__ __forceinline__ void values(float (&v)[8]) const { unpack8(u, v); }
 };
 template <>
@@ -104,18 +106,15 @@ struct Unit<float, 8> {
     a = ((gptr<const f32x4_any>)p)[0];
     b = ((gptr<const f32x4_any>)p)[1];
   }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = f32x4_t{v[0], v[1], v[2], v[3]};
+    b = f32x4_t{v[4], v[5], v[6], v[7]};
+  }
+  __device__ __forceinline__ void clear() { a = b = f32x4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY}; }
   __device__ __forceinline__ void values(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-};
-template <typename T>
-struct Unit<T, 1> {
-  T x;
-  __device__ __forceinline__ void load(gptr<const T> p) { x = *p; }
-  __device__ __forceinline__ void values(float (&v)[1]) const { v[0] = value(x); }
-  static __device__ __forceinline__ float value(uint16_t b) { return bf16_to_f32(b); }
-  static __device__ __forceinline__ float value(float f) { return f; }
 };
 __device__ __forceinline__ float element(gptr<const uint16_t> p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float element(gptr<const float> p) { return *p; }

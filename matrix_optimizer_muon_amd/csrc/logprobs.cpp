@@ -12,24 +12,33 @@ namespace {
 
 constexpr int64_t kMaxVocab = (int64_t)1 << 22;     // words of a row of logits
 constexpr int64_t kMaxKeys = 6144;                  // candidates of a row's pieces together, in the joining workgroup's LDS
-static_assert(kMaxVocab <= kMaxKeys / kTopMost * kPieceMost, "the largest vocabulary in pieces that can be joined");
+static_assert(kMaxVocab <= kMaxKeys / kTopMost * (kPieceMost - 16), "the largest vocabulary in pieces that can be joined");
 
 struct RowsPlan {
+  bool wave;
   int64_t piece, pieces;
   RowStat* stats;
   uint64_t* cand;
   size_t bytes;
 };
 
-// Columns per workgroup.  A row is one piece unless it is too long for a workgroup or the
-// rows are too few to fill the card.
+// A row is one wave's where it is short, else one workgroup's, or several pieces' where it
+// is too long for a workgroup or the rows are too few to fill the card.
 RowsPlan rows_plan(const dmuon_logprobs_problem& p, char* base) {
   RowsPlan pl{};
+  pl.wave = p.top ? p.vocab <= kWaveTop || (p.vocab <= kWaveTopMost && p.tokens >= kWaveTopRows)
+                  : p.vocab <= wave_row(p.dtype == DMUON_F32);
+  pl.piece = p.vocab;
+  pl.pieces = 1;
+  if (pl.wave) return pl;
   int64_t n = p.tokens >= 1024 ? 1 : std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
-  if (p.top == 0 && p.vocab <= kWaveRow) n = 1;
-  n = std::max<int64_t>({n, cdiv(p.vocab, kPieceMost), 1});
+  n = std::max<int64_t>(n, p.vocab <= kPieceMost ? 1 : cdiv(p.vocab, kPieceMost - 16));
   pl.piece = round_up(cdiv(p.vocab, n), 8);
   pl.pieces = cdiv(p.vocab, pl.piece);
+  if (pl.pieces > 1 && p.vocab - (pl.pieces - 1) * pl.piece < 16) {    // the last one's rest goes to the others: two units at least
+    pl.piece += 16;
+    pl.pieces = cdiv(p.vocab, pl.piece);
+  }
   if (pl.pieces == 1) return pl;
   Carver c{base};
   pl.stats = c.take<RowStat>(p.tokens * pl.pieces);
@@ -109,6 +118,7 @@ int dmuon_logprobs(const dmuon_logprobs_problem* p, float* logprobs, float* entr
     a.top = p->top;
     a.piece = (int32_t)pl.piece;
     a.pieces = (int32_t)pl.pieces;
+    a.wave_rows = pl.wave;
     a.scale = p->scale;
     a.targets = p->targets;
     a.idx64 = p->index_dtype == DMUON_I64;

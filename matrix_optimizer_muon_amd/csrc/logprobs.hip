@@ -19,56 +19,91 @@ constexpr float kNan = __builtin_nanf("");
 // ---------------------------------------------------------------------------
 // units of a row
 // ---------------------------------------------------------------------------
-// unit j of a piece of len elements, −∞ past its end
-template <typename T, int UNIT>
-__device__ __forceinline__ void edge_unit(gptr<const T> row, int j, int len, float (&v)[UNIT]) {
-#pragma unroll
-  for (int e = 0; e < UNIT; ++e) v[e] = j * UNIT + e < len ? element(row + j * UNIT + e) : -INFINITY;
-}
-template <typename T, int UNIT>
-__device__ __forceinline__ void any_unit(gptr<const T> row, int j, int len, float (&v)[UNIT]) {
-  if ((j + 1) * UNIT <= len) {
-    Unit<T, UNIT> x;
-    x.load(row + j * UNIT);
+// Unit j of a piece of len ≥ 8 elements.  The last one is the piece's last 8 elements, of
+// which those of the unit before count as −∞, so that it is one load too.
+template <typename T>
+struct Piece {
+  gptr<const T> p;
+  int len, units;
+  __device__ __forceinline__ Piece(gptr<const T> row, int n) : p(row), len(n), units((n + 7) >> 3) {}
+  __device__ __forceinline__ int start(int j) const { return (j + 1) * 8 <= len ? j * 8 : len - 8; }
+  __device__ __forceinline__ void load(Unit<T, 8>& x, int j) const { x.load(p + start(j)); }
+  // its values; element e is number start(j) + e of the piece
+  __device__ __forceinline__ void values(const Unit<T, 8>& x, int j, float (&v)[8]) const {
     x.values(v);
-  } else {
-    edge_unit<T, UNIT>(row, j, len, v);
+    if ((j + 1) * 8 > len) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (len - 8 + e < j * 8) v[e] = -INFINITY;
+    }
   }
-}
+};
 
 // ---------------------------------------------------------------------------
-// one pass over a row: with m the largest logit so far,
-//   s = Σ e^{c(z − m)},   u = Σ (z − m)·e^{c(z − m)}   (c: the scale)
-// and both multiplied by e^{c(m − m')} when m grows to m' (u first becomes
-// Σ (z − m')·…, that is u + (m − m')·s).  m starts at the lowest finite value, so that no
-// difference is −∞ − −∞: a logit of −∞ has e = 0, and its difference is kept finite for
-// the product 0·(z − m).  A NaN reaches s through its e.
+// one pass over a row.  With m the largest logit so far, c2 = scale·log₂e and the
+// reference M = m·c2 rounded once, a logit's exponent is t = z·c2 − M in one fused
+// multiply-add, and
+//   s = Σ 2^t,   u = Σ t·2^t.
+// M's rounding r = m·c2 − M is a factor 2^r of every term, so it cancels between them:
+// the entropy is ln s − ln 2·u/s, and log Σ e^(scale·(z − m)) = ln s − r·ln 2.  When m
+// grows, every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes
+// 2^e·s.  Beyond |M| = 2^29, where r could overflow the exponential, t is (z − m)·c2 and
+// r is 0.  m starts at the lowest finite value, so that no difference is −∞ − −∞; a logit
+// of −∞ has 2^t = 0 and its t is kept finite for the product.  A NaN reaches s.
+// Bound by the instructions: 16 elements are taken together, 6.6 instructions each beside
+// the maximum's bookkeeping (unpack, maximum, t, 2^t, clamp, two sums).
 // ---------------------------------------------------------------------------
-constexpr float kFar = -1e30f;           // a difference whose exponential is 0
+constexpr float kFar = -1e30f;           // an exponent whose power of 2 is 0
+constexpr float kBig = 0x1p29f;
+constexpr float kLn2 = 0.693147180559945309f;
 
 struct Running {
-  float m, s, u;
+  float m, M, s, u;
+  static __device__ __forceinline__ Running from(float m, float s, float u, float c2) { return {m, m * c2, s, u}; }
+  static __device__ __forceinline__ Running none(float c2) { return from(kLowest, 0.f, 0.f, c2); }
+  static __device__ __forceinline__ bool big(float M) { return !(fabsf(M) < kBig); }
+  static __device__ __forceinline__ float rest(float m, float M, float c2) { return big(M) ? 0.f : fmaf(m, c2, -M); }
   __device__ __forceinline__ void grow(float to, float c2) {
-    const float d = m - to;
-    const float a = __builtin_amdgcn_exp2f(d * c2);
-    u = a * fmaf(fmaxf(d, kFar), s, u);
+    const float next = to * c2;
+    const float e = fmaf(m - to, c2, rest(to, next, c2) - rest(m, M, c2));
+    const float a = __builtin_amdgcn_exp2f(e);
+    u = a * fmaf(fmaxf(e, kFar), s, u);
     s *= a;
     m = to;
+    M = next;
   }
+  // units of 8; their maxima go out
   template <int N>
-  __device__ __forceinline__ float add(const float (&v)[N], float c2) {        // returns the largest of v
-    float most = v[0];
+  __device__ __forceinline__ void add(const float (&v)[N], float (&top)[N / 8], float c2) {
 #pragma unroll
-    for (int e = 1; e < N; ++e) most = fmaxf(most, v[e]);
-    if (most > m) grow(most, c2);
+    for (int k = 0; k < N / 8; ++k) {
+      top[k] = v[8 * k];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float d = v[e] - m;
-      const float p = __builtin_amdgcn_exp2f(d * c2);
-      s += p;
-      u = fmaf(p, fmaxf(d, kFar), u);
+      for (int e = 1; e < 8; ++e) top[k] = fmaxf(top[k], v[8 * k + e]);
     }
-    return most;
+    const float most = N == 8 ? top[0] : fmaxf(top[0], top[N / 8 - 1]);
+    if (most > m) grow(most, c2);
+    if (__any(big(M))) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {                      // rare: kept short
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          const float z = h ? v[N / 2 + e] : v[e];
+          const float t = big(M) ? (z - m) * c2 : fmaf(z, c2, -M);
+          const float p = __builtin_amdgcn_exp2f(t);
+          s += p;
+          u = fmaf(p, fmaxf(t, kFar), u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float t = fmaf(v[e], c2, -M);
+        const float p = __builtin_amdgcn_exp2f(t);
+        s += p;
+        u = fmaf(p, fmaxf(t, kFar), u);
+      }
+    }
   }
 };
 
@@ -89,11 +124,12 @@ __device__ __forceinline__ void join_wave(Running& r, float c2) {
 // probability are −∞ and the entropy is 0.
 struct Row {
   float m, log_s, lse, entropy, scale;
-  __device__ __forceinline__ Row(const Running& r, float c) : m(r.m), scale(c) {
+  __device__ __forceinline__ Row(const Running& r, float c, float c2) : m(r.m), scale(c) {
     const bool none = r.s == 0.f;
-    log_s = none ? 0.f : logf(r.s);
+    const float ln = none ? 0.f : logf(r.s);
+    log_s = none ? 0.f : fmaf(-Running::rest(r.m, r.M, c2), kLn2, ln);
     lse = none ? -INFINITY : fmaf(r.m, c, log_s);
-    entropy = none ? 0.f : log_s - r.u * c / r.s;
+    entropy = none ? 0.f : ln - r.u * kLn2 / r.s;
   }
   // (z − m)·c − log s: neither term is positive, and the logarithm keeps its digits
   // beside a large m
@@ -122,47 +158,54 @@ __device__ __forceinline__ int target_kind(int64_t y, int64_t ignore, int32_t vo
   return y == ignore ? kIgnored : y >= 0 && y < vocab ? kInside : y == kElsewhere ? kShard : kOutside;
 }
 
+// the target's logit, loaded before the row so that its latency passes beside it
 template <typename T>
-__device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, int64_t y, int kind, const Row& r) {
+__device__ __forceinline__ float target_logit(const LogprobsArgs& a, int64_t row, int64_t y, int kind) {
+  return a.targets && kind == kInside ? element(glob((const T*)a.logits) + row * a.ld + y) : 0.f;
+}
+__device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, float z, int kind, const Row& r) {
   a.lse[row] = r.lse;
   a.entropy[row] = r.entropy;
-  if (!a.targets) return;
-  a.logprobs[row] = kind == kInside ? r.log_p(element(glob((const T*)a.logits) + row * a.ld + y)) : kind == kShard ? -r.lse : kNan;
+  if (a.targets) a.logprobs[row] = kind == kInside ? r.log_p(z) : kind == kShard ? -r.lse : kNan;
 }
 
 // ---------------------------------------------------------------------------
-// the k largest of a piece.  The k-th largest of the threads' maxima, tau, is not above
-// the k-th largest element, and few elements reach it.  Every wave finds it by itself, bit
-// by bit from ballots over the 256 maxima.  If more elements than the list holds are
+// the k largest of a piece, by G threads (a wave or a workgroup).  The k-th largest of many
+// disjoint parts' maxima, tau, is not above the k-th largest element, and few elements reach
+// it: only parts that do are looked at again.  If more elements than the list holds are
 // greater than tau, the k-th largest of those it took becomes the new tau (it is greater:
 // each round drops at least the rest of the list).  Elements equal to tau are needed where
 // fewer than k are greater; where many are (equal logits, words masked out by −∞) the
 // first of them in order are looked for.  Places come from counting the greater keys:
 // keys are distinct, so the result does not depend on the list's order.
 // ---------------------------------------------------------------------------
-constexpr int kStrict = 512, kTies = 256;
-
+template <int STRICT, int TIES>
 struct TopShared {
-  alignas(16) uint64_t list[kStrict + kTies];
-  float most[kThreads];                  // each thread's largest
-  int flags, strict, ties, wave[kThreads / 64];
+  static constexpr int kStrict = STRICT, kTies = TIES;
+  alignas(16) uint64_t list[STRICT + TIES];
+  int wave[kThreads / 64];
   float tau;
 };
-struct GroupShared {
-  float group[kGroups][kThreads];        // largest of each thread's groups
-  uint16_t flag[kGroups * kThreads];     // groups to read again
-};
+template <int G>
+__device__ __forceinline__ void sync() {
+  if constexpr (G > 64) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
 
-// the k-th largest of 256 values in LDS, in every lane (k ≤ 256)
-template <typename T>
-__device__ __forceinline__ float kth_of_threads(const float* most, int k) {
-  constexpr int N = kThreads / 64, low = sizeof(T) == 2 ? 16 : 0;     // bf16: 16 bits tell the values apart
-  const int lane = threadIdx.x & 63;
+// the k-th largest of the N values of each lane together, bit by bit from ballots, in every
+// lane (bf16: 16 bits tell the values apart)
+template <typename T, int N>
+__device__ __forceinline__ float kth_largest(const float (&value)[N], int k) {
+  constexpr int low = sizeof(T) == 2 ? 16 : 0;
   uint32_t key[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) key[i] = ordered(most[lane + 64 * i]) >> low;
+  for (int i = 0; i < N; ++i) key[i] = ordered(value[i]) >> low;
   uint32_t t = 0;
-#pragma unroll
+#pragma unroll 4
   for (int b = 31 - low; b >= 0; --b) {
     const uint32_t c = t | 1u << b;
     int n = 0;
@@ -172,6 +215,14 @@ __device__ __forceinline__ float kth_of_threads(const float* most, int k) {
   }
   t = __builtin_amdgcn_readfirstlane(t);
   return from_ordered(low ? t << 16 | (t & 0x8000u ? 0u : 0xffffu) : t);
+}
+// of a workgroup's threads' maxima, every wave by itself
+template <typename T>
+__device__ __forceinline__ float kth_of_threads(const float* most, int k) {
+  float v[kThreads / 64];
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) v[i] = most[(threadIdx.x & 63) + 64 * i];
+  return kth_largest<T>(v, k);
 }
 
 // the number of keys greater than `key` in list[0, n)
@@ -189,50 +240,40 @@ __device__ __forceinline__ int places_above(const uint64_t* list, int n, uint64_
   return r;
 }
 
-__device__ __forceinline__ void put_candidate(TopShared& sh, float raw, float tau, bool inside, int index) {
-  const float z = rankable(raw);
-  if (z > tau) {
-    const int i = atomicAdd(&sh.strict, 1);
-    if (i < kStrict) sh.list[i] = key_of(z, index);
-  } else if (z == tau && inside) {
-    const int i = atomicAdd(&sh.ties, 1);
-    if (i < kTies) sh.list[kStrict + i] = key_of(z, index);
-  }
-}
-
-// emit(place, key) for the min(k, len) largest of the piece, whose threads' maxima are in
-// sh.most and whose counters are 0 (behind a barrier); returns their number.  gather(tau)
-// puts the piece's elements from tau on into the list.
-template <typename T, typename G, typename F>
-__device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int len, int first, int k, G gather, F emit) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// emit(place, key) for the min(k, len) largest of the piece; returns their number.
+// gather(tau, again, strict, ties) puts the piece's elements from tau on into the list
+// and counts those greater than and equal to tau (again: the counters are to be cleared),
+// behind a barrier.
+template <typename T, int G, typename S, typename C, typename F>
+__device__ __forceinline__ int select_top(S& sh, const Piece<T>& row, int tid, int first, int k, float tau, C gather, F emit) {
+  const int lane = tid & 63, wave = tid >> 6, len = row.len;
   const int want = k < len ? k : len;
-  float tau = kth_of_threads<T>(sh.most, k);
   int strict, ties;
-  for (;;) {
-    gather(tau);
-    __syncthreads();
-    strict = sh.strict;
-    ties = sh.ties;
-    if (strict <= kStrict) break;
-    for (int i = tid; i < kStrict; i += kThreads)
-      if (places_above(sh.list, kStrict, sh.list[i]) == k - 1) sh.tau = key_value(sh.list[i]);
-    __syncthreads();
+  gather(tau, false, strict, ties);
+  while (strict > S::kStrict) {
+    for (int i = tid; i < S::kStrict; i += G)
+      if (places_above(sh.list, S::kStrict, sh.list[i]) == k - 1) sh.tau = key_value(sh.list[i]);
+    sync<G>();
     tau = sh.tau;
-    if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
-    __syncthreads();
+    sync<G>();
+    gather(tau, true, strict, ties);
   }
   if (strict >= want) {
     ties = 0;
-  } else if (ties > kTies) {
+  } else if (ties > S::kTies) {                          // then len > 8
     const int need = want - strict;
     int have = 0;
-    for (int base = 0; have < need && base * 8 < len; base += kThreads) {
-      float v[8];
-      any_unit<T, 8>(row, base + tid, len, v);
+    for (int base = 0; have < need && base < row.units; base += G) {
+      const int j = base + tid, at0 = row.start(j);
       uint32_t in = 0;
+      if (j < row.units) {
+        Unit<T, 8> x;
+        float v[8];
+        row.load(x, j);
+        row.values(x, j, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) in |= (uint32_t)(rankable(v[e]) == tau && (base + tid) * 8 + e < len) << e;
+        for (int e = 0; e < 8; ++e) in |= (uint32_t)(rankable(v[e]) == tau && at0 + e >= j * 8 && at0 + e < len) << e;
+      }
       int incl = __popc(in);
       const int n = incl;
 #pragma unroll
@@ -240,34 +281,39 @@ __device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int 
         const int up = __shfl_up(incl, o, 64);
         if (lane >= o) incl += up;
       }
-      if (lane == 63) sh.wave[wave] = incl;
-      __syncthreads();
       int at = have + incl - n, all = 0;
+      if constexpr (G > 64) {
+        if (lane == 63) sh.wave[wave] = incl;
+        __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kThreads / 64; ++w) {
-        if (w < wave) at += sh.wave[w];
-        all += sh.wave[w];
+        for (int w = 0; w < G / 64; ++w) {
+          if (w < wave) at += sh.wave[w];
+          all += sh.wave[w];
+        }
+      } else {
+        all = __shfl(incl, 63, 64);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (in >> e & 1) {
-          if (at < need) sh.list[kStrict + at] = key_of(tau, first + (base + tid) * 8 + e);
+          if (at < need) sh.list[S::kStrict + at] = key_of(tau, first + at0 + e);
           ++at;
         }
       have += all;
-      __syncthreads();
+      sync<G>();
     }
     ties = need;
   }
-  if (ties > 0) {                        // one list: the ties behind the others
+  // one list: the ties behind the others (from the front, so that none is overwritten unread)
+  for (int i = 0; i < ties; i += G) {
     uint64_t moved = 0;
-    if (tid < ties) moved = sh.list[kStrict + tid];
-    __syncthreads();
-    if (tid < ties) sh.list[strict + tid] = moved;
-    __syncthreads();
+    if (i + tid < ties) moved = sh.list[S::kStrict + i + tid];
+    sync<G>();
+    if (i + tid < ties) sh.list[strict + i + tid] = moved;
+    sync<G>();
   }
   const int n = strict + ties;
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += G) {
     const uint64_t key = sh.list[i];
     const int place = places_above(sh.list, n, key);
     if (place < want) emit(place, key);
@@ -276,147 +322,412 @@ __device__ __forceinline__ int select_top(TopShared& sh, gptr<const T> row, int 
 }
 
 // ---------------------------------------------------------------------------
-// G threads per row (or piece of one): a wave where rows are short, else a workgroup.
-// Memory bound: a thread has kGroupUnits loads of 16 bytes in flight.  With alternatives,
-// pieces of up to 2048 stay in registers, 8 elements per thread (kShort; kNarrow, for
-// vocabularies below that, takes them 256 apart, so that as many threads as possible hold
-// a maximum); of longer ones (kLong) the maxima of each thread's groups stay in LDS, and
-// only groups that reach tau are read again.
+// a piece (of 8 elements at least) streamed by G threads.  Rows start at any element; loads
+// off the 4-byte grid are slow (8192 × 50257 bf16: 193 µs, × 50258 171), so the units lie on
+// the 16-byte grid, and the up to 7 elements before and behind them are two more units,
+// from the piece's own ends, for the last two threads.  Loads past the last whole unit take
+// that one again, so that all of a batch are in flight without a branch, and count as −∞;
+// waves that are past it skip them.
 // ---------------------------------------------------------------------------
-enum : int { kNoTop, kLong, kShort, kNarrow };
+template <typename T, int G>
+struct Stream {
+  const Piece<T>& in;
+  int tid, head, full, groups;           // elements before the grid, whole units, groups of units
+  bool at_head, at_tail;                 // this thread has one of the ends
+  Unit<T, 8> edge;
 
-template <typename T, int G, int TOP>
+  __device__ __forceinline__ Stream(const Piece<T>& p, int t) : in(p), tid(t) {
+    head = (int)((16u - ((uint32_t)(uintptr_t)p.p & 15u)) & 15u) / (int)sizeof(T);
+    full = (p.len - head) >> 3;
+    groups = (full + G * kGroupUnits - 1) / (G * kGroupUnits);
+    at_head = head > 0 && tid == G - 1;
+    at_tail = (p.len - head) % 8 > 0 && tid == G - 2;
+    if (at_head || at_tail) edge.load(p.p + (at_head ? 0 : p.len - 8));
+  }
+  // an end's elements, the others −∞; element e is number edge_at() + e of the piece
+  __device__ __forceinline__ int edge_at() const { return at_head ? 0 : in.len - 8; }
+  __device__ __forceinline__ void edge_values(float (&v)[8]) const {
+    edge.values(v);
+    const int rest = (in.len - head) % 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at_head ? e >= head : e < 8 - rest) v[e] = -INFINITY;
+  }
+  __device__ __forceinline__ gptr<const T> unit(int j) const { return in.p + head + (int64_t)j * 8; }
+  // all of it into r; group(g, largest) of every group of 8 units; returns the largest of an end
+  template <typename F>
+  __device__ __forceinline__ float run(Running& r, float c2, F group) {
+    constexpr int B = sizeof(T) == 2 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
+    const int wave0 = tid & ~63, lane = tid & 63;
+    for (int g = 0; g < groups; ++g) {
+      float most = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < kGroupUnits; b += B) {
+        const int j0 = (g * kGroupUnits + b) * G;
+        if (__builtin_amdgcn_readfirstlane(j0 + wave0) >= full) break;
+        Unit<T, 8> x[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          const int j = j0 + k * G + tid;
+          x[k].load(unit(j < full ? j : full - 1));
+        }
+#pragma unroll
+        for (int k = 0; k < B; k += 2) {
+          const int left = full - __builtin_amdgcn_readfirstlane(j0 + k * G + wave0);
+          if (left <= 0) break;
+          if (left < G + 64) {                           // the last units' waves
+            if (lane >= left) x[k].clear();
+            if (lane + G >= left) x[k + 1].clear();
+          }
+          float v[16], top[2];
+          x[k].values(*(float(*)[8])&v[0]);
+          x[k + 1].values(*(float(*)[8])&v[8]);
+          r.add(v, top, c2);
+          most = fmaxf(most, fmaxf(top[0], top[1]));
+        }
+      }
+      group(g, most);
+    }
+    float top[1] = {-INFINITY};
+    if (at_head || at_tail) {
+      float v[8];
+      edge_values(v);
+      r.add(v, top, c2);
+    }
+    return top[0];
+  }
+};
+
+__device__ __forceinline__ void ignored_row(const LogprobsArgs& a, int64_t row, int tid, int threads) {
+  if (tid == 0) a.logprobs[row] = a.entropy[row] = a.lse[row] = 0.f;
+  for (int i = tid; i < a.top; i += threads) {
+    a.top_ids[row * a.top + i] = -1;
+    a.top_logprobs[row * a.top + i] = 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// a wave per row, without alternatives: no barrier, and four times the rows in flight.
+// Against a workgroup per row, bf16: 8192 × 5000 23 and 32 µs, × 10007 38 and 53, 300 × 8192
+// 7.1 and 9.5, 8192 × 16384 61 and 56; fp32: 300 × 8192 7.4 and 9.4, 8192 × 8192 54 and 54,
+// × 16384 112 and 109.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void short_row(gptr<const T> p, int len, Unit<T, 8>& x) {         // fewer than 8 elements
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < len ? element(p + e) : -INFINITY;
+  x.set(v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_logprobs_wave(LogprobsArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= a.rows) return;
+  const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
+  const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
+  if (kind == kIgnored) return ignored_row(a, row, lane, 64);
+  const Piece<T> in(glob((const T*)a.logits) + row * a.ld, a.vocab);
+  const float zy = lane == 0 ? target_logit<T>(a, row, y, kind) : 0.f;
+  const float c2 = a.scale * kLog2e;
+  Running r = Running::none(c2);
+  if (a.vocab >= 16) {
+    Stream<T, 64> stream(in, lane);
+    stream.run(r, c2, [](int, float) {});
+  } else if (lane < in.units) {
+    Unit<T, 8> x;
+    if (a.vocab < 8) short_row(in.p, a.vocab, x);
+    else in.load(x, lane);
+    float v[8], top[1];
+    if (a.vocab < 8) x.values(v);
+    else in.values(x, lane, v);
+    r.add(v, top, c2);
+  }
+  join_wave(r, c2);
+  if (lane == 0) write_row(a, row, zy, kind, Row(r, a.scale, c2));
+}
+
+// ---------------------------------------------------------------------------
+// a wave per row with alternatives, for rows of at most NB·512 units: the units' maxima stay
+// in registers, and the units from tau on are read again.  tau comes from 8 maxima per lane
+// (of parts of units where the row is short), or for few alternatives from the lanes'.
+// ---------------------------------------------------------------------------
+template <int NB>
+struct WaveShared {
+  TopShared<256, 128> top;
+  uint16_t flag[NB * 512];
+};
+template <typename T, int NB>
+__global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) {
+  __shared__ WaveShared<NB> shared[kThreads / 64];
+  const int lane = threadIdx.x & 63;
+  WaveShared<NB>& sh = shared[threadIdx.x >> 6];
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= a.rows) return;
+  const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
+  const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
+  if (kind == kIgnored) return ignored_row(a, row, lane, 64);
+  const Piece<T> in(glob((const T*)a.logits) + row * a.ld, a.vocab);
+  const float zy = lane == 0 ? target_logit<T>(a, row, y, kind) : 0.f;
+  const float c2 = a.scale * kLog2e;
+  const bool tiny = a.vocab < 8;                         // one unit, not a load
+  Running r = Running::none(c2);
+  auto take = [&](Unit<T, 8>& x, int j) {
+    if (tiny) short_row(in.p, a.vocab, x);
+    else in.load(x, j < in.units ? j : in.units - 1);
+  };
+  auto open = [&](Unit<T, 8>& x, int j, float (&v)[8]) {
+    if (j >= in.units) x.clear();
+    if (tiny || j >= in.units) x.values(v);
+    else in.values(x, j, v);
+  };
+  float top[NB * 8];
+  constexpr int B = sizeof(T) == 2 ? 8 : 4;              // loads in flight
+#pragma unroll
+  for (int b = 0; b < NB * 8; b += B) {
+    if (b * 64 < in.units) {
+      Unit<T, 8> x[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) take(x[k], (b + k) * 64 + lane);
+#pragma unroll
+      for (int k = 0; k < B; k += 2) {
+        float v[16], t[2];
+        open(x[k], (b + k) * 64 + lane, *(float(*)[8])&v[0]);
+        open(x[k + 1], (b + k + 1) * 64 + lane, *(float(*)[8])&v[8]);
+        r.add(v, t, c2);
+        top[b + k] = rankable(t[0]);
+        top[b + k + 1] = rankable(t[1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < B; ++k) top[b + k] = -INFINITY;
+    }
+  }
+  float tau;
+  if (a.top <= 32 && in.units >= 64) {
+    float one[1] = {top[0]};
+#pragma unroll
+    for (int k = 1; k < NB * 8; ++k) one[0] = fmaxf(one[0], top[k]);
+    tau = kth_largest<T>(one, a.top);
+  } else {
+    float key[8];
+    if (NB == 1 && in.units <= 256) {
+      auto parts = [&](auto count) {                     // `count` units per lane, 8 / count maxima of each
+        constexpr int N = decltype(count)::value;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          Unit<T, 8> x;
+          float v[8];
+          take(x, i * 64 + lane);
+          open(x, i * 64 + lane, v);
+#pragma unroll
+          for (int q = 0; q < 8 / N; ++q) {
+            float most = rankable(v[q * N]);
+#pragma unroll
+            for (int e = 1; e < N; ++e) most = fmaxf(most, v[q * N + e]);
+            key[i * (8 / N) + q] = most;
+          }
+        }
+      };
+      if (in.units <= 64) parts(std::integral_constant<int, 1>());
+      else if (in.units <= 128) parts(std::integral_constant<int, 2>());
+      else parts(std::integral_constant<int, 4>());
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        key[k] = top[k];
+#pragma unroll
+        for (int b = 1; b < NB; ++b) key[k] = fmaxf(key[k], top[b * 8 + k]);
+      }
+    }
+    tau = kth_largest<T>(key, a.top);
+  }
+  join_wave(r, c2);
+  const Row done(r, a.scale, c2);
+  if (lane == 0) write_row(a, row, zy, kind, done);
+  const uint64_t below = (1ull << lane) - 1;
+  auto gather = [&](float t, bool, int& strict, int& ties) {
+    strict = ties = 0;
+    int flags = 0;
+#pragma unroll
+    for (int k = 0; k < NB * 8; ++k) {
+      const bool on = top[k] >= t && k * 64 + lane < in.units;
+      const uint64_t all = __ballot(on);
+      if (on) sh.flag[flags + __popcll(all & below)] = (uint16_t)(k * 64 + lane);
+      flags += __popcll(all);
+    }
+    sync<64>();
+    for (int i = lane; i < (flags + 63 & ~63); i += 64) {
+      const bool on = i < flags;
+      const int j = on ? sh.flag[i] : in.units;
+      Unit<T, 8> x;
+      float v[8];
+      take(x, j);
+      open(x, j, v);
+      const int at = tiny ? 0 : in.start(j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = rankable(v[e]);
+        const bool own = on && at + e >= j * 8 && at + e < a.vocab;
+        const uint64_t more = __ballot(own && z > t), same = __ballot(own && z == t);
+        if (own && z > t) {
+          const int n = strict + __popcll(more & below);
+          if (n < sh.top.kStrict) sh.top.list[n] = key_of(z, at + e);
+        } else if (own && z == t) {
+          const int n = ties + __popcll(same & below);
+          if (n < sh.top.kTies) sh.top.list[sh.top.kStrict + n] = key_of(z, at + e);
+        }
+        strict += __popcll(more);
+        ties += __popcll(same);
+      }
+    }
+    sync<64>();
+  };
+  select_top<T, 64>(sh.top, in, lane, 0, a.top, tau, gather, [&](int place, uint64_t key) {
+    a.top_ids[row * a.top + place] = key_index(key);
+    a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
+  });
+}
+
+// ---------------------------------------------------------------------------
+// a workgroup per row or piece.  With alternatives, pieces of up to 2048 (kShort) stay in
+// registers, a unit per thread; of longer ones (kLong) the maxima of each thread's groups
+// stay in LDS, and only groups that reach tau are read again.
+// ---------------------------------------------------------------------------
+enum : int { kNoTop, kLong, kShort };
+struct GroupTop : TopShared<512, 256> {
+  float most[kThreads];                  // each thread's largest
+  int flags, strict, ties;
+};
+struct GroupShared {
+  float group[kGroups][kThreads];        // largest of each thread's groups
+  uint16_t flag[kGroups * kThreads];     // groups to read again
+};
+
+__device__ __forceinline__ void put_candidate(GroupTop& sh, float raw, float tau, bool own, int index) {
+  const float z = rankable(raw);
+  if (own && z > tau) {
+    const int i = atomicAdd(&sh.strict, 1);
+    if (i < sh.kStrict) sh.list[i] = key_of(z, index);
+  } else if (own && z == tau) {
+    const int i = atomicAdd(&sh.ties, 1);
+    if (i < sh.kTies) sh.list[sh.kStrict + i] = key_of(z, index);
+  }
+}
+
+template <typename T, int TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
   __shared__ Running part[kThreads / 64];
-  const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const uint32_t id = blockIdx.x * (kThreads / G) + (G == 64 ? threadIdx.x >> 6 : 0);
-  const int64_t row = id / (uint32_t)a.pieces;
-  const int piece = (int)(id - (uint32_t)row * a.pieces);
-  if (row >= a.rows) return;                             // only where a wave has its own row
+  extern __shared__ __align__(16) char top_smem[];
+  GroupTop& sh = *(GroupTop*)top_smem;
+  GroupShared& groups = *(GroupShared*)(top_smem + sizeof(GroupTop));
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / (uint32_t)a.pieces;
+  const int piece = (int)(blockIdx.x - (uint32_t)row * a.pieces);
   const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
   const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
   if (kind == kIgnored) {
-    if (piece == 0) {
-      if (tid == 0) a.logprobs[row] = a.entropy[row] = a.lse[row] = 0.f;
-      for (int i = tid; i < a.top; i += G) {
-        a.top_ids[row * a.top + i] = -1;
-        a.top_logprobs[row * a.top + i] = 0.f;
-      }
-    }
+    if (piece == 0) ignored_row(a, row, tid, kThreads);
     return;
   }
   const int first = piece * a.piece;
   const int len = a.vocab - first < a.piece ? a.vocab - first : a.piece;
-  const gptr<const T> src = glob((const T*)a.logits) + row * a.ld + first;
+  const Piece<T> in(glob((const T*)a.logits) + row * a.ld + first, len);
+  const float zy = tid == 0 && a.pieces == 1 ? target_logit<T>(a, row, y, kind) : 0.f;
   const float c2 = a.scale * kLog2e;
-  Running r = {kLowest, 0.f, 0.f};
-  extern __shared__ __align__(16) char top_smem[];
-  TopShared& sh = *(TopShared*)top_smem;
-  GroupShared& groups = *(GroupShared*)(top_smem + sizeof(TopShared));
+  Running r = Running::none(c2);
   float most = -INFINITY;                                // of this thread
-  float held[8];                                         // kShort, kNarrow: its elements
-  constexpr int B = sizeof(T) == 2 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
-  const int ngroups = (len + G * kGroupUnits * 8 - 1) / (G * kGroupUnits * 8);
+  float held[8];                                         // kShort: its unit
+  Stream<T, kThreads> stream(in, tid);
   if constexpr (TOP == kShort) {
-    any_unit<T, 8>(src, tid, len, held);
-    most = r.add(held, c2);
-  } else if constexpr (TOP == kNarrow) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) held[e] = e * kThreads + tid < len ? element(src + e * kThreads + tid) : -INFINITY;
-    most = r.add(held, c2);
+    if (tid < in.units) {
+      Unit<T, 8> x;
+      in.load(x, tid);
+      in.values(x, tid, held);
+      float top[1];
+      r.add(held, top, c2);
+      most = rankable(top[0]);
+    }
   } else {
-    for (int g = 0; g < ngroups; ++g) {
-      float top = -INFINITY;
-      if ((g + 1) * G * kGroupUnits * 8 <= len) {
-#pragma unroll
-        for (int b = 0; b < kGroupUnits; b += B) {
-          Unit<T, 8> x[B];
-#pragma unroll
-          for (int k = 0; k < B; ++k) x[k].load(src + (int64_t)((g * kGroupUnits + b + k) * G + tid) * 8);
-#pragma unroll
-          for (int k = 0; k < B; ++k) {
-            float v[8];
-            x[k].values(v);
-            const float o = r.add(v, c2);
-            if (TOP) top = fmaxf(top, o);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int k = 0; k < kGroupUnits; ++k) {
-          const int j = (g * kGroupUnits + k) * G + tid;
-          if (j * 8 >= len) break;
-          float v[8];
-          any_unit<T, 8>(src, j, len, v);
-          const float o = r.add(v, c2);
-          if (TOP) top = fmaxf(top, o);
-        }
-      }
+    const float end = stream.run(r, c2, [&](int g, float top) {
       if (TOP) {
-        top = rankable(top);
-        groups.group[g][tid] = top;
+        groups.group[g][tid] = top = rankable(top);
         most = fmaxf(most, top);
       }
-    }
+    });
+    most = fmaxf(most, rankable(end));
   }
   if constexpr (TOP) {
-    sh.most[tid] = rankable(most);
+    sh.most[tid] = most;
     if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
   }
   join_wave(r, c2);
-  if constexpr (G > 64) {
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[wave] = r;
-    __syncthreads();
-    Running all = part[0];
+  if ((tid & 63) == 0) part[tid >> 6] = r;
+  __syncthreads();
+  r = part[0];
 #pragma unroll
-    for (int w = 1; w < kThreads / 64; ++w) {
-      Running o = part[w];
-      const float m = fmaxf(all.m, o.m);
-      all.grow(m, c2);
-      o.grow(m, c2);
-      all.s += o.s;
-      all.u += o.u;
-    }
-    r = all;
+  for (int w = 1; w < kThreads / 64; ++w) {
+    Running o = part[w];
+    const float m = fmaxf(r.m, o.m);
+    r.grow(m, c2);
+    o.grow(m, c2);
+    r.s += o.s;
+    r.u += o.u;
   }
-  const Row done(r, a.scale);
+  const Row done(r, a.scale, c2);
   if (tid == 0) {
-    if (a.pieces == 1) write_row<T>(a, row, y, kind, done);
+    if (a.pieces == 1) write_row(a, row, zy, kind, done);
     else a.stats[row * a.pieces + piece] = RowStat{r.m, r.s, r.u};
   }
   if constexpr (TOP) {
-    auto gather = [&](float tau) {
+    auto gather = [&](float tau, bool again, int& strict, int& ties) {
+      if (again) {
+        if (tid == 0) sh.flags = sh.strict = sh.ties = 0;
+        __syncthreads();
+      }
       if constexpr (TOP == kLong) {
-        for (int g = 0; g < ngroups; ++g)
+        for (int g = 0; g < stream.groups; ++g)
           if (groups.group[g][tid] >= tau) groups.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
+        if (stream.at_head || stream.at_tail) {
+          float v[8];
+          stream.edge_values(v);
+          const int at = stream.edge_at(), rest = (len - stream.head) % 8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            put_candidate(sh, v[e], tau, stream.at_head ? e < stream.head : e >= 8 - rest, first + at + e);
+        }
         __syncthreads();
         const int units = sh.flags * kGroupUnits;
         for (int w = tid; w < units; w += kThreads) {
           const int f = groups.flag[w / kGroupUnits];
           const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
-          if (j * 8 >= len) continue;
+          if (j >= stream.full) continue;
+          Unit<T, 8> x;
           float v[8];
-          any_unit<T, 8>(src, j, len, v);
+          x.load(stream.unit(j));
+          x.values(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) put_candidate(sh, v[e], tau, j * 8 + e < len, first + j * 8 + e);
+          for (int e = 0; e < 8; ++e) put_candidate(sh, v[e], tau, true, first + stream.head + j * 8 + e);
         }
-      } else if (sh.most[tid] >= tau) {
+      } else if (tid < in.units && most >= tau) {
+        const int at = in.start(tid);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int at = TOP == kShort ? tid * 8 + e : e * kThreads + tid;
-          put_candidate(sh, held[e], tau, at < len, first + at);
-        }
+        for (int e = 0; e < 8; ++e) put_candidate(sh, held[e], tau, at + e >= tid * 8, first + at + e);
       }
+      __syncthreads();
+      strict = sh.strict;
+      ties = sh.ties;
     };
+    const float tau = kth_of_threads<T>(sh.most, a.top);
     if (a.pieces == 1) {
-      select_top(sh, src, len, first, a.top, gather, [&](int place, uint64_t key) {
+      select_top<T, kThreads>(sh, in, tid, first, a.top, tau, gather, [&](int place, uint64_t key) {
         a.top_ids[row * a.top + place] = key_index(key);
         a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
       });
     } else {
       uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
-      const int n = select_top(sh, src, len, first, a.top, gather, [&](int place, uint64_t key) { out[place] = key; });
+      const int n = select_top<T, kThreads>(sh, in, tid, first, a.top, tau, gather, [&](int place, uint64_t key) { out[place] = key; });
       for (int i = n + tid; i < a.top; i += kThreads) out[i] = 0;
     }
   }
@@ -430,6 +741,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   extern __shared__ __align__(16) char join_smem[];
   __shared__ Running whole;
+  constexpr int kStrict = GroupTop::kStrict;
   __shared__ alignas(16) uint64_t list[kStrict];
   __shared__ float most[kThreads];
   __shared__ uint64_t next_tau;
@@ -441,17 +753,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   if (kind == kIgnored) return;                          // written by the first piece's workgroup
   const float c2 = a.scale * kLog2e;
   if (tid < 64) {
-    Running r = {kLowest, 0.f, 0.f};
+    const float zy = target_logit<T>(a, row, y, kind);
+    Running r = Running::none(c2);
     if (tid < a.pieces) {
       const RowStat s = a.stats[row * a.pieces + tid];
-      r.m = s.m;
-      r.s = s.s;
-      r.u = s.u;
+      r = Running::from(s.m, s.s, s.u, c2);
     }
     join_wave(r, c2);
     if (tid == 0) {
       whole = r;
-      write_row<T>(a, row, y, kind, Row(r, a.scale));
+      write_row(a, row, zy, kind, Row(r, a.scale, c2));
     }
   }
   if (a.top == 0) return;
@@ -467,7 +778,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   most[tid] = mine ? key_value(mine) : -INFINITY;
   if (tid == 0) count = 0;
   __syncthreads();
-  const Row done(whole, a.scale);
+  const Row done(whole, a.scale, c2);
   uint64_t tau = key_of(kth_of_threads<T>(most, a.top), -1);       // the least key of that value
   for (;;) {
     for (int i = tid; i < n; i += kThreads)
@@ -520,31 +831,40 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const float entropy = a.grad_entropy ? a.entropy[row] : 0.f;
   const bool takes_part = kind != kIgnored && kind != kOutside && !(g == 0.f && h == 0.f) && !(lse == -INFINITY);
   const int target = kind == kInside ? (int)y : -1;
+  const Piece<T> in(src, a.vocab);
+  Unit<T, 8> x[kGradUnits];
 #pragma unroll
   for (int k = 0; k < kGradUnits; ++k) {
     const int j = j0 + k * G;
-    if (j * 8 >= a.vocab) break;
+    if (takes_part && j < in.units && a.vocab >= 8) in.load(x[k], j);
+  }
+  if (takes_part && j0 == 0 && a.vocab < 8) short_row(src, a.vocab, x[0]);
+#pragma unroll
+  for (int k = 0; k < kGradUnits; ++k) {
+    const int j = j0 + k * G;
+    if (j >= in.units) break;
+    const int at = a.vocab < 8 ? 0 : in.start(j);
     float v[8];
     if (takes_part) {
-      any_unit<T, 8>(src, j, a.vocab, v);
+      x[k].values(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float l = fmaf(v[e], a.scale, -lse);
         l = l < -200.f ? -200.f : l;                     // a NaN stays
         const float p = __builtin_amdgcn_exp2f(l * kLog2e);
         const float d = -p * fmaf(h, l + entropy, g);
-        v[e] = a.scale * (j * 8 + e == target ? d + g : d);
+        v[e] = a.scale * (at + e == target ? d + g : d);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
     if ((j + 1) * 8 <= a.vocab) {
-      store_unit(dst + j * 8, v);
-    } else {
+      store_unit(dst + at, v);
+    } else {                                             // its own elements: the others are another thread's, also in place
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (j * 8 + e < a.vocab) store_element(dst + j * 8 + e, v[e]);
+        if (at + e >= j * 8 && at + e < a.vocab) store_element(dst + at + e, v[e]);
     }
   }
 }
@@ -554,15 +874,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
 // ---------------------------------------------------------------------------
 template <typename T>
 static int logprobs(const LogprobsArgs& a, void* stream) {
-  const unsigned work = (unsigned)(a.rows * a.pieces);
-  constexpr unsigned few = sizeof(TopShared), all = sizeof(TopShared) + sizeof(GroupShared);
-  if (a.top) {
-    if (a.vocab < kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kNarrow>), work, kThreads, few, a);
-    if (a.piece <= kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kShort>), work, kThreads, few, a);
-    DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kLong>), work, kThreads, all, a);
+  const unsigned work = (unsigned)(a.rows * a.pieces), waves = (unsigned)cdiv(a.rows, kThreads / 64);
+  if (a.wave_rows) {
+    if (!a.top) DMUON_LAUNCH(PH_LOGPROBS, stream, k_logprobs_wave<T>, waves, kThreads, 0, a);
+    if (a.vocab <= kWaveTop) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs_wave_top<T, 1>), waves, kThreads, 0, a);
+    DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs_wave_top<T, 3>), waves, kThreads, 0, a);
   }
-  if (a.vocab <= kWaveRow) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, 64, kNoTop>), (unsigned)cdiv(work, kThreads / 64), kThreads, 0, a);
-  DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kThreads, kNoTop>), work, kThreads, 0, a);
+  if (!a.top) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kNoTop>), work, kThreads, 0, a);
+  if (a.piece <= kPieceLeast) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kShort>), work, kThreads, sizeof(GroupTop), a);
+  DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kLong>), work, kThreads, sizeof(GroupTop) + sizeof(GroupShared), a);
 }
 int launch_logprobs(const LogprobsArgs& a, int f32, void* stream) { return f32 ? logprobs<float>(a, stream) : logprobs<uint16_t>(a, stream); }
 int launch_logprobs_join(const LogprobsArgs& a, int f32, void* stream) {

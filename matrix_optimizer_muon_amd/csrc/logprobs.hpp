@@ -15,11 +15,16 @@ constexpr int kGroups = 8;               // such groups per thread at most
 constexpr int kPieceMost = kThreads * kGroupUnits * 8 * kGroups;     // 131072 columns per workgroup
 constexpr int kPieceLeast = kThreads * 8;                            // 2048
 constexpr int kPiecesMost = 64;          // pieces of one row (a wave joins them)
-constexpr int kWaveRow = 64 * kGroupUnits * 8;       // 4096: rows up to this, without alternatives, take one wave each
+// Rows that take one wave each: without alternatives up to 12288 words (fp32 8192), with
+// them up to 4096, or 12288 where there are rows enough.
+inline int64_t wave_row(bool f32) { return f32 ? 8192 : 12288; }
+constexpr int kWaveTop = 64 * 8 * 8;                 // 4096: the units' maxima of a row in 8 registers
+constexpr int kWaveTopMost = 3 * kWaveTop;           // 12288: in 24
+constexpr int kWaveTopRows = 512;
 constexpr int kGradUnits = 4;            // units of 8 elements per thread of the gradient
 constexpr int kGradWave = 64 * kGradUnits * 8;       // 2048: rows up to this take one wave each
 
-// Σ exp(scale·(z − m)) and Σ (z − m)·exp(scale·(z − m)) of a row's piece, m its largest logit
+// Σ 2^t and Σ t·2^t of a row's piece, m its largest logit and t its exponents (see logprobs.hip)
 struct RowStat {
   float m, s, u;
 };
@@ -31,6 +36,7 @@ struct LogprobsArgs {
   int32_t vocab;
   int32_t top;                 // alternatives, 0: none
   int32_t piece, pieces;       // columns per workgroup, workgroups per row
+  int32_t wave_rows;           // 1: a wave per row
   float scale;
   const void* targets;         // or null: every row takes part, none has a target
   int32_t idx64;
