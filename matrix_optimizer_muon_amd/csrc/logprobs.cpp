@@ -39,6 +39,10 @@ RowsPlan rows_plan(const dmuon_logprobs_problem& p, char* base) {
     pl.piece += 16;
     pl.pieces = cdiv(p.vocab, pl.piece);
   }
+  // Pieces with alternatives by a wave each, or by a workgroup each where they do not fill
+  // the card: 1 × 128000 with 20 alternatives 13.7 and 12.5 µs, 32 × 50257 14.2 and 13.4,
+  // 64 × 128000 17.7 and 20.0, with 64 of them 23.8 and 28.
+  pl.wave = p.top && pl.piece <= kWaveTop && p.tokens * pl.pieces > 1024;
   if (pl.pieces == 1) return pl;
   Carver c{base};
   pl.stats = c.take<RowStat>(p.tokens * pl.pieces);

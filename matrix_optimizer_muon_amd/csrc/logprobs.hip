@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave(LogprobsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// a wave per row with alternatives, for rows of at most NB·512 units: the units' maxima stay
+// a wave per row or piece with alternatives, for at most NB·512 units: the units' maxima stay
 // in registers, and the units from tau on are read again.  tau comes from 8 maxima per lane
 // (of parts of units where the row is short), or for few alternatives from the lanes'.
 // ---------------------------------------------------------------------------
@@ -463,18 +463,25 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
   __shared__ WaveShared<NB> shared[kThreads / 64];
   const int lane = threadIdx.x & 63;
   WaveShared<NB>& sh = shared[threadIdx.x >> 6];
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const uint32_t id = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const int64_t row = id / (uint32_t)a.pieces;
+  const int piece = (int)(id - (uint32_t)row * a.pieces);
   if (row >= a.rows) return;
   const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
   const int kind = a.targets ? target_kind(y, a.ignore, a.vocab) : kInside;
-  if (kind == kIgnored) return ignored_row(a, row, lane, 64);
-  const Piece<T> in(glob((const T*)a.logits) + row * a.ld, a.vocab);
-  const float zy = lane == 0 ? target_logit<T>(a, row, y, kind) : 0.f;
+  if (kind == kIgnored) {
+    if (piece == 0) ignored_row(a, row, lane, 64);
+    return;
+  }
+  const int first = piece * a.piece;
+  const int len = a.vocab - first < a.piece ? a.vocab - first : a.piece;
+  const Piece<T> in(glob((const T*)a.logits) + row * a.ld + first, len);
+  const float zy = lane == 0 && a.pieces == 1 ? target_logit<T>(a, row, y, kind) : 0.f;
   const float c2 = a.scale * kLog2e;
-  const bool tiny = a.vocab < 8;                         // one unit, not a load
+  const bool tiny = len < 8;                         // one unit, not a load
   Running r = Running::none(c2);
   auto take = [&](Unit<T, 8>& x, int j) {
-    if (tiny) short_row(in.p, a.vocab, x);
+    if (tiny) short_row(in.p, len, x);
     else in.load(x, j < in.units ? j : in.units - 1);
   };
   auto open = [&](Unit<T, 8>& x, int j, float (&v)[8]) {
@@ -545,7 +552,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
   }
   join_wave(r, c2);
   const Row done(r, a.scale, c2);
-  if (lane == 0) write_row(a, row, zy, kind, done);
+  if (lane == 0) {
+    if (a.pieces == 1) write_row(a, row, zy, kind, done);
+    else a.stats[row * a.pieces + piece] = RowStat{r.m, r.s, r.u};
+  }
   const uint64_t below = (1ull << lane) - 1;
   auto gather = [&](float t, bool, int& strict, int& ties) {
     strict = ties = 0;
@@ -569,14 +579,14 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = rankable(v[e]);
-        const bool own = on && at + e >= j * 8 && at + e < a.vocab;
+        const bool own = on && at + e >= j * 8 && at + e < len;
         const uint64_t more = __ballot(own && z > t), same = __ballot(own && z == t);
         if (own && z > t) {
           const int n = strict + __popcll(more & below);
-          if (n < sh.top.kStrict) sh.top.list[n] = key_of(z, at + e);
+          if (n < sh.top.kStrict) sh.top.list[n] = key_of(z, first + at + e);
         } else if (own && z == t) {
           const int n = ties + __popcll(same & below);
-          if (n < sh.top.kTies) sh.top.list[sh.top.kStrict + n] = key_of(z, at + e);
+          if (n < sh.top.kTies) sh.top.list[sh.top.kStrict + n] = key_of(z, first + at + e);
         }
         strict += __popcll(more);
         ties += __popcll(same);
@@ -584,10 +594,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
     }
     sync<64>();
   };
-  select_top<T, 64>(sh.top, in, lane, 0, a.top, tau, gather, [&](int place, uint64_t key) {
-    a.top_ids[row * a.top + place] = key_index(key);
-    a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
-  });
+  if (a.pieces == 1) {
+    select_top<T, 64>(sh.top, in, lane, first, a.top, tau, gather, [&](int place, uint64_t key) {
+      a.top_ids[row * a.top + place] = key_index(key);
+      a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
+    });
+  } else {
+    uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
+    const int n = select_top<T, 64>(sh.top, in, lane, first, a.top, tau, gather, [&](int place, uint64_t key) { out[place] = key; });
+    for (int i = n + lane; i < a.top; i += 64) out[i] = 0;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -735,7 +751,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
 
 // ---------------------------------------------------------------------------
 // the pieces of a row joined: statistics by one wave, then the k largest of the pieces'
-// sorted candidates, all in LDS, by the same rule as in a piece.
+// sorted candidates, all in LDS, by the same rule as in a piece.  The candidates go to the
+// threads by rank, all pieces' first ones first: the largest lie in different threads, and
+// tau is near the k-th (by piece, 63 pieces of 64 candidates: 17.5 µs, 64 of 128: 31.6;
+// by rank 7.5 and 9.7).
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
@@ -771,7 +790,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
   uint64_t mine = 0;
 #pragma unroll 8
   for (int i = tid; i < n; i += kThreads) {
-    const uint64_t key = a.cand[row * n + i];
+    const uint32_t rank = (uint32_t)i / (uint32_t)a.pieces, p = (uint32_t)i - rank * a.pieces;
+    const uint64_t key = a.cand[row * n + p * a.top + rank];
     keys[i] = key;
     mine = key > mine ? key : mine;
   }
@@ -874,10 +894,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
 // ---------------------------------------------------------------------------
 template <typename T>
 static int logprobs(const LogprobsArgs& a, void* stream) {
-  const unsigned work = (unsigned)(a.rows * a.pieces), waves = (unsigned)cdiv(a.rows, kThreads / 64);
+  const unsigned work = (unsigned)(a.rows * a.pieces), waves = (unsigned)cdiv(work, kThreads / 64);
   if (a.wave_rows) {
     if (!a.top) DMUON_LAUNCH(PH_LOGPROBS, stream, k_logprobs_wave<T>, waves, kThreads, 0, a);
-    if (a.vocab <= kWaveTop) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs_wave_top<T, 1>), waves, kThreads, 0, a);
+    if (a.piece <= kWaveTop) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs_wave_top<T, 1>), waves, kThreads, 0, a);
     DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs_wave_top<T, 3>), waves, kThreads, 0, a);
   }
   if (!a.top) DMUON_LAUNCH(PH_LOGPROBS, stream, (k_logprobs<T, kNoTop>), work, kThreads, 0, a);
