@@ -406,6 +406,19 @@ __device__ __forceinline__ void ignored_row(const LogprobsArgs& a, int64_t row, 
   }
 }
 
+// an alternative of a row, or of a piece: its candidate; the candidates that a piece lacks
+__device__ __forceinline__ void put_alternative(const LogprobsArgs& a, int64_t row, int piece, int place, uint64_t key, const Row& r) {
+  if (a.pieces == 1) {
+    a.top_ids[row * a.top + place] = key_index(key);
+    a.top_logprobs[row * a.top + place] = r.log_p(key_value(key));
+  } else {
+    a.cand[(row * a.pieces + piece) * a.top + place] = key;
+  }
+}
+__device__ __forceinline__ void no_alternatives(const LogprobsArgs& a, int64_t row, int piece, int from, int tid, int threads) {
+  for (int i = from + tid; i < a.top; i += threads) a.cand[(row * a.pieces + piece) * a.top + i] = 0;
+}
+
 // ---------------------------------------------------------------------------
 // a wave per row, without alternatives: no barrier, and four times the rows in flight.
 // Against a workgroup per row, bf16: 8192 × 5000 23 and 32 µs, × 10007 38 and 53, 300 × 8192
@@ -493,12 +506,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
   constexpr int B = sizeof(T) == 2 ? 8 : 4;              // loads in flight
 #pragma unroll
   for (int b = 0; b < NB * 8; b += B) {
+#pragma unroll
+    for (int k = 0; k < B; ++k) top[b + k] = -INFINITY;
     if (b * 64 < in.units) {
       Unit<T, 8> x[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) take(x[k], (b + k) * 64 + lane);
 #pragma unroll
       for (int k = 0; k < B; k += 2) {
+        if ((b + k) * 64 >= in.units) break;
         float v[16], t[2];
         open(x[k], (b + k) * 64 + lane, *(float(*)[8])&v[0]);
         open(x[k + 1], (b + k + 1) * 64 + lane, *(float(*)[8])&v[8]);
@@ -506,9 +522,6 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
         top[b + k] = rankable(t[0]);
         top[b + k + 1] = rankable(t[1]);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < B; ++k) top[b + k] = -INFINITY;
     }
   }
   float tau;
@@ -594,16 +607,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
     }
     sync<64>();
   };
-  if (a.pieces == 1) {
-    select_top<T, 64>(sh.top, in, lane, first, a.top, tau, gather, [&](int place, uint64_t key) {
-      a.top_ids[row * a.top + place] = key_index(key);
-      a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
-    });
-  } else {
-    uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
-    const int n = select_top<T, 64>(sh.top, in, lane, first, a.top, tau, gather, [&](int place, uint64_t key) { out[place] = key; });
-    for (int i = n + lane; i < a.top; i += 64) out[i] = 0;
-  }
+  const int n = select_top<T, 64>(sh.top, in, lane, first, a.top, tau, gather,
+                                  [&](int place, uint64_t key) { put_alternative(a, row, piece, place, key, done); });
+  if (a.pieces > 1) no_alternatives(a, row, piece, n, lane, 64);
 }
 
 // ---------------------------------------------------------------------------
@@ -703,6 +709,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
         __syncthreads();
       }
       if constexpr (TOP == kLong) {
+#pragma unroll 1
         for (int g = 0; g < stream.groups; ++g)
           if (groups.group[g][tid] >= tau) groups.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
         if (stream.at_head || stream.at_tail) {
@@ -715,6 +722,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
         }
         __syncthreads();
         const int units = sh.flags * kGroupUnits;
+#pragma unroll 1
         for (int w = tid; w < units; w += kThreads) {
           const int f = groups.flag[w / kGroupUnits];
           const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
@@ -736,16 +744,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
       ties = sh.ties;
     };
     const float tau = kth_of_threads<T>(sh.most, a.top);
-    if (a.pieces == 1) {
-      select_top<T, kThreads>(sh, in, tid, first, a.top, tau, gather, [&](int place, uint64_t key) {
-        a.top_ids[row * a.top + place] = key_index(key);
-        a.top_logprobs[row * a.top + place] = done.log_p(key_value(key));
-      });
-    } else {
-      uint64_t* out = a.cand + (row * a.pieces + piece) * a.top;
-      const int n = select_top<T, kThreads>(sh, in, tid, first, a.top, tau, gather, [&](int place, uint64_t key) { out[place] = key; });
-      for (int i = n + tid; i < a.top; i += kThreads) out[i] = 0;
-    }
+    const int n = select_top<T, kThreads>(sh, in, tid, first, a.top, tau, gather,
+                                          [&](int place, uint64_t key) { put_alternative(a, row, piece, place, key, done); });
+    if (a.pieces > 1) no_alternatives(a, row, piece, n, tid, kThreads);
   }
 }
 
