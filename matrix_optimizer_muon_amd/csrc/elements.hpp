@@ -95,6 +95,7 @@ template <>
 struct Unit<uint16_t, 8> {
   u32x4_t u;
   __device__ __forceinline__ void load(gptr<const uint16_t> p) { u = *(gptr<const u32x4_any>)p; }
+  __device__ __forceinline__ void load_once(gptr<const uint16_t> p) { u = __builtin_nontemporal_load((gptr<const u32x4_any>)p); }
   __device__ __forceinline__ void set(const float (&v)[8]) { u = pack8(v); }
   __device__ __forceinline__ void clear() { u = u32x4_t{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }     // −∞
   __device__ __forceinline__ void values(float (&v)[8]) const { unpack8(u, v); }
@@ -105,6 +106,10 @@ struct Unit<float, 8> {
   __device__ __forceinline__ void load(gptr<const float> p) {
     a = ((gptr<const f32x4_any>)p)[0];
     b = ((gptr<const f32x4_any>)p)[1];
+  }
+  __device__ __forceinline__ void load_once(gptr<const float> p) {
+    a = __builtin_nontemporal_load((gptr<const f32x4_any>)p);
+    b = __builtin_nontemporal_load((gptr<const f32x4_any>)p + 1);
   }
   __device__ __forceinline__ void set(const float (&v)[8]) {
     a = f32x4_t{v[0], v[1], v[2], v[3]};
