@@ -54,7 +54,7 @@ int make_plan(const dmuon_grad_tensor* t, int32_t n, bool clip, ClipPlan& pl) {
     chunks += cdiv(x.numel, kClipChunk);
     ++used;
   }
-  if (chunks > INT32_MAX) return fail(DMUON_E_SHAPE, "too many tensors and elements");
+  if (chunks > (int64_t)1 << 30) return fail(DMUON_E_SHAPE, "too many tensors and elements");
   pl.n = used;
   pl.chunks = (int32_t)chunks;
   pl.groups = (int32_t)std::min<int64_t>(chunks, kClipGroups);
