@@ -480,9 +480,11 @@ int dmuon_ckpt8_wgrad(const dmuon_ckpt8_wgrad_problem* problem, void* workspace,
  * dmuon_ce_problem; with p_s = exp(lse_s − lse),
  *   lse = log Σ exp lse_s,   logprob = Σ (logprob_s + lse_s) − lse,
  *   entropy = lse − Σ p_s·(lse_s − entropy_s),
- * and the backward calls get the joined lse and entropy.
- * 0 ≤ tokens ≤ 2^24, 1 ≤ vocab ≤ 2^22, fewer than 2^32 threads in a launch: 256 (64 for
- * short rows) per row and 8192 columns of the gradient, or 131072 of the others. */
+ * (a shard whose lse is -inf adds nothing to the sums), and the backward calls get the
+ * joined lse and entropy.
+ * 0 ≤ tokens ≤ 2^24, 1 ≤ vocab ≤ 2^22, and a launch of fewer than 2^32 threads: 64 per row
+ * of up to 2048 columns, else 256 per row and 8192 columns of the gradient or 131072 of the
+ * others. */
 typedef struct {
   int64_t tokens, vocab;
   int32_t dtype;

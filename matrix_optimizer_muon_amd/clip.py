@@ -93,10 +93,11 @@ class ClipGradNorm:
                 torch.cuda.current_stream().synchronize()      # the tables are in place before a call on any stream
 
     def __call__(self, stream=None):
+        import torch
         if self._n == 0:
             return self.norm
         with _on(stream, self.norm, self.workspace) as on:
-            if on.handle.value not in self._seen:
+            if on.handle.value not in self._seen and not torch.cuda.is_current_stream_capturing():
                 st = _b.resolve_stream(None)
                 _b.keep_until_done(self.workspace, [st])
                 _b.keep_until_done(self.norm, [st])

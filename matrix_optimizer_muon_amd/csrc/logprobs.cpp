@@ -64,8 +64,10 @@ int check_rows(const dmuon_logprobs_problem* p, bool backward) {
     return fail(DMUON_E_CFG, "top must be in [0, 128] and at most vocab");
   if (p->tokens > 0 && !p->logits) return fail(DMUON_E_NULL, "logits must be set");
   if (p->tokens > 0) {
-    const int64_t work = backward ? p->tokens * cdiv(p->vocab, kThreads * kGradUnits * 8) : p->tokens * rows_plan(*p, nullptr).pieces;
-    if (!launchable(work, kThreads)) return fail(DMUON_E_SHAPE, "tokens × vocab is too large for one launch");
+    const RowsPlan pl = backward ? RowsPlan{} : rows_plan(*p, nullptr);
+    const bool waves = backward ? p->vocab <= kGradWave : pl.wave;
+    const int64_t work = p->tokens * (backward ? cdiv(p->vocab, kThreads * kGradUnits * 8) : pl.pieces);
+    if (!launchable(work, waves ? 64 : kThreads)) return fail(DMUON_E_SHAPE, "tokens × vocab is too large for one launch");
   }
   return DMUON_OK;
 }

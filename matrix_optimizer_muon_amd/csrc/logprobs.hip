@@ -47,14 +47,13 @@ struct Piece {
 // M's rounding r = m·c2 − M is a factor 2^r of every term, so it cancels between them:
 // the entropy is ln s − ln 2·u/s, and log Σ e^(scale·(z − m)) = ln s − r·ln 2.  When m
 // grows, every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes
-// 2^e·s.  Beyond |M| = 2^29, where r could overflow the exponential, t is (z − m)·c2 and
-// r is 0.  m starts at the lowest finite value, so that no difference is −∞ − −∞; a logit
+// 2^e·s.  Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts at the lowest finite value, so that no difference is −∞ − −∞; a logit
 // of −∞ has 2^t = 0 and its t is kept finite for the product.  A NaN reaches s.
 // Bound by the instructions: 16 elements are taken together, 6.6 instructions each beside
 // the maximum's bookkeeping (unpack, maximum, t, 2^t, clamp, two sums).
 // ---------------------------------------------------------------------------
 constexpr float kFar = -1e30f;           // an exponent whose power of 2 is 0
-constexpr float kBig = 0x1p29f;
+constexpr float kBig = 0x1p24f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 struct Running {

@@ -60,7 +60,7 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100,
     A vocabulary in shards: call each with its columns and the shifted targets,
     ``TARGET_ELSEWHERE`` where that is not one of its columns.  Then lse is the logsumexp of
     the shards', the log probability sum(logprobs_s + lse_s) - lse, the entropy
-    lse - sum(exp(lse_s - lse)*(lse_s - entropy_s)).
+    lse - sum(exp(lse_s - lse)*(lse_s - entropy_s)); a shard whose lse is -inf adds nothing.
     """
     import torch
     _no_graph("token_logprobs", logits=logits)
@@ -113,9 +113,9 @@ def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_e
         raise ValueError("grad_logprobs needs targets")
     ld = prob.vocab
     if out is not None:
+        ld = _matrix(out, "out")[2]
         if out.shape != logits.shape or out.dtype != logits.dtype:
             raise ValueError("out must have the logits' shape and type")
-        ld = _matrix(out, "out")[2]
     with _on(stream, logits, targets, lse, entropy, grad_logprobs, grad_entropy, out) as on:
         if out is None:
             out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)

@@ -4,8 +4,9 @@ fp64 implementations (needs an MI355X).
 Tolerances are worst-case bounds from the arithmetic.  With x = scale·z, X the row's
 largest x, p the probabilities, k1 = Σ p·|x − X| and k2 = Σ p·(x − X)²:
 
-* an exponent (z − m)·(scale·log2 e) is off by 3·2^-24 of itself (the difference, the
-  product, the constant), exp2 by 2^-23 of its result;
+* an exponent (z − m)·(scale·log2 e) is off by 3·2^-24 of itself (the difference or the
+  reference, the product, the constant), exp2 by 2^-23 of its result; the reference's own
+  rounding, at most 1/2, is common to all terms;
 * a thread adds up n ≤ 64 + V/256 terms of one sign and multiplies its sums at most n/8
   times when its largest grows (4·2^-24 each), the others join in ten more steps: the sum S
   is off by soft = (2n + 128)·2^-24 of itself, plus 3·2^-24·k1 of it from the exponents;
@@ -158,6 +159,36 @@ def test_sizes(T, V, dtype):
     for top in sorted({0, 1, min(V, 5), min(V, 64), min(V, 128)}):
         check(z, y, top=top, what=f"{T}x{V} top {top}")
     check_grad(z, y, g, h, what=f"{T}x{V}")
+
+
+# where the kernels change: a unit, a wave's row with and without alternatives, a
+# workgroup's row, and rows enough for waves over longer ones
+BORDERS = [(3, 8), (3, 9), (5, 15), (5, 16), (5, 17), (4, 511), (4, 512), (4, 513), (4, 1025), (4, 2056), (3, 4095), (3, 4103), (2, 8192), (2, 8193),
+           (2, 12288), (2, 12289), (600, 4100), (512, 12288), (511, 12288), (513, 12289), (1024, 20000), (1023, 20000), (1, 131073), (17, 40007)]
+
+
+@TYPES
+@pytest.mark.parametrize("T,V", BORDERS)
+def test_borders_between_the_kernels(T, V, dtype):
+    z, y, g, h = inputs(T, V, dtype, 900 + T + V, ignored=0.0 if T < 6 else 0.2)
+    for top in sorted({0, 3, min(V, 32), min(V, 33), min(V, 128)}):
+        check(z, y, 0.9, top=top, what=f"{T}x{V} top {top}")
+    check_grad(z, y, g, h, 0.9, what=f"{T}x{V}")
+
+
+@TYPES
+@pytest.mark.parametrize("V", [100, 9000, 40000])
+def test_large_logits(V, dtype):
+    """Logits whose exponents have no fraction bits left, beside each other and alone."""
+    for size in (1e4, 1e8, 1e9, 1e20, 2e38):
+        z, y, g, h = inputs(6, V, dtype, 40)
+        z = (z.float() * 1e-3 * size).clamp(-size, size).to(dtype)
+        z[1] = torch.where(torch.arange(V, device="cuda") % 5 == 0, z[1].abs().max(), z[1])      # equal largest ones
+        z[2] = -z[2].abs()
+        z[3, ::2] = -math.inf
+        y[3] = 1
+        check(z, y, top=20, what=f"{size}")
+        check_grad(z, y, g, h, what=f"{size}")
 
 
 @TYPES

@@ -50,7 +50,7 @@ def nothing_is_enqueued(monkeypatch):
 BAD = [(dict(dtype=7), -4), (dict(index_dtype=5), -4), (dict(tokens=-1), -3), (dict(tokens=(1 << 24) + 1), -3), (dict(vocab=0, ld=0), -3),
        (dict(vocab=(1 << 22) + 1, ld=1 << 23), -3), (dict(ld=999), -3), (dict(ld=(1 << 40) + 1), -3), (dict(tokens=256, ld=1 << 40), -3),
        (dict(scale=0.0), -5), (dict(scale=-1.0), -5), (dict(scale=math.inf), -5), (dict(scale=math.nan), -5), (dict(scale=2.0 ** -21), -5),
-       (dict(scale=2.0 ** 21), -5), (dict(logits=None), -1), (dict(tokens=1 << 24), -3)]
+       (dict(scale=2.0 ** 21), -5), (dict(logits=None), -1), (dict(tokens=1 << 24, vocab=100000, ld=100000), -3)]
 
 
 @pytest.mark.parametrize("kw,code", BAD)
@@ -74,6 +74,8 @@ def test_refusals_of_outputs():
         assert fwd(rows(top=top)) == -5
     assert fwd(rows(vocab=4, ld=4)) == -5                       # more alternatives than words
     assert bwd(rows(top=-1)) == -8                              # not read
+    many = rows(tokens=1 << 24, vocab=8, ld=8)                  # a wave per row: 2^30 threads
+    assert fwd(many) == -8 and bwd(many, ld=8) == -8
     assert fwd(p, lp=at(4)) == -7 and fwd(p, H=at(1) + 64) == -7 and fwd(p, ids=at(7) + 8) == -7
     assert bwd(p, lse=None) == -1 and bwd(p, out=None) == -1 and bwd(p, g=None, h=None) == -1 and bwd(p, H=None) == -1
     assert bwd(rows(targets=None)) == -1
