@@ -73,6 +73,7 @@ int check_rows(const dmuon_logprobs_problem* p, bool backward) {
 }
 
 void rows_ranges(const dmuon_logprobs_problem& p, bool logits, std::vector<Range>& rs) {
+  rs.reserve(8);
   if (logits) add_range(rs, p.logits, strided_bytes(p.tokens, p.vocab, p.ld, type_bytes(p.dtype)), true);
   add_range(rs, p.targets, p.tokens * (p.index_dtype == DMUON_I64 ? 8 : 4), true);
 }

@@ -37,11 +37,24 @@ def _three(shape, device):
     return torch.empty((3, *shape), dtype=torch.float32, device=device).unbind(0)
 
 
+# Calls of few rows take about as long as their arguments' checks: what is plainly right is
+# told at a glance, and the rest goes through the checks that say what is wrong.
+def _check_rows(t, what, dtype, shape):
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.shape == shape and t.is_contiguous() and dtype in (None, t.dtype)):
+        _dense(t, what, dtype, shape)
+
+
 def _rows_problem(logits, targets, scale, top, ignore_index):
-    tokens, vocab, ld = _matrix(logits, "logits")
+    import torch
+    if isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.is_cuda and logits.is_contiguous():
+        tokens, vocab = logits.shape
+        ld = vocab
+    else:
+        tokens, vocab, ld = _matrix(logits, "logits")
     icode = _b.I64
     if targets is not None:
-        _dense(targets, "targets", None, logits.shape[:-1])
+        _check_rows(targets, "targets", None, logits.shape[:-1])
         icode = _index_code(targets, "targets")
     return _b.LogprobsProblem(tokens, vocab, _float_code(logits.dtype, "logits"), icode, logits.data_ptr(), ld,
                               None if targets is None else targets.data_ptr(), int(ignore_index), float(scale), int(top))
@@ -84,16 +97,13 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100,
 
 def _check_row_grads(shape, lse, entropy, grad_logprobs, grad_entropy):
     import torch
-    _dense(lse, "lse", torch.float32, shape)
     if grad_logprobs is None and grad_entropy is None:
         raise ValueError("grad_logprobs or grad_entropy must be given")
-    if grad_logprobs is not None:
-        _dense(grad_logprobs, "grad_logprobs", torch.float32, shape)
-    if grad_entropy is not None:
-        _dense(grad_entropy, "grad_entropy", torch.float32, shape)
-        if entropy is None:
-            raise ValueError("grad_entropy needs entropy")
-        _dense(entropy, "entropy", torch.float32, shape)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    for t, what in ((lse, "lse"), (entropy, "entropy"), (grad_logprobs, "grad_logprobs"), (grad_entropy, "grad_entropy")):
+        if t is not None or what == "lse":
+            _check_rows(t, what, torch.float32, shape)
 
 
 def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_entropy=None, *, scale=1.0, ignore_index=-100,
