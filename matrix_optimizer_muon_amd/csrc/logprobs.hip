@@ -353,13 +353,14 @@ struct Stream {
       if (at_head ? e >= head : e < 8 - rest) v[e] = -INFINITY;
   }
   __device__ __forceinline__ gptr<const T> unit(int j) const { return in.p + head + (int64_t)j * 8; }
-  // all of it into r; group(g, largest) of every group of 8 units; returns the largest of an end
+  // all of it into r; group(g, largest, largest) of both halves of every group of 8 units;
+  // returns the largest of an end
   template <typename F>
   __device__ __forceinline__ float run(Running& r, float c2, F group) {
     constexpr int B = sizeof(T) == 2 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
     const int wave0 = tid & ~63, lane = tid & 63;
     for (int g = 0; g < groups; ++g) {
-      float most = -INFINITY;
+      float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int b = 0; b < kGroupUnits; b += B) {
         const int j0 = (g * kGroupUnits + b) * G;
@@ -382,10 +383,11 @@ struct Stream {
           x[k].values(*(float(*)[8])&v[0]);
           x[k + 1].values(*(float(*)[8])&v[8]);
           r.add(v, top, c2);
-          most = fmaxf(most, fmaxf(top[0], top[1]));
+          float& half = most[(b + k) / (kGroupUnits / 2)];
+          half = fmaxf(half, fmaxf(top[0], top[1]));
         }
       }
-      group(g, most);
+      group(g, most[0], most[1]);
     }
     float top[1] = {-INFINITY};
     if (at_head || at_tail) {
@@ -446,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave(LogprobsArgs a) {
   Running r = Running::none(c2);
   if (a.vocab >= 16) {
     Stream<T, 64> stream(in, lane);
-    stream.run(r, c2, [](int, float) {});
+    stream.run(r, c2, [](int, float, float) {});
   } else if (lane < in.units) {
     Unit<T, 8> x;
     if (a.vocab < 8) short_row(in.p, a.vocab, x);
@@ -613,8 +615,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
 
 // ---------------------------------------------------------------------------
 // a workgroup per row or piece.  With alternatives, pieces of up to 2048 (kShort) stay in
-// registers, a unit per thread; of longer ones (kLong) the maxima of each thread's groups
-// stay in LDS, and only groups that reach tau are read again.
+// registers, a unit per thread; of longer ones (kLong) the maxima of every 4 units of a
+// thread stay in LDS, and only those that reach tau are read again.
 // ---------------------------------------------------------------------------
 enum : int { kNoTop, kLong, kShort };
 struct GroupTop : TopShared<512, 256> {
@@ -622,8 +624,8 @@ struct GroupTop : TopShared<512, 256> {
   int flags, strict, ties;
 };
 struct GroupShared {
-  float group[kGroups][kThreads];        // largest of each thread's groups
-  uint16_t flag[kGroups * kThreads];     // groups to read again
+  uint16_t bound[2 * kGroups][kThreads]; // largest of each thread's 4 units, ordered bits rounded up
+  uint16_t flag[2 * kGroups * kThreads]; // those to read again
 };
 
 __device__ __forceinline__ void put_candidate(GroupTop& sh, float raw, float tau, bool own, int index) {
@@ -671,10 +673,13 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
       most = rankable(top[0]);
     }
   } else {
-    const float end = stream.run(r, c2, [&](int g, float top) {
+    const float end = stream.run(r, c2, [&](int g, float lo, float hi) {
       if (TOP) {
-        groups.group[g][tid] = top = rankable(top);
-        most = fmaxf(most, top);
+        lo = rankable(lo);
+        hi = rankable(hi);
+        groups.bound[2 * g][tid] = (uint16_t)((ordered(lo) + 0xffffu) >> 16);
+        groups.bound[2 * g + 1][tid] = (uint16_t)((ordered(hi) + 0xffffu) >> 16);
+        most = fmaxf(most, fmaxf(lo, hi));
       }
     });
     most = fmaxf(most, rankable(end));
@@ -709,8 +714,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
       }
       if constexpr (TOP == kLong) {
 #pragma unroll 1
-        for (int g = 0; g < stream.groups; ++g)
-          if (groups.group[g][tid] >= tau) groups.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
+        for (int g = 0; g < 2 * stream.groups; ++g)
+          if (groups.bound[g][tid] >= ordered(tau) >> 16) groups.flag[atomicAdd(&sh.flags, 1)] = (uint16_t)(g * kThreads + tid);
         if (stream.at_head || stream.at_tail) {
           float v[8];
           stream.edge_values(v);
@@ -720,11 +725,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
             put_candidate(sh, v[e], tau, stream.at_head ? e < stream.head : e >= 8 - rest, first + at + e);
         }
         __syncthreads();
-        const int units = sh.flags * kGroupUnits;
+        constexpr int half = kGroupUnits / 2;
+        const int units = sh.flags * half;
 #pragma unroll 1
         for (int w = tid; w < units; w += kThreads) {
-          const int f = groups.flag[w / kGroupUnits];
-          const int j = (f / kThreads * kGroupUnits + w % kGroupUnits) * kThreads + f % kThreads;
+          const int f = groups.flag[w / half];
+          const int j = (f / kThreads * half + w % half) * kThreads + f % kThreads;
           if (j >= stream.full) continue;
           Unit<T, 8> x;
           float v[8];
