@@ -17,7 +17,9 @@
  *   and, for the owner's small and 1-D parameters (the "adamw" route), one
  *   AdamW step per element (dmuon_adamw_step); and the training operators that
  *   produce gradients in the layout the steps read (dmuon_linear_ce,
- *   dmuon_embedding, dmuon_ckpt8_*).
+ *   dmuon_embedding, dmuon_ckpt8_*), score tokens for policy gradients and
+ *   distillation (dmuon_logprobs, dmuon_linear_logprobs, with their gradients)
+ *   and bound the gradients' common norm (dmuon_grad_*).
  *
  *   DMuon "架构设计" (Architecture design) page, §1 (the Newton–Schulz
  *   equation with coefficients α, β, γ = a, b, c) and §2 (the owner alone runs

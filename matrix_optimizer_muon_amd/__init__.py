@@ -11,7 +11,10 @@ unless a ``stream`` is given.
     lpt_assign(rows, cols, batch, layer_id, n_slots, ...)   # host only
 
 and, from ``training``, the operators that produce gradients the steps read:
-cross entropy over a large vocabulary, embedding, 8-bit activation checkpoints.
+cross entropy over a large vocabulary, embedding, 8-bit activation checkpoints; from
+``logprobs``, log probabilities of given tokens with entropies, alternatives and gradients,
+out of logits or out of hidden states; from ``clip``, the norm over many gradients and
+clipping by it, between the backward pass and the steps.
 """
 from __future__ import annotations
 

@@ -47,8 +47,9 @@ struct Piece {
 // M's rounding r = m·c2 − M is a factor 2^r of every term, so it cancels between them:
 // the entropy is ln s − ln 2·u/s, and log Σ e^(scale·(z − m)) = ln s − r·ln 2.  When m
 // grows, every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes
-// 2^e·s.  Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts at the lowest finite value, so that no difference is −∞ − −∞; a logit
-// of −∞ has 2^t = 0 and its t is kept finite for the product.  A NaN reaches s.
+// 2^e·s.  Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts
+// at the lowest finite value, so that no difference is −∞ − −∞; a logit of −∞ has 2^t = 0
+// and its t is kept finite for the product.  A NaN reaches s.
 // Bound by the instructions: 16 elements are taken together, 6.6 instructions each beside
 // the maximum's bookkeeping (unpack, maximum, t, 2^t, clamp, two sums).
 // ---------------------------------------------------------------------------
@@ -616,7 +617,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
 // ---------------------------------------------------------------------------
 // a workgroup per row or piece.  With alternatives, pieces of up to 2048 (kShort) stay in
 // registers, a unit per thread; of longer ones (kLong) the maxima of every 4 units of a
-// thread stay in LDS, and only those that reach tau are read again.
+// thread stay in LDS, and only those that reach tau are read again: with 64 alternatives
+// 2001 × 50257 bf16 takes 55 µs without and 62 with one maximum per 8 units, 47 without
+// alternatives.  Without them 8192 × 128000 bf16 takes 356 µs (5.9 TB/s of a read's 6.2),
+// where the instructions of a unit still pass behind its load.
 // ---------------------------------------------------------------------------
 enum : int { kNoTop, kLong, kShort };
 struct GroupTop : TopShared<512, 256> {
@@ -837,7 +841,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
 // the gradient, element by element: with l = c·z − lse and p = e^l,
 //   dz = c·(g·[v = target] − p·(g + h·(l + H)))     (g, h: of the log probability, the entropy)
 // l is kept from −200 on (e^−200 is 0 in fp32), so that 0·−∞ does not arise.  Rows that
-// take no part are zeros and their logits are not read.  Memory bound.
+// take no part are zeros and their logits are not read.  Memory bound: 4096 × 128000 bf16,
+// a quarter of the rows ignored, 325 µs, 5.6 TB/s of what is read and written; 512 × 10007
+// fp32 12 µs.  A thread takes 4 units, all loads in flight, so a row of up to 2048 words is
+// a wave's, and a longer one is spread over workgroups of 8192 words.
 // ---------------------------------------------------------------------------
 template <typename T, int G>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) {
