@@ -843,8 +843,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
 // l is kept from −200 on (e^−200 is 0 in fp32), so that 0·−∞ does not arise.  Rows that
 // take no part are zeros and their logits are not read.  Memory bound: 4096 × 128000 bf16,
 // a quarter of the rows ignored, 325 µs, 5.6 TB/s of what is read and written; 512 × 10007
-// fp32 12 µs.  A thread takes 4 units, all loads in flight, so a row of up to 2048 words is
-// a wave's, and a longer one is spread over workgroups of 8192 words.
+// fp32 12 µs.  A thread takes at most 4 units, all loads in flight, so a row of up to 2048
+// words is a wave's, and a longer one is shared evenly by workgroups of at most 8192 words
+// (all but the last full: 8192 × 10007 bf16 82 µs, so 66; fp32 163 and 138).
 // ---------------------------------------------------------------------------
 template <typename T, int G>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) {
@@ -853,7 +854,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const int64_t row = id / (uint32_t)a.pieces;
   const int piece = (int)(id - (uint32_t)row * a.pieces);
   if (row >= a.rows) return;
-  const int j0 = piece * G * kGradUnits + tid;           // this thread's units: j0 + k·G
+  const int j0 = piece * a.units + tid;                  // this thread's units: j0 + k·G
   const gptr<const T> src = glob((const T*)a.logits) + row * a.ld;
   const gptr<T> dst = glob((T*)a.out) + row * a.ldo;
   const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
@@ -865,17 +866,18 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const bool takes_part = kind != kIgnored && kind != kOutside && !(g == 0.f && h == 0.f) && !(lse == -INFINITY);
   const int target = kind == kInside ? (int)y : -1;
   const Piece<T> in(src, a.vocab);
+  const int end = (piece + 1) * a.units < in.units ? (piece + 1) * a.units : in.units;
   Unit<T, 8> x[kGradUnits];
 #pragma unroll
   for (int k = 0; k < kGradUnits; ++k) {
     const int j = j0 + k * G;
-    if (takes_part && j < in.units && a.vocab >= 8) in.load(x[k], j);
+    if (takes_part && j < end && a.vocab >= 8) in.load(x[k], j);
   }
   if (takes_part && j0 == 0 && a.vocab < 8) short_row(src, a.vocab, x[0]);
 #pragma unroll
   for (int k = 0; k < kGradUnits; ++k) {
     const int j = j0 + k * G;
-    if (j >= in.units) break;
+    if (j >= end) break;
     const int at = a.vocab < 8 ? 0 : in.start(j);
     float v[8];
     if (takes_part) {

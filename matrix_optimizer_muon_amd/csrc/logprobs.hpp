@@ -57,6 +57,7 @@ struct LogprobsGradArgs {
   int64_t rows;
   int32_t vocab;
   int32_t pieces;              // workgroups (or waves) per row
+  int32_t units;               // units of 8 elements of each
   float scale;
   const void* targets;         // or null
   int32_t idx64;
