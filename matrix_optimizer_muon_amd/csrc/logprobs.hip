@@ -845,7 +845,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
 // a quarter of the rows ignored, 325 µs, 5.6 TB/s of what is read and written; 512 × 10007
 // fp32 12 µs.  A thread takes at most 4 units, all loads in flight, so a row of up to 2048
 // words is a wave's, and a longer one is shared evenly by workgroups of at most 8192 words
-// (all but the last full: 8192 × 10007 bf16 82 µs, so 66; fp32 163 and 138).
+// (all but the last full: 8192 × 10007 bf16 82 µs, so 66; fp32 163 and 138).  Aligned bf16
+// rows, a wave's loads of which are whole lines, are read nontemporally (2048 × 128000 183
+// µs, else 195; 4096 × 32000 87 and 92; but 300 × 50257, odd rows, 14.8 and 13.1, and fp32
+// 8192 × 10000, where two loads share a line, 142 and 130).
 // ---------------------------------------------------------------------------
 template <typename T, int G>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) {
@@ -868,10 +871,18 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const Piece<T> in(src, a.vocab);
   const int end = (piece + 1) * a.units < in.units ? (piece + 1) * a.units : in.units;
   Unit<T, 8> x[kGradUnits];
+  if (sizeof(T) == 2 && a.aligned) {
 #pragma unroll
-  for (int k = 0; k < kGradUnits; ++k) {
-    const int j = j0 + k * G;
-    if (takes_part && j < end && a.vocab >= 8) in.load(x[k], j);
+    for (int k = 0; k < kGradUnits; ++k) {
+      const int j = j0 + k * G;
+      if (takes_part && j < end) x[k].load_once(in.p + in.start(j));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kGradUnits; ++k) {
+      const int j = j0 + k * G;
+      if (takes_part && j < end && a.vocab >= 8) in.load(x[k], j);
+    }
   }
   if (takes_part && j0 == 0 && a.vocab < 8) short_row(src, a.vocab, x[0]);
 #pragma unroll

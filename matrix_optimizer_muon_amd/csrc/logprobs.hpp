@@ -58,6 +58,7 @@ struct LogprobsGradArgs {
   int32_t vocab;
   int32_t pieces;              // workgroups (or waves) per row
   int32_t units;               // units of 8 elements of each
+  int32_t aligned;             // the logits' rows start on 16 bytes and hold a unit
   float scale;
   const void* targets;         // or null
   int32_t idx64;
