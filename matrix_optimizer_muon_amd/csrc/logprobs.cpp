@@ -11,6 +11,7 @@ namespace dmuon {
 namespace {
 
 constexpr int64_t kMaxVocab = (int64_t)1 << 22;     // words of a row of logits
+constexpr int64_t kCaches = (int64_t)256 << 20;     // bytes: what the last cache before memory holds
 constexpr int64_t kMaxKeys = 6144;                  // candidates of a row's pieces together, in the joining workgroup's LDS
 static_assert(kMaxVocab <= kMaxKeys / kTopMost * (kPieceMost - 16), "the largest vocabulary in pieces that can be joined");
 
@@ -126,6 +127,7 @@ int dmuon_logprobs(const dmuon_logprobs_problem* p, float* logprobs, float* entr
     a.piece = (int32_t)pl.piece;
     a.pieces = (int32_t)pl.pieces;
     a.wave_rows = pl.wave;
+    a.once = p->dtype == DMUON_BF16 && p->tokens * p->vocab * 2 > kCaches;
     a.scale = p->scale;
     a.targets = p->targets;
     a.idx64 = p->index_dtype == DMUON_I64;

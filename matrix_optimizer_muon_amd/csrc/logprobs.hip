@@ -327,7 +327,10 @@ __device__ __forceinline__ int select_top(S& sh, const Piece<T>& row, int tid, i
 // the 16-byte grid, and the up to 7 elements before and behind them are two more units,
 // from the piece's own ends, for the last two threads.  Loads past the last whole unit take
 // that one again, so that all of a batch are in flight without a branch, and count as −∞;
-// waves that are past it skip them.
+// waves that are past it skip them.  ONCE: nontemporal loads, for bf16 logits that exceed
+// the caches (8192 × 128000 312 µs, else 356, 4096 × 50257 74 and 79; of logits that fit,
+// the gradient that reads them next loses more: 8192 × 2000 both passes 25 and 23, 512 ×
+// 32000 28 and 24).
 // ---------------------------------------------------------------------------
 template <typename T, int G>
 struct Stream {
@@ -356,7 +359,7 @@ struct Stream {
   __device__ __forceinline__ gptr<const T> unit(int j) const { return in.p + head + (int64_t)j * 8; }
   // all of it into r; group(g, largest, largest) of both halves of every group of 8 units;
   // returns the largest of an end
-  template <typename F>
+  template <bool ONCE, typename F>
   __device__ __forceinline__ float run(Running& r, float c2, F group) {
     constexpr int B = sizeof(T) == 2 ? kGroupUnits : kGroupUnits / 2;       // loads in flight
     const int wave0 = tid & ~63, lane = tid & 63;
@@ -370,7 +373,8 @@ struct Stream {
 #pragma unroll
         for (int k = 0; k < B; ++k) {
           const int j = j0 + k * G + tid;
-          x[k].load(unit(j < full ? j : full - 1));
+          if (ONCE) x[k].load_once(unit(j < full ? j : full - 1));
+          else x[k].load(unit(j < full ? j : full - 1));
         }
 #pragma unroll
         for (int k = 0; k < B; k += 2) {
@@ -449,7 +453,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave(LogprobsArgs a) {
   Running r = Running::none(c2);
   if (a.vocab >= 16) {
     Stream<T, 64> stream(in, lane);
-    stream.run(r, c2, [](int, float, float) {});
+    const auto group = [](int, float, float) {};
+    if (sizeof(T) == 2 && a.once) stream.template run<true>(r, c2, group);
+    else stream.template run<false>(r, c2, group);
   } else if (lane < in.units) {
     Unit<T, 8> x;
     if (a.vocab < 8) short_row(in.p, a.vocab, x);
@@ -619,8 +625,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
 // registers, a unit per thread; of longer ones (kLong) the maxima of every 4 units of a
 // thread stay in LDS, and only those that reach tau are read again: with 64 alternatives
 // 2001 × 50257 bf16 takes 55 µs without and 62 with one maximum per 8 units, 47 without
-// alternatives.  Without them 8192 × 128000 bf16 takes 356 µs (5.9 TB/s of a read's 6.2),
-// where the instructions of a unit still pass behind its load.
+// alternatives.  Without them 8192 × 128000 bf16 takes 312 µs (6.7 TB/s), where the
+// instructions of a unit still pass behind its load.
 // ---------------------------------------------------------------------------
 enum : int { kNoTop, kLong, kShort };
 struct GroupTop : TopShared<512, 256> {
@@ -677,7 +683,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
       most = rankable(top[0]);
     }
   } else {
-    const float end = stream.run(r, c2, [&](int g, float lo, float hi) {
+    const auto group = [&](int g, float lo, float hi) {
       if (TOP) {
         lo = rankable(lo);
         hi = rankable(hi);
@@ -685,7 +691,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
         groups.bound[2 * g + 1][tid] = (uint16_t)((ordered(hi) + 0xffffu) >> 16);
         most = fmaxf(most, fmaxf(lo, hi));
       }
-    });
+    };
+    const float end = sizeof(T) == 2 && a.once ? stream.template run<true>(r, c2, group) : stream.template run<false>(r, c2, group);
     most = fmaxf(most, rankable(end));
   }
   if constexpr (TOP) {
