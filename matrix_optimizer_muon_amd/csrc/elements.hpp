@@ -111,6 +111,16 @@ struct Unit<float, 8> {
     a = __builtin_nontemporal_load((gptr<const f32x4_any>)p);
     b = __builtin_nontemporal_load((gptr<const f32x4_any>)p + 1);
   }
+  // two quads that do not follow each other
+  template <bool ONCE>
+  __device__ __forceinline__ void load_quads(gptr<const float> p, gptr<const float> q) {
+    a = ONCE ? __builtin_nontemporal_load((gptr<const f32x4_any>)p) : *(gptr<const f32x4_any>)p;
+    b = ONCE ? __builtin_nontemporal_load((gptr<const f32x4_any>)q) : *(gptr<const f32x4_any>)q;
+  }
+  __device__ __forceinline__ void clear_quads(bool first, bool second) {
+    if (first) a = f32x4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (second) b = f32x4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  }
   __device__ __forceinline__ void set(const float (&v)[8]) {
     a = f32x4_t{v[0], v[1], v[2], v[3]};
     b = f32x4_t{v[4], v[5], v[6], v[7]};

@@ -127,7 +127,7 @@ int dmuon_logprobs(const dmuon_logprobs_problem* p, float* logprobs, float* entr
     a.piece = (int32_t)pl.piece;
     a.pieces = (int32_t)pl.pieces;
     a.wave_rows = pl.wave;
-    a.once = p->dtype == DMUON_BF16 && p->tokens * p->vocab * 2 > kCaches;
+    a.once = p->tokens * p->vocab * (int64_t)type_bytes(p->dtype) > kCaches && (p->top == 0 || (p->dtype == DMUON_BF16 && p->vocab > 1024 * p->top));
     a.scale = p->scale;
     a.targets = p->targets;
     a.idx64 = p->index_dtype == DMUON_I64;

@@ -327,12 +327,15 @@ __device__ __forceinline__ int select_top(S& sh, const Piece<T>& row, int tid, i
 // the 16-byte grid, and the up to 7 elements before and behind them are two more units,
 // from the piece's own ends, for the last two threads.  Loads past the last whole unit take
 // that one again, so that all of a batch are in flight without a branch, and count as −∞;
-// waves that are past it skip them.  ONCE: nontemporal loads, for bf16 logits that exceed
-// the caches (8192 × 128000 312 µs, else 356, 4096 × 50257 74 and 79; of logits that fit,
-// the gradient that reads them next loses more: 8192 × 2000 both passes 25 and 23, 512 ×
-// 32000 28 and 24).
+// waves that are past it skip them.  ONCE: nontemporal loads, for logits that exceed the
+// caches (bf16 8192 × 128000 312 µs, else 356, 4096 × 50257 74 and 79, fp32 4096 × 128000
+// 319 and 358; of logits that fit, the gradient that reads them next loses more: 8192 × 2000
+// both passes 25 and 23, 512 × 32000 28 and 24).  With alternatives the units that are read
+// again miss then: worth it for bf16 rows of more than 1024 words an alternative (4096 ×
+// 128000 with 20 of them 178 and 200 µs, with 64 187 and 201; 8192 × 32000 with 20 110 and
+// 111, with 64 128 and 121).
 // ---------------------------------------------------------------------------
-template <typename T, int G>
+template <typename T, int G, bool AGAIN>
 struct Stream {
   const Piece<T>& in;
   int tid, head, full, groups;           // elements before the grid, whole units, groups of units
@@ -356,7 +359,33 @@ struct Stream {
     for (int e = 0; e < 8; ++e)
       if (at_head ? e >= head : e < 8 - rest) v[e] = -INFINITY;
   }
-  __device__ __forceinline__ gptr<const T> unit(int j) const { return in.p + head + (int64_t)j * 8; }
+  // Unit j is 8 elements one after another, or of fp32 that is read once two quads 64 quads
+  // apart, so that each load of a wave is whole lines (AGAIN: units are read again one by one,
+  // 64 alternatives of 8192 × 32000 207 µs, with quads 228); past the end its elements are
+  // not its own.
+  static constexpr bool kQuads = sizeof(T) == 4 && !AGAIN;
+  __device__ __forceinline__ bool own(int j, int e) const {
+    return kQuads ? (j & 63) + (e < 4 ? 0 : 64) < 2 * (full - (j & ~63)) : j < full;
+  }
+  __device__ __forceinline__ int index(int j, int e) const {
+    return head + (kQuads ? (j & ~63) * 8 + (j & 63) * 4 + (e < 4 ? e : 252 + e) : j * 8 + e);
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load(Unit<T, 8>& x, int j) const {
+    if constexpr (kQuads) {
+      const int last = 2 * full - 1, a = (j & ~63) * 2 + (j & 63);
+      x.template load_quads<ONCE>(in.p + head + (a < last ? a : last) * 4, in.p + head + (a + 64 < last ? a + 64 : last) * 4);
+    } else if (ONCE) {
+      x.load_once(in.p + head + (j < full ? j : full - 1) * 8);
+    } else {
+      x.load(in.p + head + (j < full ? j : full - 1) * 8);
+    }
+  }
+  // left: units from this wave's first one on
+  __device__ __forceinline__ void clear(Unit<T, 8>& x, int lane, int left) const {
+    if constexpr (kQuads) x.clear_quads(lane >= 2 * left, lane + 64 >= 2 * left);
+    else if (lane >= left) x.clear();
+  }
   // all of it into r; group(g, largest, largest) of both halves of every group of 8 units;
   // returns the largest of an end
   template <bool ONCE, typename F>
@@ -371,18 +400,14 @@ struct Stream {
         if (__builtin_amdgcn_readfirstlane(j0 + wave0) >= full) break;
         Unit<T, 8> x[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-          const int j = j0 + k * G + tid;
-          if (ONCE) x[k].load_once(unit(j < full ? j : full - 1));
-          else x[k].load(unit(j < full ? j : full - 1));
-        }
+        for (int k = 0; k < B; ++k) load<ONCE>(x[k], j0 + k * G + tid);
 #pragma unroll
         for (int k = 0; k < B; k += 2) {
           const int left = full - __builtin_amdgcn_readfirstlane(j0 + k * G + wave0);
           if (left <= 0) break;
           if (left < G + 64) {                           // the last units' waves
-            if (lane >= left) x[k].clear();
-            if (lane + G >= left) x[k + 1].clear();
+            clear(x[k], lane, left);
+            clear(x[k + 1], lane, left - G);
           }
           float v[16], top[2];
           x[k].values(*(float(*)[8])&v[0]);
@@ -452,9 +477,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave(LogprobsArgs a) {
   const float c2 = a.scale * kLog2e;
   Running r = Running::none(c2);
   if (a.vocab >= 16) {
-    Stream<T, 64> stream(in, lane);
+    Stream<T, 64, false> stream(in, lane);
     const auto group = [](int, float, float) {};
-    if (sizeof(T) == 2 && a.once) stream.template run<true>(r, c2, group);
+    if (a.once) stream.template run<true>(r, c2, group);
     else stream.template run<false>(r, c2, group);
   } else if (lane < in.units) {
     Unit<T, 8> x;
@@ -672,7 +697,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
   Running r = Running::none(c2);
   float most = -INFINITY;                                // of this thread
   float held[8];                                         // kShort: its unit
-  Stream<T, kThreads> stream(in, tid);
+  Stream<T, kThreads, TOP == kLong> stream(in, tid);
   if constexpr (TOP == kShort) {
     if (tid < in.units) {
       Unit<T, 8> x;
@@ -692,7 +717,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
         most = fmaxf(most, fmaxf(lo, hi));
       }
     };
-    const float end = sizeof(T) == 2 && a.once ? stream.template run<true>(r, c2, group) : stream.template run<false>(r, c2, group);
+    const float end = (TOP == kNoTop || sizeof(T) == 2) && a.once ? stream.template run<true>(r, c2, group) : stream.template run<false>(r, c2, group);
     most = fmaxf(most, rankable(end));
   }
   if constexpr (TOP) {
@@ -742,13 +767,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a) {
         for (int w = tid; w < units; w += kThreads) {
           const int f = groups.flag[w / half];
           const int j = (f / kThreads * half + w % half) * kThreads + f % kThreads;
-          if (j >= stream.full) continue;
           Unit<T, 8> x;
           float v[8];
-          x.load(stream.unit(j));
+          stream.template load<false>(x, j);
           x.values(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) put_candidate(sh, v[e], tau, true, first + stream.head + j * 8 + e);
+          for (int e = 0; e < 8; ++e) put_candidate(sh, v[e], tau, stream.own(j, e), first + stream.index(j, e));
         }
       } else if (tid < in.units && most >= tau) {
         const int at = in.start(tid);

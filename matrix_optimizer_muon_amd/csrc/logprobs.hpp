@@ -37,7 +37,7 @@ struct LogprobsArgs {
   int32_t top;                 // alternatives, 0: none
   int32_t piece, pieces;       // columns per workgroup, workgroups per row
   int32_t wave_rows;           // 1: a wave per row
-  int32_t once;                // 1: bf16 logits that exceed the caches
+  int32_t once;                // 1: read nontemporally
   float scale;
   const void* targets;         // or null: every row takes part, none has a target
   int32_t idx64;
