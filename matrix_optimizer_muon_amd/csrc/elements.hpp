@@ -131,6 +131,14 @@ struct Unit<float, 8> {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 };
+template <>
+struct Unit<float, 4> {
+  f32x4_t a;
+  __device__ __forceinline__ void load(gptr<const float> p) { a = *(gptr<const f32x4_any>)p; }
+  __device__ __forceinline__ void load_once(gptr<const float> p) { a = __builtin_nontemporal_load((gptr<const f32x4_any>)p); }
+  __device__ __forceinline__ void set(const float (&v)[4]) { a = f32x4_t{v[0], v[1], v[2], v[3]}; }
+  __device__ __forceinline__ void values(float (&v)[4]) const { v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; }
+};
 __device__ __forceinline__ float element(gptr<const uint16_t> p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float element(gptr<const float> p) { return *p; }
 __device__ __forceinline__ void store_unit(gptr<uint16_t> p, const float (&v)[8]) {
@@ -139,6 +147,9 @@ __device__ __forceinline__ void store_unit(gptr<uint16_t> p, const float (&v)[8]
 __device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[8]) {
   __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
   __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, (gptr<f32x4_any>)p + 1);
+}
+__device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[4]) {
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
 }
 __device__ __forceinline__ void store_element(gptr<uint16_t> p, float v) { *p = f32_to_bf16(v); }
 __device__ __forceinline__ void store_element(gptr<float> p, float v) { *p = v; }

@@ -176,8 +176,9 @@ int dmuon_logprobs_backward(const dmuon_logprobs_problem* p, const float* lse, c
     a.rows = p->tokens;
     a.vocab = (int32_t)p->vocab;
     a.pieces = p->vocab <= kGradWave ? 1 : (int32_t)cdiv(p->vocab, kThreads * kGradUnits * 8);
-    a.units = (int32_t)round_up(cdiv(cdiv(p->vocab, 8), a.pieces), 8);
-    a.aligned = p->vocab >= 8 && (uintptr_t)p->logits % 16 == 0 && p->ld * (int64_t)type_bytes(p->dtype) % 16 == 0;
+    const int64_t bytes = (int64_t)type_bytes(p->dtype);
+    a.units = (int32_t)round_up(cdiv(cdiv(p->vocab * bytes, 16), a.pieces), 8);
+    a.aligned = p->vocab * bytes >= 16 && (uintptr_t)p->logits % 16 == 0 && p->ld * bytes % 16 == 0;
     a.scale = p->scale;
     a.targets = p->targets;
     a.idx64 = p->index_dtype == DMUON_I64;

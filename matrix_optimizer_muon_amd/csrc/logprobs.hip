@@ -873,13 +873,14 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a) {
 //   dz = c·(g·[v = target] − p·(g + h·(l + H)))     (g, h: of the log probability, the entropy)
 // l is kept from −200 on (e^−200 is 0 in fp32), so that 0·−∞ does not arise.  Rows that
 // take no part are zeros and their logits are not read.  Memory bound: 4096 × 128000 bf16,
-// a quarter of the rows ignored, 325 µs, 5.6 TB/s of what is read and written; 512 × 10007
-// fp32 12 µs.  A thread takes at most 4 units, all loads in flight, so a row of up to 2048
+// a quarter of the rows ignored, 318 µs, 5.8 TB/s of what is read and written; 512 × 10007
+// fp32 10 µs.  A thread takes 32 elements at most, all loads in flight, so a row of up to 2048
 // words is a wave's, and a longer one is shared evenly by workgroups of at most 8192 words
-// (all but the last full: 8192 × 10007 bf16 82 µs, so 66; fp32 163 and 138).  Aligned bf16
-// rows, a wave's loads of which are whole lines, are read nontemporally (2048 × 128000 183
-// µs, else 195; 4096 × 32000 87 and 92; but 300 × 50257, odd rows, 14.8 and 13.1, and fp32
-// 8192 × 10000, where two loads share a line, 142 and 130).
+// (all but the last full: 8192 × 10007 bf16 82 µs, so 66).  A unit is 16 bytes, so that
+// every load and store of a wave is whole lines (fp32 units of 8 elements, two of each:
+// 2048 × 128000 423 µs, so 357).  Aligned rows are read nontemporally (bf16 2048 × 128000
+// 183 µs, else 195, 4096 × 32000 87 and 92; but odd rows share their lines with the next
+// unit: 300 × 50257 14.8 and 13.1).
 // ---------------------------------------------------------------------------
 template <typename T, int G>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) {
@@ -888,7 +889,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const int64_t row = id / (uint32_t)a.pieces;
   const int piece = (int)(id - (uint32_t)row * a.pieces);
   if (row >= a.rows) return;
-  const int j0 = piece * a.units + tid;                  // this thread's units: j0 + k·G
+  constexpr int W = 16 / sizeof(T), N = kGradUnits * 8 / W;
+  const int j0 = piece * a.units + tid;                  // this thread's units of 16 bytes: j0 + k·G
   const gptr<const T> src = glob((const T*)a.logits) + row * a.ld;
   const gptr<T> dst = glob((T*)a.out) + row * a.ldo;
   const int64_t y = a.targets ? load_index(a.targets, a.idx64, row) : 0;
@@ -899,33 +901,38 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
   const float entropy = a.grad_entropy ? a.entropy[row] : 0.f;
   const bool takes_part = kind != kIgnored && kind != kOutside && !(g == 0.f && h == 0.f) && !(lse == -INFINITY);
   const int target = kind == kInside ? (int)y : -1;
-  const Piece<T> in(src, a.vocab);
-  const int end = (piece + 1) * a.units < in.units ? (piece + 1) * a.units : in.units;
-  Unit<T, 8> x[kGradUnits];
-  if (sizeof(T) == 2 && a.aligned) {
+  const int units = (a.vocab + W - 1) / W, end = (piece + 1) * a.units < units ? (piece + 1) * a.units : units;
+  const auto start = [&](int j) { return (j + 1) * W <= a.vocab ? j * W : a.vocab - W; };      // the last: the row's last W
+  Unit<T, W> x[N];
+  if (a.aligned) {
 #pragma unroll
-    for (int k = 0; k < kGradUnits; ++k) {
+    for (int k = 0; k < N; ++k) {
       const int j = j0 + k * G;
-      if (takes_part && j < end) x[k].load_once(in.p + in.start(j));
+      if (takes_part && j < end) x[k].load_once(src + start(j));
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < kGradUnits; ++k) {
+    for (int k = 0; k < N; ++k) {
       const int j = j0 + k * G;
-      if (takes_part && j < end && a.vocab >= 8) in.load(x[k], j);
+      if (takes_part && j < end && a.vocab >= W) x[k].load(src + start(j));
     }
   }
-  if (takes_part && j0 == 0 && a.vocab < 8) short_row(src, a.vocab, x[0]);
+  if (takes_part && j0 == 0 && a.vocab < W) {
+    float v[W];
 #pragma unroll
-  for (int k = 0; k < kGradUnits; ++k) {
+    for (int e = 0; e < W; ++e) v[e] = e < a.vocab ? element(src + e) : 0.f;
+    x[0].set(v);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
     const int j = j0 + k * G;
     if (j >= end) break;
-    const int at = a.vocab < 8 ? 0 : in.start(j);
-    float v[8];
+    const int at = a.vocab < W ? 0 : start(j);
+    float v[W];
     if (takes_part) {
       x[k].values(v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < W; ++e) {
         float l = fmaf(v[e], a.scale, -lse);
         l = l < -200.f ? -200.f : l;                     // a NaN stays
         const float p = __builtin_amdgcn_exp2f(l * kLog2e);
@@ -934,14 +941,14 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LogprobsGradArgs a) 
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int e = 0; e < W; ++e) v[e] = 0.f;
     }
-    if ((j + 1) * 8 <= a.vocab) {
+    if ((j + 1) * W <= a.vocab) {
       store_unit(dst + at, v);
     } else {                                             // its own elements: the others are another thread's, also in place
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e >= j * 8 && at + e < a.vocab) store_element(dst + at + e, v[e]);
+      for (int e = 0; e < W; ++e)
+        if (at + e >= j * W && at + e < a.vocab) store_element(dst + at + e, v[e]);
     }
   }
 }

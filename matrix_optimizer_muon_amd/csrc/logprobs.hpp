@@ -21,7 +21,7 @@ inline int64_t wave_row(bool f32) { return f32 ? 8192 : 12288; }
 constexpr int kWaveTop = 64 * 8 * 8;                 // 4096: the units' maxima of a row in 8 registers
 constexpr int kWaveTopMost = 3 * kWaveTop;           // 12288: in 24
 constexpr int kWaveTopRows = 512;
-constexpr int kGradUnits = 4;            // units of 8 elements per thread of the gradient
+constexpr int kGradUnits = 4;            // times 8 elements per thread of the gradient
 constexpr int kGradWave = 64 * kGradUnits * 8;       // 2048: rows up to this take one wave each
 
 // Σ 2^t and Σ t·2^t of a row's piece, m its largest logit and t its exponents (see logprobs.hip)
@@ -58,7 +58,7 @@ struct LogprobsGradArgs {
   int64_t rows;
   int32_t vocab;
   int32_t pieces;              // workgroups (or waves) per row
-  int32_t units;               // units of 8 elements of each
+  int32_t units;               // units of 16 bytes of each
   int32_t aligned;             // the logits' rows start on 16 bytes and hold a unit
   float scale;
   const void* targets;         // or null
