@@ -62,43 +62,49 @@ __device__ __forceinline__ double sum_workgroup(double v, double* shared) {
   return (shared[0] + shared[1]) + (shared[2] + shared[3]);
 }
 
-// one chunk: a thread's units 256 apart, all loads in flight, and at a tensor's end at most
-// 7 elements.  ONCE: nontemporal, for the last reading of the data; the sums' loads leave
-// what fits in the caches for the scaling (29 × 16 Mi bf16: 482 µs, with nontemporal loads in
-// both 483, in neither 553; 7 × 11 Mi: 75, 83 and 77).
+// one chunk: a thread's units of 16 bytes 256 apart, so that every access of a wave is whole
+// lines (fp32 units of 8 elements, two accesses of each: 5 × 200 M clipped in 2351 µs, so
+// 2062), 4 loads in flight (8: 78 registers for 50, and bf16 5% slower), and at a tensor's
+// end at most 7 elements.  ONCE: nontemporal, for the last reading of the data; the sums'
+// loads leave what fits in the caches for the scaling (29 × 16 Mi bf16: 482 µs, with
+// nontemporal loads in both 483, in neither 553; 7 × 11 Mi: 75, 83 and 77).
 template <bool ONCE, typename T, typename F, typename G>
-__device__ __forceinline__ void chunk(gptr<const T> p, int64_t e0, int64_t e1, F unit, G single) {
-  constexpr int B = kClipChunk / 8 / kThreads;
-  const int units = (int)(e1 - e0) >> 3;
-  Unit<T, 8> x[B];
+__device__ __forceinline__ void chunk(gptr<const T> p, int n, F unit, G single) {
+  constexpr int W = 16 / sizeof(T), B = 4;
+  const int units = n / W;
+#pragma unroll 1
+  for (int h = 0; h < kClipChunk / (B * W * kThreads); ++h) {
+    const int j0 = threadIdx.x + h * (B * kThreads);
+    Unit<T, W> x[B];
 #pragma unroll
-  for (int k = 0; k < B; ++k) {
-    const int j = threadIdx.x + k * kThreads;
-    if (j < units) {
-      if (ONCE) x[k].load_once(p + e0 + j * 8);
-      else x[k].load(p + e0 + j * 8);
+    for (int k = 0; k < B; ++k) {
+      const int j = j0 + k * kThreads;
+      if (j < units) {
+        if (ONCE) x[k].load_once(p + j * W);
+        else x[k].load(p + j * W);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int j = j0 + k * kThreads;
+      if (j >= units) break;
+      float v[W];
+      x[k].values(v);
+      unit(j * W, v);
     }
   }
-#pragma unroll
-  for (int k = 0; k < B; ++k) {
-    const int j = threadIdx.x + k * kThreads;
-    if (j >= units) break;
-    float v[8];
-    x[k].values(v);
-    unit(e0 + j * 8, v);
-  }
-  const int64_t e = e0 + units * 8 + threadIdx.x;
-  if (e < e1) single(e, element(p + e));
+  const int e = units * W + threadIdx.x;
+  if (e < n) single(e, element(p + e));
 }
 
 template <typename T>
 __device__ __forceinline__ void add_squares(gptr<const T> p, int64_t e0, int64_t e1, double (&sum)[2]) {
-  chunk<false>(p, e0, e1,
-        [&](int64_t, const float (&v)[8]) {
+  chunk<false>(p + e0, (int)(e1 - e0),
+        [&](int, const auto& v) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e & 1] = fma((double)v[e], (double)v[e], sum[e & 1]);
+          for (int e = 0; e < 16 / (int)sizeof(T); ++e) sum[e & 1] = fma((double)v[e], (double)v[e], sum[e & 1]);
         },
-        [&](int64_t, float v) { sum[0] = fma((double)v, (double)v, sum[0]); });
+        [&](int, float v) { sum[0] = fma((double)v, (double)v, sum[0]); });
 }
 
 __global__ __launch_bounds__(kThreads) void k_grad_norm(ClipTable tab) {
@@ -142,13 +148,14 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm_join(ClipTable tab, floa
 // ---------------------------------------------------------------------------
 template <typename T, typename O>
 __device__ __forceinline__ void scale_chunk(gptr<const T> p, gptr<O> out, int64_t e0, int64_t e1, float c) {
-  chunk<true>(p, e0, e1,
-        [&](int64_t at, float (&v)[8]) {
+  out += e0;
+  chunk<true>(p + e0, (int)(e1 - e0),
+        [&](int at, auto& v) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= c;
+          for (int e = 0; e < 16 / (int)sizeof(T); ++e) v[e] *= c;
           store_unit(out + at, v);
         },
-        [&](int64_t at, float v) { store_element(out + at, v * c); });
+        [&](int at, float v) { store_element(out + at, v * c); });
 }
 
 __global__ __launch_bounds__(kThreads) void k_grad_clip(ClipTable tab, ClipScalars s) {

@@ -148,6 +148,11 @@ __device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[8]) {
   __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
   __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, (gptr<f32x4_any>)p + 1);
 }
+__device__ __forceinline__ void store_unit(gptr<uint16_t> p, const float (&v)[4]) {
+  typedef uint16_t quad __attribute__((ext_vector_type(4)));
+  typedef quad quad_any __attribute__((aligned(2)));
+  __builtin_nontemporal_store(quad{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])}, (gptr<quad_any>)p);
+}
 __device__ __forceinline__ void store_unit(gptr<float> p, const float (&v)[4]) {
   __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (gptr<f32x4_any>)p);
 }
