@@ -338,6 +338,37 @@ def test_strides_and_alignment(V, pad, shift, dtype):
     assert torch.isnan(buf).all()
 
 
+@TYPES
+@pytest.mark.parametrize("V", [4099, 65543])
+def test_beyond_the_caches(V, dtype):
+    """More than 256 MiB of logits, rows of every alignment."""
+    T = (257 << 20) // (V * dtype.itemsize) + 8
+    z, y, g, h = inputs(T, V, dtype, 60, ignored=0.1)
+    z[5, 3:] = -math.inf
+    z[6] = -math.inf
+    for top in (0, 20, 64, 65):
+        check(z, y, top=top, what=f"{T}x{V} top {top}")
+    check_grad(z, y, g, h, what=f"{T}x{V}")
+
+
+@TYPES
+@pytest.mark.parametrize("V,ld", [(3, 8), (4, 8), (7, 16), (8, 8), (9, 16), (2049, 2056), (8193, 8200), (10007, 10008), (16390, 16392), (16390, 16400)])
+def test_gradient_of_aligned_rows(V, ld, dtype):
+    """Rows that start on 16 bytes and do not end there, also in place; what lies between stays."""
+    z, y, g, h = inputs(37, V, dtype, 61 + V, ignored=0.2)
+    want = check_grad(z, y, g, h, 0.9)
+    buf = torch.full((37, ld), 7.0, device="cuda", dtype=dtype)
+    rows = buf[:, :V]
+    rows.copy_(z)
+    check(rows, y, 0.9, top=2)
+    first = mm().token_logprobs(z, y, scale=0.9)
+    assert mm().token_logprobs_backward(rows, y, first.lse, first.entropy, g, h, scale=0.9, out=rows) is rows
+    assert torch.equal(rows, want)
+    assert (buf[:, V:] == 7.0).all()
+    rows.copy_(z)
+    assert torch.equal(mm().token_logprobs_backward(rows, y, first.lse, first.entropy, g, h, scale=0.9), want)
+
+
 def test_offsets_past_32_bits():
     """Rows more than 2^31 elements apart."""
     V, ld = 1000, 2 ** 30 + 24
