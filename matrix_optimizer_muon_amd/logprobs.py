@@ -31,10 +31,10 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[object] = None
 
 
-def _three(shape, device):
+def _three(shape, like):
     """Three fp32 results of one allocation."""
     import torch
-    return torch.empty((3, *shape), dtype=torch.float32, device=device).unbind(0)
+    return like.new_empty((3, *shape), dtype=torch.float32).unbind(0)
 
 
 # Calls of few rows take about as long as their arguments' checks: what is plainly right is
@@ -80,16 +80,16 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100,
     prob = _rows_problem(logits, targets, scale, top, ignore_index)
     need = ctypes.c_size_t(0)
     _b.check(_b.lib().dmuon_logprobs_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
-    shape, dev = logits.shape[:-1], logits.device
+    shape = logits.shape[:-1]
     with _on(stream, logits, targets) as on:
-        logprobs, entropy, lse = _three(shape, dev)
+        logprobs, entropy, lse = _three(shape, logits)
         if targets is None:
             logprobs = None
         ids = best = None
         if top:
-            ids = torch.empty((*shape, top), dtype=torch.int64, device=dev)
-            best = torch.empty((*shape, top), dtype=torch.float32, device=dev)
-        ws = _ws_args(on.workspace(workspace, need.value, dev)) if need.value else (None, 0)
+            ids = logits.new_empty((*shape, top), dtype=torch.int64)
+            best = logits.new_empty((*shape, top), dtype=torch.float32)
+        ws = _ws_args(on.workspace(workspace, need.value, logits.device)) if need.value else (None, 0)
         _b.check(_b.lib().dmuon_logprobs(ctypes.byref(prob), _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(ids), _ptr(best),
                                          *ws, on.handle))
     return TokenLogprobs(logprobs, entropy, lse, ids, best)
@@ -116,7 +116,6 @@ def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_e
     of the logits' shape and type, or writes ``out``, which may have strided rows and may be
     ``logits`` itself.
     """
-    import torch
     prob = _rows_problem(logits, targets, scale, 0, ignore_index)
     _check_row_grads(logits.shape[:-1], lse, entropy, grad_logprobs, grad_entropy)
     if grad_logprobs is not None and targets is None:
@@ -128,7 +127,7 @@ def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_e
             raise ValueError("out must have the logits' shape and type")
     with _on(stream, logits, targets, lse, entropy, grad_logprobs, grad_entropy, out) as on:
         if out is None:
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+            out = logits.new_empty(logits.shape)
         _b.check(_b.lib().dmuon_logprobs_backward(ctypes.byref(prob), _ptr(lse), _ptr(entropy), _ptr(grad_logprobs),
                                                   _ptr(grad_entropy), _ptr(out), ld, on.handle))
     return out
@@ -150,7 +149,7 @@ def linear_token_logprobs(h, w, targets, *, scale=1.0, ignore_index=-100, worksp
     _no_graph("linear_token_logprobs", h=h, w=w)
     prob = _ce_problem(h, w, targets, ignore_index)
     with _on(stream, h, w, targets) as on:
-        logprobs, entropy, lse = _three(targets.shape, h.device)
+        logprobs, entropy, lse = _three(targets.shape, h)
         ws = _linear_workspace(prob, 0, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_logprobs(ctypes.byref(prob), float(scale), _ptr(logprobs), _ptr(entropy), _ptr(lse),
                                                 *_ws_args(ws), on.handle))
@@ -165,7 +164,6 @@ def linear_token_logprobs_backward(h, w, targets, lse, entropy, grad_logprobs, g
     lse, entropy, grad_logprobs and grad_entropy as in ``token_logprobs_backward``; grad_h,
     grad_w, ``need_h`` and ``need_w`` as in ``linear_cross_entropy_backward``.
     """
-    import torch
     prob = _ce_problem(h, w, targets, ignore_index)
     _check_row_grads(targets.shape, lse, entropy, grad_logprobs, grad_entropy)
     for t, what, like, need in ((grad_h, "grad_h", h, need_h), (grad_w, "grad_w", w, need_w)):
@@ -175,9 +173,9 @@ def linear_token_logprobs_backward(h, w, targets, lse, entropy, grad_logprobs, g
             _dense(t, what, like.dtype, like.shape)
     with _on(stream, h, w, targets, lse, entropy, grad_logprobs, grad_entropy, grad_h, grad_w) as on:
         if need_h and grad_h is None:
-            grad_h = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+            grad_h = h.new_empty(h.shape)
         if need_w and grad_w is None:
-            grad_w = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+            grad_w = w.new_empty(w.shape)
         ws = _linear_workspace(prob, 1, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_logprobs_backward(ctypes.byref(prob), float(scale), _ptr(lse), _ptr(entropy),
                                                          _ptr(grad_logprobs), _ptr(grad_entropy), _ptr(grad_h), _ptr(grad_w),

@@ -31,7 +31,7 @@ CKPT_BLOCK = 32          # columns that share one exponent byte
 
 
 def _ptr(t):
-    return ctypes.c_void_p(None if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _no_graph(call, **tensors):
@@ -159,7 +159,7 @@ def _on(stream, *tensors):
 
 
 def _ws_args(ws):
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _ce_problem(h, w, targets, ignore_index):
