@@ -28,11 +28,11 @@ struct RowsPlan {
 RowsPlan rows_plan(const dmuon_logprobs_problem& p, char* base) {
   RowsPlan pl{};
   pl.wave = p.top ? p.vocab <= kWaveTop || (p.vocab <= kWaveTopMost && p.tokens >= kWaveTopRows)
-                  : p.vocab <= wave_row(p.dtype == DMUON_F32);
+                  : p.vocab <= wave_row(p.dtype == DMUON_F32, p.tokens);
   pl.piece = p.vocab;
   pl.pieces = 1;
   if (pl.wave) return pl;
-  int64_t n = p.tokens >= 1024 ? 1 : std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
+  int64_t n = p.tokens >= kRowsEnough ? 1 : std::min<int64_t>({cdiv(2048, p.tokens), cdiv(p.vocab, kPieceLeast), kPiecesMost, p.top ? kMaxKeys / p.top : kPiecesMost});
   n = std::max<int64_t>(n, p.vocab <= kPieceMost ? 1 : cdiv(p.vocab, kPieceMost - 16));
   pl.piece = round_up(cdiv(p.vocab, n), 8);
   pl.pieces = cdiv(p.vocab, pl.piece);

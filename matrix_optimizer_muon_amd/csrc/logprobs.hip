@@ -452,9 +452,9 @@ __device__ __forceinline__ void no_alternatives(const LogprobsArgs& a, int64_t r
 
 // ---------------------------------------------------------------------------
 // a wave per row, without alternatives: no barrier, and four times the rows in flight.
-// Against a workgroup per row, bf16: 8192 × 5000 23 and 32 µs, × 10007 38 and 53, 300 × 8192
-// 7.1 and 9.5, 8192 × 16384 61 and 56; fp32: 300 × 8192 7.4 and 9.4, 8192 × 8192 54 and 54,
-// × 16384 112 and 109.
+// Against a workgroup per row (300 rows: several), bf16: 8192 × 5000 21 and 28 µs, × 12288 39
+// and 41, × 16384 52 and 51, 1500 × 12300 15.1 and 12.5, 300 × 8192 7.0 and 9.4; fp32: 8192 ×
+// 3000 21 and 25, × 5000 32 and 30, × 8192 49 and 46, 300 × 8192 7.5 and 9.3.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void short_row(gptr<const T> p, int len, Unit<T, 8>& x) {         // fewer than 8 elements

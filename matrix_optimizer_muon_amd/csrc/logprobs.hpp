@@ -14,10 +14,12 @@ constexpr int kGroupUnits = 8;           // units of 8 elements that a thread ta
 constexpr int kGroups = 8;               // such groups per thread at most
 constexpr int kPieceMost = kThreads * kGroupUnits * 8 * kGroups;     // 131072 columns per workgroup
 constexpr int kPieceLeast = kThreads * 8;                            // 2048
+constexpr int kRowsEnough = 1024;        // rows from which on none is cut into pieces to fill the card
 constexpr int kPiecesMost = 64;          // pieces of one row (a wave joins them)
-// Rows that take one wave each: without alternatives up to 12288 words (fp32 8192), with
-// them up to 4096, or 12288 where there are rows enough.
-inline int64_t wave_row(bool f32) { return f32 ? 8192 : 12288; }
+// Rows that take one wave each: without alternatives up to 12288 words (fp32 4096, or 8192
+// where the rows are so few that workgroups would share them), with them up to 4096, or
+// 12288 where there are rows enough.
+inline int64_t wave_row(bool f32, int64_t rows) { return !f32 ? 12288 : rows < kRowsEnough ? 8192 : 4096; }
 constexpr int kWaveTop = 64 * 8 * 8;                 // 4096: the units' maxima of a row in 8 registers
 constexpr int kWaveTopMost = 3 * kWaveTop;           // 12288: in 24
 constexpr int kWaveTopRows = 512;

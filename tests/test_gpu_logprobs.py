@@ -164,7 +164,8 @@ def test_sizes(T, V, dtype):
 # where the kernels change: a unit, a wave's row with and without alternatives, a
 # workgroup's row, and rows enough for waves over longer ones
 BORDERS = [(3, 8), (3, 9), (5, 15), (5, 16), (5, 17), (4, 511), (4, 512), (4, 513), (4, 1025), (4, 2056), (3, 4095), (3, 4103), (2, 8192), (2, 8193),
-           (2, 12288), (2, 12289), (600, 4100), (512, 12288), (511, 12288), (513, 12289), (1024, 20000), (1023, 20000), (1, 131073), (17, 40007)]
+           (2, 12288), (2, 12289), (600, 4100), (512, 12288), (511, 12288), (513, 12289), (1024, 20000), (1023, 20000), (1, 131073), (17, 40007),
+           (1024, 4097), (1024, 8191), (1023, 8193)]
 
 
 @TYPES
