@@ -73,8 +73,9 @@ class ClipGradNorm:
     gradients go (bf16 or fp32 of the same shapes, for instance views of a packed reduce
     buffer), None: in place.  Every call enqueues the norm and the clipping on ``stream``
     and returns ``norm``, a 0-dim fp32 tensor that the next call overwrites.  The tensors
-    must keep their storage; ``max_norm`` may be changed between calls.  A captured graph
-    holds this object's workspace: do not let a replay and another call overlap.
+    must keep their storage; ``max_norm`` may be changed between calls.  Calls on
+    different streams and replays of a captured graph share this object's workspace and must
+    not overlap.
     """
 
     def __init__(self, grads, max_norm, *, outs=None, eps=1e-6, workspace=None, stream=None):
