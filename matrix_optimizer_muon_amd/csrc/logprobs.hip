@@ -296,7 +296,7 @@ __device__ __forceinline__ int select_top(S& sh, const Piece<T>& row, int tid, i
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (in >> e & 1) {
-          if (at < need) sh.list[S::kStrict + at] = key_of(tau, first + at0 + e);
+          if (at < need) sh.list[S::kStrict + at] = key_of(rankable(tau), first + at0 + e);
           ++at;
         }
       have += all;
@@ -576,10 +576,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
           open(x, i * 64 + lane, v);
 #pragma unroll
           for (int q = 0; q < 8 / N; ++q) {
-            float most = rankable(v[q * N]);
+            float most = v[q * N];
 #pragma unroll
             for (int e = 1; e < N; ++e) most = fmaxf(most, v[q * N + e]);
-            key[i * (8 / N) + q] = most;
+            key[i * (8 / N) + q] = rankable(most);
           }
         }
       };
