@@ -44,10 +44,14 @@ struct Piece {
 // reference M = m·c2 rounded once, a logit's exponent is t = z·c2 − M in one fused
 // multiply-add, and
 //   s = Σ 2^t,   u = Σ t·2^t.
-// M's rounding r = m·c2 − M is a factor 2^r of every term, so it cancels between them:
-// the entropy is ln s − ln 2·u/s, and log Σ e^(scale·(z − m)) = ln s − r·ln 2.  When m
-// grows, every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes
-// 2^e·s.  Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts
+// M's rounding r = m·c2 − M is a factor 2^r of every term.  With R = 2^r, computed as the
+// largest logit's own term is,
+//   S = Σ e^(scale·(z − m)) = s/R,   entropy = ln S − ln 2·(u − r·s)/s.
+// s holds R at least once, so S ≥ 1, and S = 1 where nothing else is left: no log
+// probability is above 0 and no entropy below, and both keep their digits for a word that is
+// nearly certain (ln S as ln s − r·ln 2 was off by 6·10⁻⁸ of either sign).  When m grows,
+// every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes 2^e·s.
+// Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts
 // at the lowest finite value, so that no difference is −∞ − −∞; a logit of −∞ has 2^t = 0
 // and its t is kept finite for the product.  A NaN reaches s.
 // Bound by the instructions: 16 elements are taken together, 6.6 instructions each beside
@@ -126,10 +130,12 @@ struct Row {
   float m, log_s, lse, entropy, scale;
   __device__ __forceinline__ Row(const Running& r, float c, float c2) : m(r.m), scale(c) {
     const bool none = r.s == 0.f;
-    const float ln = none ? 0.f : logf(r.s);
-    log_s = none ? 0.f : fmaf(-Running::rest(r.m, r.M, c2), kLn2, ln);
+    const float rest = Running::rest(r.m, r.M, c2);
+    log_s = none ? 0.f : logf(r.s / __builtin_amdgcn_exp2f(rest));
+    float below = fmaf(-rest, r.s, r.u);                 // Σ (t − r)·2^t: no term is positive
+    below = below > 0.f ? 0.f : below;                   // a NaN stays
     lse = none ? -INFINITY : fmaf(r.m, c, log_s);
-    entropy = none ? 0.f : ln - r.u * kLn2 / r.s;
+    entropy = none ? 0.f : log_s - below * kLn2 / r.s;
   }
   // (z − m)·c − log s: neither term is positive, and the logarithm keeps its digits
   // beside a large m
