@@ -4,7 +4,8 @@
     clip_grad_norm(grads, max_norm, outs=None)      # in place, or into outs; returns the norm
     clip = ClipGradNorm(grads, max_norm)            # prepared: clip() each step
 
-Nothing waits for the GPU: the norm stays on the device.
+No call waits for the GPU: the norm stays on the device.  (The constructor of
+``ClipGradNorm`` waits for its tables once.)
 """
 from __future__ import annotations
 
@@ -71,11 +72,13 @@ class ClipGradNorm:
 
     grads: bf16 or fp32 GPU tensors of any shape, contiguous; outs: where the clipped
     gradients go (bf16 or fp32 of the same shapes, for instance views of a packed reduce
-    buffer), None: in place.  Every call enqueues the norm and the clipping on ``stream``
-    and returns ``norm``, a 0-dim fp32 tensor that the next call overwrites.  The tensors
-    must keep their storage; ``max_norm`` may be changed between calls.  Calls on
-    different streams and replays of a captured graph share this object's workspace and must
-    not overlap.
+    buffer), None: in place.  The constructor writes the tables of these tensors into the
+    workspace and waits for that; it cannot be captured, the calls can.  Every call enqueues
+    the norm and the clipping on ``stream`` and returns ``norm``, a 0-dim fp32 tensor that the
+    next call overwrites.  The tensors must keep their storage; it is not handed out again
+    before the queued calls are done, but what a captured graph uses the caller keeps alive.
+    ``max_norm`` may be changed between calls.  Calls on different streams and replays of a
+    captured graph share this object's workspace and must not overlap.
     """
 
     def __init__(self, grads, max_norm, *, outs=None, eps=1e-6, workspace=None, stream=None):
@@ -99,9 +102,10 @@ class ClipGradNorm:
             return self.norm
         with _on(stream, self.norm, self.workspace) as on:
             if on.handle.value not in self._seen and not torch.cuda.is_current_stream_capturing():
+                # all that the queued kernels use outlives this object, on every stream it is called on
                 st = _b.resolve_stream(None)
-                _b.keep_until_done(self.workspace, [st])
-                _b.keep_until_done(self.norm, [st])
+                for t in (self.workspace, self.norm, *self._tensors[0], *self._tensors[1]):
+                    _b.keep_until_done(t, [st])
                 self._seen.add(on.handle.value)
             _b.check(_b.lib().dmuon_grad_clip_run(self._arr, self._n, self.max_norm, self.eps, 1, _ptr(self.norm),
                                                   *_ws_args(self.workspace), on.handle))
