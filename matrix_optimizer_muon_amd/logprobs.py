@@ -23,7 +23,7 @@ __all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_backward", "linear
 class TokenLogprobs(NamedTuple):
     """Per token: ``logprobs`` of its target, ``entropy`` and ``lse`` of its scaled logits
     (fp32), and with alternatives ``top_ids`` (int64) and ``top_logprobs`` (fp32) [..., top].
-    What was not asked for is None."""
+    What was not asked for is None.  Each is a tensor of its own."""
     logprobs: Optional[object]
     entropy: object
     lse: object
@@ -31,10 +31,12 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[object] = None
 
 
-def _three(shape, like):
-    """Three fp32 results of one allocation."""
+def _results(shape, like):
+    """Three fp32 results.  Each is an allocation of its own: views of one could not be changed
+    in place once a Function returned them, and would share a version with what it saved."""
     import torch
-    return like.new_empty((3, *shape), dtype=torch.float32).unbind(0)
+    first = like.new_empty(shape, dtype=torch.float32)
+    return first, torch.empty_like(first), torch.empty_like(first)
 
 
 # Calls of few rows take about as long as their arguments' checks: what is plainly right is
@@ -82,13 +84,13 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, ignore_index=-100,
     _b.check(_b.lib().dmuon_logprobs_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
     shape = logits.shape[:-1]
     with _on(stream, logits, targets) as on:
-        logprobs, entropy, lse = _three(shape, logits)
+        logprobs, entropy, lse = _results(shape, logits)
         if targets is None:
             logprobs = None
         ids = best = None
         if top:
             ids = logits.new_empty((*shape, top), dtype=torch.int64)
-            best = logits.new_empty((*shape, top), dtype=torch.float32)
+            best = torch.empty_like(ids, dtype=torch.float32)
         ws = _ws_args(on.workspace(workspace, need.value, logits.device)) if need.value else (None, 0)
         _b.check(_b.lib().dmuon_logprobs(ctypes.byref(prob), _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(ids), _ptr(best),
                                          *ws, on.handle))
@@ -149,7 +151,7 @@ def linear_token_logprobs(h, w, targets, *, scale=1.0, ignore_index=-100, worksp
     _no_graph("linear_token_logprobs", h=h, w=w)
     prob = _ce_problem(h, w, targets, ignore_index)
     with _on(stream, h, w, targets) as on:
-        logprobs, entropy, lse = _three(targets.shape, h)
+        logprobs, entropy, lse = _results(targets.shape, h)
         ws = _linear_workspace(prob, 0, workspace, on, h.device)
         _b.check(_b.lib().dmuon_linear_logprobs(ctypes.byref(prob), float(scale), _ptr(logprobs), _ptr(entropy), _ptr(lse),
                                                 *_ws_args(ws), on.handle))
