@@ -138,8 +138,9 @@ __global__ __launch_bounds__(kScanThreads) void k_ce_scan(CeScanArgs a) {
     uint64_t in[kScanRows];
 #pragma unroll
     for (int k = 0; k < kScanRows; ++k) {
-      const bool some = ENT ? !(g[k] == 0.f && ge[ENT ? k : 0] == 0.f) && !(l[k] == -INFINITY) : !(g[k] == 0.f);
-      const bool part = y[k] != a.ignore && (!a.backward || ((in_vocab(y[k], a.vocab) || y[k] == kElsewhere) && some));
+      // (the loss's own test stands in the condition: before it, its scan takes 0.6 µs more)
+      const bool some = ENT && !(g[k] == 0.f && ge[ENT ? k : 0] == 0.f) && !(l[k] == -INFINITY);
+      const bool part = y[k] != a.ignore && (!a.backward || ((in_vocab(y[k], a.vocab) || y[k] == kElsewhere) && (ENT ? some : !(g[k] == 0.f))));
       in[k] = __ballot(part);
       if (part && fabsf(g[k]) < INFINITY) gm = fmaxf(gm, fabsf(g[k]));
       if constexpr (ENT)
@@ -728,8 +729,8 @@ __device__ __forceinline__ int live_block(int G) {
 //   backward: dZ(t, v) = scale·(g_t·([v = target] − p) − e_t·p·(l + entropy_t)), l = x − lse_t,
 //             p = exp l, l kept from −200 on (p is 0 there) so that 0·−∞ does not arise.
 // A compile-time choice: the loss's own kernels carry none of it.  It costs 0 to 4% of a
-// tile: 4096 tokens × 4096, vocabulary 32000, forward 955 µs under the profiler where the
-// loss took 977 on another card; 2400 rows × 2048, 25000 words a piece, backward 264 and 256.
+// tile, in turn with the loss on one card: 4096 tokens × 4096, vocabulary 32000, forward 881
+// and 868 µs; 2400 rows × 2048, 25000 words a piece, backward 254 and 245; fp32 101 and 101.
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kFar = -1e30f;               // a difference whose exponential is 0
 // (m, s) joined with another pair; a NaN in s stays
@@ -948,6 +949,7 @@ __global__ __launch_bounds__(S::Threads) void k_ce_logits(CeLogitsArgs g) {
 // ---------------------------------------------------------------------------
 // The scan and the packing of so few tokens, in one launch: every wave finds the
 // tokens' places by itself with one ballot.
+template <bool ENT>
 __global__ __launch_bounds__(kThreads) void k_ce_few_start(CeScanArgs a, PackArgs p) {
   __shared__ int place[kThreads / 64][kFewTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -964,7 +966,7 @@ __global__ __launch_bounds__(kThreads) void k_ce_few_start(CeScanArgs a, PackArg
     } else if (here) {
       a.losses[lane] = 0.f;
       a.lse[lane] = 0.f;
-      if (a.entropy) a.entropy[lane] = 0.f;
+      if constexpr (ENT) a.entropy[lane] = 0.f;
     }
     if (lane == 0) *a.count = count;
   }
@@ -2071,7 +2073,9 @@ int launch_ce_logits(const CeLogitsArgs& a, int backward, int f32, void* stream)
   return a.with_entropy ? ce_logits_of<Small, true>(a, backward, f32, stream) : ce_logits_of<Small, false>(a, backward, f32, stream);
 }
 int launch_ce_few_start(const CeScanArgs& a, const PackArgs& p, void* stream) {
-  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_few_start, (unsigned)cdiv(cdiv(a.tokens, 8) * (p.ldd / 64), kThreads / 64), kThreads, 0, a, p);
+  const unsigned grid = (unsigned)cdiv(cdiv(a.tokens, 8) * (p.ldd / 64), kThreads / 64);
+  if (a.entropy) DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_few_start<true>, grid, kThreads, 0, a, p);
+  DMUON_LAUNCH(PH_CE_PACK, stream, k_ce_few_start<false>, grid, kThreads, 0, a, p);
 }
 template <bool ENT>
 static int ce_few(const CeFewArgs& a, int f32, void* stream) {

@@ -57,18 +57,19 @@ struct CeScanArgs {
   const float* lse_in;         // backward
   float* losses;               // forward: zeroed where ignored
   float* lse;
-  float* entropy;              // the same, or null
-  const float* grad_entropy;   // backward of the log probabilities: or null
-  const float* entropy_in;     // with grad_entropy
   int32_t* rows;               // token of compact row i
   int32_t* pos;                // compact row of token t, or −1
   int32_t* tgt;                // target of compact row i, kTgtElsewhere or kTgtNone
   float* clse;                 // backward: lse of compact row i
   float* cg;                   // backward: gradient weight of compact row i
-  float* ce;                   // ... of its entropy
-  float* cent;                 // its entropy
   int32_t* count;              // number of compact rows
   float* gmax;                 // backward: largest |weight|
+  // log probabilities with entropies (behind the loss's arguments, whose loads stay as they were)
+  float* entropy;              // forward: zeroed where ignored
+  const float* grad_entropy;   // backward: or null
+  const float* entropy_in;     // with grad_entropy
+  float* ce;                   // backward: gradient weight of compact row i's entropy
+  float* cent;                 // its entropy
 };
 
 struct CeStat {
@@ -96,12 +97,6 @@ struct CeLogitsArgs {
   // forward
   CeStat* stats;               // [vocabulary tile][tokens]
   float* zt;                   // target's logit
-  // log probabilities with entropies: the logits' scale and these statistics instead
-  int32_t with_entropy;
-  float scale;
-  CeStatU* stats_u;
-  const float* ce;             // backward: weights of the entropies, and the entropies
-  const float* cent;
   // backward
   const float* clse;
   const float* cg;
@@ -109,6 +104,12 @@ struct CeLogitsArgs {
   uint16_t* dz;                // [plane][tokens][ldz]
   int64_t dz_plane;
   int32_t ldz;
+  // log probabilities with entropies: the logits' scale and these statistics instead (last, as above)
+  int32_t with_entropy;
+  float scale;
+  CeStatU* stats_u;
+  const float* ce;             // backward: weights of the entropies, and the entropies
+  const float* cent;
 };
 
 // losses of few tokens: W in place, hidden states in fragment order
