@@ -511,7 +511,9 @@ int dmuon_logprobs(const dmuon_logprobs_problem* problem, float* logprobs, float
 /* With g, e the gradients of logprob and entropy (device fp32 [tokens], either may be
  * NULL; a row where both are 0 has none) and l = x − lse:
  *   grad_logits(t, v) = scale·(g(t)·([v = target(t)] − p) − e(t)·p·(l + entropy(t)))
- * lse, entropy: as dmuon_logprobs wrote them (entropy is read with grad_entropy only).
+ * lse, entropy: as dmuon_logprobs wrote them (entropy is read with grad_entropy only).  lse
+ * being fp32, p = exp l is off by 2^-24·|lse| of itself; from |lse| = 2^16 on, where that is
+ * more than bf16's own rounding, it is held to at most 1.
  * grad_logits: device [tokens, vocab], row stride ld_grad, of the logits' dtype; it may
  * be the logits themselves, with their stride. */
 int dmuon_logprobs_backward(const dmuon_logprobs_problem* problem, const float* lse, const float* entropy,

@@ -82,6 +82,15 @@ __device__ __forceinline__ int64_t load_index(const void* p, int idx64, int64_t 
   return (int64_t)(((uint64_t)(uint32_t)(idx64 ? hi : lo >> 31) << 32) | (uint32_t)lo);
 }
 
+// l = x − lse as the gradients of log probabilities take it: from −200 on, where e^l is 0 in
+// fp32, so that 0·−∞ does not arise.  lse is rounded to fp32, and the largest x of a row may come
+// out above it by half a step.  From |lse| = 2^16 on, where that is more than a rounding to
+// bf16, l is at most 0: e^l stays at most 1 for any finite logits (x = −1.25·10⁹ throughout,
+// a row masked out: l up to 64 else).  A NaN stays.
+__device__ __forceinline__ float log_p_of(float x_less_lse, float lse) {
+  return x_less_lse == x_less_lse ? __builtin_amdgcn_fmed3f(x_less_lse, -200.f, fabsf(lse) < 0x1p16f ? 1.f : 0.f) : x_less_lse;
+}
+
 // ---------------------------------------------------------------------------
 // units: 8 consecutive elements (or one) as they were loaded, from any element on, so that
 // rows of every alignment move 16 bytes at a time: the types are aligned to one element only.
