@@ -77,7 +77,8 @@ class ClipGradNorm:
     the norm and the clipping on ``stream`` and returns ``norm``, a 0-dim fp32 tensor that the
     next call overwrites.  The tensors must keep their storage; it is not handed out again
     before the queued calls are done, but what a captured graph uses the caller keeps alive.
-    ``max_norm`` may be changed between calls.  Calls on different streams and replays of a
+    ``max_norm`` may be changed between calls.  Where the norm is not finite the gradients
+    pass unscaled, so that the caller can skip the step.  Calls on different streams and replays of a
     captured graph share this object's workspace and must not overlap.
     """
 

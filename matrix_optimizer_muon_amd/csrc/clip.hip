@@ -13,7 +13,7 @@ namespace dmuon {
 // ---------------------------------------------------------------------------
 // the list of tensors, in chunks of 8192 elements: workgroup b takes the chunks b,
 // b + groups, …, so that all of them work in one moving window of memory (contiguous ranges
-// per workgroup, 2048 places at once: 5 × 214 Mi bf16 clipped 1176 µs, so 1140), and looks a
+// per workgroup, 2048 places at once: 1122 M bf16 elements clipped 1176 µs, so 1140), and looks a
 // chunk's tensor up with a search of 64 probes a step when the last one is passed.
 // f(problem, first element, end).
 // ---------------------------------------------------------------------------
@@ -52,7 +52,7 @@ __device__ __forceinline__ bool walk(const ClipTable& tab, F f) {
 
 // ---------------------------------------------------------------------------
 // sums of squares in 64 bits: a square of an fp32 value is exact there, nothing overflows or
-// vanishes, and the order is fixed.  Memory bound: 5 × 214 Mi bf16 in 350 µs, 6.4 TB/s.
+// vanishes, and the order is fixed.  Memory bound: 1045 M bf16 elements in 351 µs, 5.95 TB/s.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ double sum_workgroup(double v, double* shared) {
 #pragma unroll
@@ -145,9 +145,10 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm_join(ClipTable tab, floa
 // is a fraction and a power of 2 that follows the product, so that gradients near fp32's end
 // keep their digits (an instruction per element; no time, it passes behind the loads).  Every
 // workgroup joins the partial sums for itself (16 KiB from the caches) instead of waiting for
-// another launch.  In place
-// nothing is written where c is 1.  Memory bound: what exceeds the caches is read twice
-// (5 × 214 Mi bf16: 705 µs, 6.4 TB/s; with the norm 1054 µs; 65 × 4096: 3.6 + 4.3 µs).
+// another launch.  In place nothing is written where c is 1.  Memory bound: what exceeds the
+// caches is read twice (1045 M bf16 elements: 706 µs, 5.9 TB/s; with the norm 1057 to 1064;
+// 65 × 4096: 3.6 + 4.3 µs).  Into fp32 bf16 gradients take 1914, 4.4 TB/s: a thread's two
+// stores of 16 bytes lie next to each other, so that each of a wave's is half of every line.
 // ---------------------------------------------------------------------------
 struct Factor {
   float c;

@@ -9,7 +9,7 @@
 
 namespace dmuon {
 
-constexpr int kClipChunk = kThreads * 32;    // elements per chunk: 4 units of 8 per thread
+constexpr int kClipChunk = kThreads * 32;    // elements per chunk: 32 per thread, in units of 16 bytes
 constexpr int kClipGroups = 2048;            // workgroups at most: 8 for every CU
 
 // One tensor as the kernels see it.

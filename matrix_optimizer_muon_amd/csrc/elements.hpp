@@ -92,7 +92,7 @@ __device__ __forceinline__ float log_p_of(float x_less_lse, float lse) {
 }
 
 // ---------------------------------------------------------------------------
-// units: 8 consecutive elements (or one) as they were loaded, from any element on, so that
+// units: 8 consecutive elements (fp32: or 4) as they were loaded, from any element on, so that
 // rows of every alignment move 16 bytes at a time: the types are aligned to one element only.
 // ---------------------------------------------------------------------------
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));

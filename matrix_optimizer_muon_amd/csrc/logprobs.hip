@@ -53,7 +53,9 @@ struct Piece {
 // every t moves by e = (m − m')·c2 + r' − r: u becomes 2^e·(u + e·s), s becomes 2^e·s.
 // Beyond |M| = 2^24, where r could pass 1/2, t is (z − m)·c2 and r is 0.  m starts
 // at the lowest finite value, so that no difference is −∞ − −∞; a logit of −∞ has 2^t = 0
-// and its t is kept finite for the product.  A NaN reaches s.
+// and its t is kept finite for the product.  A NaN reaches s.  A lane that has seen nothing but
+// −∞ counts as beyond 2^24, and its wave takes that slower form meanwhile: 8192 × 32000 bf16 with
+// 99% of the words masked out 101 µs, with none 89 (fp32 171 and 165).
 // Bound by the instructions: 16 elements are taken together, 6.6 instructions each beside
 // the maximum's bookkeeping (unpack, maximum, t, 2^t, clamp, two sums).
 // ---------------------------------------------------------------------------
@@ -89,7 +91,7 @@ struct Running {
     if (most > m) grow(most, c2);
     if (__any(big(M))) {
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {                      // rare: kept short
+      for (int h = 0; h < 2; ++h) {                      // kept short
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
           const float z = h ? v[N / 2 + e] : v[e];
@@ -656,8 +658,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_wave_top(LogprobsArgs a) 
 // registers, a unit per thread; of longer ones (kLong) the maxima of every 4 units of a
 // thread stay in LDS, and only those that reach tau are read again: with 64 alternatives
 // 2001 × 50257 bf16 takes 55 µs without and 62 with one maximum per 8 units, 47 without
-// alternatives.  Without them 8192 × 128000 bf16 takes 312 µs (6.7 TB/s), where the
-// instructions of a unit still pass behind its load.
+// alternatives.  Without them 8192 × 128000 bf16 takes 312 µs (6.7 TB/s) at 2.1 GHz and more,
+// where the instructions of a unit still pass behind its load; 378 at the 1.66 GHz that the
+// card falls to for some milliseconds when such calls follow each other.
 // ---------------------------------------------------------------------------
 enum : int { kNoTop, kLong, kShort };
 struct GroupTop : TopShared<512, 256> {

@@ -18,10 +18,16 @@ constexpr int kRowsEnough = 1024;        // rows from which on none is cut into 
 constexpr int kPiecesMost = 64;          // pieces of one row (a wave joins them)
 // Rows that take one wave each: without alternatives up to 12288 words (fp32 4096, or 8192
 // where the rows are so few that workgroups would share them), with them up to 4096, or
-// 12288 where there are rows enough.
+// 12288 where there are rows enough.  fp32, by a wave and by workgroups: 50 × 5000 5.4 and
+// 6.8 µs, 300 × 8192 7.6 and 9.5, 1000 × 8192 9.0 and 14.2; from 1024 rows on 1024 × 4200 7.5
+// and 7.1, 2048 × 8192 14.4 and 14.2, 4096 × 6500 25.2 and 24.1.
 inline int64_t wave_row(bool f32, int64_t rows) { return !f32 ? 12288 : rows < kRowsEnough ? 8192 : 4096; }
 constexpr int kWaveTop = 64 * 8 * 8;                 // 4096: the units' maxima of a row in 8 registers
 constexpr int kWaveTopMost = 3 * kWaveTop;           // 12288: in 24
+// With 20 alternatives by a wave and by workgroups, bf16 (fp32): 256 × 12288 15.2 and 13.9 µs
+// (17.3 and 16.8), 512 × 12288 16.6 and 17.1 (18.0 and 19.1), 800 × 8192 13.7 and 19.4 (15.7 and
+// 21.8), 4096 × 8192 25.2 and 28.5 (34.9 and 36.7).  From 1024 rows on a workgroup has a row to
+// itself, and is ahead while all rows are in flight: 1024 × 8192 14.8 and 12.0 (16.4 and 14.9).
 constexpr int kWaveTopRows = 512;
 constexpr int kGradUnits = 4;            // times 8 elements per thread of the gradient
 constexpr int kGradWave = 64 * kGradUnits * 8;       // 2048: rows up to this take one wave each

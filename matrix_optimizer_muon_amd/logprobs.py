@@ -114,7 +114,8 @@ def token_logprobs_backward(logits, targets, lse, entropy, grad_logprobs, grad_e
 
     lse, entropy: as ``token_logprobs`` returned them (of a vocabulary in shards: the
     joined ones); grad_logprobs, grad_entropy: fp32 of the same shape, the gradients of
-    each token's log probability and entropy (either may be None).  Returns a dense tensor
+    each token's log probability and entropy (either may be None); contiguous, which the
+    expanded ones that ``sum()`` hands to a Function's backward are not.  Returns a dense tensor
     of the logits' shape and type, or writes ``out``, which may have strided rows and may be
     ``logits`` itself.
     """

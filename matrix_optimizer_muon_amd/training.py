@@ -216,7 +216,8 @@ def linear_cross_entropy_backward(h, w, targets, lse, grad_losses, *, ignore_ind
     lse: as ``linear_cross_entropy`` returned it (of a vocabulary in shards: the
     joined one, with each shard's targets as there; grad_h is then the sum of the
     shards' results); grad_losses: fp32 of the same
-    shape, the gradient of each token's loss (for a mean, 1/n everywhere); a token
+    shape and contiguous (the expanded one that ``sum()`` hands to a Function's backward
+    is not), the gradient of each token's loss (for a mean, 1/n everywhere); a token
     whose entry is 0 is left out like an ignored one.  Returns (grad_h, grad_w) in
     h's dtype, dense, of h's and w's shape; ``grad_h`` / ``grad_w`` name tensors to
     write (for instance views of a packed reduce buffer), ``need_h`` / ``need_w`` =
